@@ -6,3 +6,6 @@ from .qlora import (  # noqa: F401
     linear_bwd_grouped, linear_fwd, linear_fwd_grouped, linear_fwd_noalloc, linear_fwd_workspace_bytes, load_4bit, load_4bit_info, nf4_codebook, quantize_dq,
     quantize_nf4, save_4bit, table_4bit,
 )
+from .generate import (  # noqa: F401
+    KV_TYPES, KVCache, attend_paged, attend_paged_workspace_bytes, kv_read, kv_write, rope, rope_table,
+)

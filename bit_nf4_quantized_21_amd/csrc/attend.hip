@@ -1,0 +1,600 @@
+// Attention of new tokens over the paged key/value cache (gfx950).
+//
+// Query i of a sequence with n new tokens and `length` stored ones (the new
+// ones among them) stands at position length - n + i and sees the keys j with
+// j < length, j <= position (causal) and j > position - window (window > 0):
+//     s_j = scale q.k_j,   out = sum_j exp(s_j) v_j / sum_j exp(s_j),
+//     lse = log sum_j exp(s_j);   a query that sees nothing gives 0 and -inf.
+// One pass over the keys with a running maximum and sum per query, in fp32 and
+// base 2.  The queries of a group of heads share their key/value head, so a
+// tile's rows are (token, head of the group) pairs of one key/value head.
+#include <algorithm>
+#include <cmath>
+
+#include "common.hpp"
+#include "device_state.hpp"
+#include "kvcache.hpp"
+#include "timing.hpp"
+
+namespace qlora {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kMaxChunk = 16384;  // keys of a split: bounds the page list in LDS
+
+struct AttendArgs {
+  KVPool pool;
+  HeadsView q;
+  int64_t tokens;
+  const int32_t* pages;
+  int64_t width;
+  const int32_t* starts;
+  const int32_t* lengths;
+  int32_t batch, group, max_new, max_len;
+  float scale2;  // scale * log2(e)
+  int32_t causal, window;
+  uint16_t* out;
+  float* lse;
+  float* part_o;   // [splits][tokens][q heads][dim]
+  float* part_ml;  // [splits][tokens][q heads][2]
+  int32_t splits, chunk, tiles;  // keys per split (a multiple of 128), row tiles
+  float levels[16];              // decode table of a 4-bit cache
+  int* status;
+};
+
+// A sequence's tokens and length, held inside what the caller's sizes allow.
+struct Seq {
+  int64_t first;  // row of its first new token
+  int n, len;
+  bool bad;
+};
+__device__ __forceinline__ Seq load_seq(const AttendArgs& a, int b) {
+  int64_t s0 = a.starts[b], s1 = a.starts[b + 1];
+  int64_t len = a.lengths[b];
+  Seq q;
+  q.bad = false;
+  if (s0 < 0 || s0 > a.tokens) { s0 = s0 < 0 ? 0 : a.tokens; q.bad = true; }
+  if (s1 < s0 || s1 > a.tokens) { s1 = s1 < s0 ? s0 : a.tokens; q.bad = true; }
+  if (s1 - s0 > a.max_new) { s1 = s0 + a.max_new; q.bad = true; }
+  int64_t cap = a.width << a.pool.shift;
+  if (cap > a.max_len) cap = a.max_len;
+  if (len < 0 || len > cap) { len = len < 0 ? 0 : cap; q.bad = true; }
+  q.first = s0;
+  q.n = (int)(s1 - s0);
+  q.len = (int)len;
+  return q;
+}
+
+// Keys [lo, hi) that query i sees.
+__device__ __forceinline__ int seen_hi(const AttendArgs& a, const Seq& q, int i) {
+  const int at = q.len - q.n + i + 1;
+  return a.causal ? (at < q.len ? at : q.len) : q.len;
+}
+__device__ __forceinline__ int seen_lo(const AttendArgs& a, const Seq& q, int i) {
+  const int at = q.len - q.n + i + 1 - a.window;
+  return a.window && at > 0 ? at : 0;
+}
+
+// Cross-lane reductions over the four 16-lane groups that share a query.
+__device__ __forceinline__ float max_groups(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16, 64));
+  return fmaxf(x, __shfl_xor(x, 32, 64));
+}
+__device__ __forceinline__ float sum_groups(float x) {
+  x += __shfl_xor(x, 16, 64);
+  return x + __shfl_xor(x, 32, 64);
+}
+
+template <int KT>
+struct Bits {
+  static constexpr int per = KT == kKVBF16 ? 16 : KT == kKVINT8 ? 8 : 4;
+};
+
+// 8 consecutive int8 codes -> 8 bf16 (exact).
+__device__ __forceinline__ bf16x8 int8_to_bf16x8(uint32_t a, uint32_t b) {
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[j] = (float)(int8_t)(a >> (8 * j));
+    f[4 + j] = (float)(int8_t)(b >> (8 * j));
+  }
+  return to_bf16x8(f);
+}
+
+// ---------------------------------------------------------------------------
+// Streaming kernel: 16 * NQ rows of one sequence and key/value head against
+// one split of its keys.  Each of the four waves takes every fourth step of 32
+// keys straight from memory into MFMA operands, with its own running maximum
+// and sum; the waves meet once, in LDS, at the end.
+//
+// S^T = K Q^T by 16x16x32 MFMAs: lane (r = lane & 15, g = lane >> 4) loads the
+// contiguous dims [g DP/4, (g + 1) DP/4) of key r (of each 16-key block) and
+// of query r, so a row is read by four lanes and the dims' order inside the
+// contraction is the same on both sides.  The scores of query r and keys
+// 4g..4g+3 of each block land on lane (r, g).  O^T = V^T P^T takes its keys in
+// that order: element e of lane group g is key 4g + e of block 0 (e < 4) or
+// key 4g + e - 4 of block 1, so the weights go from registers to the MFMA as
+// they are, and lane (r, g) loads dims [r DP/16, (r + 1) DP/16) of those 8
+// keys; MFMA m of the DP/16 takes dim m of each.
+// ---------------------------------------------------------------------------
+template <int KT, int DP, int NQ, bool EXACT>
+__global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
+  constexpr int BITS = Bits<KT>::per;
+  constexpr int NT = DP / 32;               // QK steps
+  constexpr int NM = DP / 16;               // PV MFMAs
+  constexpr int KW = DP / 4 * BITS / 32;    // dwords of a key's quarter row
+  constexpr int VB = DP / 16 * BITS / 8;    // bytes of a value's sixteenth row
+  constexpr int VW = VB < 4 ? 1 : VB / 4;
+  constexpr int OS = DP + 4;                // padded LDS row of the outputs
+  __shared__ __align__(16) float s_o[4 * 16 * OS];
+  __shared__ float s_m[4][16 * NQ], s_l[4][16 * NQ];
+  __shared__ int s_page[kMaxChunk / 16 + 1];
+  __shared__ uint32_t s_lut[KT == kKVNF4 ? 256 : 1];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+  uint32_t id = blockIdx.x;
+  const int split = (int)(id % (uint32_t)a.splits);
+  id /= (uint32_t)a.splits;
+  const int tile = (int)(id % (uint32_t)a.tiles);
+  id /= (uint32_t)a.tiles;
+  const int H = a.pool.heads, h = (int)(id % (uint32_t)H), b = (int)(id / (uint32_t)H);
+  const Seq sq = load_seq(a, b);
+  if (sq.bad && tid == 0) atomicOr(a.status, kStatusIndex);
+  const int G = a.group, rows = sq.n * G, row0 = tile * 16 * NQ;
+  if (row0 >= rows) return;
+  const int i_first = row0 / G, i_last = (min(rows, row0 + 16 * NQ) - 1) / G;
+  const int hi = seen_hi(a, sq, i_last), lo = seen_lo(a, sq, i_first);
+  const int k0 = (lo & ~15) + split * a.chunk;
+  if (split > 0 && k0 >= hi) return;
+  const int k1 = min(hi, k0 + a.chunk);
+  // Steps inside [full_lo, full_hi) are seen by every row.
+  const int full_hi = seen_hi(a, sq, i_first), full_lo = seen_lo(a, sq, i_last);
+
+  const int shift = a.pool.shift, first_page = k0 >> shift;
+  for (int p = tid; k0 < k1 && p <= ((k1 - 1) >> shift) - first_page; p += 256) {
+    int page = a.pages[(int64_t)b * a.width + first_page + p];
+    if (page < 0 || page >= a.pool.pages) {
+      atomicOr(a.status, kStatusIndex);
+      page = 0;
+    }
+    s_page[p] = page;
+  }
+  if (KT == kKVNF4) {
+    float lo_v = a.levels[0], hi_v = a.levels[0];
+#pragma unroll
+    for (int e = 1; e < 16; ++e) {
+      lo_v = (tid & 15) == e ? a.levels[e] : lo_v;
+      hi_v = (tid >> 4) == e ? a.levels[e] : hi_v;
+    }
+    s_lut[tid] = pack_bf16x2(lo_v, hi_v);
+  }
+  __syncthreads();
+
+  const int D = a.pool.dim;
+  // Queries: row m of the tile is token m / G, head h * G + m % G.
+  bf16x8 q[NQ][NT];
+  int my_lo[NQ], my_hi[NQ];
+#pragma unroll
+  for (int x = 0; x < NQ; ++x) {
+    const int row = row0 + 16 * x + r;
+    const bool ok = row < rows;
+    const int i = ok ? row / G : 0, gh = ok ? row - i * G : 0;
+    my_lo[x] = seen_lo(a, sq, i);
+    my_hi[x] = ok ? seen_hi(a, sq, i) : 0;
+    const uint16_t* p = a.q.data + (sq.first + i) * a.q.token_stride + (int64_t)(h * G + gh) * a.q.head_stride;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int d = g * (DP / 4) + t * 8;
+      u32x4 w = {0, 0, 0, 0};
+      if (ok && (EXACT || d < D)) w = *reinterpret_cast<const u32x4*>(p + d);
+      q[x][t] = as_bf16x8(w);
+    }
+  }
+
+  f32x4 o[NQ][NM];
+  float m[NQ], l[NQ];
+#pragma unroll
+  for (int x = 0; x < NQ; ++x) {
+    m[x] = -INFINITY;
+    l[x] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < NM; ++t) o[x][t] = f32x4{0, 0, 0, 0};
+  }
+
+  const int64_t row_bytes = kv_row_bytes(a.pool.type, D);
+  const int k_off = g * (DP / 4) * BITS / 8, v_off = r * VB;
+  for (int j0 = k0 + 32 * wave; j0 < k1; j0 += 128) {
+    uint32_t kw[2][KW], vw[8][VW];
+    float4 ks[2], vs[2];
+    // The last block's page may lie past the list: its keys are not seen.
+    const int last = ((k1 - 1) >> shift) - first_page;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int j = j0 + 16 * c;
+      const int pi = min((j >> shift) - first_page, last);
+      const int64_t base = (((int64_t)s_page[pi] * H + h) << shift) + (j & ((1 << shift) - 1));
+      const uint8_t* kp = a.pool.k + (base + r) * row_bytes + k_off;
+      if (EXACT) {
+#pragma unroll
+        for (int w = 0; w < KW; w += (KW % 4 == 0 ? 4 : 2)) {
+          if (KW % 4 == 0) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(kp + 4 * w);
+            kw[c][w] = v[0]; kw[c][w + 1] = v[1]; kw[c][(w + 2) % KW] = v[2]; kw[c][(w + 3) % KW] = v[3];
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(kp + 4 * w);
+            kw[c][w] = v.x; kw[c][w + 1] = v.y;
+          }
+        }
+      } else {
+        constexpr int SW = KW / NT;  // dwords of 8 elements
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const bool in = g * (DP / 4) + t * 8 < D;
+#pragma unroll
+          for (int w = 0; w < SW; ++w) kw[c][t * SW + w] = in ? reinterpret_cast<const uint32_t*>(kp)[t * SW + w] : 0u;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint8_t* vp = a.pool.v + (base + 4 * g + e) * row_bytes + v_off;
+        uint32_t(&w)[VW] = vw[4 * c + e];
+        if (EXACT || r * (DP / 16) < D) {
+          if (VB >= 16) {
+#pragma unroll
+            for (int x = 0; x < VW; x += 4) {
+              const u32x4 v = *reinterpret_cast<const u32x4*>(vp + 4 * x);
+              w[x] = v[0]; w[(x + 1) % VW] = v[1]; w[(x + 2) % VW] = v[2]; w[(x + 3) % VW] = v[3];
+            }
+          } else if (VB == 8) {
+            const uint2 v = *reinterpret_cast<const uint2*>(vp);
+            w[0] = v.x; w[1 % VW] = v.y;
+          } else if (VB == 4) {
+            w[0] = *reinterpret_cast<const uint32_t*>(vp);
+          } else {
+            w[0] = *reinterpret_cast<const uint16_t*>(vp);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < VW; ++x) w[x] = 0;
+        }
+      }
+      if (KT != kKVBF16) {
+        ks[c] = *reinterpret_cast<const float4*>(a.pool.ks + base + 4 * g);
+        vs[c] = *reinterpret_cast<const float4*>(a.pool.vs + base + 4 * g);
+      } else {
+        ks[c] = vs[c] = make_float4(1, 1, 1, 1);
+      }
+    }
+
+    f32x4 s[NQ][2];
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) s[x][0] = s[x][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        bf16x8 ka;
+        if constexpr (KT == kKVBF16) {
+          ka = as_bf16x8(kw[c][4 * t], kw[c][4 * t + 1], kw[c][4 * t + 2], kw[c][4 * t + 3]);
+        } else if constexpr (KT == kKVINT8) {
+          ka = int8_to_bf16x8(kw[c][2 * t], kw[c][2 * t + 1]);
+        } else {
+          const uint32_t w = kw[c][t];
+          ka = as_bf16x8(s_lut[w & 255u], s_lut[(w >> 8) & 255u], s_lut[(w >> 16) & 255u], s_lut[w >> 24]);
+        }
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) s[x][c] = mfma16(ka, q[x][t], s[x][c]);
+      }
+
+    const bool edge = j0 < full_lo || j0 + 32 > full_hi;
+    // Keys of the edge: those that no row of the tile sees hold anything (the
+    // tail of a page, a page that was given back), so their values become 0;
+    // a bf16 value that is not finite must not reach rows that do not see its
+    // key through 0 * inf, so it becomes 0 too and the rows that do see it get
+    // a NaN weight instead.
+    bool wild[8] = {};
+    if (KT == kKVBF16 && edge) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = j0 + 16 * (e / 4) + 4 * g + e % 4;
+        const bool any = j >= lo && j < hi;
+        bool bad = false;
+#pragma unroll
+        for (int x = 0; x < VW; ++x) {
+          uint32_t w = any ? vw[e][x] : 0u;
+          if ((w & 0x7F80u) == 0x7F80u) { w &= 0xFFFF0000u; bad = true; }
+          if ((w & 0x7F800000u) == 0x7F800000u) { w &= 0xFFFFu; bad = true; }
+          vw[e][x] = w;
+        }
+        wild[e] = ((__ballot(bad) >> (16 * g)) & 0xFFFFu) != 0;
+      }
+    }
+
+    bf16x8 pb[NQ];
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) {
+      float p[8];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float kk[4] = {ks[c].x, ks[c].y, ks[c].z, ks[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[4 * c + e] = s[x][c][e] * (KT == kKVBF16 ? a.scale2 : a.scale2 * kk[e]);
+      }
+      uint32_t hidden = 0;
+      if (edge) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int j = j0 + 16 * (e / 4) + 4 * g + e % 4;
+          if (j < my_lo[x] || j >= my_hi[x]) {
+            hidden |= 1u << e;
+            p[e] = -INFINITY;
+          }
+        }
+      }
+      float top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
+      top = fmaxf(max_groups(top), m[x]);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      if (__any(top > m[x])) {
+        const float f = __builtin_amdgcn_exp2f(m[x] - ref);
+        l[x] *= f;
+#pragma unroll
+        for (int t = 0; t < NM; ++t) o[x][t] *= f;
+        m[x] = top;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(p[e] - ref);
+      l[x] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+      if (KT != kKVBF16) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float vv[4] = {vs[c].x, vs[c].y, vs[c].z, vs[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[4 * c + e] = (hidden >> (4 * c + e)) & 1u ? 0.0f : p[4 * c + e] * vv[e];
+        }
+      } else if (edge) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (wild[e] && !((hidden >> e) & 1u)) p[e] = __uint_as_float(0x7FC00000u);
+      }
+      // The weights enter the second product as bf16 (their sum stays fp32):
+      // half a unit in the 8th bit of each, against the output's own rounding
+      // to as many bits.
+      pb[x] = to_bf16x8(p);
+    }
+
+    // Values of dim t for the lane's 8 keys, two keys to a dword.
+#pragma unroll
+    for (int t = 0; t < NM; ++t) {
+      uint32_t w[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t(&va)[VW] = vw[2 * c];
+        const uint32_t(&vb)[VW] = vw[2 * c + 1];
+        if constexpr (KT == kKVBF16) {
+          w[c] = __builtin_amdgcn_perm(vb[t / 2], va[t / 2], t & 1 ? 0x07060302u : 0x05040100u);
+        } else if constexpr (KT == kKVINT8) {
+          w[c] = pack_bf16x2((float)(int8_t)(va[t / 4] >> (8 * (t % 4))), (float)(int8_t)(vb[t / 4] >> (8 * (t % 4))));
+        } else {
+          const uint32_t ca = (va[t / 8] >> (4 * (t % 8))) & 15u, cb = (vb[t / 8] >> (4 * (t % 8))) & 15u;
+          w[c] = s_lut[ca | (cb << 4)];
+        }
+      }
+      const bf16x8 vt = as_bf16x8(w[0], w[1], w[2], w[3]);
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) o[x][t] = mfma16(vt, pb[x], o[x][t]);
+    }
+  }
+
+  // The four waves' sums meet.  Lane (r, g) holds, of query r, the dims
+  // g DP/4 + i NM + t (register i of MFMA t).
+#pragma unroll
+  for (int x = 0; x < NQ; ++x) {
+    l[x] = sum_groups(l[x]);
+    if (g == 0) {
+      s_m[wave][16 * x + r] = m[x];
+      s_l[wave][16 * x + r] = l[x];
+    }
+  }
+  __syncthreads();
+  const int Hq = H * G;
+#pragma unroll
+  for (int x = 0; x < NQ; ++x) {
+    {
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, s_m[w][16 * x + r]);
+      const float f = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[x] - top);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < NM; t += 4)
+          *reinterpret_cast<float4*>(s_o + (wave * 16 + r) * OS + g * (DP / 4) + i * NM + t) =
+              make_float4(o[x][t][i] * f, o[x][t + 1][i] * f, o[x][t + 2][i] * f, o[x][t + 3][i] * f);
+    }
+    __syncthreads();
+    const int qr = tid >> 4, part = tid & 15, row = row0 + 16 * x + qr;
+    if (row < rows) {
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, s_m[w][16 * x + qr]);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) sum += s_l[w][16 * x + qr] * (top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(s_m[w][16 * x + qr] - top));
+      const int i = row / G, gh = row - i * G;
+      const int64_t at = (sq.first + i) * Hq + h * G + gh;
+      const float inv = a.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+      if (part == 0) {
+        if (a.splits > 1) {
+          float* ml = a.part_ml + ((int64_t)split * a.tokens * Hq + at) * 2;
+          ml[0] = top;
+          ml[1] = sum;
+        } else if (a.lse) {
+          a.lse[at] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+        }
+      }
+      if (EXACT || part * NM < D) {
+#pragma unroll
+        for (int t = 0; t < NM; t += 4) {
+          float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float4 p = *reinterpret_cast<const float4*>(s_o + (w * 16 + qr) * OS + part * NM + t);
+            v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+          }
+          if (a.splits > 1) {
+            *reinterpret_cast<float4*>(a.part_o + ((int64_t)split * a.tokens * Hq + at) * D + part * NM + t) = v;
+          } else {
+            *reinterpret_cast<uint2*>(a.out + at * D + part * NM + t) =
+                make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the splits of a row: one wave per (token, query head).
+template <int DP>
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int tile_rows) {
+  constexpr int NE = DP / 64;
+  const int lane = threadIdx.x & 63, b = blockIdx.y;
+  const int H = a.pool.heads, G = a.group, Hq = H * G, D = a.pool.dim;
+  const int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const Seq sq = load_seq(a, b);
+  if (e >= (int64_t)sq.n * Hq) return;
+  const int i = (int)(e / Hq), hq = (int)(e - (int64_t)i * Hq), rows = sq.n * G;
+  const int row0 = (i * G + hq % G) / tile_rows * tile_rows;
+  const int hi = seen_hi(a, sq, (min(rows, row0 + tile_rows) - 1) / G), lo = seen_lo(a, sq, row0 / G) & ~15;
+  const int n = hi <= lo ? 1 : (hi - lo + a.chunk - 1) / a.chunk;
+  const int64_t at = (sq.first + i) * Hq + hq, step = a.tokens * Hq;
+  float top = -INFINITY;
+  for (int s = 0; s < n; ++s) top = fmaxf(top, a.part_ml[(s * step + at) * 2]);
+  float sum = 0.0f, acc[NE] = {};
+  for (int s = 0; s < n; ++s) {
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (s * step + at) * 2);
+    const float f = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+    sum += ml.y * f;
+#pragma unroll
+    for (int x = 0; x < NE; ++x) {
+      const int d = lane + 64 * x;
+      if (d < D) acc[x] += a.part_o[(s * step + at) * D + d] * f;
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int x = 0; x < NE; ++x) {
+    const int d = lane + 64 * x;
+    if (d < D) a.out[at * D + d] = (uint16_t)(pack_bf16x2(acc[x] * inv, 0.0f) & 0xFFFFu);
+  }
+  if (lane == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+// How a problem is cut: rows per tile, row tiles, splits of the keys and the
+// keys of a split.
+struct Plan {
+  int nq, tile_rows;
+  int64_t tiles, splits, chunk;
+};
+
+Plan make_plan(const AttendProblem& p) {
+  Plan r{};
+  const int64_t group = p.q.heads / p.pool.heads, rows = p.max_new * group;
+  r.nq = rows > 16 ? 2 : 1;
+  r.tile_rows = 16 * r.nq;
+  r.tiles = std::max<int64_t>(1, (rows + r.tile_rows - 1) / r.tile_rows);
+  // Keys that a tile can see.
+  int64_t span = p.max_len;
+  if (p.window > 0 && p.causal) span = std::min<int64_t>(span, (int64_t)p.window + r.tile_rows + 16);
+  // Workgroups wanted: four per CU, each with at least 256 keys.
+  const int64_t work = std::max<int64_t>(1, (int64_t)p.batch * p.pool.heads * r.tiles);
+  int64_t splits = std::min((1024 + work - 1) / work, (span + 255) / 256);
+  splits = std::max<int64_t>(splits, 1);
+  r.chunk = ((span + 15 + splits - 1) / splits + 127) / 128 * 128;
+  r.chunk = std::min<int64_t>(std::max<int64_t>(r.chunk, 128), kMaxChunk);
+  r.splits = std::max<int64_t>(1, (span + 15 + r.chunk - 1) / r.chunk);
+  return r;
+}
+
+template <int KT, int DP, int NQ>
+void stream_dim(const AttendArgs& a, unsigned grid, hipStream_t s) {
+  if (a.pool.dim == DP) hipLaunchKernelGGL((attend_stream_kernel<KT, DP, NQ, true>), dim3(grid), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((attend_stream_kernel<KT, DP, NQ, false>), dim3(grid), dim3(256), 0, s, a);
+}
+template <int KT, int NQ>
+void stream_type(const AttendArgs& a, unsigned grid, hipStream_t s) {
+  if (a.pool.dim <= 64) stream_dim<KT, 64, NQ>(a, grid, s);
+  else if (a.pool.dim <= 128) stream_dim<KT, 128, NQ>(a, grid, s);
+  else stream_dim<KT, 256, NQ>(a, grid, s);
+}
+template <int NQ>
+void stream_rows(const AttendArgs& a, unsigned grid, hipStream_t s) {
+  if (a.pool.type == kKVBF16) stream_type<kKVBF16, NQ>(a, grid, s);
+  else if (a.pool.type == kKVINT8) stream_type<kKVINT8, NQ>(a, grid, s);
+  else stream_type<kKVNF4, NQ>(a, grid, s);
+}
+
+}  // namespace
+
+bool attend_fits(const AttendProblem& p) {
+  const Plan r = make_plan(p);
+  const int64_t groups = (int64_t)p.batch * p.pool.heads;
+  return r.tiles < (int64_t(1) << 31) && groups * r.tiles < (int64_t(1) << 31) &&
+         groups * r.tiles * r.splits < (int64_t(1) << 31);
+}
+
+size_t attend_workspace_bytes(const AttendProblem& p) {
+  const Plan r = make_plan(p);
+  if (r.splits <= 1) return 0;
+  const int64_t rows = r.splits * p.tokens * p.q.heads;
+  return (size_t)(rows * 2 * 4 + 255) / 256 * 256 + (size_t)rows * p.pool.dim * 4;
+}
+
+hipError_t launch_attend(const AttendProblem& p, const float table[16], void* ws, hipStream_t s) {
+  AttendArgs a{};
+  hipError_t e = hipSuccess;
+  a.status = status_word(&e);
+  if (!a.status) return e;
+  const Plan r = make_plan(p);
+  a.pool = p.pool;
+  a.q = p.q;
+  a.tokens = p.tokens;
+  a.pages = p.pages;
+  a.width = p.width;
+  a.starts = p.starts;
+  a.lengths = p.lengths;
+  a.batch = p.batch;
+  a.group = p.q.heads / p.pool.heads;
+  a.max_new = p.max_new;
+  a.max_len = p.max_len;
+  a.scale2 = p.scale * kLog2e;
+  a.causal = p.causal;
+  a.window = p.window;
+  a.out = p.out;
+  a.lse = p.lse;
+  a.splits = (int32_t)r.splits;
+  a.chunk = (int32_t)r.chunk;
+  a.tiles = (int32_t)r.tiles;
+  for (int c = 0; c < 16; ++c) a.levels[c] = table ? table[c] : 0.0f;
+  if (r.splits > 1) {
+    const size_t ml = (size_t)(r.splits * p.tokens * p.q.heads * 2 * 4 + 255) / 256 * 256;
+    a.part_ml = static_cast<float*>(ws);
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + ml);
+  }
+  {
+    KernelTimer kt_("attend_stream_kernel", s);
+    const unsigned grid = (unsigned)(p.batch * p.pool.heads * r.tiles * r.splits);
+    if (r.nq == 1) stream_rows<1>(a, grid, s);
+    else stream_rows<2>(a, grid, s);
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess || r.splits == 1) return e;
+  KernelTimer kt_("attend_join_kernel", s);
+  const dim3 grid((unsigned)(((int64_t)p.max_new * p.q.heads + 3) / 4), (unsigned)p.batch);
+  if (p.pool.dim <= 64) hipLaunchKernelGGL(attend_join_kernel<64>, grid, dim3(256), 0, s, a, r.tile_rows);
+  else if (p.pool.dim <= 128) hipLaunchKernelGGL(attend_join_kernel<128>, grid, dim3(256), 0, s, a, r.tile_rows);
+  else hipLaunchKernelGGL(attend_join_kernel<256>, grid, dim3(256), 0, s, a, r.tile_rows);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

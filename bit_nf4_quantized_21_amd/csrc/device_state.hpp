@@ -8,6 +8,7 @@
 namespace qlora {
 
 constexpr int kStatusSplitWait = 1;  // a split-contraction finisher stopped waiting for its slices
+constexpr int kStatusIndex = 2;      // a page, slot, position, length or start in device memory was out of range
 
 // Device address of the current device's status word (looked up once per
 // device with hipGetSymbolAddress); nullptr with *err set on failure.

@@ -1,0 +1,83 @@
+// Rotary positions, the paged key/value cache and attention over it: host
+// structures shared by the kernels' launchers and the C entry points.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace qlora {
+
+struct Midpoints;
+
+// Element types of a cache (values of qlora_kv_type).
+enum KVType { kKVBF16 = 0, kKVINT8 = 1, kKVNF4 = 2, kKVINT4 = 3, kKVFP4 = 4, kKVTypes = 5 };
+
+// [tokens, heads, dim] bf16 with the dims of a head contiguous.
+struct HeadsView {
+  uint16_t* data;
+  int64_t token_stride, head_stride;  // elements
+  int32_t heads;
+};
+
+// Page p holds, head by head, its page_size rows of `dim` elements; row
+// (p, h, s) is number ((p * heads + h) << shift) + s of codes and scales.
+struct KVPool {
+  uint8_t* k;
+  uint8_t* v;
+  float* ks;  // one fp32 scale per row (null for bf16)
+  float* vs;
+  int32_t type, heads, dim, shift;  // page_size = 1 << shift
+  int64_t pages;
+};
+
+// Bytes of a row's codes.
+__host__ __device__ __forceinline__ int64_t kv_row_bytes(int type, int dim) {
+  return type == kKVBF16 ? 2 * dim : type == kKVINT8 ? dim : dim / 2;
+}
+
+// A cos/sin table and the positions that pick its rows; table = null: no
+// rotation.
+struct RopeTable {
+  const float* table;  // [n][rot / 2][2]
+  int64_t n;
+  const int32_t* positions;  // [tokens]
+  int32_t rot, interleaved;
+};
+
+struct RopeTableArgs {
+  int64_t n;
+  int32_t rot, scaling;
+  double base, factor, original, low, high, amplitude;
+};
+hipError_t launch_rope_table(const RopeTableArgs& a, float* table, hipStream_t s);
+
+hipError_t launch_rope(int64_t T, int32_t dim, const RopeTable& t, bool inverse, const HeadsView& q,
+                       const HeadsView& q_out, const HeadsView& k, const HeadsView& k_out, hipStream_t s);
+
+hipError_t launch_kv_write(const KVPool& pool, int64_t T, const HeadsView& k, const HeadsView& v,
+                           const int64_t* slots, const RopeTable& rope, const Midpoints& mp, hipStream_t s);
+hipError_t launch_kv_read(const KVPool& pool, int64_t T, const int64_t* slots, uint16_t* k, uint16_t* v,
+                          const float table[16], hipStream_t s);
+
+struct AttendProblem {
+  KVPool pool;
+  HeadsView q;
+  int64_t tokens;
+  int32_t batch;
+  const int32_t* pages;  // [batch][width]
+  int64_t width;
+  const int32_t* starts;   // [batch + 1]
+  const int32_t* lengths;  // [batch]
+  int32_t max_new, max_len;
+  float scale;
+  int32_t causal, window;
+  uint16_t* out;
+  float* lse;  // may be null
+};
+size_t attend_workspace_bytes(const AttendProblem& p);
+// False when a launch of this problem would exceed a grid or index limit.
+bool attend_fits(const AttendProblem& p);
+hipError_t launch_attend(const AttendProblem& p, const float table[16], void* ws, hipStream_t s);
+
+}  // namespace qlora

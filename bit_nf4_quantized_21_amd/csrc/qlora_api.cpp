@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <string>
@@ -14,6 +15,7 @@
 #include "common.hpp"
 #include "device_state.hpp"
 #include "kernels.hpp"
+#include "kvcache.hpp"
 #include "storage.hpp"
 #include "timing.hpp"
 
@@ -129,6 +131,9 @@ const char* qlora_status_string(int status) {
       return "QLORA_ERR_SCRATCH: the problem needs more scratch than the no-allocation entry point holds";
     case QLORA_ERR_DEVICE:
       return "QLORA_ERR_DEVICE: a kernel's bounded wait ran out; results since the last status query are unreliable";
+    case QLORA_ERR_INDEX:
+      return "QLORA_ERR_INDEX: a page, slot, position, length or start was out of range; results since the last "
+             "status query are unreliable";
     default: return "unknown qlora_status";
   }
 }
@@ -139,7 +144,7 @@ int qlora_device_status(void* stream) {
   int bits = 0;
   const int st = hip_status(qlora::take_status((hipStream_t)stream, &bits));
   if (st != QLORA_OK) return st;
-  return bits ? QLORA_ERR_DEVICE : QLORA_OK;
+  return bits & qlora::kStatusSplitWait ? QLORA_ERR_DEVICE : bits ? QLORA_ERR_INDEX : QLORA_OK;
 }
 
 void qlora_timing_enable(int on) { qlora::timing_enable(on != 0); }
@@ -458,6 +463,201 @@ int qlora_linear_bwd(const uint16_t* dY, const uint16_t* X, const float* XA, int
                      size_t workspace_bytes, void* stream) {
   return qlora_linear_bwd_4bit(qlora::kQNF4, dY, X, XA, T, K, N, codes, q8, s2, A, B, r, alpha, dX, dA, dB, workspace,
                                workspace_bytes, stream);
+}
+
+namespace {
+// 31-bit extents keep every index and byte count of the kernels inside int64.
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+
+int check_dim(int32_t dim) { return dim >= 16 && dim <= 256 && dim % 16 == 0 ? QLORA_OK : QLORA_ERR_UNSUPPORTED; }
+
+int check_heads(const qlora_heads* h, qlora::HeadsView* out) {
+  if (!h) return QLORA_ERR_NULL;
+  if (h->heads < 1 || h->heads > (1 << 16)) return QLORA_ERR_SHAPE;
+  if (h->token_stride % 8 != 0 || h->head_stride % 8 != 0) return QLORA_ERR_ALIGN;
+  if (std::llabs(h->token_stride) > (int64_t(1) << 32) || std::llabs(h->head_stride) > (int64_t(1) << 32))
+    return QLORA_ERR_SHAPE;
+  if (!h->data) return QLORA_ERR_NULL;
+  if (!aligned16(h->data)) return QLORA_ERR_ALIGN;
+  *out = qlora::HeadsView{h->data, h->token_stride, h->head_stride, h->heads};
+  return QLORA_OK;
+}
+
+int check_rope(int32_t dim, int32_t rot, int32_t interleaved, const float* table, int64_t n, const int32_t* positions,
+               qlora::RopeTable* out) {
+  if (rot < 16 || rot > dim || rot % 16 != 0 || (interleaved != 0 && interleaved != 1)) return QLORA_ERR_UNSUPPORTED;
+  if (n < 1 || n > kMaxTokens) return QLORA_ERR_SHAPE;
+  if (!table || !positions) return QLORA_ERR_NULL;
+  if (!aligned16(table) || (reinterpret_cast<uintptr_t>(positions) & 3u)) return QLORA_ERR_ALIGN;
+  *out = qlora::RopeTable{table, n, positions, rot, interleaved};
+  return QLORA_OK;
+}
+
+// `buffers` = false: only the cache's shape (workspace queries).
+int check_cache(const qlora_kv_cache* c, bool buffers, qlora::KVPool* out) {
+  if (!c) return QLORA_ERR_NULL;
+  if (c->type < 0 || c->type >= qlora::kKVTypes) return QLORA_ERR_UNSUPPORTED;
+  int st = check_dim(c->dim);
+  if (st != QLORA_OK) return st;
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return QLORA_ERR_UNSUPPORTED;
+  if (c->heads < 1 || c->heads > (1 << 16) || c->pages < 1 || c->pages > INT32_MAX) return QLORA_ERR_SHAPE;
+  int shift = 0;
+  while ((1 << shift) < c->page_size) ++shift;
+  if (buffers) {
+    if (!c->k || !c->v) return QLORA_ERR_NULL;
+    if (!aligned16(c->k) || !aligned16(c->v)) return QLORA_ERR_ALIGN;
+    if (c->type != qlora::kKVBF16) {
+      if (!c->k_scale || !c->v_scale) return QLORA_ERR_NULL;
+      if (!aligned16(c->k_scale) || !aligned16(c->v_scale)) return QLORA_ERR_ALIGN;
+    }
+  }
+  *out = qlora::KVPool{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_scale, c->v_scale,
+                       c->type, c->heads, c->dim, shift, c->pages};
+  return QLORA_OK;
+}
+
+// The stored 4-bit type of a cache (NF4 where it has none: not used then).
+const TypeTables* cache_tables(int32_t type) {
+  return type_tables(type == qlora::kKVINT4 ? qlora::kQINT4 : type == qlora::kKVFP4 ? qlora::kQFP4 : qlora::kQNF4);
+}
+
+int check_attend(const qlora_kv_cache* cache, bool buffers, int64_t tokens, int32_t q_heads, int32_t batch,
+                 int64_t pages_per_seq, int64_t max_new, int64_t max_len, int32_t causal, int64_t window,
+                 qlora::AttendProblem* p) {
+  int st = check_cache(cache, buffers, &p->pool);
+  if (st != QLORA_OK) return st;
+  if (tokens < 0 || tokens > kMaxTokens || batch < 0 || max_new < 0 || max_len < 0 || max_len > kMaxTokens || window < 0)
+    return QLORA_ERR_SHAPE;
+  if (q_heads < 1 || q_heads > (1 << 16) || q_heads % cache->heads != 0) return QLORA_ERR_SHAPE;
+  if (causal != 0 && causal != 1) return QLORA_ERR_UNSUPPORTED;
+  if (pages_per_seq < 0 || (pages_per_seq << p->pool.shift) < max_len || pages_per_seq > kMaxTokens) return QLORA_ERR_SHAPE;
+  if (max_new > tokens) max_new = tokens;
+  if (batch > 65535) return QLORA_ERR_SHAPE;
+  p->tokens = tokens;
+  p->q.heads = q_heads;
+  p->batch = batch;
+  p->width = pages_per_seq;
+  p->max_new = (int32_t)max_new;
+  p->max_len = (int32_t)max_len;
+  p->causal = causal;
+  p->window = (int32_t)(window > max_len ? 0 : window);  // a window over everything hides nothing
+  return qlora::attend_fits(*p) ? QLORA_OK : QLORA_ERR_SHAPE;
+}
+}  // namespace
+
+int qlora_rope_table(int64_t positions, int32_t rot, double base, int32_t scaling, double factor, double original,
+                     double low, double high, double amplitude, float* table, void* stream) {
+  if (rot < 16 || rot > 256 || rot % 16 != 0) return QLORA_ERR_UNSUPPORTED;
+  if (scaling < QLORA_ROPE_NONE || scaling > QLORA_ROPE_BANDS) return QLORA_ERR_UNSUPPORTED;
+  if (!(base > 0.0) || !std::isfinite(base) || !(amplitude > 0.0) || !std::isfinite(amplitude))
+    return QLORA_ERR_UNSUPPORTED;
+  if (scaling != QLORA_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return QLORA_ERR_UNSUPPORTED;
+  if (scaling == QLORA_ROPE_BANDS && (!(original >= 1.0) || !std::isfinite(original) || !(low >= 0.0) ||
+                                      !(high > low) || !std::isfinite(high)))
+    return QLORA_ERR_UNSUPPORTED;
+  if (positions < 0 || positions > kMaxTokens) return QLORA_ERR_SHAPE;
+  if (positions == 0) return QLORA_OK;
+  if (!table) return QLORA_ERR_NULL;
+  if (!aligned16(table)) return QLORA_ERR_ALIGN;
+  const qlora::RopeTableArgs a{positions, rot, scaling, base, factor, original, low, high, amplitude};
+  return hip_status(qlora::launch_rope_table(a, table, (hipStream_t)stream));
+}
+
+int qlora_rope(int64_t T, int32_t dim, int32_t rot, int32_t interleaved, int32_t inverse, const float* table,
+               int64_t table_positions, const int32_t* positions, const qlora_heads* q, const qlora_heads* q_out,
+               const qlora_heads* k, const qlora_heads* k_out, void* stream) {
+  int st = check_dim(dim);
+  if (st != QLORA_OK) return st;
+  if (inverse != 0 && inverse != 1) return QLORA_ERR_UNSUPPORTED;
+  if (T < 0 || T > kMaxTokens) return QLORA_ERR_SHAPE;
+  if (T == 0) return QLORA_OK;
+  qlora::RopeTable t{};
+  if ((st = check_rope(dim, rot, interleaved, table, table_positions, positions, &t)) != QLORA_OK) return st;
+  qlora::HeadsView qi{}, qo{}, ki{}, ko{};
+  if ((st = check_heads(q, &qi)) != QLORA_OK || (st = check_heads(q_out, &qo)) != QLORA_OK) return st;
+  if (qo.heads != qi.heads) return QLORA_ERR_SHAPE;
+  if (k || k_out) {
+    if ((st = check_heads(k, &ki)) != QLORA_OK || (st = check_heads(k_out, &ko)) != QLORA_OK) return st;
+    if (ko.heads != ki.heads) return QLORA_ERR_SHAPE;
+  }
+  if (T * (int64_t)(qi.heads + ki.heads) > (int64_t(1) << 35)) return QLORA_ERR_SHAPE;
+  return hip_status(qlora::launch_rope(T, dim, t, inverse != 0, qi, qo, ki, ko, (hipStream_t)stream));
+}
+
+int qlora_kv_write(const qlora_kv_cache* cache, int64_t T, const qlora_heads* k, const qlora_heads* v,
+                   const int64_t* slots, const float* table, int64_t table_positions, const int32_t* positions,
+                   int32_t rot, int32_t interleaved, void* stream) {
+  if (T < 0 || T > kMaxTokens) return QLORA_ERR_SHAPE;
+  if (T == 0) return QLORA_OK;
+  qlora::KVPool pool{};
+  int st = check_cache(cache, true, &pool);
+  if (st != QLORA_OK) return st;
+  qlora::HeadsView kv{}, vv{};
+  if ((st = check_heads(k, &kv)) != QLORA_OK || (st = check_heads(v, &vv)) != QLORA_OK) return st;
+  if (kv.heads != pool.heads || vv.heads != pool.heads || T * (int64_t)pool.heads > (int64_t(1) << 34))
+    return QLORA_ERR_SHAPE;
+  if (!slots) return QLORA_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(slots) & 7u) return QLORA_ERR_ALIGN;
+  qlora::RopeTable t{};
+  if (table && (st = check_rope(pool.dim, rot, interleaved, table, table_positions, positions, &t)) != QLORA_OK)
+    return st;
+  const TypeTables* tt = cache_tables(pool.type);
+  if (!tt) return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_kv_write(pool, T, kv, vv, slots, t, tt->mp, (hipStream_t)stream));
+}
+
+int qlora_kv_read(const qlora_kv_cache* cache, int64_t T, const int64_t* slots, uint16_t* k, uint16_t* v,
+                  void* stream) {
+  if (T < 0 || T > kMaxTokens) return QLORA_ERR_SHAPE;
+  if (T == 0) return QLORA_OK;
+  qlora::KVPool pool{};
+  const int st = check_cache(cache, true, &pool);
+  if (st != QLORA_OK) return st;
+  if (T * (int64_t)pool.heads > (int64_t(1) << 34)) return QLORA_ERR_SHAPE;
+  if (!slots || !k || !v) return QLORA_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(slots) & 7u) || !aligned16(k) || !aligned16(v)) return QLORA_ERR_ALIGN;
+  const TypeTables* tt = cache_tables(pool.type);
+  if (!tt) return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_kv_read(pool, T, slots, k, v, tt->cb.c, (hipStream_t)stream));
+}
+
+size_t qlora_attend_paged_workspace_bytes(const qlora_kv_cache* cache, int64_t tokens, int32_t q_heads, int32_t batch,
+                                          int64_t max_new, int64_t max_len, int32_t causal, int64_t window) {
+  qlora::AttendProblem p{};
+  if (check_attend(cache, false, tokens, q_heads, batch, kMaxTokens / 16, max_new, max_len, causal, window, &p) !=
+      QLORA_OK)
+    return 0;
+  if (tokens == 0 || batch == 0 || max_new == 0) return 0;
+  return qlora::attend_workspace_bytes(p);
+}
+
+int qlora_attend_paged(const qlora_kv_cache* cache, int64_t tokens, const qlora_heads* q, int32_t batch,
+                       const int32_t* pages, int64_t pages_per_seq, const int32_t* starts, const int32_t* lengths,
+                       int64_t max_new, int64_t max_len, float scale, int32_t causal, int64_t window, uint16_t* out,
+                       float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  qlora::AttendProblem p{};
+  if (!q) return QLORA_ERR_NULL;
+  int st = check_attend(cache, true, tokens, q->heads, batch, pages_per_seq, max_new, max_len, causal, window, &p);
+  if (st != QLORA_OK) return st;
+  if (!std::isfinite(scale)) return QLORA_ERR_UNSUPPORTED;
+  if (tokens == 0 || batch == 0 || max_new == 0) return QLORA_OK;
+  if ((st = check_heads(q, &p.q)) != QLORA_OK) return st;
+  if ((max_len > 0 && !pages) || !starts || !lengths || !out) return QLORA_ERR_NULL;
+  if (!aligned16(out) || ((reinterpret_cast<uintptr_t>(pages) | reinterpret_cast<uintptr_t>(starts) |
+                           reinterpret_cast<uintptr_t>(lengths) | reinterpret_cast<uintptr_t>(lse)) & 3u))
+    return QLORA_ERR_ALIGN;
+  const size_t need = qlora::attend_workspace_bytes(p);
+  if (need && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
+  if (need && !aligned16(workspace)) return QLORA_ERR_ALIGN;
+  p.pages = pages;
+  p.starts = starts;
+  p.lengths = lengths;
+  p.scale = scale;
+  p.out = out;
+  p.lse = lse;
+  const TypeTables* tt = cache_tables(p.pool.type);
+  if (!tt) return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_attend(p, tt->cb.c, workspace, (hipStream_t)stream));
 }
 
 int qlora_save_4bit(const char* path, int32_t qtype, int64_t N, int64_t K, const uint8_t* codes, const uint8_t* q8,

@@ -34,6 +34,21 @@ class LinearBwdDesc(ctypes.Structure):
                 ("dB", ctypes.c_void_p), ("K", ctypes.c_int64), ("N", ctypes.c_int64)]
 
 
+class Heads(ctypes.Structure):
+    """qlora_heads: a view of [tokens, heads, dim] values (device pointer)."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    """qlora_kv_cache: a paged key/value cache (device pointers)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+_c_d, _c_heads, _c_cache = ctypes.c_double, ctypes.POINTER(Heads), ctypes.POINTER(KVCacheDesc)
+
 _SIGNATURES = {
     "qlora_quantize_nf4": (ctypes.c_int, [_c_p, _c_i64, _c_i32, _c_p, _c_p, _c_p]),
     "qlora_quantize_nf4_bf16": (ctypes.c_int, [_c_p, _c_i64, _c_i32, _c_p, _c_p, _c_p]),
@@ -68,6 +83,15 @@ _SIGNATURES = {
     "qlora_adamw_workspace_bytes": (_c_sz, [_c_i64]),
     "qlora_adamw_step": (ctypes.c_int, [_c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i32, _c_f, _c_f, _c_f, _c_f, _c_f,
                                         _c_f, _c_p, _c_p, _c_sz, _c_p]),
+    "qlora_rope_table": (ctypes.c_int, [_c_i64, _c_i32, _c_d, _c_i32, _c_d, _c_d, _c_d, _c_d, _c_d, _c_p, _c_p]),
+    "qlora_rope": (ctypes.c_int, [_c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _c_p, _c_i64, _c_p, _c_heads, _c_heads,
+                                  _c_heads, _c_heads, _c_p]),
+    "qlora_kv_write": (ctypes.c_int, [_c_cache, _c_i64, _c_heads, _c_heads, _c_p, _c_p, _c_i64, _c_p, _c_i32, _c_i32,
+                                      _c_p]),
+    "qlora_kv_read": (ctypes.c_int, [_c_cache, _c_i64, _c_p, _c_p, _c_p, _c_p]),
+    "qlora_attend_paged_workspace_bytes": (_c_sz, [_c_cache, _c_i64, _c_i32, _c_i32, _c_i64, _c_i64, _c_i32, _c_i64]),
+    "qlora_attend_paged": (ctypes.c_int, [_c_cache, _c_i64, _c_heads, _c_i32, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i64,
+                                          _c_f, _c_i32, _c_i64, _c_p, _c_p, _c_p, _c_sz, _c_p]),
     "qlora_timing_enable": (None, [ctypes.c_int]),
     "qlora_timing_read": (ctypes.c_int, [ctypes.c_char_p, _c_sz]),
     "qlora_nf4_codebook": (None, [ctypes.POINTER(ctypes.c_float)]),

@@ -55,7 +55,9 @@ typedef enum {
   QLORA_ERR_WORKSPACE = -6,   /* workspace NULL or smaller than the *_workspace_bytes query */
   QLORA_ERR_DEVICE = -7,      /* a kernel's bounded wait ran out (reported by qlora_device_status) */
   QLORA_ERR_SCRATCH = -8,     /* the problem needs more than the no-allocation entry point's scratch */
-  QLORA_ERR_IO = -9           /* a file is missing, unreadable, malformed, or of another type or shape */
+  QLORA_ERR_IO = -9,          /* a file is missing, unreadable, malformed, or of another type or shape */
+  QLORA_ERR_INDEX = -10       /* a page, slot, position, length or start in device memory was out of range (reported
+                                 by qlora_device_status) */
 } qlora_status;
 
 /*
@@ -355,6 +357,167 @@ int qlora_adamw_step(int64_t n, uint16_t* param, float* master, float* m, float*
                      void* stream);
 
 /*
+ * The attention side of generation with a quantized model (QLoRA project
+ * page, inference features: 4-bit inference and batched generation): rotary
+ * positions between the q/k/v linears and the cache, a paged key/value cache
+ * that is quantized as it is written, and attention of new tokens over it.
+ * Indices that the host cannot see (positions, slots, page numbers, starts,
+ * lengths) are checked by the kernels: one out of range never causes an
+ * access out of bounds, it sets a bit that qlora_device_status returns as
+ * QLORA_ERR_INDEX, and the results of that call are then unreliable.
+ *
+ * A view of [tokens, heads, dim] bf16 values whose dims are contiguous: a
+ * tensor of its own or a part of a fused q/k/v output.  Strides are in
+ * elements and multiples of 8 (a head starts on 16 bytes).
+ */
+typedef struct {
+  uint16_t* data; /* read only where a call says "in" */
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t heads;
+} qlora_heads;
+
+/*
+ * Table of rotations: table[p][i] = (cos, sin)(p * f_i) * amplitude, computed
+ * in fp64 and rounded to fp32 once, for pair i of rot / 2 and position p.
+ *   positions  rows p = 0 .. positions - 1 (0 = no-op).
+ *   rot        rotated dims: a multiple of 16 in [16, 256].
+ *   base       f_i = base^(-2 i / rot), base > 0.
+ *   scaling    QLORA_ROPE_NONE;
+ *              QLORA_ROPE_LINEAR: every f_i divided by factor;
+ *              QLORA_ROPE_BASE:   base * factor^(rot / (rot - 2)), so that the
+ *                slowest pair is slowed by factor and the fastest not at all;
+ *              QLORA_ROPE_BANDS:  a pair that makes at least `high` turns
+ *                over `original` positions keeps f_i, one that makes at most
+ *                `low` gets f_i / factor, linear in the turns between.
+ *   factor     >= 1; original >= 1 and 0 <= low < high for bands (ignored by
+ *              the others); amplitude > 0 multiplies cos and sin.
+ *   table      out: [positions][rot / 2][2] fp32.
+ */
+typedef enum { QLORA_ROPE_NONE = 0, QLORA_ROPE_LINEAR = 1, QLORA_ROPE_BASE = 2, QLORA_ROPE_BANDS = 3 } qlora_rope_scaling;
+int qlora_rope_table(int64_t positions, int32_t rot, double base, int32_t scaling, double factor, double original,
+                     double low, double high, double amplitude, float* table, void* stream);
+
+/*
+ * Rotary positions: pair i of a head, (a, b), becomes
+ *     (a c - b s, b c + a s),   (c, s) = table[positions[token]][i],
+ * in fp32, rounded to bf16 once.  Half layout (interleaved = 0): a = x[i],
+ * b = x[i + rot/2]; interleaved layout: a = x[2i], b = x[2i + 1].  Dims from
+ * rot on are copied.  inverse = 1 negates s: the transpose of the forward,
+ * and so its gradient (dq, dk from the rotated ones' gradients).
+ *   T          tokens (0 = no-op).       dim  a multiple of 16 in [16, 256].
+ *   rot        a multiple of 16 in [16, dim].
+ *   table, table_positions               from qlora_rope_table (or like it).
+ *   positions  [T] int32, 0 <= position < table_positions.
+ *   q, k       in: views of T tokens; k may be NULL (one tensor is rotated).
+ *   q_out, k_out  out: views with the same number of heads.  An output may be
+ *              its own input (the same data and strides), not overlap it else.
+ */
+int qlora_rope(int64_t T, int32_t dim, int32_t rot, int32_t interleaved, int32_t inverse, const float* table,
+               int64_t table_positions, const int32_t* positions, const qlora_heads* q, const qlora_heads* q_out,
+               const qlora_heads* k, const qlora_heads* k_out, void* stream);
+
+/*
+ * A paged key/value cache.  Slot s is row s % page_size of page s / page_size.
+ * Page p holds, for each head, page_size consecutive rows of `dim` keys (in
+ * k) and values (in v): [pages][heads][page_size][row].
+ *   type       QLORA_KV_BF16  rows of dim bf16, no scales (NULL);
+ *              QLORA_KV_INT8  rows of dim int8, code * scale;
+ *              QLORA_KV_NF4, _INT4, _FP4  rows of dim / 2 bytes, low nibble
+ *                first, table[code] * scale (see qlora_4bit_table).
+ *   k_scale, v_scale  [pages][heads][page_size] fp32: one per row.
+ *   dim        a multiple of 16 in [16, 256];  heads >= 1.
+ *   page_size  a power of two in [16, 1024];   pages >= 1.
+ * How a row x is quantized, all in fp32, with top = max |x|, u = 1 / top:
+ *   int8   code = nearest integer to x * (127 u) (ties to even),
+ *          scale = top * fp32(1/127);
+ *   4 bit  the level reached by x * u: #{boundaries m : x * u > m}, m the
+ *          fp32 midpoints between the type's levels; scale = top.
+ * A row with top < 1e-30 is stored as zeros; one that holds an infinity or a
+ * NaN gets a NaN scale and reads back as NaN.
+ */
+typedef enum {
+  QLORA_KV_BF16 = 0,
+  QLORA_KV_INT8 = 1,
+  QLORA_KV_NF4 = 2,
+  QLORA_KV_INT4 = 3,
+  QLORA_KV_FP4 = 4
+} qlora_kv_type;
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages;
+  int32_t type;
+  int32_t heads;
+  int32_t dim;
+  int32_t page_size;
+} qlora_kv_cache;
+
+/*
+ * Stores the keys and values of T tokens, quantized as they are written.
+ *   k, v   in: views of T tokens with the cache's heads.
+ *   slots  [T] int64: the slot of each token; a negative one is skipped
+ *          (padding).  Two tokens must not name the same slot.
+ *   table  NULL, or a table of rotations: the keys are then rotated first, as
+ *          by qlora_rope (rot, interleaved, table_positions, positions as
+ *          there), without being rounded in between.
+ */
+int qlora_kv_write(const qlora_kv_cache* cache, int64_t T, const qlora_heads* k, const qlora_heads* v,
+                   const int64_t* slots, const float* table, int64_t table_positions, const int32_t* positions,
+                   int32_t rot, int32_t interleaved, void* stream);
+
+/*
+ * Reads rows back as the values they stand for, rounded to bf16.
+ *   slots  [T] int64, in any order and repeated at will; a negative one gives
+ *          zeros.
+ *   k, v   [T, heads, dim] bf16 out, contiguous.
+ */
+int qlora_kv_read(const qlora_kv_cache* cache, int64_t T, const int64_t* slots, uint16_t* k, uint16_t* v,
+                  void* stream);
+
+/*
+ * Attention of new tokens over the cache, in which their own keys and values
+ * are already stored.  Sequence b has the new tokens starts[b] ..
+ * starts[b+1] - 1 of q and lengths[b] stored tokens, the new ones the last of
+ * them; stored token j is row j % page_size of page pages[b][j / page_size].
+ * New token i of n stands at position p = length - n + i and sees token j if
+ *     j < length,   j <= p if causal,   j > p - window if window > 0.
+ *   out = sum_j w_j v_j,  w = softmax over the seen j of scale * (q . k_j),
+ *   lse = log(sum_j exp(scale * (q . k_j))).
+ * A token that sees nothing (no length, or more new than stored ones) gives
+ * zeros and lse = -inf.  What tokens that a row does not see hold (the end of
+ * a page, a page given back) does not matter, whether finite or not.
+ * Query head x uses key/value head x / (q heads / cache heads).
+ *   tokens   rows of q, out and lse.  q  in: view of `tokens` tokens; its
+ *            heads a multiple of the cache's.
+ *   batch    sequences;  starts [batch+1] and lengths [batch] int32 with
+ *            starts[0] = 0 and starts[batch] = tokens.
+ *   pages    [batch][pages_per_seq] int32.
+ *   max_new, max_len  upper bounds of starts[b+1] - starts[b] and lengths[b]
+ *            (the launch is sized by them; no call reads device memory on the
+ *            host); a sequence beyond them is cut and reported as
+ *            QLORA_ERR_INDEX.  0 <= max_len <= pages_per_seq * page_size and
+ *            max_len <= 2^30.
+ *   out      [tokens, q heads, dim] bf16.
+ *   lse      [tokens, q heads] fp32, or NULL.
+ *   workspace  qlora_attend_paged_workspace_bytes bytes (the partial sums
+ *            when the keys are split over workgroups).
+ * Scores, the running maximum and sum and the output's accumulation are fp32;
+ * keys and values enter the products as bf16 (int8 codes and FP4 levels are
+ * exact there; NF4 and Int4 levels are rounded to bf16, their row scales are
+ * not) and the weights are rounded to bf16 before the second product.
+ * Deterministic: splits are joined in a fixed order.
+ */
+size_t qlora_attend_paged_workspace_bytes(const qlora_kv_cache* cache, int64_t tokens, int32_t q_heads, int32_t batch,
+                                          int64_t max_new, int64_t max_len, int32_t causal, int64_t window);
+int qlora_attend_paged(const qlora_kv_cache* cache, int64_t tokens, const qlora_heads* q, int32_t batch,
+                       const int32_t* pages, int64_t pages_per_seq, const int32_t* starts, const int32_t* lengths,
+                       int64_t max_new, int64_t max_len, float scale, int32_t causal, int64_t window, uint16_t* out,
+                       float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Support: dequantize codes + double-quantized constants to a dense weight.
  *   out_is_bf16 = 1: out is uint16_t[n] bf16 (the compute weight W' above);
  *   out_is_bf16 = 0: out is float[n], fp32(c[code] * fp32(q8*s2/255)).
@@ -432,7 +595,8 @@ int qlora_last_hip_error(void);
  * a tile (a guard that is never reached when every slice runs); if the
  * bound ever ran out, the finishing workgroup sets a status bit on the
  * device and stores an incomplete sum.  This call waits for `stream`,
- * returns QLORA_ERR_DEVICE if any bit is set (the outputs of the calls since
+ * returns QLORA_ERR_DEVICE if that bit is set, QLORA_ERR_INDEX if a kernel of
+ * the attention side met an index out of range (the outputs of the calls since
  * the previous query are then unreliable) and clears the bits; QLORA_OK
  * otherwise, or QLORA_ERR_HIP if the wait or the read failed.  Host-blocking.
  */
