@@ -10,6 +10,7 @@
 // tile's rows are (token, head of the group) pairs of one key/value head.
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "common.hpp"
 #include "device_state.hpp"
@@ -39,7 +40,8 @@ struct AttendArgs {
   float* part_o;   // [splits][tokens][q heads][dim]
   float* part_ml;  // [splits][tokens][q heads][2]
   int32_t splits, chunk, tiles;  // keys per split (a multiple of 128), row tiles
-  float levels[16];              // decode table of a 4-bit cache
+  uint32_t levels[16];  // 4-bit cache: bf16 level (low half) and what it misses of the value (high half)
+  float unit;           // value = level * unit * scale of the row
   int* status;
 };
 
@@ -76,20 +78,33 @@ __device__ __forceinline__ int seen_lo(const AttendArgs& a, const Seq& q, int i)
   return a.window && at > 0 ? at : 0;
 }
 
-// Cross-lane reductions over the four 16-lane groups that share a query.
+// Maximum and sum over the four 16-lane groups that share a query, by row
+// swaps between registers (no LDS crossbar): swapping a copy of x with itself
+// leaves rows 0, 0, 2, 2 in one register and 1, 1, 3, 3 in the other, then
+// the halves likewise.
+template <typename F>
+__device__ __forceinline__ float over_groups(float x, F f) {
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return f(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
 __device__ __forceinline__ float max_groups(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16, 64));
-  return fmaxf(x, __shfl_xor(x, 32, 64));
+  return over_groups(x, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ __forceinline__ float sum_groups(float x) {
-  x += __shfl_xor(x, 16, 64);
-  return x + __shfl_xor(x, 32, 64);
+  return over_groups(x, [](float a, float b) { return a + b; });
 }
 
+// How a cache's rows become MFMA operands.  Int8 codes and the levels of Int4
+// (k) and FP4 (m, whole halves) are exact in bf16; their 1/7 and 1/6 go to the
+// row's scale.  An NF4 level is not: rounded to bf16 it would be off by up to
+// 2^-9, the same way in every row, which a sum over 10^5 keys does not average
+// out (7 % of such an output's norm, measured); it enters as the sum of two
+// bf16 values (2^-17), each with its own MFMA.
+enum Operand { kOpBF16, kOpINT8, kOpLevel, kOpLevel2 };
 template <int KT>
-struct Bits {
-  static constexpr int per = KT == kKVBF16 ? 16 : KT == kKVINT8 ? 8 : 4;
-};
+constexpr int kBitsOf = KT == kOpBF16 ? 16 : KT == kOpINT8 ? 8 : 4;
 
 // 8 consecutive int8 codes -> 8 bf16 (exact).
 __device__ __forceinline__ bf16x8 int8_to_bf16x8(uint32_t a, uint32_t b) {
@@ -101,6 +116,16 @@ __device__ __forceinline__ bf16x8 int8_to_bf16x8(uint32_t a, uint32_t b) {
   }
   return to_bf16x8(f);
 }
+
+// The bf16 levels of the two codes of a byte (offset: 8 times the byte).
+template <int KT>
+__device__ __forceinline__ uint2 level_pair(const uint2* lut, uint32_t offset) {
+  const char* p = reinterpret_cast<const char*>(lut) + offset;
+  if constexpr (KT == kOpLevel2) return *reinterpret_cast<const uint2*>(p);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(p), 0u);
+}
+
+constexpr float kSlack = 8.0f;
 
 // ---------------------------------------------------------------------------
 // Streaming kernel: 16 * NQ rows of one sequence and key/value head against
@@ -120,7 +145,8 @@ __device__ __forceinline__ bf16x8 int8_to_bf16x8(uint32_t a, uint32_t b) {
 // ---------------------------------------------------------------------------
 template <int KT, int DP, int NQ, bool EXACT>
 __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
-  constexpr int BITS = Bits<KT>::per;
+  constexpr bool FOUR = KT == kOpLevel || KT == kOpLevel2;
+  constexpr int BITS = kBitsOf<KT>;
   constexpr int NT = DP / 32;               // QK steps
   constexpr int NM = DP / 16;               // PV MFMAs
   constexpr int KW = DP / 4 * BITS / 32;    // dwords of a key's quarter row
@@ -130,9 +156,10 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
   __shared__ __align__(16) float s_o[4 * 16 * OS];
   __shared__ float s_m[4][16 * NQ], s_l[4][16 * NQ];
   __shared__ int s_page[kMaxChunk / 16 + 1];
-  __shared__ uint32_t s_lut[KT == kKVNF4 ? 256 : 1];
+  __shared__ uint2 s_lut[FOUR ? 256 : 1];   // a byte's two levels: (bf16 pair, what it misses)
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   uint32_t id = blockIdx.x;
   const int split = (int)(id % (uint32_t)a.splits);
   id /= (uint32_t)a.splits;
@@ -151,8 +178,8 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
   // Steps inside [full_lo, full_hi) are seen by every row.
   const int full_hi = seen_hi(a, sq, i_first), full_lo = seen_lo(a, sq, i_last);
 
-  const int shift = a.pool.shift, first_page = k0 >> shift;
-  for (int p = tid; k0 < k1 && p <= ((k1 - 1) >> shift) - first_page; p += 256) {
+  const int shift = a.pool.shift, first_page = k0 >> shift, last = ((k1 - 1) >> shift) - first_page;
+  for (int p = tid; k0 < k1 && p <= last; p += 256) {
     int page = a.pages[(int64_t)b * a.width + first_page + p];
     if (page < 0 || page >= a.pool.pages) {
       atomicOr(a.status, kStatusIndex);
@@ -160,16 +187,15 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
     }
     s_page[p] = page;
   }
-  if (KT == kKVNF4) {
-    float lo_v = a.levels[0], hi_v = a.levels[0];
+  if (FOUR) {
+    uint32_t lo_v = a.levels[0], hi_v = a.levels[0];
 #pragma unroll
     for (int e = 1; e < 16; ++e) {
       lo_v = (tid & 15) == e ? a.levels[e] : lo_v;
       hi_v = (tid >> 4) == e ? a.levels[e] : hi_v;
     }
-    s_lut[tid] = pack_bf16x2(lo_v, hi_v);
+    s_lut[tid] = make_uint2((lo_v & 0xFFFFu) | (hi_v << 16), (lo_v >> 16) | (hi_v & 0xFFFF0000u));
   }
-  __syncthreads();
 
   const int D = a.pool.dim;
   // Queries: row m of the tile is token m / G, head h * G + m % G.
@@ -191,6 +217,7 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
       q[x][t] = as_bf16x8(w);
     }
   }
+  __syncthreads();
 
   f32x4 o[NQ][NM];
   float m[NQ], l[NQ];
@@ -203,28 +230,35 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
   }
 
   const int64_t row_bytes = kv_row_bytes(a.pool.type, D);
-  const int k_off = g * (DP / 4) * BITS / 8, v_off = r * VB;
-  for (int j0 = k0 + 32 * wave; j0 < k1; j0 += 128) {
-    uint32_t kw[2][KW], vw[8][VW];
+  const uint32_t k_off = r * (uint32_t)row_bytes + g * (DP / 4) * BITS / 8;
+  const uint32_t v_off = 4 * g * (uint32_t)row_bytes + r * VB;
+  const float s2 = a.scale2 * a.unit;
+
+  // A step's rows as they are stored.
+  struct Stage {
+    uint32_t k[2][KW], v[8][VW];
     float4 ks[2], vs[2];
-    // The last block's page may lie past the list: its keys are not seen.
-    const int last = ((k1 - 1) >> shift) - first_page;
+  };
+  auto load = [&](Stage& st, int j0) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int j = j0 + 16 * c;
-      const int pi = min((j >> shift) - first_page, last);
-      const int64_t base = (((int64_t)s_page[pi] * H + h) << shift) + (j & ((1 << shift) - 1));
-      const uint8_t* kp = a.pool.k + (base + r) * row_bytes + k_off;
-      if (EXACT) {
+      // The second block's page may lie past the list: its keys are not seen.
+      const int page = __builtin_amdgcn_readfirstlane(s_page[min((j >> shift) - first_page, last)]);
+      const int64_t base = (((int64_t)page * H + h) << shift) + (j & ((1 << shift) - 1));
+      const uint8_t* kb = a.pool.k + base * row_bytes;
+      const uint8_t* vb = a.pool.v + base * row_bytes;
+      const uint8_t* kp = kb + k_off;
+      if constexpr (EXACT) {
+        if constexpr (KW % 4 == 0) {
 #pragma unroll
-        for (int w = 0; w < KW; w += (KW % 4 == 0 ? 4 : 2)) {
-          if (KW % 4 == 0) {
+          for (int w = 0; w < KW; w += 4) {
             const u32x4 v = *reinterpret_cast<const u32x4*>(kp + 4 * w);
-            kw[c][w] = v[0]; kw[c][w + 1] = v[1]; kw[c][(w + 2) % KW] = v[2]; kw[c][(w + 3) % KW] = v[3];
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(kp + 4 * w);
-            kw[c][w] = v.x; kw[c][w + 1] = v.y;
+            st.k[c][w] = v[0]; st.k[c][w + 1] = v[1]; st.k[c][w + 2] = v[2]; st.k[c][w + 3] = v[3];
           }
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(kp);
+          st.k[c][0] = v.x; st.k[c][1] = v.y;
         }
       } else {
         constexpr int SW = KW / NT;  // dwords of 8 elements
@@ -232,24 +266,24 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
         for (int t = 0; t < NT; ++t) {
           const bool in = g * (DP / 4) + t * 8 < D;
 #pragma unroll
-          for (int w = 0; w < SW; ++w) kw[c][t * SW + w] = in ? reinterpret_cast<const uint32_t*>(kp)[t * SW + w] : 0u;
+          for (int w = 0; w < SW; ++w) st.k[c][t * SW + w] = in ? reinterpret_cast<const uint32_t*>(kp)[t * SW + w] : 0u;
         }
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint8_t* vp = a.pool.v + (base + 4 * g + e) * row_bytes + v_off;
-        uint32_t(&w)[VW] = vw[4 * c + e];
+        const uint8_t* vp = vb + v_off + e * (uint32_t)row_bytes;
+        uint32_t(&w)[VW] = st.v[4 * c + e];
         if (EXACT || r * (DP / 16) < D) {
-          if (VB >= 16) {
+          if constexpr (VB >= 16) {
 #pragma unroll
             for (int x = 0; x < VW; x += 4) {
               const u32x4 v = *reinterpret_cast<const u32x4*>(vp + 4 * x);
-              w[x] = v[0]; w[(x + 1) % VW] = v[1]; w[(x + 2) % VW] = v[2]; w[(x + 3) % VW] = v[3];
+              w[x] = v[0]; w[x + 1] = v[1]; w[x + 2] = v[2]; w[x + 3] = v[3];
             }
-          } else if (VB == 8) {
+          } else if constexpr (VB == 8) {
             const uint2 v = *reinterpret_cast<const uint2*>(vp);
-            w[0] = v.x; w[1 % VW] = v.y;
-          } else if (VB == 4) {
+            w[0] = v.x; w[1] = v.y;
+          } else if constexpr (VB == 4) {
             w[0] = *reinterpret_cast<const uint32_t*>(vp);
           } else {
             w[0] = *reinterpret_cast<const uint16_t*>(vp);
@@ -259,14 +293,14 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
           for (int x = 0; x < VW; ++x) w[x] = 0;
         }
       }
-      if (KT != kKVBF16) {
-        ks[c] = *reinterpret_cast<const float4*>(a.pool.ks + base + 4 * g);
-        vs[c] = *reinterpret_cast<const float4*>(a.pool.vs + base + 4 * g);
-      } else {
-        ks[c] = vs[c] = make_float4(1, 1, 1, 1);
+      if constexpr (KT != kOpBF16) {
+        st.ks[c] = reinterpret_cast<const float4*>(a.pool.ks + base)[g];
+        st.vs[c] = reinterpret_cast<const float4*>(a.pool.vs + base)[g];
       }
     }
+  };
 
+  auto compute = [&](Stage& st, int j0) {
     f32x4 s[NQ][2];
 #pragma unroll
     for (int x = 0; x < NQ; ++x) s[x][0] = s[x][1] = f32x4{0, 0, 0, 0};
@@ -275,13 +309,20 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         bf16x8 ka;
-        if constexpr (KT == kKVBF16) {
-          ka = as_bf16x8(kw[c][4 * t], kw[c][4 * t + 1], kw[c][4 * t + 2], kw[c][4 * t + 3]);
-        } else if constexpr (KT == kKVINT8) {
-          ka = int8_to_bf16x8(kw[c][2 * t], kw[c][2 * t + 1]);
+        if constexpr (KT == kOpBF16) {
+          ka = as_bf16x8(st.k[c][4 * t], st.k[c][4 * t + 1], st.k[c][4 * t + 2], st.k[c][4 * t + 3]);
+        } else if constexpr (KT == kOpINT8) {
+          ka = int8_to_bf16x8(st.k[c][2 * t], st.k[c][2 * t + 1]);
         } else {
-          const uint32_t w = kw[c][t];
-          ka = as_bf16x8(s_lut[w & 255u], s_lut[(w >> 8) & 255u], s_lut[(w >> 16) & 255u], s_lut[w >> 24]);
+          uint2 w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = level_pair<KT>(s_lut, byte_x8(st.k[c][t], e));
+          ka = as_bf16x8(w[0].x, w[1].x, w[2].x, w[3].x);
+          if constexpr (KT == kOpLevel2) {
+            const bf16x8 kl = as_bf16x8(w[0].y, w[1].y, w[2].y, w[3].y);
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) s[x][c] = mfma16(kl, q[x][t], s[x][c]);
+          }
         }
 #pragma unroll
         for (int x = 0; x < NQ; ++x) s[x][c] = mfma16(ka, q[x][t], s[x][c]);
@@ -293,8 +334,8 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
     // a bf16 value that is not finite must not reach rows that do not see its
     // key through 0 * inf, so it becomes 0 too and the rows that do see it get
     // a NaN weight instead.
-    bool wild[8] = {};
-    if (KT == kKVBF16 && edge) {
+    uint32_t wild = 0;
+    if (KT == kOpBF16 && edge) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int j = j0 + 16 * (e / 4) + 4 * g + e % 4;
@@ -302,12 +343,12 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
         bool bad = false;
 #pragma unroll
         for (int x = 0; x < VW; ++x) {
-          uint32_t w = any ? vw[e][x] : 0u;
+          uint32_t w = any ? st.v[e][x] : 0u;
           if ((w & 0x7F80u) == 0x7F80u) { w &= 0xFFFF0000u; bad = true; }
           if ((w & 0x7F800000u) == 0x7F800000u) { w &= 0xFFFFu; bad = true; }
-          vw[e][x] = w;
+          st.v[e][x] = w;
         }
-        wild[e] = ((__ballot(bad) >> (16 * g)) & 0xFFFFu) != 0;
+        wild |= ((__ballot(bad) >> (16 * g)) & 0xFFFFu) != 0 ? 1u << e : 0u;
       }
     }
 
@@ -316,11 +357,7 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
     for (int x = 0; x < NQ; ++x) {
       float p[8];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float kk[4] = {ks[c].x, ks[c].y, ks[c].z, ks[c].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[4 * c + e] = s[x][c][e] * (KT == kKVBF16 ? a.scale2 : a.scale2 * kk[e]);
-      }
+      for (int e = 0; e < 8; ++e) p[e] = s[x][e / 4][e % 4] * (KT == kOpBF16 ? s2 : s2 * reinterpret_cast<const float*>(&st.ks[e / 4])[e % 4]);
       uint32_t hidden = 0;
       if (edge) {
 #pragma unroll
@@ -332,57 +369,94 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
           }
         }
       }
+      // The reference of the exponents follows the maximum only when it has
+      // grown by 2^kSlack: weights stay below 2^kSlack and nothing is rescaled
+      // in nearly every step.
       float top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
-      top = fmaxf(max_groups(top), m[x]);
-      const float ref = top == -INFINITY ? 0.0f : top;
-      if (__any(top > m[x])) {
-        const float f = __builtin_amdgcn_exp2f(m[x] - ref);
+      top = max_groups(top);
+      if (__any(top > m[x] + kSlack)) {
+        top = fmaxf(top, m[x]);
+        const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[x] - top);
         l[x] *= f;
 #pragma unroll
         for (int t = 0; t < NM; ++t) o[x][t] *= f;
         m[x] = top;
       }
+      const float ref = m[x] == -INFINITY ? 0.0f : m[x];
 #pragma unroll
       for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(p[e] - ref);
       l[x] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-      if (KT != kKVBF16) {
+      if constexpr (KT != kOpBF16) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float vv[4] = {vs[c].x, vs[c].y, vs[c].z, vs[c].w};
+        for (int e = 0; e < 8; ++e) p[e] *= reinterpret_cast<const float*>(&st.vs[e / 4])[e % 4];
+        if (edge) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[4 * c + e] = (hidden >> (4 * c + e)) & 1u ? 0.0f : p[4 * c + e] * vv[e];
+          for (int e = 0; e < 8; ++e) p[e] = (hidden >> e) & 1u ? 0.0f : p[e];  // also where the scale is no number
         }
       } else if (edge) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (wild[e] && !((hidden >> e) & 1u)) p[e] = __uint_as_float(0x7FC00000u);
+          if ((wild & ~hidden) >> e & 1u) p[e] = __uint_as_float(0x7FC00000u);
       }
       // The weights enter the second product as bf16 (their sum stays fp32):
-      // half a unit in the 8th bit of each, against the output's own rounding
-      // to as many bits.
+      // half a unit in the 8th bit of each, to either side, against the
+      // output's own rounding to as many bits.
       pb[x] = to_bf16x8(p);
     }
 
     // Values of dim t for the lane's 8 keys, two keys to a dword.
+    uint32_t even[4][VW], odd[4][VW];  // 4 bits: the codes of two keys side by side, dims 2n and 2n + 1
+    if constexpr (FOUR) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t va = st.v[2 * c][w], vb = st.v[2 * c + 1][w];
+          even[c][w] = (va & 0x0F0F0F0Fu) | ((vb << 4) & 0xF0F0F0F0u);
+          odd[c][w] = ((va >> 4) & 0x0F0F0F0Fu) | (vb & 0xF0F0F0F0u);
+        }
+    }
 #pragma unroll
     for (int t = 0; t < NM; ++t) {
-      uint32_t w[4];
+      uint2 w[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint32_t(&va)[VW] = vw[2 * c];
-        const uint32_t(&vb)[VW] = vw[2 * c + 1];
-        if constexpr (KT == kKVBF16) {
-          w[c] = __builtin_amdgcn_perm(vb[t / 2], va[t / 2], t & 1 ? 0x07060302u : 0x05040100u);
-        } else if constexpr (KT == kKVINT8) {
-          w[c] = pack_bf16x2((float)(int8_t)(va[t / 4] >> (8 * (t % 4))), (float)(int8_t)(vb[t / 4] >> (8 * (t % 4))));
+        const uint32_t(&va)[VW] = st.v[2 * c];
+        const uint32_t(&vb)[VW] = st.v[2 * c + 1];
+        if constexpr (KT == kOpBF16) {
+          w[c].x = __builtin_amdgcn_perm(vb[t / 2], va[t / 2], t & 1 ? 0x07060302u : 0x05040100u);
+        } else if constexpr (KT == kOpINT8) {
+          w[c].x = pack_bf16x2((float)(int8_t)(va[t / 4] >> (8 * (t % 4))), (float)(int8_t)(vb[t / 4] >> (8 * (t % 4))));
         } else {
-          const uint32_t ca = (va[t / 8] >> (4 * (t % 8))) & 15u, cb = (vb[t / 8] >> (4 * (t % 8))) & 15u;
-          w[c] = s_lut[ca | (cb << 4)];
+          w[c] = level_pair<KT>(s_lut, byte_x8((t & 1 ? odd : even)[c][t / 8], t % 8 / 2));
         }
       }
-      const bf16x8 vt = as_bf16x8(w[0], w[1], w[2], w[3]);
+      if constexpr (KT == kOpLevel2) {
+        const bf16x8 vl = as_bf16x8(w[0].y, w[1].y, w[2].y, w[3].y);
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) o[x][t] = mfma16(vl, pb[x], o[x][t]);
+      }
+      const bf16x8 vt = as_bf16x8(w[0].x, w[1].x, w[2].x, w[3].x);
 #pragma unroll
       for (int x = 0; x < NQ; ++x) o[x][t] = mfma16(vt, pb[x], o[x][t]);
+    }
+  };
+
+  // The next step's rows load while this one's are used; past the last step
+  // they are its own again (a load that may not happen would make the wait for
+  // the ones before it a wait for all).
+  int j = k0 + 32 * wave;
+  if (j < k1) {
+    const int end = j + (k1 - 1 - j) / 128 * 128;  // this wave's last step
+    Stage st[2];
+    load(st[0], j);
+    for (;;) {
+      load(st[1], min(j + 128, end));
+      compute(st[0], j);
+      if ((j += 128) >= k1) break;
+      load(st[0], min(j + 128, end));
+      compute(st[1], j);
+      if ((j += 128) >= k1) break;
     }
   }
 
@@ -422,7 +496,7 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
       for (int w = 0; w < 4; ++w) sum += s_l[w][16 * x + qr] * (top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(s_m[w][16 * x + qr] - top));
       const int i = row / G, gh = row - i * G;
       const int64_t at = (sq.first + i) * Hq + h * G + gh;
-      const float inv = a.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float inv = sum == 0.0f ? 0.0f : a.unit / sum;
       if (part == 0) {
         if (a.splits > 1) {
           float* ml = a.part_ml + ((int64_t)split * a.tokens * Hq + at) * 2;
@@ -454,40 +528,77 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
   }
 }
 
-// Joins the splits of a row: one wave per (token, query head).
+// Joins the splits of a row: one workgroup per (token, query head).  The
+// splits' references and sums first, then their outputs, 256 / (DP / 4) splits
+// at a time, in a fixed order.
 template <int DP>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int tile_rows) {
-  constexpr int NE = DP / 64;
-  const int lane = threadIdx.x & 63, b = blockIdx.y;
+  constexpr int L = DP / 4, P = 256 / L;  // lanes of a row, splits at a time
+  __shared__ __align__(16) float4 s_acc[P][L];
+  __shared__ float s_red[2][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.y;
   const int H = a.pool.heads, G = a.group, Hq = H * G, D = a.pool.dim;
-  const int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const Seq sq = load_seq(a, b);
+  const int e = blockIdx.x;
   if (e >= (int64_t)sq.n * Hq) return;
-  const int i = (int)(e / Hq), hq = (int)(e - (int64_t)i * Hq), rows = sq.n * G;
+  const int i = e / Hq, hq = e - i * Hq, rows = sq.n * G;
   const int row0 = (i * G + hq % G) / tile_rows * tile_rows;
   const int hi = seen_hi(a, sq, (min(rows, row0 + tile_rows) - 1) / G), lo = seen_lo(a, sq, row0 / G) & ~15;
   const int n = hi <= lo ? 1 : (hi - lo + a.chunk - 1) / a.chunk;
   const int64_t at = (sq.first + i) * Hq + hq, step = a.tokens * Hq;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + at;
   float top = -INFINITY;
-  for (int s = 0; s < n; ++s) top = fmaxf(top, a.part_ml[(s * step + at) * 2]);
-  float sum = 0.0f, acc[NE] = {};
-  for (int s = 0; s < n; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (s * step + at) * 2);
-    const float f = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
-    sum += ml.y * f;
+  for (int s = tid; s < n; s += 256) top = fmaxf(top, ml[s * step].x);
 #pragma unroll
-    for (int x = 0; x < NE; ++x) {
-      const int d = lane + 64 * x;
-      if (d < D) acc[x] += a.part_o[(s * step + at) * D + d] * f;
+  for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+  if (lane == 0) s_red[0][wave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3]));
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f;
+  for (int s = tid; s < n; s += 256) {
+    const float2 v = ml[s * step];
+    sum += v.y * __builtin_amdgcn_exp2f(v.x - ref);
+  }
+#pragma unroll
+  for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  if (lane == 0) s_red[1][wave] = sum;
+  const int c = tid % L, part = tid / L;
+  float4 acc = make_float4(0, 0, 0, 0);
+  if (4 * c < D) {
+#pragma unroll 4
+    for (int s = part; s < n; s += P) {
+      const float f = __builtin_amdgcn_exp2f(ml[s * step].x - ref);
+      const float4 v = *reinterpret_cast<const float4*>(a.part_o + (s * step + at) * D + 4 * c);
+      acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
     }
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  s_acc[part][c] = acc;
+  __syncthreads();
+  sum = (s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]);
+  if (tid < L && 4 * tid < D) {
 #pragma unroll
-  for (int x = 0; x < NE; ++x) {
-    const int d = lane + 64 * x;
-    if (d < D) a.out[at * D + d] = (uint16_t)(pack_bf16x2(acc[x] * inv, 0.0f) & 0xFFFFu);
+    for (int p = 1; p < P; ++p) {
+      const float4 v = s_acc[p][tid];
+      acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    }
+    const float inv = sum == 0.0f ? 0.0f : a.unit / sum;
+    *reinterpret_cast<uint2*>(a.out + at * D + 4 * tid) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   }
-  if (lane == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (tid == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+uint32_t bf16_round_host(float f) {  // finite f
+  uint32_t u;
+  std::memcpy(&u, &f, 4);
+  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+float bf16_value_host(uint32_t h) {
+  const uint32_t u = h << 16;
+  float f;
+  std::memcpy(&f, &u, 4);
+  return f;
 }
 
 // How a problem is cut: rows per tile, row tiles, splits of the keys and the
@@ -529,9 +640,10 @@ void stream_type(const AttendArgs& a, unsigned grid, hipStream_t s) {
 }
 template <int NQ>
 void stream_rows(const AttendArgs& a, unsigned grid, hipStream_t s) {
-  if (a.pool.type == kKVBF16) stream_type<kKVBF16, NQ>(a, grid, s);
-  else if (a.pool.type == kKVINT8) stream_type<kKVINT8, NQ>(a, grid, s);
-  else stream_type<kKVNF4, NQ>(a, grid, s);
+  if (a.pool.type == kKVBF16) stream_type<kOpBF16, NQ>(a, grid, s);
+  else if (a.pool.type == kKVINT8) stream_type<kOpINT8, NQ>(a, grid, s);
+  else if (a.pool.type == kKVNF4) stream_type<kOpLevel2, NQ>(a, grid, s);
+  else stream_type<kOpLevel, NQ>(a, grid, s);
 }
 
 }  // namespace
@@ -575,7 +687,12 @@ hipError_t launch_attend(const AttendProblem& p, const float table[16], void* ws
   a.splits = (int32_t)r.splits;
   a.chunk = (int32_t)r.chunk;
   a.tiles = (int32_t)r.tiles;
-  for (int c = 0; c < 16; ++c) a.levels[c] = table ? table[c] : 0.0f;
+  a.unit = p.pool.type == kKVINT4 ? 1.0f / 7.0f : p.pool.type == kKVFP4 ? 1.0f / 6.0f : 1.0f;
+  for (int c = 0; c < 16; ++c) {
+    const float f = p.pool.type == kKVINT4 ? std::rint(table[c] * 7.0f) : p.pool.type == kKVFP4 ? std::rint(table[c] * 12.0f) / 2.0f : table[c];
+    const uint32_t hi = bf16_round_host(f);
+    a.levels[c] = hi | bf16_round_host(f - bf16_value_host(hi)) << 16;
+  }
   if (r.splits > 1) {
     const size_t ml = (size_t)(r.splits * p.tokens * p.q.heads * 2 * 4 + 255) / 256 * 256;
     a.part_ml = static_cast<float*>(ws);
@@ -590,7 +707,7 @@ hipError_t launch_attend(const AttendProblem& p, const float table[16], void* ws
   }
   if (e != hipSuccess || r.splits == 1) return e;
   KernelTimer kt_("attend_join_kernel", s);
-  const dim3 grid((unsigned)(((int64_t)p.max_new * p.q.heads + 3) / 4), (unsigned)p.batch);
+  const dim3 grid((unsigned)((int64_t)p.max_new * p.q.heads), (unsigned)p.batch);
   if (p.pool.dim <= 64) hipLaunchKernelGGL(attend_join_kernel<64>, grid, dim3(256), 0, s, a, r.tile_rows);
   else if (p.pool.dim <= 128) hipLaunchKernelGGL(attend_join_kernel<128>, grid, dim3(256), 0, s, a, r.tile_rows);
   else hipLaunchKernelGGL(attend_join_kernel<256>, grid, dim3(256), 0, s, a, r.tile_rows);
