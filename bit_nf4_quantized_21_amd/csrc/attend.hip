@@ -12,110 +12,12 @@
 #include <cmath>
 #include <cstring>
 
-#include "common.hpp"
-#include "device_state.hpp"
-#include "kvcache.hpp"
+#include "attend.hpp"
 #include "timing.hpp"
 
 namespace qlora {
 
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kMaxChunk = 16384;  // keys of a split: bounds the page list in LDS
-
-struct AttendArgs {
-  KVPool pool;
-  HeadsView q;
-  int64_t tokens;
-  const int32_t* pages;
-  int64_t width;
-  const int32_t* starts;
-  const int32_t* lengths;
-  int32_t batch, group, max_new, max_len;
-  float scale2;  // scale * log2(e)
-  int32_t causal, window;
-  uint16_t* out;
-  float* lse;
-  float* part_o;   // [splits][tokens][q heads][dim]
-  float* part_ml;  // [splits][tokens][q heads][2]
-  int32_t splits, chunk, tiles;  // keys per split (a multiple of 128), row tiles
-  uint32_t levels[16];  // 4-bit cache: bf16 level (low half) and what it misses of the value (high half)
-  float unit;           // value = level * unit * scale of the row
-  int* status;
-};
-
-// A sequence's tokens and length, held inside what the caller's sizes allow.
-struct Seq {
-  int64_t first;  // row of its first new token
-  int n, len;
-  bool bad;
-};
-__device__ __forceinline__ Seq load_seq(const AttendArgs& a, int b) {
-  int64_t s0 = a.starts[b], s1 = a.starts[b + 1];
-  int64_t len = a.lengths[b];
-  Seq q;
-  q.bad = false;
-  if (s0 < 0 || s0 > a.tokens) { s0 = s0 < 0 ? 0 : a.tokens; q.bad = true; }
-  if (s1 < s0 || s1 > a.tokens) { s1 = s1 < s0 ? s0 : a.tokens; q.bad = true; }
-  if (s1 - s0 > a.max_new) { s1 = s0 + a.max_new; q.bad = true; }
-  int64_t cap = a.width << a.pool.shift;
-  if (cap > a.max_len) cap = a.max_len;
-  if (len < 0 || len > cap) { len = len < 0 ? 0 : cap; q.bad = true; }
-  q.first = s0;
-  q.n = (int)(s1 - s0);
-  q.len = (int)len;
-  return q;
-}
-
-// Keys [lo, hi) that query i sees.
-__device__ __forceinline__ int seen_hi(const AttendArgs& a, const Seq& q, int i) {
-  const int at = q.len - q.n + i + 1;
-  return a.causal ? (at < q.len ? at : q.len) : q.len;
-}
-__device__ __forceinline__ int seen_lo(const AttendArgs& a, const Seq& q, int i) {
-  const int at = q.len - q.n + i + 1 - a.window;
-  return a.window && at > 0 ? at : 0;
-}
-
-// Maximum and sum over the four 16-lane groups that share a query, by row
-// swaps between registers (no LDS crossbar): swapping a copy of x with itself
-// leaves rows 0, 0, 2, 2 in one register and 1, 1, 3, 3 in the other, then
-// the halves likewise.
-template <typename F>
-__device__ __forceinline__ float over_groups(float x, F f) {
-  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
-  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return f(__uint_as_float(q[0]), __uint_as_float(q[1]));
-}
-__device__ __forceinline__ float max_groups(float x) {
-  return over_groups(x, [](float a, float b) { return fmaxf(a, b); });
-}
-__device__ __forceinline__ float sum_groups(float x) {
-  return over_groups(x, [](float a, float b) { return a + b; });
-}
-
-// How a cache's rows become MFMA operands.  Int8 codes and the levels of Int4
-// (k) and FP4 (m, whole halves) are exact in bf16; their 1/7 and 1/6 go to the
-// row's scale.  An NF4 level is not: rounded to bf16 it would be off by up to
-// 2^-9, the same way in every row, which a sum over 10^5 keys does not average
-// out (7 % of such an output's norm, measured); it enters as the sum of two
-// bf16 values (2^-17), each with its own MFMA.
-enum Operand { kOpBF16, kOpINT8, kOpLevel, kOpLevel2 };
-template <int KT>
-constexpr int kBitsOf = KT == kOpBF16 ? 16 : KT == kOpINT8 ? 8 : 4;
-
-// 8 consecutive int8 codes -> 8 bf16 (exact).
-__device__ __forceinline__ bf16x8 int8_to_bf16x8(uint32_t a, uint32_t b) {
-  float f[8];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f[j] = (float)(int8_t)(a >> (8 * j));
-    f[4 + j] = (float)(int8_t)(b >> (8 * j));
-  }
-  return to_bf16x8(f);
-}
 
 // The bf16 levels of the two codes of a byte (offset: 8 times the byte).
 template <int KT>
@@ -124,8 +26,6 @@ __device__ __forceinline__ uint2 level_pair(const uint2* lut, uint32_t offset) {
   if constexpr (KT == kOpLevel2) return *reinterpret_cast<const uint2*>(p);
   return make_uint2(*reinterpret_cast<const uint32_t*>(p), 0u);
 }
-
-constexpr float kSlack = 8.0f;
 
 // ---------------------------------------------------------------------------
 // Streaming kernel: 16 * NQ rows of one sequence and key/value head against
@@ -604,26 +504,27 @@ float bf16_value_host(uint32_t h) {
 // How a problem is cut: rows per tile, row tiles, splits of the keys and the
 // keys of a split.
 struct Plan {
-  int nq, tile_rows;
+  bool tile;  // the tile kernel, else the streaming one
+  int tile_rows;
   int64_t tiles, splits, chunk;
 };
 
 Plan make_plan(const AttendProblem& p) {
   Plan r{};
   const int64_t group = p.q.heads / p.pool.heads, rows = p.max_new * group;
-  r.nq = rows > 16 ? 2 : 1;
-  r.tile_rows = 16 * r.nq;
+  r.tile = rows > 32;
+  r.tile_rows = r.tile ? kTileRows : rows > 16 ? 32 : 16;
   r.tiles = std::max<int64_t>(1, (rows + r.tile_rows - 1) / r.tile_rows);
-  // Keys that a tile can see.
+  // Keys that a tile can see, from a multiple of 16 on.
   int64_t span = p.max_len;
-  if (p.window > 0 && p.causal) span = std::min<int64_t>(span, (int64_t)p.window + r.tile_rows + 16);
-  // Workgroups wanted: four per CU, each with at least 256 keys.
+  if (p.window > 0 && p.causal) span = std::min<int64_t>(span, (int64_t)p.window + r.tile_rows);
+  span += 15;
   const int64_t work = std::max<int64_t>(1, (int64_t)p.batch * p.pool.heads * r.tiles);
-  int64_t splits = std::min((1024 + work - 1) / work, (span + 255) / 256);
-  splits = std::max<int64_t>(splits, 1);
-  r.chunk = ((span + 15 + splits - 1) / splits + 127) / 128 * 128;
+  const int64_t want = r.tile ? 512 : 1024, least = r.tile ? 512 : 256;
+  const int64_t splits = std::max<int64_t>(1, std::min((want + work - 1) / work, span / least));
+  r.chunk = ((span + splits - 1) / splits + 127) / 128 * 128;
   r.chunk = std::min<int64_t>(std::max<int64_t>(r.chunk, 128), kMaxChunk);
-  r.splits = std::max<int64_t>(1, (span + 15 + r.chunk - 1) / r.chunk);
+  r.splits = std::max<int64_t>(1, (span + r.chunk - 1) / r.chunk);
   return r;
 }
 
@@ -692,16 +593,21 @@ hipError_t launch_attend(const AttendProblem& p, const float table[16], void* ws
     const float f = p.pool.type == kKVINT4 ? std::rint(table[c] * 7.0f) : p.pool.type == kKVFP4 ? std::rint(table[c] * 12.0f) / 2.0f : table[c];
     const uint32_t hi = bf16_round_host(f);
     a.levels[c] = hi | bf16_round_host(f - bf16_value_host(hi)) << 16;
+    a.values[c] = table[c];
   }
   if (r.splits > 1) {
     const size_t ml = (size_t)(r.splits * p.tokens * p.q.heads * 2 * 4 + 255) / 256 * 256;
     a.part_ml = static_cast<float*>(ws);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + ml);
   }
-  {
+  if (r.tile) {
+    KernelTimer kt_("attend_tile_kernel", s);
+    launch_attend_tile(a, s);
+    e = hipGetLastError();
+  } else {
     KernelTimer kt_("attend_stream_kernel", s);
     const unsigned grid = (unsigned)(p.batch * p.pool.heads * r.tiles * r.splits);
-    if (r.nq == 1) stream_rows<1>(a, grid, s);
+    if (r.tile_rows == 16) stream_rows<1>(a, grid, s);
     else stream_rows<2>(a, grid, s);
     e = hipGetLastError();
   }

@@ -1,0 +1,422 @@
+// Attention over the paged cache, many rows at a time (gfx950): prompts,
+// chunks of prompts, and single tokens of large head groups.
+//
+// A workgroup of four waves owns 128 rows, 32 per wave, and walks the keys in
+// tiles of 64 that it holds in LDS as bf16, two tiles deep: the next tile's
+// rows are on their way from memory to registers while this one is used, and
+// are written (dequantized) to the other half before the one barrier of the
+// step.  With 128 rows a row of the cache is dequantized once for 128 queries.
+//
+// S^T = K Q^T by 32x32x16 MFMAs: lane (r = lane & 31, h = lane >> 5) ends up
+// with the scores of query r against keys 8 (i / 4) + 4 h + i % 4 of each
+// 32-key block (register i).  O^T = V^T P^T takes its 16 keys per MFMA in that
+// order (element e of half h: key 4 h + e, or 8 + 4 h + e - 4), so the weights
+// go from the scores' registers into the MFMA; V^T comes from the row-major
+// tile by transposing LDS reads, four keys of one dim per lane.  Rows are
+// swizzled in 16-byte chunks so that both reads meet every bank once.
+#include "attend.hpp"
+
+namespace qlora {
+
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kTileKeys = 64;
+
+// Chunk (16 bytes) of a row at which chunk c is kept, for keys (read down the
+// rows, one chunk per lane) and for values (read four rows by 64 bytes).
+template <int DP>
+__device__ __forceinline__ int k_chunk(int key, int c) {
+  return c ^ (DP == 64 ? (key >> 1) & 7 : key & 15);
+}
+template <int DP>
+__device__ __forceinline__ int v_chunk(int key, int c) {
+  return c ^ (DP == 64 ? ((key >> 1) & 1) << 2 : (key & 3) << 2);
+}
+
+template <int OP, int DP, bool EXACT>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(AttendArgs a) {
+  constexpr bool CODES = OP == kOpINT8 || OP == kOpLevel;  // exact operands, scales on scores and weights
+  constexpr int BITS = kBitsOf<OP>;
+  constexpr int NT = DP / 16, NB = DP / 32;
+  constexpr int EL = BITS == 16 ? 8 : 16;                // elements per staged piece
+  constexpr int PW = EL * BITS / 32;                     // its dwords
+  constexpr int PR = DP / EL;                            // pieces of a row
+  constexpr int NP = kTileKeys * PR / 256;               // pieces per thread
+  __shared__ __align__(16) uint16_t s_k[2][kTileKeys * DP], s_v[2][kTileKeys * DP];
+  __shared__ __align__(16) float s_sc[CODES ? 2 : 1][2][kTileKeys];
+  __shared__ __align__(16) uint8_t s_wild[2][kTileKeys];
+  __shared__ int s_page[kMaxChunk / 16 + 1];
+  __shared__ uint2 s_lut[BITS == 4 ? 256 : 1];
+
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h2 = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int H = a.pool.heads, G = a.group;
+  // Each XCD walks a contiguous run of (sequence, head): its L2 serves the
+  // run's keys to all tiles.  The last tiles of a head see the most keys and
+  // go first.
+  const uint32_t total = (uint32_t)a.batch * H * a.tiles * a.splits, per = (total + 7) / 8;
+  uint32_t id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (id >= total || (blockIdx.x >> 3) >= per) return;
+  const int split = (int)(id % (uint32_t)a.splits);
+  id /= (uint32_t)a.splits;
+  const int tile = a.tiles - 1 - (int)(id % (uint32_t)a.tiles);
+  id /= (uint32_t)a.tiles;
+  const int h = (int)(id % (uint32_t)H), b = (int)(id / (uint32_t)H);
+  const Seq sq = load_seq(a, b);
+  if (sq.bad && tid == 0) atomicOr(a.status, kStatusIndex);
+  const int rows = sq.n * G, row0 = tile * kTileRows;
+  if (row0 >= rows) return;
+  const int i_first = row0 / G, i_last = (min(rows, row0 + kTileRows) - 1) / G;
+  const int hi = seen_hi(a, sq, i_last), lo = seen_lo(a, sq, i_first);
+  const int k0 = (lo & ~15) + split * a.chunk;
+  if (split > 0 && k0 >= hi) return;
+  const int k1 = min(hi, k0 + a.chunk);
+  const int full_hi = seen_hi(a, sq, i_first), full_lo = seen_lo(a, sq, i_last);
+
+  const int shift = a.pool.shift, first_page = k0 >> shift, last = ((k1 - 1) >> shift) - first_page;
+  for (int p = tid; k0 < k1 && p <= last; p += 256) {
+    int page = a.pages[(int64_t)b * a.width + first_page + p];
+    if (page < 0 || page >= a.pool.pages) {
+      atomicOr(a.status, kStatusIndex);
+      page = 0;
+    }
+    s_page[p] = page;
+  }
+  if (BITS == 4) {
+    // A byte's two levels: a pair of bf16 (exact levels), or two fp32 values.
+    uint32_t x = 0, y = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint32_t v = OP == kOpLevel ? a.levels[e] & 0xFFFFu : __float_as_uint(a.values[e]);
+      x = (tid & 15) == e ? v : x;
+      y = (tid >> 4) == e ? v : y;
+    }
+    s_lut[tid] = OP == kOpLevel ? make_uint2(x | (y << 16), 0) : make_uint2(x, y);
+  }
+
+  const int D = a.pool.dim;
+  const float s2 = fmaxf(fabsf(a.scale2 * (CODES ? a.unit : 1.0f)), 1.2e-38f);
+  const uint32_t flip = a.scale2 < 0.0f ? 0x80008000u : 0u;  // the scale's sign goes to q
+  const int wrow = row0 + 32 * wave, row = wrow + r;
+  const bool wave_rows = wrow < rows, ok = row < rows;
+  const int qi = ok ? row / G : 0, qg = ok ? row - qi * G : 0;
+  const int my_lo = seen_lo(a, sq, qi), my_hi = ok ? seen_hi(a, sq, qi) : 0;
+  // Keys that some row of the wave sees, and those that all of them see.
+  const int wi_first = min(wrow, rows - 1) / G, wi_last = (min(rows, wrow + 32) - 1) / G;
+  const int w_lo = seen_lo(a, sq, wi_first), w_hi = wave_rows ? seen_hi(a, sq, wi_last) : 0;
+  const int wf_lo = seen_lo(a, sq, wi_last), wf_hi = seen_hi(a, sq, wi_first);
+  bf16x8 q[NT];
+  {
+    const uint16_t* p = a.q.data + (sq.first + qi) * a.q.token_stride + (int64_t)(h * G + qg) * a.q.head_stride;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int d = t * 16 + h2 * 8;
+      u32x4 w = {0, 0, 0, 0};
+      if (ok && (EXACT || d < D)) w = *reinterpret_cast<const u32x4*>(p + d);
+      w ^= flip;
+      q[t] = as_bf16x8(w);
+    }
+  }
+  f32x16 o[NB];
+#pragma unroll
+  for (int t = 0; t < NB; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[t][i] = 0.0f;
+  float m = -INFINITY, l = 0.0f;
+  __syncthreads();
+
+  const int64_t row_bytes = kv_row_bytes(a.pool.type, D);
+  uint32_t kr[NP][PW], vr[NP][PW];
+  float scale_k = 0.0f, scale_v = 0.0f;
+  float piece_ks[OP == kOpLevel2 ? NP : 1], piece_vs[OP == kOpLevel2 ? NP : 1];
+  auto base_of = [&](int j) -> int64_t {
+    const int page = s_page[min((j >> shift) - first_page, last)];
+    return (((int64_t)page * H + h) << shift) + (j & ((1 << shift) - 1));
+  };
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+      const int id = tid + 256 * n, key = id / PR, pc = id % PR;
+      const int64_t base = base_of(j0 + key);
+      const uint8_t* kp = a.pool.k + base * row_bytes + pc * (PW * 4);
+      const uint8_t* vp = a.pool.v + base * row_bytes + pc * (PW * 4);
+      if (EXACT || pc * EL < D) {
+        if constexpr (PW == 4) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(kp), y = *reinterpret_cast<const u32x4*>(vp);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) { kr[n][w] = x[w]; vr[n][w] = y[w]; }
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(kp), y = *reinterpret_cast<const uint2*>(vp);
+          kr[n][0] = x.x; kr[n][1] = x.y; vr[n][0] = y.x; vr[n][1] = y.y;
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < PW; ++w) kr[n][w] = vr[n][w] = 0;
+      }
+      if constexpr (OP == kOpLevel2) {
+        piece_ks[n] = a.pool.ks[base];
+        piece_vs[n] = a.pool.vs[base];
+      }
+    }
+    if constexpr (CODES) {
+      const int64_t base = base_of(j0 + (tid & 63));
+      if (tid < 64) scale_k = a.pool.ks[base];
+      else if (tid < 128) scale_v = a.pool.vs[base];
+    }
+  };
+  // A staged piece as bf16 pairs.
+  auto widen = [&](const uint32_t (&w)[PW], float sc, uint32_t (&out)[EL / 2]) {
+    if constexpr (OP == kOpBF16) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[e] = w[e];
+    } else if constexpr (OP == kOpINT8) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        out[2 * e] = pack_bf16x2((float)(int8_t)w[e], (float)(int8_t)(w[e] >> 8));
+        out[2 * e + 1] = pack_bf16x2((float)(int8_t)(w[e] >> 16), (float)(int8_t)(w[e] >> 24));
+      }
+    } else {
+      const char* lut = reinterpret_cast<const char*>(s_lut);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const char* p = lut + byte_x8(w[e / 4], e % 4);
+        if constexpr (OP == kOpLevel) {
+          out[e] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+          // Rounded as the product level * scale: the scales differ from row
+          // to row, so the roundings do too and average out over the keys.
+          const float2 f = *reinterpret_cast<const float2*>(p);
+          out[e] = pack_bf16x2(f.x * sc, f.y * sc);
+        }
+      }
+    }
+  };
+  auto store = [&](int buf, int j0) {
+    const bool edge = j0 < full_lo || j0 + kTileKeys > full_hi;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+      const int id = tid + 256 * n, key = id / PR, pc = id % PR;
+      uint32_t x[EL / 2], y[EL / 2];
+      widen(kr[n], OP == kOpLevel2 ? piece_ks[OP == kOpLevel2 ? n : 0] : 1.0f, x);
+      widen(vr[n], OP == kOpLevel2 ? piece_vs[OP == kOpLevel2 ? n : 0] : 1.0f, y);
+      if (!CODES && edge) {
+        // A value that no row sees is 0; one that is not finite becomes 0 (it
+        // must not reach rows that do not see its key through 0 * inf) and its
+        // key is marked: the rows that see it get a NaN weight.
+        const bool any = j0 + key >= lo && j0 + key < hi;
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < EL / 2; ++e) {
+          uint32_t w = any ? y[e] : 0u;
+          if ((w & 0x7F80u) == 0x7F80u) { w &= 0xFFFF0000u; bad = true; }
+          if ((w & 0x7F800000u) == 0x7F800000u) { w &= 0xFFFFu; bad = true; }
+          y[e] = w;
+        }
+        // PR lanes in a row hold the key.
+        const uint64_t all = __ballot(bad) >> ((lane / PR) * PR);
+        if (pc == 0) s_wild[buf][key] = (all & ((PR < 64 ? (uint64_t)1 << (PR & 63) : 0) - 1)) != 0;
+      }
+#pragma unroll
+      for (int c = 0; c < EL / 8; ++c) {
+        const int ch = pc * (EL / 8) + c;
+        *reinterpret_cast<u32x4*>(s_k[buf] + key * DP + k_chunk<DP>(key, ch) * 8) =
+            u32x4{x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]};
+        *reinterpret_cast<u32x4*>(s_v[buf] + key * DP + v_chunk<DP>(key, ch) * 8) =
+            u32x4{y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]};
+      }
+    }
+    if constexpr (CODES) {
+      if (tid < 64) s_sc[buf][0][tid] = scale_k * s2;
+      else if (tid < 128) s_sc[buf][1][tid - 64] = scale_v;
+    }
+  };
+
+  auto compute = [&](int buf, int j0) {
+    f32x16 s[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[c][i] = 0.0f;
+      const int key = 32 * c + r;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(s_k[buf] + key * DP + k_chunk<DP>(key, 2 * t + h2) * 8);
+        s[c] = mfma32(as_bf16x8(w), q[t], s[c]);
+      }
+    }
+    if constexpr (CODES) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 f = *reinterpret_cast<const float4*>(&s_sc[buf][0][32 * c + 8 * i + 4 * h2]);
+          s[c][4 * i] *= f.x; s[c][4 * i + 1] *= f.y; s[c][4 * i + 2] *= f.z; s[c][4 * i + 3] *= f.w;
+        }
+    }
+    const float k2 = CODES ? 1.0f : s2;
+    const bool edge = j0 < wf_lo || j0 + kTileKeys > wf_hi;
+    if (edge) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int j = j0 + 32 * c + 8 * (i / 4) + 4 * h2 + i % 4;
+          if (j < my_lo || j >= my_hi) s[c][i] = -INFINITY;
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[0][i]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[1][i]);
+    {
+      const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+      top = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])) * k2;
+    }
+    if (__any(top > m + kSlack)) {
+      top = fmaxf(top, m);
+      const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+      l *= f;
+#pragma unroll
+      for (int t = 0; t < NB; ++t) o[t] *= f;
+      m = top;
+    }
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[c][i] = __builtin_amdgcn_exp2f(CODES ? s[c][i] - ref : __builtin_fmaf(s[c][i], k2, -ref));
+        sum += s[c][i];
+      }
+    l += sum;
+    if constexpr (CODES) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 f = *reinterpret_cast<const float4*>(&s_sc[buf][1][32 * c + 8 * i + 4 * h2]);
+          s[c][4 * i] *= f.x; s[c][4 * i + 1] *= f.y; s[c][4 * i + 2] *= f.z; s[c][4 * i + 3] *= f.w;
+        }
+      if (edge) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int j = j0 + 32 * c + 8 * (i / 4) + 4 * h2 + i % 4;
+            if (j < my_lo || j >= my_hi) s[c][i] = 0.0f;  // also where the scale is no number
+          }
+      }
+    } else if (j0 < full_lo || j0 + kTileKeys > full_hi) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = 32 * c + 8 * (i / 4) + 4 * h2 + i % 4, j = j0 + key;
+          if (s_wild[buf][key] && j >= my_lo && j < my_hi) s[c][i] = __uint_as_float(0x7FC00000u);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      // The weights enter the second product as bf16, their sum stays fp32.
+      float p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = s[n / 2][8 * (n % 2) + e];
+      const bf16x8 pb = to_bf16x8(p);
+#pragma unroll
+      for (int t = 0; t < NB; ++t) {
+        const int col = 32 * t + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+        s16x4 v[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int key = 16 * n + 8 * e + 4 * h2 + ((lane & 15) >> 2);
+          v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_s16x4*)(s_v[buf] + key * DP + v_chunk<DP>(key, col / 8) * 8 + (col & 7)));
+        }
+        const u32x4 w = {__builtin_bit_cast(uint2, v[0]).x, __builtin_bit_cast(uint2, v[0]).y,
+                         __builtin_bit_cast(uint2, v[1]).x, __builtin_bit_cast(uint2, v[1]).y};
+        o[t] = mfma32(as_bf16x8(w), pb, o[t]);
+      }
+    }
+  };
+
+  if (k0 < k1) {
+    load(k0);
+    store(0, k0);
+    __syncthreads();
+    int buf = 0;
+    for (int j0 = k0; j0 < k1; j0 += kTileKeys, buf ^= 1) {
+      const bool more = j0 + kTileKeys < k1;
+      if (more) load(j0 + kTileKeys);
+      if (j0 < w_hi && j0 + kTileKeys > w_lo) compute(buf, j0);
+      if (more) store(buf ^ 1, j0 + kTileKeys);
+      __syncthreads();
+    }
+  }
+
+  {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+    l = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  if (!ok) return;
+  const int Hq = H * G;
+  const int64_t at = (sq.first + qi) * Hq + h * G + qg;
+  if (a.splits > 1) {
+    const int64_t to = (int64_t)split * a.tokens * Hq + at;
+    if (h2 == 0) {
+      a.part_ml[2 * to] = m;
+      a.part_ml[2 * to + 1] = l;
+    }
+#pragma unroll
+    for (int t = 0; t < NB; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int d = 32 * t + 8 * i + 4 * h2;
+        if (EXACT || d < D)
+          *reinterpret_cast<float4*>(a.part_o + to * D + d) =
+              make_float4(o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]);
+      }
+    return;
+  }
+  const float inv = l == 0.0f ? 0.0f : (CODES ? a.unit : 1.0f) / l;
+  if (h2 == 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+#pragma unroll
+  for (int t = 0; t < NB; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = 32 * t + 8 * i + 4 * h2;
+      if (EXACT || d < D)
+        *reinterpret_cast<uint2*>(a.out + at * D + d) =
+            make_uint2(pack_bf16x2(o[t][4 * i] * inv, o[t][4 * i + 1] * inv),
+                       pack_bf16x2(o[t][4 * i + 2] * inv, o[t][4 * i + 3] * inv));
+    }
+}
+
+template <int OP, int DP>
+void tile_dim(const AttendArgs& a, dim3 grid, hipStream_t s) {
+  if (a.pool.dim == DP) hipLaunchKernelGGL((attend_tile_kernel<OP, DP, true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((attend_tile_kernel<OP, DP, false>), grid, dim3(256), 0, s, a);
+}
+template <int OP>
+void tile_op(const AttendArgs& a, dim3 grid, hipStream_t s) {
+  if (a.pool.dim <= 64) tile_dim<OP, 64>(a, grid, s);
+  else if (a.pool.dim <= 128) tile_dim<OP, 128>(a, grid, s);
+  else tile_dim<OP, 256>(a, grid, s);
+}
+
+}  // namespace
+
+void launch_attend_tile(const AttendArgs& a, hipStream_t s) {
+  const int64_t total = (int64_t)a.batch * a.pool.heads * a.tiles * a.splits;
+  const dim3 grid((unsigned)((total + 7) / 8 * 8));
+  if (a.pool.type == kKVBF16) tile_op<kOpBF16>(a, grid, s);
+  else if (a.pool.type == kKVINT8) tile_op<kOpINT8>(a, grid, s);
+  else if (a.pool.type == kKVNF4) tile_op<kOpLevel2>(a, grid, s);
+  else tile_op<kOpLevel>(a, grid, s);
+}
+
+}  // namespace qlora
