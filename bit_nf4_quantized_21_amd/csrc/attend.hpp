@@ -86,9 +86,9 @@ __device__ __forceinline__ float sum_groups(float x) {
 // How a cache's rows become MFMA operands.  Int8 codes and the levels of Int4
 // (k) and FP4 (m, whole halves) are exact in bf16; their 1/7 and 1/6 go to the
 // row's scale.  An NF4 level is not: rounded to bf16 it would be off by up to
-// 2^-9, the same way in every row, which a sum over 10^5 keys does not average
+// 2^-8, the same way in every row, which a sum over 10^5 keys does not average
 // out (7 % of such an output's norm, measured); it enters as the sum of two
-// bf16 values (2^-17), each with its own MFMA.
+// bf16 values (2^-16), each with its own MFMA.
 enum Operand { kOpBF16, kOpINT8, kOpLevel, kOpLevel2 };
 template <int KT>
 constexpr int kBitsOf = KT == kOpBF16 ? 16 : KT == kOpINT8 ? 8 : 4;
