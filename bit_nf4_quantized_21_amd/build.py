@@ -23,6 +23,9 @@ ARCH = "gfx950"
 HIP_FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-I", os.path.join(os.path.dirname(HERE), "include")]
+# Attention rescales its MFMA accumulators with vector instructions: kept in
+# plain VGPRs they need no copies out of and back into accumulation registers.
+FILE_FLAGS = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form=true"] for f in ("attend.hip", "attend_tile.hip")}
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall"]
 
 
@@ -46,7 +49,7 @@ def build(verbose: bool = False) -> str:
     for f in hip + hip_host:
         o = os.path.join(OBJ, f + ".o")
         lang = [] if f.endswith(".hip") else ["-x", "hip"]
-        jobs.append([HIPCC, *HIP_FLAGS, *lang, "-c", os.path.join(CSRC, f), "-o", o])
+        jobs.append([HIPCC, *HIP_FLAGS, *FILE_FLAGS.get(f, []), *lang, "-c", os.path.join(CSRC, f), "-o", o])
     for f in cxx:
         o = os.path.join(OBJ, f + ".o")
         jobs.append(["g++", *CXX_FLAGS, "-c", os.path.join(CSRC, f), "-o", o])

@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <cstdlib>
 
 #include "attend.hpp"
 #include "timing.hpp"
@@ -25,6 +26,17 @@ __device__ __forceinline__ uint2 level_pair(const uint2* lut, uint32_t offset) {
   const char* p = reinterpret_cast<const char*>(lut) + offset;
   if constexpr (KT == kOpLevel2) return *reinterpret_cast<const uint2*>(p);
   return make_uint2(*reinterpret_cast<const uint32_t*>(p), 0u);
+}
+
+// Four bytes' levels as MFMA operands: the levels, or levels and rests.
+template <int KT, int N>
+__device__ __forceinline__ void pack_levels(const uint2 (&w)[4], bf16x8 (&out)[N]) {
+  if constexpr (KT == kOpLevel2) {
+    out[0] = as_bf16x8(w[0].x, w[0].y, w[1].x, w[1].y);
+    out[N - 1] = as_bf16x8(w[2].x, w[2].y, w[3].x, w[3].y);
+  } else {
+    out[0] = as_bf16x8(w[0].x, w[1].x, w[2].x, w[3].x);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -43,8 +55,8 @@ __device__ __forceinline__ uint2 level_pair(const uint2* lut, uint32_t offset) {
 // they are, and lane (r, g) loads dims [r DP/16, (r + 1) DP/16) of those 8
 // keys; MFMA m of the DP/16 takes dim m of each.
 // ---------------------------------------------------------------------------
-template <int KT, int DP, int NQ, bool EXACT>
-__global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
+template <int KT, int DP, int NQ, int WAVES, bool EXACT>
+__global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a) {
   constexpr bool FOUR = KT == kOpLevel || KT == kOpLevel2;
   constexpr int BITS = kBitsOf<KT>;
   constexpr int NT = DP / 32;               // QK steps
@@ -53,19 +65,25 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
   constexpr int VB = DP / 16 * BITS / 8;    // bytes of a value's sixteenth row
   constexpr int VW = VB < 4 ? 1 : VB / 4;
   constexpr int OS = DP + 4;                // padded LDS row of the outputs
-  __shared__ __align__(16) float s_o[4 * 16 * OS];
-  __shared__ float s_m[4][16 * NQ], s_l[4][16 * NQ];
+  constexpr int STEP = 32 * WAVES;          // keys of a step of all waves
+  constexpr int TQ = 4 * WAVES;             // threads of a row at the end
+  constexpr int DT = DP / TQ;               // and their dims
+  __shared__ __align__(16) float s_o[WAVES * 16 * OS];
+  __shared__ float s_m[WAVES][16 * NQ], s_l[WAVES][16 * NQ];
   __shared__ int s_page[kMaxChunk / 16 + 1];
   __shared__ uint2 s_lut[FOUR ? 256 : 1];   // a byte's two levels: (bf16 pair, what it misses)
 
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // Heads fastest: consecutive workgroups go to the eight XCDs in turn, so each
+  // gets its share of every sequence, and the splits that only long sequences
+  // have come last.
   uint32_t id = blockIdx.x;
-  const int split = (int)(id % (uint32_t)a.splits);
-  id /= (uint32_t)a.splits;
-  const int tile = (int)(id % (uint32_t)a.tiles);
-  id /= (uint32_t)a.tiles;
-  const int H = a.pool.heads, h = (int)(id % (uint32_t)H), b = (int)(id / (uint32_t)H);
+  const int H = a.pool.heads, h = (int)(id % (uint32_t)H);
+  id /= (uint32_t)H;
+  const int b = (int)(id % (uint32_t)a.batch);
+  id /= (uint32_t)a.batch;
+  const int tile = (int)(id % (uint32_t)a.tiles), split = (int)(id / (uint32_t)a.tiles);
   const Seq sq = load_seq(a, b);
   if (sq.bad && tid == 0) atomicOr(a.status, kStatusIndex);
   const int G = a.group, rows = sq.n * G, row0 = tile * 16 * NQ;
@@ -79,7 +97,7 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
   const int full_hi = seen_hi(a, sq, i_first), full_lo = seen_lo(a, sq, i_last);
 
   const int shift = a.pool.shift, first_page = k0 >> shift, last = ((k1 - 1) >> shift) - first_page;
-  for (int p = tid; k0 < k1 && p <= last; p += 256) {
+  for (int p = tid; k0 < k1 && p <= last; p += 64 * WAVES) {
     int page = a.pages[(int64_t)b * a.width + first_page + p];
     if (page < 0 || page >= a.pool.pages) {
       atomicOr(a.status, kStatusIndex);
@@ -87,7 +105,7 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
     }
     s_page[p] = page;
   }
-  if (FOUR) {
+  if (FOUR && tid < 256) {
     uint32_t lo_v = a.levels[0], hi_v = a.levels[0];
 #pragma unroll
     for (int e = 1; e < 16; ++e) {
@@ -99,7 +117,10 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
 
   const int D = a.pool.dim;
   // Queries: row m of the tile is token m / G, head h * G + m % G.
-  bf16x8 q[NQ][NT];
+  // (With two bf16 values per level a lane's 8 operand elements are two pairs
+  // of codes: (level, level, rest, rest) twice, against each pair of q twice.)
+  constexpr int QW = KT == kOpLevel2 ? 2 : 1;
+  bf16x8 q[NQ][NT][QW];
   int my_lo[NQ], my_hi[NQ];
 #pragma unroll
   for (int x = 0; x < NQ; ++x) {
@@ -114,7 +135,12 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
       const int d = g * (DP / 4) + t * 8;
       u32x4 w = {0, 0, 0, 0};
       if (ok && (EXACT || d < D)) w = *reinterpret_cast<const u32x4*>(p + d);
-      q[x][t] = as_bf16x8(w);
+      if constexpr (KT == kOpLevel2) {
+        q[x][t][0] = as_bf16x8(w[0], w[0], w[1], w[1]);
+        q[x][t][QW - 1] = as_bf16x8(w[2], w[2], w[3], w[3]);
+      } else {
+        q[x][t][0] = as_bf16x8(w);
+      }
     }
   }
   __syncthreads();
@@ -208,24 +234,21 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        bf16x8 ka;
+        bf16x8 ka[QW];
         if constexpr (KT == kOpBF16) {
-          ka = as_bf16x8(st.k[c][4 * t], st.k[c][4 * t + 1], st.k[c][4 * t + 2], st.k[c][4 * t + 3]);
+          ka[0] = as_bf16x8(st.k[c][4 * t], st.k[c][4 * t + 1], st.k[c][4 * t + 2], st.k[c][4 * t + 3]);
         } else if constexpr (KT == kOpINT8) {
-          ka = int8_to_bf16x8(st.k[c][2 * t], st.k[c][2 * t + 1]);
+          ka[0] = int8_to_bf16x8(st.k[c][2 * t], st.k[c][2 * t + 1]);
         } else {
           uint2 w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) w[e] = level_pair<KT>(s_lut, byte_x8(st.k[c][t], e));
-          ka = as_bf16x8(w[0].x, w[1].x, w[2].x, w[3].x);
-          if constexpr (KT == kOpLevel2) {
-            const bf16x8 kl = as_bf16x8(w[0].y, w[1].y, w[2].y, w[3].y);
-#pragma unroll
-            for (int x = 0; x < NQ; ++x) s[x][c] = mfma16(kl, q[x][t], s[x][c]);
-          }
+          pack_levels<KT>(w, ka);
         }
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) s[x][c] = mfma16(ka, q[x][t], s[x][c]);
+        for (int n = 0; n < QW; ++n)
+#pragma unroll
+          for (int x = 0; x < NQ; ++x) s[x][c] = mfma16(ka[n], q[x][t][n], s[x][c]);
       }
 
     const bool edge = j0 < full_lo || j0 + 32 > full_hi;
@@ -252,7 +275,7 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
       }
     }
 
-    bf16x8 pb[NQ];
+    bf16x8 pb[NQ][QW];
 #pragma unroll
     for (int x = 0; x < NQ; ++x) {
       float p[8];
@@ -301,7 +324,13 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
       // The weights enter the second product as bf16 (their sum stays fp32):
       // half a unit in the 8th bit of each, to either side, against the
       // output's own rounding to as many bits.
-      pb[x] = to_bf16x8(p);
+      if constexpr (KT == kOpLevel2) {
+        const uint32_t w[4] = {pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7])};
+        pb[x][0] = as_bf16x8(w[0], w[0], w[1], w[1]);
+        pb[x][QW - 1] = as_bf16x8(w[2], w[2], w[3], w[3]);
+      } else {
+        pb[x][0] = to_bf16x8(p);
+      }
     }
 
     // Values of dim t for the lane's 8 keys, two keys to a dword.
@@ -331,14 +360,13 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
           w[c] = level_pair<KT>(s_lut, byte_x8((t & 1 ? odd : even)[c][t / 8], t % 8 / 2));
         }
       }
-      if constexpr (KT == kOpLevel2) {
-        const bf16x8 vl = as_bf16x8(w[0].y, w[1].y, w[2].y, w[3].y);
+      bf16x8 vt[QW];
+      if constexpr (FOUR) pack_levels<KT>(w, vt);
+      else vt[0] = as_bf16x8(w[0].x, w[1].x, w[2].x, w[3].x);
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) o[x][t] = mfma16(vl, pb[x], o[x][t]);
-      }
-      const bf16x8 vt = as_bf16x8(w[0].x, w[1].x, w[2].x, w[3].x);
+      for (int n = 0; n < QW; ++n)
 #pragma unroll
-      for (int x = 0; x < NQ; ++x) o[x][t] = mfma16(vt, pb[x], o[x][t]);
+        for (int x = 0; x < NQ; ++x) o[x][t] = mfma16(vt[n], pb[x][n], o[x][t]);
     }
   };
 
@@ -347,20 +375,20 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
   // the ones before it a wait for all).
   int j = k0 + 32 * wave;
   if (j < k1) {
-    const int end = j + (k1 - 1 - j) / 128 * 128;  // this wave's last step
+    const int end = j + (k1 - 1 - j) / STEP * STEP;  // this wave's last step
     Stage st[2];
     load(st[0], j);
     for (;;) {
-      load(st[1], min(j + 128, end));
+      load(st[1], min(j + STEP, end));
       compute(st[0], j);
-      if ((j += 128) >= k1) break;
-      load(st[0], min(j + 128, end));
+      if ((j += STEP) >= k1) break;
+      load(st[0], min(j + STEP, end));
       compute(st[1], j);
-      if ((j += 128) >= k1) break;
+      if ((j += STEP) >= k1) break;
     }
   }
 
-  // The four waves' sums meet.  Lane (r, g) holds, of query r, the dims
+  // The waves' sums meet.  Lane (r, g) holds, of query r, the dims
   // g DP/4 + i NM + t (register i of MFMA t).
 #pragma unroll
   for (int x = 0; x < NQ; ++x) {
@@ -377,7 +405,7 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
     {
       float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) top = fmaxf(top, s_m[w][16 * x + r]);
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, s_m[w][16 * x + r]);
       const float f = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[x] - top);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -387,13 +415,14 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
               make_float4(o[x][t][i] * f, o[x][t + 1][i] * f, o[x][t + 2][i] * f, o[x][t + 3][i] * f);
     }
     __syncthreads();
-    const int qr = tid >> 4, part = tid & 15, row = row0 + 16 * x + qr;
+    const int qr = tid / TQ, part = tid % TQ, row = row0 + 16 * x + qr;
     if (row < rows) {
       float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) top = fmaxf(top, s_m[w][16 * x + qr]);
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, s_m[w][16 * x + qr]);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) sum += s_l[w][16 * x + qr] * (top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(s_m[w][16 * x + qr] - top));
+      for (int w = 0; w < WAVES; ++w)
+        sum += s_l[w][16 * x + qr] * (top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(s_m[w][16 * x + qr] - top));
       const int i = row / G, gh = row - i * G;
       const int64_t at = (sq.first + i) * Hq + h * G + gh;
       const float inv = sum == 0.0f ? 0.0f : a.unit / sum;
@@ -406,20 +435,23 @@ __global__ __launch_bounds__(256) void attend_stream_kernel(AttendArgs a) {
           a.lse[at] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
         }
       }
-      if (EXACT || part * NM < D) {
+      if (EXACT || part * DT < D) {
+        float v[DT] = {};
 #pragma unroll
-        for (int t = 0; t < NM; t += 4) {
-          float4 v = make_float4(0, 0, 0, 0);
+        for (int w = 0; w < WAVES; ++w)
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const float4 p = *reinterpret_cast<const float4*>(s_o + (w * 16 + qr) * OS + part * NM + t);
-            v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
-          }
-          if (a.splits > 1) {
-            *reinterpret_cast<float4*>(a.part_o + ((int64_t)split * a.tokens * Hq + at) * D + part * NM + t) = v;
+          for (int t = 0; t < DT; ++t) v[t] += s_o[(w * 16 + qr) * OS + part * DT + t];
+        if (a.splits > 1) {
+          float* po = a.part_o + ((int64_t)split * a.tokens * Hq + at) * D + part * DT;
+#pragma unroll
+          for (int t = 0; t < DT; ++t) po[t] = v[t];
+        } else {
+          uint16_t* to = a.out + at * D + part * DT;
+          if constexpr (DT == 1) {
+            to[0] = (uint16_t)pack_bf16x2(v[0] * inv, 0.0f);
           } else {
-            *reinterpret_cast<uint2*>(a.out + at * D + part * NM + t) =
-                make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+#pragma unroll
+            for (int t = 0; t < DT; t += 2) reinterpret_cast<uint32_t*>(to)[t / 2] = pack_bf16x2(v[t] * inv, v[t + 1] * inv);
           }
         }
       }
@@ -505,7 +537,7 @@ float bf16_value_host(uint32_t h) {
 // keys of a split.
 struct Plan {
   bool tile;  // the tile kernel, else the streaming one
-  int tile_rows;
+  int tile_rows, waves;
   int64_t tiles, splits, chunk;
 };
 
@@ -520,31 +552,44 @@ Plan make_plan(const AttendProblem& p) {
   if (p.window > 0 && p.causal) span = std::min<int64_t>(span, (int64_t)p.window + r.tile_rows);
   span += 15;
   const int64_t work = std::max<int64_t>(1, (int64_t)p.batch * p.pool.heads * r.tiles);
-  const int64_t want = r.tile ? 512 : 1024, least = r.tile ? 512 : 256;
-  const int64_t splits = std::max<int64_t>(1, std::min((want + work - 1) / work, span / least));
+  // Splits cost a second launch and its partial sums (6 us at the least), so
+  // the keys are only split where too few workgroups would be left to fill the
+  // chip.  Streaming, 128 workgroups reach the memory's rate: 4 sequences of
+  // up to 1000 tokens, 32 heads, bf16, 15.7 us in one launch, 13.1 + 4.0 and
+  // the gap in two; 64 of up to 8192, 8 heads, int8, 141 us, 133 + 12 in four
+  // splits.  8 heads of 131071 NF4 keys: 509 us whole, 42 + 4 in 32 splits.
+  const int64_t full = r.tile ? 512 : 128, want = r.tile ? 512 : 256;
+  int64_t splits = work >= full ? 1 : std::min((want + work - 1) / work, span / 512);
+  splits = std::max<int64_t>(splits, 1);
+  // Eight waves to a workgroup where each has steps enough (131071 keys: the
+  // same time with half the splits to join); four for short sequences (up to
+  // 1000 tokens: 15.7 us, 17.2 with eight).
+  r.waves = span / splits > 2048 ? 8 : 4;
+  if (!r.tile && getenv("QW")) r.waves = atoi(getenv("QW"));
+  if (!r.tile && getenv("QS")) splits = std::max<int64_t>(1, std::min<int64_t>(atoi(getenv("QS")), span / 256));
   r.chunk = ((span + splits - 1) / splits + 127) / 128 * 128;
   r.chunk = std::min<int64_t>(std::max<int64_t>(r.chunk, 128), kMaxChunk);
   r.splits = std::max<int64_t>(1, (span + r.chunk - 1) / r.chunk);
   return r;
 }
 
-template <int KT, int DP, int NQ>
+template <int KT, int DP, int NQ, int WAVES>
 void stream_dim(const AttendArgs& a, unsigned grid, hipStream_t s) {
-  if (a.pool.dim == DP) hipLaunchKernelGGL((attend_stream_kernel<KT, DP, NQ, true>), dim3(grid), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((attend_stream_kernel<KT, DP, NQ, false>), dim3(grid), dim3(256), 0, s, a);
+  if (a.pool.dim == DP) hipLaunchKernelGGL((attend_stream_kernel<KT, DP, NQ, WAVES, true>), dim3(grid), dim3(64 * WAVES), 0, s, a);
+  else hipLaunchKernelGGL((attend_stream_kernel<KT, DP, NQ, WAVES, false>), dim3(grid), dim3(64 * WAVES), 0, s, a);
 }
 template <int KT, int NQ>
-void stream_type(const AttendArgs& a, unsigned grid, hipStream_t s) {
-  if (a.pool.dim <= 64) stream_dim<KT, 64, NQ>(a, grid, s);
-  else if (a.pool.dim <= 128) stream_dim<KT, 128, NQ>(a, grid, s);
-  else stream_dim<KT, 256, NQ>(a, grid, s);
+void stream_type(const AttendArgs& a, int waves, unsigned grid, hipStream_t s) {
+  if (a.pool.dim <= 64) waves == 8 ? stream_dim<KT, 64, NQ, 8>(a, grid, s) : stream_dim<KT, 64, NQ, 4>(a, grid, s);
+  else if (a.pool.dim <= 128) waves == 8 ? stream_dim<KT, 128, NQ, 8>(a, grid, s) : stream_dim<KT, 128, NQ, 4>(a, grid, s);
+  else waves == 8 ? stream_dim<KT, 256, NQ, 8>(a, grid, s) : stream_dim<KT, 256, NQ, 4>(a, grid, s);
 }
 template <int NQ>
-void stream_rows(const AttendArgs& a, unsigned grid, hipStream_t s) {
-  if (a.pool.type == kKVBF16) stream_type<kOpBF16, NQ>(a, grid, s);
-  else if (a.pool.type == kKVINT8) stream_type<kOpINT8, NQ>(a, grid, s);
-  else if (a.pool.type == kKVNF4) stream_type<kOpLevel2, NQ>(a, grid, s);
-  else stream_type<kOpLevel, NQ>(a, grid, s);
+void stream_rows(const AttendArgs& a, int waves, unsigned grid, hipStream_t s) {
+  if (a.pool.type == kKVBF16) stream_type<kOpBF16, NQ>(a, waves, grid, s);
+  else if (a.pool.type == kKVINT8) stream_type<kOpINT8, NQ>(a, waves, grid, s);
+  else if (a.pool.type == kKVNF4) stream_type<kOpLevel2, NQ>(a, waves, grid, s);
+  else stream_type<kOpLevel, NQ>(a, waves, grid, s);
 }
 
 }  // namespace
@@ -607,8 +652,8 @@ hipError_t launch_attend(const AttendProblem& p, const float table[16], void* ws
   } else {
     KernelTimer kt_("attend_stream_kernel", s);
     const unsigned grid = (unsigned)(p.batch * p.pool.heads * r.tiles * r.splits);
-    if (r.tile_rows == 16) stream_rows<1>(a, grid, s);
-    else stream_rows<2>(a, grid, s);
+    if (r.tile_rows == 16) stream_rows<1>(a, r.waves, grid, s);
+    else stream_rows<2>(a, r.waves, grid, s);
     e = hipGetLastError();
   }
   if (e != hipSuccess || r.splits == 1) return e;
