@@ -11,7 +11,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
-#include <cstdlib>
 
 #include "attend.hpp"
 #include "timing.hpp"
@@ -20,12 +19,16 @@ namespace qlora {
 
 namespace {
 
-// The bf16 levels of the two codes of a byte (offset: 8 times the byte).
+// The levels of the two codes in byte q of x, from the LDS table at address 0
+// (`lut`): an entry per byte, a bf16 pair, or for kOpLevel2 that and the pair
+// of what it misses.  (A table of 16 single codes, whose reads never meet in a
+// bank, needs twice the reads and four more instructions a pair: 131071 NF4
+// keys 54.7 us, 41 this way.)
 template <int KT>
-__device__ __forceinline__ uint2 level_pair(const uint2* lut, uint32_t offset) {
-  const char* p = reinterpret_cast<const char*>(lut) + offset;
-  if constexpr (KT == kOpLevel2) return *reinterpret_cast<const uint2*>(p);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(p), 0u);
+__device__ __forceinline__ uint2 level_pair(const uint32_t* lut, uint32_t x, int q) {
+  const char* p = reinterpret_cast<const char*>(lut);
+  if constexpr (KT == kOpLevel2) return *reinterpret_cast<const uint2*>(p + byte_x8(x, q));
+  return make_uint2(*reinterpret_cast<const uint32_t*>(p + byte_x4(x, q)), 0u);
 }
 
 // Four bytes' levels as MFMA operands: the levels, or levels and rests.
@@ -68,10 +71,20 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
   constexpr int STEP = 32 * WAVES;          // keys of a step of all waves
   constexpr int TQ = 4 * WAVES;             // threads of a row at the end
   constexpr int DT = DP / TQ;               // and their dims
-  __shared__ __align__(16) float s_o[WAVES * 16 * OS];
-  __shared__ float s_m[WAVES][16 * NQ], s_l[WAVES][16 * NQ];
-  __shared__ int s_page[kMaxChunk / 16 + 1];
-  __shared__ uint2 s_lut[FOUR ? 256 : 1];   // a byte's two levels: (bf16 pair, what it misses)
+  // One LDS object with the table of levels first: at address 0 a byte's
+  // offset is its address.
+  struct __align__(16) Shared {
+    uint32_t lut[KT == kOpLevel2 ? 512 : KT == kOpLevel ? 256 : 4];
+    float o[WAVES * 16 * OS];
+    float m[WAVES][16 * NQ], l[WAVES][16 * NQ];
+    int page[kMaxChunk / 16 + 1];
+  };
+  __shared__ Shared sh;
+  auto& s_lut = sh.lut;
+  auto& s_o = sh.o;
+  auto& s_m = sh.m;
+  auto& s_l = sh.l;
+  auto& s_page = sh.page;
 
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -106,13 +119,15 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
     s_page[p] = page;
   }
   if (FOUR && tid < 256) {
-    uint32_t lo_v = a.levels[0], hi_v = a.levels[0];
+    uint32_t x = a.levels[0], y = a.levels[0];
 #pragma unroll
     for (int e = 1; e < 16; ++e) {
-      lo_v = (tid & 15) == e ? a.levels[e] : lo_v;
-      hi_v = (tid >> 4) == e ? a.levels[e] : hi_v;
+      x = (tid & 15) == e ? a.levels[e] : x;
+      y = (tid >> 4) == e ? a.levels[e] : y;
     }
-    s_lut[tid] = make_uint2((lo_v & 0xFFFFu) | (hi_v << 16), (lo_v >> 16) | (hi_v & 0xFFFF0000u));
+    const uint32_t pair = (x & 0xFFFFu) | (y << 16), rest = (x >> 16) | (y & 0xFFFF0000u);
+    if constexpr (KT == kOpLevel2) reinterpret_cast<uint2*>(s_lut)[tid] = make_uint2(pair, rest);
+    else s_lut[tid] = pair;
   }
 
   const int D = a.pool.dim;
@@ -164,17 +179,18 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
   struct Stage {
     uint32_t k[2][KW], v[8][VW];
     float4 ks[2], vs[2];
+  } st;
+  // First row of a 16-key block (blocks lie within a page).
+  auto block = [&](int j) -> int64_t {
+    // The second block's page may lie past the list: its keys are not seen.
+    const int page = __builtin_amdgcn_readfirstlane(s_page[min((j >> shift) - first_page, last)]);
+    return (((int64_t)page * H + h) << shift) + (j & ((1 << shift) - 1));
   };
-  auto load = [&](Stage& st, int j0) {
+  auto load_k = [&](int j0) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int j = j0 + 16 * c;
-      // The second block's page may lie past the list: its keys are not seen.
-      const int page = __builtin_amdgcn_readfirstlane(s_page[min((j >> shift) - first_page, last)]);
-      const int64_t base = (((int64_t)page * H + h) << shift) + (j & ((1 << shift) - 1));
-      const uint8_t* kb = a.pool.k + base * row_bytes;
-      const uint8_t* vb = a.pool.v + base * row_bytes;
-      const uint8_t* kp = kb + k_off;
+      const int64_t base = block(j0 + 16 * c);
+      const uint8_t* kp = a.pool.k + base * row_bytes + k_off;
       if constexpr (EXACT) {
         if constexpr (KW % 4 == 0) {
 #pragma unroll
@@ -195,6 +211,14 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
           for (int w = 0; w < SW; ++w) st.k[c][t * SW + w] = in ? reinterpret_cast<const uint32_t*>(kp)[t * SW + w] : 0u;
         }
       }
+      if constexpr (KT != kOpBF16) st.ks[c] = reinterpret_cast<const float4*>(a.pool.ks + base)[g];
+    }
+  };
+  auto load_v = [&](int j0) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int64_t base = block(j0 + 16 * c);
+      const uint8_t* vb = a.pool.v + base * row_bytes;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint8_t* vp = vb + v_off + e * (uint32_t)row_bytes;
@@ -219,37 +243,73 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
           for (int x = 0; x < VW; ++x) w[x] = 0;
         }
       }
-      if constexpr (KT != kOpBF16) {
-        st.ks[c] = reinterpret_cast<const float4*>(a.pool.ks + base)[g];
-        st.vs[c] = reinterpret_cast<const float4*>(a.pool.vs + base)[g];
-      }
+      if constexpr (KT != kOpBF16) st.vs[c] = reinterpret_cast<const float4*>(a.pool.vs + base)[g];
     }
   };
 
-  auto compute = [&](Stage& st, int j0) {
+  // Levels of dims t .. t + TG - 1 of the lane's 8 values: the codes of two
+  // keys, side by side in a byte, name both levels.
+  constexpr int TG = 4;
+  uint2 vl[FOUR ? 2 : 1][TG][4];
+  auto look_up = [&](int t0) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t va = st.v[2 * c][t0 / 8], vb = st.v[2 * c + 1][t0 / 8];
+      const uint32_t even = (va & 0x0F0F0F0Fu) | ((vb << 4) & 0xF0F0F0F0u);
+      const uint32_t odd = ((va >> 4) & 0x0F0F0F0Fu) | (vb & 0xF0F0F0F0u);
+#pragma unroll
+      for (int t = 0; t < TG; ++t)
+        vl[t0 / TG % 2][t][c] = level_pair<KT>(s_lut, t & 1 ? odd : even, (t0 + t) % 8 / 2);
+    }
+  };
+
+  // One step; the next one's keys load once this one's are used up, and its
+  // values likewise: loads are always in flight, in the same registers.
+  auto compute = [&](int j0, int next) {
     f32x4 s[NQ][2];
 #pragma unroll
     for (int x = 0; x < NQ; ++x) s[x][0] = s[x][1] = f32x4{0, 0, 0, 0};
+    // 4 bits: the lookups of a group go out before the group before it is used
+    // (the fences keep the compiler from pairing each with its use, which would
+    // wait for LDS at every one).
+    constexpr int KG = NT < 4 ? NT : 4;
+    uint2 kl[FOUR ? 2 : 1][KG][4];
+    auto look_up_k = [&](int n) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+      for (int t = 0; t < KG; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        bf16x8 ka[QW];
-        if constexpr (KT == kOpBF16) {
-          ka[0] = as_bf16x8(st.k[c][4 * t], st.k[c][4 * t + 1], st.k[c][4 * t + 2], st.k[c][4 * t + 3]);
-        } else if constexpr (KT == kOpINT8) {
-          ka[0] = int8_to_bf16x8(st.k[c][2 * t], st.k[c][2 * t + 1]);
-        } else {
-          uint2 w[4];
+        for (int e = 0; e < 4; ++e)
+          kl[n % 2][t][e] = level_pair<KT>(s_lut, st.k[(n * KG + t) / NT][(n * KG + t) % NT], e);
+    };
+    if constexpr (FOUR) look_up_k(0);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = level_pair<KT>(s_lut, byte_x8(st.k[c][t], e));
-          pack_levels<KT>(w, ka);
+    for (int n = 0; n < 2 * NT; ++n) {
+      const int c = n / NT, t = n % NT;
+      bf16x8 ka[QW];
+      if constexpr (KT == kOpBF16) {
+        ka[0] = as_bf16x8(st.k[c][4 * t], st.k[c][4 * t + 1], st.k[c][4 * t + 2], st.k[c][4 * t + 3]);
+      } else if constexpr (KT == kOpINT8) {
+        ka[0] = int8_to_bf16x8(st.k[c][2 * t], st.k[c][2 * t + 1]);
+      } else {
+        if (n % KG == 0) {
+          if (n + KG < 2 * NT) look_up_k(n / KG + 1);
+          __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int n = 0; n < QW; ++n)
-#pragma unroll
-          for (int x = 0; x < NQ; ++x) s[x][c] = mfma16(ka[n], q[x][t][n], s[x][c]);
+        pack_levels<KT>(kl[n / KG % 2][n % KG], ka);
       }
+#pragma unroll
+      for (int w = 0; w < QW; ++w)
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) s[x][c] = mfma16(ka[w], q[x][t][w], s[x][c]);
+    }
+
+    if constexpr (KT != kOpBF16) {
+#pragma unroll
+      for (int x = 0; x < NQ; ++x)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[x][e / 4][e % 4] *= reinterpret_cast<const float*>(&st.ks[e / 4])[e % 4];
+    }
+    load_k(next);
 
     const bool edge = j0 < full_lo || j0 + 32 > full_hi;
     // Keys of the edge: those that no row of the tile sees hold anything (the
@@ -275,12 +335,16 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
       }
     }
 
-    bf16x8 pb[NQ][QW];
+    if constexpr (FOUR) {
+      look_up(0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    bf16x8 pb[NQ][2][QW];
 #pragma unroll
     for (int x = 0; x < NQ; ++x) {
       float p[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = s[x][e / 4][e % 4] * (KT == kOpBF16 ? s2 : s2 * reinterpret_cast<const float*>(&st.ks[e / 4])[e % 4]);
+      for (int e = 0; e < 8; ++e) p[e] = s[x][e / 4][e % 4] * s2;
       uint32_t hidden = 0;
       if (edge) {
 #pragma unroll
@@ -321,71 +385,69 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
         for (int e = 0; e < 8; ++e)
           if ((wild & ~hidden) >> e & 1u) p[e] = __uint_as_float(0x7FC00000u);
       }
-      // The weights enter the second product as bf16 (their sum stays fp32):
-      // half a unit in the 8th bit of each, to either side, against the
-      // output's own rounding to as many bits.
-      if constexpr (KT == kOpLevel2) {
-        const uint32_t w[4] = {pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7])};
-        pb[x][0] = as_bf16x8(w[0], w[0], w[1], w[1]);
-        pb[x][QW - 1] = as_bf16x8(w[2], w[2], w[3], w[3]);
-      } else {
-        pb[x][0] = to_bf16x8(p);
+      // The weights enter the second product as two bf16 values, their sum off
+      // by 2^-16: one alone (2^-8) would show beside the output's own rounding,
+      // and the matrix units have time while the rows stream.
+      uint32_t w[2][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[0][e] = pack_bf16x2(p[2 * e], p[2 * e + 1]);
+        w[1][e] = pack_bf16x2(p[2 * e] - bf16_lo(w[0][e]), p[2 * e + 1] - bf16_hi(w[0][e]));
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        if constexpr (KT == kOpLevel2) {
+          pb[x][n][0] = as_bf16x8(w[n][0], w[n][0], w[n][1], w[n][1]);
+          pb[x][n][QW - 1] = as_bf16x8(w[n][2], w[n][2], w[n][3], w[n][3]);
+        } else {
+          pb[x][n][0] = as_bf16x8(w[n][0], w[n][1], w[n][2], w[n][3]);
+        }
       }
     }
 
-    // Values of dim t for the lane's 8 keys, two keys to a dword.
-    uint32_t even[4][VW], odd[4][VW];  // 4 bits: the codes of two keys side by side, dims 2n and 2n + 1
-    if constexpr (FOUR) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          const uint32_t va = st.v[2 * c][w], vb = st.v[2 * c + 1][w];
-          even[c][w] = (va & 0x0F0F0F0Fu) | ((vb << 4) & 0xF0F0F0F0u);
-          odd[c][w] = ((va >> 4) & 0x0F0F0F0Fu) | (vb & 0xF0F0F0F0u);
-        }
-    }
+    // Values of dim t for the lane's 8 keys, two keys to a dword; for 4 bits
+    // the lookups of a group of dims go out while the last group is used.
 #pragma unroll
     for (int t = 0; t < NM; ++t) {
-      uint2 w[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t(&va)[VW] = st.v[2 * c];
-        const uint32_t(&vb)[VW] = st.v[2 * c + 1];
-        if constexpr (KT == kOpBF16) {
-          w[c].x = __builtin_amdgcn_perm(vb[t / 2], va[t / 2], t & 1 ? 0x07060302u : 0x05040100u);
-        } else if constexpr (KT == kOpINT8) {
-          w[c].x = pack_bf16x2((float)(int8_t)(va[t / 4] >> (8 * (t % 4))), (float)(int8_t)(vb[t / 4] >> (8 * (t % 4))));
-        } else {
-          w[c] = level_pair<KT>(s_lut, byte_x8((t & 1 ? odd : even)[c][t / 8], t % 8 / 2));
-        }
-      }
       bf16x8 vt[QW];
-      if constexpr (FOUR) pack_levels<KT>(w, vt);
-      else vt[0] = as_bf16x8(w[0].x, w[1].x, w[2].x, w[3].x);
+      if constexpr (FOUR) {
+        if (t % TG == 0) {
+          if (t + TG < NM) look_up(t + TG);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        pack_levels<KT>(vl[t / TG % 2][t % TG], vt);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t(&va)[VW] = st.v[2 * c];
+          const uint32_t(&vb)[VW] = st.v[2 * c + 1];
+          if constexpr (KT == kOpBF16)
+            w[c] = __builtin_amdgcn_perm(vb[t / 2], va[t / 2], t & 1 ? 0x07060302u : 0x05040100u);
+          else
+            w[c] = pack_bf16x2((float)(int8_t)(va[t / 4] >> (8 * (t % 4))), (float)(int8_t)(vb[t / 4] >> (8 * (t % 4))));
+        }
+        vt[0] = as_bf16x8(w[0], w[1], w[2], w[3]);
+      }
 #pragma unroll
       for (int n = 0; n < QW; ++n)
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) o[x][t] = mfma16(vt[n], pb[x][n], o[x][t]);
+        for (int x = 0; x < NQ; ++x) {
+          o[x][t] = mfma16(vt[n], pb[x][1][n], o[x][t]);
+          o[x][t] = mfma16(vt[n], pb[x][0][n], o[x][t]);
+        }
     }
+    load_v(next);
   };
 
-  // The next step's rows load while this one's are used; past the last step
-  // they are its own again (a load that may not happen would make the wait for
-  // the ones before it a wait for all).
   int j = k0 + 32 * wave;
   if (j < k1) {
     const int end = j + (k1 - 1 - j) / STEP * STEP;  // this wave's last step
-    Stage st[2];
-    load(st[0], j);
-    for (;;) {
-      load(st[1], min(j + STEP, end));
-      compute(st[0], j);
-      if ((j += STEP) >= k1) break;
-      load(st[0], min(j + STEP, end));
-      compute(st[1], j);
-      if ((j += STEP) >= k1) break;
-    }
+    load_k(j);
+    load_v(j);
+    // Past the last step the rows loaded are its own again: a load that may
+    // not happen would make the wait for the ones before it a wait for all.
+    for (; j < k1; j += STEP) compute(j, min(j + STEP, end));
   }
 
   // The waves' sums meet.  Lane (r, g) holds, of query r, the dims
@@ -555,18 +617,16 @@ Plan make_plan(const AttendProblem& p) {
   // Splits cost a second launch and its partial sums (6 us at the least), so
   // the keys are only split where too few workgroups would be left to fill the
   // chip.  Streaming, 128 workgroups reach the memory's rate: 4 sequences of
-  // up to 1000 tokens, 32 heads, bf16, 15.7 us in one launch, 13.1 + 4.0 and
-  // the gap in two; 64 of up to 8192, 8 heads, int8, 141 us, 133 + 12 in four
-  // splits.  8 heads of 131071 NF4 keys: 509 us whole, 42 + 4 in 32 splits.
+  // up to 1000 tokens, 32 heads, bf16, 16.0 us in one launch, 13.0 + 4.0 and
+  // the gap in two; 64 of up to 8192, 8 heads, int8, 145 us, 134 + 12 in four
+  // splits.  8 heads of 131071 NF4 keys: 43 + 4 us in 32 splits of eight waves,
+  // 44 + 5.5 in 64 of four.
   const int64_t full = r.tile ? 512 : 128, want = r.tile ? 512 : 256;
   int64_t splits = work >= full ? 1 : std::min((want + work - 1) / work, span / 512);
   splits = std::max<int64_t>(splits, 1);
-  // Eight waves to a workgroup where each has steps enough (131071 keys: the
-  // same time with half the splits to join); four for short sequences (up to
-  // 1000 tokens: 15.7 us, 17.2 with eight).
-  r.waves = span / splits > 2048 ? 8 : 4;
-  if (!r.tile && getenv("QW")) r.waves = atoi(getenv("QW"));
-  if (!r.tile && getenv("QS")) splits = std::max<int64_t>(1, std::min<int64_t>(atoi(getenv("QS")), span / 256));
+  // Eight waves to a workgroup where each has steps enough; four for short
+  // sequences (those 4 of up to 1000 tokens: 16.1 us, 17.8 with eight).
+  r.waves = span / splits > 2048 && r.tile_rows == 16 ? 8 : 4;
   r.chunk = ((span + splits - 1) / splits + 127) / 128 * 128;
   r.chunk = std::min<int64_t>(std::max<int64_t>(r.chunk, 128), kMaxChunk);
   r.splits = std::max<int64_t>(1, (span + r.chunk - 1) / r.chunk);
