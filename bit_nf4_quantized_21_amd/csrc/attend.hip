@@ -27,8 +27,8 @@ namespace {
 template <int KT>
 __device__ __forceinline__ uint2 level_pair(const uint32_t* lut, uint32_t x, int q) {
   const char* p = reinterpret_cast<const char*>(lut);
-  if constexpr (KT == kOpLevel2) return *reinterpret_cast<const uint2*>(p + byte_x8(x, q));
-  return make_uint2(*reinterpret_cast<const uint32_t*>(p + byte_x4(x, q)), 0u);
+  if constexpr (KT == kOpLevel2) return *reinterpret_cast<const uint2*>(p + lut_offset<8>(x, q));
+  return make_uint2(*reinterpret_cast<const uint32_t*>(p + lut_offset<4>(x, q)), 0u);
 }
 
 // Four bytes' levels as MFMA operands: the levels, or levels and rests.
@@ -91,17 +91,17 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
   // Heads fastest: consecutive workgroups go to the eight XCDs in turn, so each
   // gets its share of every sequence, and the splits that only long sequences
   // have come last.
-  uint32_t id = blockIdx.x;
-  const int H = a.pool.heads, h = (int)(id % (uint32_t)H);
-  id /= (uint32_t)H;
-  const int b = (int)(id % (uint32_t)a.batch);
-  id /= (uint32_t)a.batch;
-  const int tile = (int)(id % (uint32_t)a.tiles), split = (int)(id / (uint32_t)a.tiles);
+  const int H = a.pool.heads;
+  int id = (int)blockIdx.x, next = uniform_div(id, H);
+  const int h = id - next * H;
+  id = next;
+  next = uniform_div(id, a.batch);
+  const int b = id - next * a.batch, split = uniform_div(next, a.tiles), tile = next - split * a.tiles;
   const Seq sq = load_seq(a, b);
   if (sq.bad && tid == 0) atomicOr(a.status, kStatusIndex);
   const int G = a.group, rows = sq.n * G, row0 = tile * 16 * NQ;
   if (row0 >= rows) return;
-  const int i_first = row0 / G, i_last = (min(rows, row0 + 16 * NQ) - 1) / G;
+  const int i_first = uniform_div(row0, G), i_last = uniform_div(min(rows, row0 + 16 * NQ) - 1, G);
   const int hi = seen_hi(a, sq, i_last), lo = seen_lo(a, sq, i_first);
   const int k0 = (lo & ~15) + split * a.chunk;
   if (split > 0 && k0 >= hi) return;
@@ -349,8 +349,8 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
       if (edge) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int j = j0 + 16 * (e / 4) + 4 * g + e % 4;
-          if (j < my_lo[x] || j >= my_hi[x]) {
+          const int at = 16 * (e / 4) + e % 4;
+          if (at < my_lo[x] - j0 - 4 * g || at >= my_hi[x] - j0 - 4 * g) {
             hidden |= 1u << e;
             p[e] = -INFINITY;
           }
@@ -607,7 +607,7 @@ Plan make_plan(const AttendProblem& p) {
   Plan r{};
   const int64_t group = p.q.heads / p.pool.heads, rows = p.max_new * group;
   r.tile = rows > 32;
-  r.tile_rows = r.tile ? kTileRows : rows > 16 ? 32 : 16;
+  r.tile_rows = r.tile ? kTileRows : rows > 16 && p.pool.dim <= 128 ? 32 : 16;
   r.tiles = std::max<int64_t>(1, (rows + r.tile_rows - 1) / r.tile_rows);
   // Keys that a tile can see, from a multiple of 16 on.
   int64_t span = p.max_len;
@@ -626,7 +626,7 @@ Plan make_plan(const AttendProblem& p) {
   splits = std::max<int64_t>(splits, 1);
   // Eight waves to a workgroup where each has steps enough; four for short
   // sequences (those 4 of up to 1000 tokens: 16.1 us, 17.8 with eight).
-  r.waves = span / splits > 2048 && r.tile_rows == 16 ? 8 : 4;
+  r.waves = span / splits > 2048 && r.tile_rows == 16 && p.pool.dim <= 128 ? 8 : 4;
   r.chunk = ((span + splits - 1) / splits + 127) / 128 * 128;
   r.chunk = std::min<int64_t>(std::max<int64_t>(r.chunk, 128), kMaxChunk);
   r.splits = std::max<int64_t>(1, (span + r.chunk - 1) / r.chunk);
@@ -640,9 +640,14 @@ void stream_dim(const AttendArgs& a, unsigned grid, hipStream_t s) {
 }
 template <int KT, int NQ>
 void stream_type(const AttendArgs& a, int waves, unsigned grid, hipStream_t s) {
-  if (a.pool.dim <= 64) waves == 8 ? stream_dim<KT, 64, NQ, 8>(a, grid, s) : stream_dim<KT, 64, NQ, 4>(a, grid, s);
-  else if (a.pool.dim <= 128) waves == 8 ? stream_dim<KT, 128, NQ, 8>(a, grid, s) : stream_dim<KT, 128, NQ, 4>(a, grid, s);
-  else waves == 8 ? stream_dim<KT, 256, NQ, 8>(a, grid, s) : stream_dim<KT, 256, NQ, 4>(a, grid, s);
+  if constexpr (NQ == 2) {  // four waves, heads of up to 128 (see make_plan)
+    if (a.pool.dim <= 64) stream_dim<KT, 64, 2, 4>(a, grid, s);
+    else stream_dim<KT, 128, 2, 4>(a, grid, s);
+  } else {
+    if (a.pool.dim > 128) stream_dim<KT, 256, 1, 4>(a, grid, s);
+    else if (a.pool.dim > 64) waves == 8 ? stream_dim<KT, 128, 1, 8>(a, grid, s) : stream_dim<KT, 128, 1, 4>(a, grid, s);
+    else waves == 8 ? stream_dim<KT, 64, 1, 8>(a, grid, s) : stream_dim<KT, 64, 1, 4>(a, grid, s);
+  }
 }
 template <int NQ>
 void stream_rows(const AttendArgs& a, int waves, unsigned grid, hipStream_t s) {

@@ -32,6 +32,12 @@ struct AttendArgs {
   int* status;
 };
 
+// Quotient of values that are the same on every lane, in a scalar register
+// (the division itself runs on vector units).
+__device__ __forceinline__ int uniform_div(int a, int b) {
+  return __builtin_amdgcn_readfirstlane((int)((uint32_t)a / (uint32_t)b));
+}
+
 // A sequence's tokens and length, held inside what the caller's sizes allow.
 struct Seq {
   int64_t first;  // row of its first new token
@@ -39,8 +45,9 @@ struct Seq {
   bool bad;
 };
 __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int b) {
-  int64_t s0 = a.starts[b], s1 = a.starts[b + 1];
-  int64_t len = a.lengths[b];
+  // (Uniform: kept in scalar registers.)
+  int64_t s0 = __builtin_amdgcn_readfirstlane(a.starts[b]), s1 = __builtin_amdgcn_readfirstlane(a.starts[b + 1]);
+  int64_t len = __builtin_amdgcn_readfirstlane(a.lengths[b]);
   Seq q;
   q.bad = false;
   if (s0 < 0 || s0 > a.tokens) { s0 = s0 < 0 ? 0 : a.tokens; q.bad = true; }
@@ -92,6 +99,16 @@ __device__ __forceinline__ float sum_groups(float x) {
 enum Operand { kOpBF16, kOpINT8, kOpLevel, kOpLevel2 };
 template <int KT>
 constexpr int kBitsOf = KT == kOpBF16 ? 16 : KT == kOpINT8 ? 8 : 4;
+
+// SIZE times byte q of x (one instruction once compiled).  Not the inline
+// assembly of the linear layers' lookups: its writes are no vector instructions
+// to the compiler's hazard checks, and here its target may be a register that a
+// matrix instruction still reads as its addend (wrong sums now and then with
+// 256-wide heads).
+template <int SIZE>
+__device__ __forceinline__ uint32_t lut_offset(uint32_t x, int q) {
+  return ((x >> (8 * q)) & 255u) * SIZE;
+}
 
 // 8 consecutive int8 codes -> 8 bf16 (exact).
 __device__ __forceinline__ bf16x8 int8_to_bf16x8(uint32_t a, uint32_t b) {

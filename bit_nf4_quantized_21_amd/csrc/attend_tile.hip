@@ -22,6 +22,8 @@ namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(1))) void gptr_t;
+typedef __attribute__((address_space(3))) void lptr_t;
 
 constexpr int kTileKeys = 64;
 
@@ -40,12 +42,16 @@ template <int OP, int DP, bool EXACT>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(AttendArgs a) {
   constexpr bool CODES = OP == kOpINT8 || OP == kOpLevel;  // exact operands, scales on scores and weights
   constexpr int BITS = kBitsOf<OP>;
+  constexpr bool ASYNC = OP == kOpBF16 && EXACT;         // rows go from memory to LDS as they are
   constexpr int NT = DP / 16, NB = DP / 32;
   constexpr int EL = BITS == 16 ? 8 : 16;                // elements per staged piece
   constexpr int PW = EL * BITS / 32;                     // its dwords
   constexpr int PR = DP / EL;                            // pieces of a row
   constexpr int NP = kTileKeys * PR / 256;               // pieces per thread
-  __shared__ __align__(16) uint16_t s_k[2][kTileKeys * DP], s_v[2][kTileKeys * DP];
+  // Each half of the two tiles is an object of its own: the compiler waits for
+  // a copy into LDS before any read that might see it.
+  __shared__ __align__(16) uint16_t s_k0[kTileKeys * DP], s_v0[kTileKeys * DP];
+  __shared__ __align__(16) uint16_t s_k1[kTileKeys * DP], s_v1[kTileKeys * DP];
   __shared__ __align__(16) float s_sc[CODES ? 2 : 1][2][kTileKeys];
   __shared__ __align__(16) uint8_t s_wild[2][kTileKeys];
   __shared__ int s_page[kMaxChunk / 16 + 1];
@@ -54,22 +60,24 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h2 = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int H = a.pool.heads, G = a.group;
-  // Each XCD walks a contiguous run of (sequence, head): its L2 serves the
-  // run's keys to all tiles.  The last tiles of a head see the most keys and
-  // go first.
-  const uint32_t total = (uint32_t)a.batch * H * a.tiles * a.splits, per = (total + 7) / 8;
-  uint32_t id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (id >= total || (blockIdx.x >> 3) >= per) return;
-  const int split = (int)(id % (uint32_t)a.splits);
-  id /= (uint32_t)a.splits;
-  const int tile = a.tiles - 1 - (int)(id % (uint32_t)a.tiles);
-  id /= (uint32_t)a.tiles;
-  const int h = (int)(id % (uint32_t)H), b = (int)(id / (uint32_t)H);
+  // The last row tiles see the most keys and go first, over all heads: what is
+  // left at the end is short.  Heads are fastest, so that where their number is
+  // a multiple of eight each stays on one XCD, whose L2 serves its keys to all
+  // of its tiles.  (Head by head, 52 heads of 4096 causal rows took 20 %
+  // longer: 1.2 waves per SIMD on average, the last head's long tiles alone.)
+  int id = (int)blockIdx.x, next = uniform_div(id, H);
+  const int h = id - next * H;
+  id = next;
+  next = uniform_div(id, a.batch);
+  const int b = id - next * a.batch;
+  id = next;
+  next = uniform_div(id, a.splits);
+  const int split = id - next * a.splits, tile = a.tiles - 1 - next;
   const Seq sq = load_seq(a, b);
   if (sq.bad && tid == 0) atomicOr(a.status, kStatusIndex);
   const int rows = sq.n * G, row0 = tile * kTileRows;
   if (row0 >= rows) return;
-  const int i_first = row0 / G, i_last = (min(rows, row0 + kTileRows) - 1) / G;
+  const int i_first = uniform_div(row0, G), i_last = uniform_div(min(rows, row0 + kTileRows) - 1, G);
   const int hi = seen_hi(a, sq, i_last), lo = seen_lo(a, sq, i_first);
   const int k0 = (lo & ~15) + split * a.chunk;
   if (split > 0 && k0 >= hi) return;
@@ -104,10 +112,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
   const bool wave_rows = wrow < rows, ok = row < rows;
   const int qi = ok ? row / G : 0, qg = ok ? row - qi * G : 0;
   const int my_lo = seen_lo(a, sq, qi), my_hi = ok ? seen_hi(a, sq, qi) : 0;
-  // Keys that some row of the wave sees, and those that all of them see.
-  const int wi_first = min(wrow, rows - 1) / G, wi_last = (min(rows, wrow + 32) - 1) / G;
+  // Keys that some row of the wave sees.
+  const int wi_first = uniform_div(min(wrow, rows - 1), G), wi_last = uniform_div(min(rows, wrow + 32) - 1, G);
   const int w_lo = seen_lo(a, sq, wi_first), w_hi = wave_rows ? seen_hi(a, sq, wi_last) : 0;
-  const int wf_lo = seen_lo(a, sq, wi_last), wf_hi = seen_hi(a, sq, wi_first);
   bf16x8 q[NT];
   {
     const uint16_t* p = a.q.data + (sq.first + qi) * a.q.token_stride + (int64_t)(h * G + qg) * a.q.head_stride;
@@ -128,28 +135,44 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
   float m = -INFINITY, l = 0.0f;
   __syncthreads();
 
-  const int64_t row_bytes = kv_row_bytes(a.pool.type, D);
-  uint32_t kr[NP][PW], vr[NP][PW];
+  // Piece n of a thread is chunk lane % PR of key lane / PR of a run of 64 / PR
+  // keys, which lies in one page: its address is the wave's plus the lane's.
+  const uint32_t row_bytes = (uint32_t)kv_row_bytes(a.pool.type, D);
+  const int pc = lane % PR, wave_key = wave * (64 / PR), lane_key = lane / PR;
+  const uint32_t lane_off = lane_key * row_bytes + pc * (PW * 4);
+  uint32_t kr[ASYNC ? 1 : NP][PW], vr[ASYNC ? 1 : NP][PW];
   float scale_k = 0.0f, scale_v = 0.0f;
   float piece_ks[OP == kOpLevel2 ? NP : 1], piece_vs[OP == kOpLevel2 ? NP : 1];
-  auto base_of = [&](int j) -> int64_t {
-    const int page = s_page[min((j >> shift) - first_page, last)];
-    return (((int64_t)page * H + h) << shift) + (j & ((1 << shift) - 1));
+  // Pages of the pieces of the tile to load next, read one tile ahead.
+  int pages[NP];
+  auto read_pages = [&](int j0) {
+#pragma unroll
+    for (int n = 0; n < NP; ++n)
+      pages[n] = s_page[min(((j0 + wave_key + (256 / PR) * n) >> shift) - first_page, last)];
   };
-  auto load = [&](int j0) {
+  auto load = [&](uint16_t* to_k, uint16_t* to_v, int j0) {
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
-      const int id = tid + 256 * n, key = id / PR, pc = id % PR;
-      const int64_t base = base_of(j0 + key);
-      const uint8_t* kp = a.pool.k + base * row_bytes + pc * (PW * 4);
-      const uint8_t* vp = a.pool.v + base * row_bytes + pc * (PW * 4);
-      if (EXACT || pc * EL < D) {
+      const int j = j0 + wave_key + (256 / PR) * n;
+      const int64_t base =
+          (((int64_t)__builtin_amdgcn_readfirstlane(pages[n]) * H + h) << shift) + (j & ((1 << shift) - 1));
+      const uint8_t* kp = a.pool.k + base * row_bytes;
+      const uint8_t* vp = a.pool.v + base * row_bytes;
+      if constexpr (ASYNC) asm("" : "+s"(kp), "+s"(vp));  // kept in scalar registers: the lanes add 32 bits
+      if constexpr (ASYNC) {
+        // Straight to LDS, lane by lane: the swizzle picks the lane's source.
+        const int key = wave_key + lane_key + (256 / PR) * n;
+        const uint32_t ko = lane_key * row_bytes + k_chunk<DP>(key, pc) * 16;
+        const uint32_t vo = lane_key * row_bytes + v_chunk<DP>(key, pc) * 16;
+        __builtin_amdgcn_global_load_lds((const gptr_t*)(kp + ko), (lptr_t*)(to_k + (wave_key + (256 / PR) * n) * DP), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((const gptr_t*)(vp + vo), (lptr_t*)(to_v + (wave_key + (256 / PR) * n) * DP), 16, 0, 0);
+      } else if (EXACT || pc * EL < D) {
         if constexpr (PW == 4) {
-          const u32x4 x = *reinterpret_cast<const u32x4*>(kp), y = *reinterpret_cast<const u32x4*>(vp);
+          const u32x4 x = *reinterpret_cast<const u32x4*>(kp + lane_off), y = *reinterpret_cast<const u32x4*>(vp + lane_off);
 #pragma unroll
           for (int w = 0; w < 4; ++w) { kr[n][w] = x[w]; vr[n][w] = y[w]; }
         } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(kp), y = *reinterpret_cast<const uint2*>(vp);
+          const uint2 x = *reinterpret_cast<const uint2*>(kp + lane_off), y = *reinterpret_cast<const uint2*>(vp + lane_off);
           kr[n][0] = x.x; kr[n][1] = x.y; vr[n][0] = y.x; vr[n][1] = y.y;
         }
       } else {
@@ -157,15 +180,17 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
         for (int w = 0; w < PW; ++w) kr[n][w] = vr[n][w] = 0;
       }
       if constexpr (OP == kOpLevel2) {
-        piece_ks[n] = a.pool.ks[base];
-        piece_vs[n] = a.pool.vs[base];
+        piece_ks[n] = a.pool.ks[base + lane_key];
+        piece_vs[n] = a.pool.vs[base + lane_key];
       }
     }
     if constexpr (CODES) {
-      const int64_t base = base_of(j0 + (tid & 63));
-      if (tid < 64) scale_k = a.pool.ks[base];
-      else if (tid < 128) scale_v = a.pool.vs[base];
+      const int j = j0 + lane, page = s_page[min((j >> shift) - first_page, last)];
+      const int64_t base = (((int64_t)page * H + h) << shift) + (j & ((1 << shift) - 1));
+      if (wave == 0) scale_k = a.pool.ks[base];
+      else if (wave == 1) scale_v = a.pool.vs[base];
     }
+    read_pages(j0 + kTileKeys);
   };
   // A staged piece as bf16 pairs.
   auto widen = [&](const uint32_t (&w)[PW], float sc, uint32_t (&out)[EL / 2]) {
@@ -182,7 +207,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
       const char* lut = reinterpret_cast<const char*>(s_lut);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const char* p = lut + byte_x8(w[e / 4], e % 4);
+        const char* p = lut + lut_offset<8>(w[e / 4], e % 4);
         if constexpr (OP == kOpLevel) {
           out[e] = *reinterpret_cast<const uint32_t*>(p);
         } else {
@@ -194,59 +219,110 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
       }
     }
   };
-  auto store = [&](int buf, int j0) {
-    const bool edge = j0 < full_lo || j0 + kTileKeys > full_hi;
+  // A value that no row sees becomes 0; one that is not finite becomes 0 too
+  // (it must not reach rows that do not see its key through 0 * inf) and its
+  // key is marked: the rows that see it get a NaN weight.  w: a piece of key
+  // `key`, which PR lanes in a row hold.
+  auto tame = [&](uint32_t* w, int words, int buf, int key, int j0) {
+    const bool any = j0 + key >= lo && j0 + key < hi;
+    bool bad = false;
+    for (int e = 0; e < words; ++e) {
+      uint32_t x = any ? w[e] : 0u;
+      if ((x & 0x7F80u) == 0x7F80u) { x &= 0xFFFF0000u; bad = true; }
+      if ((x & 0x7F800000u) == 0x7F800000u) { x &= 0xFFFFu; bad = true; }
+      w[e] = x;
+    }
+    const uint64_t all = __ballot(bad) >> ((lane / PR) * PR);
+    if (pc == 0) s_wild[buf][key] = (all & (((uint64_t)1 << PR) - 1)) != 0;
+  };
+  auto on_edge = [&](int j0) { return j0 < full_lo || j0 + kTileKeys > full_hi; };
+  // What is left to do for a tile once its rows are here, before the barrier.
+  auto store = [&](uint16_t* to_k, uint16_t* to_v, int buf, int j0) {
+    if constexpr (!ASYNC) {
+      const bool edge = on_edge(j0);
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      const int id = tid + 256 * n, key = id / PR, pc = id % PR;
-      uint32_t x[EL / 2], y[EL / 2];
-      widen(kr[n], OP == kOpLevel2 ? piece_ks[OP == kOpLevel2 ? n : 0] : 1.0f, x);
-      widen(vr[n], OP == kOpLevel2 ? piece_vs[OP == kOpLevel2 ? n : 0] : 1.0f, y);
-      if (!CODES && edge) {
-        // A value that no row sees is 0; one that is not finite becomes 0 (it
-        // must not reach rows that do not see its key through 0 * inf) and its
-        // key is marked: the rows that see it get a NaN weight.
-        const bool any = j0 + key >= lo && j0 + key < hi;
-        bool bad = false;
+      for (int n = 0; n < NP; ++n) {
+        const int key = wave_key + lane_key + (256 / PR) * n;
+        uint32_t x[EL / 2], y[EL / 2];
+        widen(kr[n], OP == kOpLevel2 ? piece_ks[OP == kOpLevel2 ? n : 0] : 1.0f, x);
+        widen(vr[n], OP == kOpLevel2 ? piece_vs[OP == kOpLevel2 ? n : 0] : 1.0f, y);
+        if (!CODES && edge) tame(y, EL / 2, buf, key, j0);
 #pragma unroll
-        for (int e = 0; e < EL / 2; ++e) {
-          uint32_t w = any ? y[e] : 0u;
-          if ((w & 0x7F80u) == 0x7F80u) { w &= 0xFFFF0000u; bad = true; }
-          if ((w & 0x7F800000u) == 0x7F800000u) { w &= 0xFFFFu; bad = true; }
-          y[e] = w;
+        for (int c = 0; c < EL / 8; ++c) {
+          const int ch = pc * (EL / 8) + c;
+          *reinterpret_cast<u32x4*>(to_k + key * DP + k_chunk<DP>(key, ch) * 8) =
+              u32x4{x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]};
+          *reinterpret_cast<u32x4*>(to_v + key * DP + v_chunk<DP>(key, ch) * 8) =
+              u32x4{y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]};
         }
-        // PR lanes in a row hold the key.
-        const uint64_t all = __ballot(bad) >> ((lane / PR) * PR);
-        if (pc == 0) s_wild[buf][key] = (all & ((PR < 64 ? (uint64_t)1 << (PR & 63) : 0) - 1)) != 0;
-      }
-#pragma unroll
-      for (int c = 0; c < EL / 8; ++c) {
-        const int ch = pc * (EL / 8) + c;
-        *reinterpret_cast<u32x4*>(s_k[buf] + key * DP + k_chunk<DP>(key, ch) * 8) =
-            u32x4{x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]};
-        *reinterpret_cast<u32x4*>(s_v[buf] + key * DP + v_chunk<DP>(key, ch) * 8) =
-            u32x4{y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]};
       }
     }
     if constexpr (CODES) {
-      if (tid < 64) s_sc[buf][0][tid] = scale_k * s2;
-      else if (tid < 128) s_sc[buf][1][tid - 64] = scale_v;
+      if (wave == 0) {
+        s_sc[buf][0][lane] = scale_k * s2;
+      } else if (wave == 1) {
+        // The codes are finite; a scale that is not is treated as such a value.
+        const bool bad = (__float_as_uint(scale_v) & 0x7F800000u) == 0x7F800000u, any = j0 + lane >= lo && j0 + lane < hi;
+        s_sc[buf][1][lane] = bad && on_edge(j0) ? 0.0f : scale_v;
+        s_wild[buf][lane] = bad && any;
+      }
+    }
+    __syncthreads();
+    if (ASYNC && on_edge(j0)) {
+#pragma unroll
+      for (int n = 0; n < NP; ++n) {
+        const int key = wave_key + lane_key + (256 / PR) * n;
+        u32x4* at = reinterpret_cast<u32x4*>(to_v + key * DP + pc * 8);
+        uint32_t w[4] = {(*at)[0], (*at)[1], (*at)[2], (*at)[3]};
+        tame(w, 4, buf, key, j0);
+        *at = u32x4{w[0], w[1], w[2], w[3]};
+      }
+      __syncthreads();
     }
   };
 
-  auto compute = [&](int buf, int j0) {
+  // Where the lane's operands lie in a tile: chunk 2 t + h2 of key r (32 keys
+  // further, the same), and of the four keys the lane names to a transposing
+  // read, dims 32 t + its part.  The swizzles only exchange the chunks of
+  // different t, so one address per t serves every key block.
+  int k_at[NT], v_at[NB];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) k_at[t] = r * DP + k_chunk<DP>(r, 2 * t + h2) * 8;
+#pragma unroll
+  for (int t = 0; t < NB; ++t) {
+    const int key = 4 * h2 + ((lane & 15) >> 2), col = 32 * t + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    v_at[t] = key * DP + v_chunk<DP>(key, col / 8) * 8 + (col & 7);
+  }
+
+  auto compute = [&](const uint16_t* tk, const uint16_t* tv, int buf, int j0) {
+    // Keys come from LDS two MFMA pairs ahead of their use.
     f32x16 s[2];
+    u32x4 kf[3][2];
+    auto read_k = [&](int t) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < 2; ++c) kf[t % 3][c] = *reinterpret_cast<const u32x4*>(tk + k_at[t] + 32 * c * DP);
+    };
+    read_k(0);
+    if (NT > 1) read_k(1);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[c][i] = 0.0f;
-      const int key = 32 * c + r;
+    for (int t = 0; t < NT; ++t) {
+      if (t + 2 < NT) read_k(t + 2);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(s_k[buf] + key * DP + k_chunk<DP>(key, 2 * t + h2) * 8);
-        s[c] = mfma32(as_bf16x8(w), q[t], s[c]);
-      }
+      for (int c = 0; c < 2; ++c) s[c] = mfma32(as_bf16x8(kf[t % 3][c]), q[t], t ? s[c] : f32x16{});
     }
+    // The first values are on their way while the scores become weights.
+    s16x4 vf[2][2][2];  // two dim blocks at a time
+    auto read_v = [&](int i) {
+      const int n = i / (NB / 2), t0 = i % (NB / 2) * 2;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          vf[i % 2][t][e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tv + v_at[t0 + t] + (16 * n + 8 * e) * DP));
+    };
+    read_v(0);
+    __builtin_amdgcn_sched_barrier(0);
     if constexpr (CODES) {
 #pragma unroll
       for (int c = 0; c < 2; ++c)
@@ -257,15 +333,30 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
         }
     }
     const float k2 = CODES ? 1.0f : s2;
-    const bool edge = j0 < wf_lo || j0 + kTileKeys > wf_hi;
+    const bool edge = on_edge(j0);
+    // Bounds of the keys that the lane's row sees, against the register's own
+    // place 32 c + 8 (i / 4) + i % 4.
+    const int from = my_lo - j0 - 4 * h2, to = my_hi - j0 - 4 * h2;
     if (edge) {
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int j = j0 + 32 * c + 8 * (i / 4) + 4 * h2 + i % 4;
-          if (j < my_lo || j >= my_hi) s[c][i] = -INFINITY;
+          const int at = 32 * c + 8 * (i / 4) + i % 4;
+          if (at < from || at >= to) s[c][i] = -INFINITY;
         }
+      uint32_t wild[8], some = 0;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) some |= wild[n] = *reinterpret_cast<const uint32_t*>(&s_wild[buf][8 * n + 4 * h2]);
+      if (__any(some != 0)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+              const int at = 32 * c + 8 * (i / 4) + i % 4;
+              if ((wild[4 * c + i / 4] >> (8 * (i % 4)) & 255u) && at >= from && at < to) s[c][i] = __uint_as_float(0x7FC00000u);
+            }
+      }
     }
     float top = s[0][0];
 #pragma unroll
@@ -302,23 +393,6 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
           const float4 f = *reinterpret_cast<const float4*>(&s_sc[buf][1][32 * c + 8 * i + 4 * h2]);
           s[c][4 * i] *= f.x; s[c][4 * i + 1] *= f.y; s[c][4 * i + 2] *= f.z; s[c][4 * i + 3] *= f.w;
         }
-      if (edge) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int j = j0 + 32 * c + 8 * (i / 4) + 4 * h2 + i % 4;
-            if (j < my_lo || j >= my_hi) s[c][i] = 0.0f;  // also where the scale is no number
-          }
-      }
-    } else if (j0 < full_lo || j0 + kTileKeys > full_hi) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = 32 * c + 8 * (i / 4) + 4 * h2 + i % 4, j = j0 + key;
-          if (s_wild[buf][key] && j >= my_lo && j < my_hi) s[c][i] = __uint_as_float(0x7FC00000u);
-        }
     }
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
@@ -329,32 +403,31 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
       const bf16x8 pb = to_bf16x8(p);
 #pragma unroll
       for (int t = 0; t < NB; ++t) {
-        const int col = 32 * t + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-        s16x4 v[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int key = 16 * n + 8 * e + 4 * h2 + ((lane & 15) >> 2);
-          v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s16x4*)(s_v[buf] + key * DP + v_chunk<DP>(key, col / 8) * 8 + (col & 7)));
+        const int i = (n * NB + t) / 2;
+        if (t % 2 == 0) {
+          if (i + 1 < 2 * NB) read_v(i + 1);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        const u32x4 w = {__builtin_bit_cast(uint2, v[0]).x, __builtin_bit_cast(uint2, v[0]).y,
-                         __builtin_bit_cast(uint2, v[1]).x, __builtin_bit_cast(uint2, v[1]).y};
-        o[t] = mfma32(as_bf16x8(w), pb, o[t]);
+        const uint2 x = __builtin_bit_cast(uint2, vf[i % 2][t % 2][0]), y = __builtin_bit_cast(uint2, vf[i % 2][t % 2][1]);
+        o[t] = mfma32(as_bf16x8(x.x, x.y, y.x, y.y), pb, o[t]);
       }
     }
   };
 
   if (k0 < k1) {
-    load(k0);
-    store(0, k0);
-    __syncthreads();
-    int buf = 0;
-    for (int j0 = k0; j0 < k1; j0 += kTileKeys, buf ^= 1) {
+    read_pages(k0);
+    load(s_k0, s_v0, k0);
+    store(s_k0, s_v0, 0, k0);
+    auto step = [&](uint16_t* k, uint16_t* v, uint16_t* next_k, uint16_t* next_v, int buf, int j0) {
       const bool more = j0 + kTileKeys < k1;
-      if (more) load(j0 + kTileKeys);
-      if (j0 < w_hi && j0 + kTileKeys > w_lo) compute(buf, j0);
-      if (more) store(buf ^ 1, j0 + kTileKeys);
-      __syncthreads();
+      if (more) load(next_k, next_v, j0 + kTileKeys);
+      if (j0 < w_hi && j0 + kTileKeys > w_lo) compute(k, v, buf, j0);
+      if (more) store(next_k, next_v, buf ^ 1, j0 + kTileKeys);
+      return more;
+    };
+    for (int j0 = k0;; j0 += 2 * kTileKeys) {
+      if (!step(s_k0, s_v0, s_k1, s_v1, 0, j0)) break;
+      if (!step(s_k1, s_v1, s_k0, s_v0, 1, j0 + kTileKeys)) break;
     }
   }
 
@@ -412,7 +485,7 @@ void tile_op(const AttendArgs& a, dim3 grid, hipStream_t s) {
 
 void launch_attend_tile(const AttendArgs& a, hipStream_t s) {
   const int64_t total = (int64_t)a.batch * a.pool.heads * a.tiles * a.splits;
-  const dim3 grid((unsigned)((total + 7) / 8 * 8));
+  const dim3 grid((unsigned)total);
   if (a.pool.type == kKVBF16) tile_op<kOpBF16>(a, grid, s);
   else if (a.pool.type == kKVINT8) tile_op<kOpINT8>(a, grid, s);
   else if (a.pool.type == kKVNF4) tile_op<kOpLevel2>(a, grid, s);

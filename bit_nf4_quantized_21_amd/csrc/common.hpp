@@ -215,29 +215,6 @@ __device__ __forceinline__ uint32_t byte_x8(uint32_t x, int q) {
   }
 }
 
-// 4 * byte q of x, likewise.
-template <int Q>
-__device__ __forceinline__ uint32_t byte_x4(uint32_t x) {
-  uint32_t r;
-  if constexpr (Q == 0)
-    asm("v_lshlrev_b32_sdwa %0, 2, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_0" : "=v"(r) : "v"(x));
-  else if constexpr (Q == 1)
-    asm("v_lshlrev_b32_sdwa %0, 2, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_1" : "=v"(r) : "v"(x));
-  else if constexpr (Q == 2)
-    asm("v_lshlrev_b32_sdwa %0, 2, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_2" : "=v"(r) : "v"(x));
-  else
-    asm("v_lshlrev_b32_sdwa %0, 2, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_3" : "=v"(r) : "v"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t byte_x4(uint32_t x, int q) {
-  switch (q) {
-    case 0: return byte_x4<0>(x);
-    case 1: return byte_x4<1>(x);
-    case 2: return byte_x4<2>(x);
-    default: return byte_x4<3>(x);
-  }
-}
-
 // Pair table of the codebook at LDS address 0: entry b (b = one code byte,
 // element 2q in its low nibble) holds (c[b & 15], c[b >> 4]), so one 8-byte
 // LDS read returns the codebook values of two consecutive elements and its

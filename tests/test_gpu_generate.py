@@ -428,6 +428,18 @@ def test_a_later_tokens_bad_row_reaches_only_those_that_see_it(n, kv, bad):
     b.check(out, lse, skip=(0,))
 
 
+@pytest.mark.parametrize("kv", at.KV_TYPES)
+@pytest.mark.parametrize("D", [64, 80, 128, 256])
+def test_the_same_bits_every_time(D, kv):
+    for seqs in (SMALL, MIXED, LARGE):
+        b = Batch(seqs, 2, 1, D, kv, 16, seed=17)
+        q = _dev(b.q)
+        first = [t.clone() for t in b.run(q=q)]
+        for _ in range(10):
+            for x, y in zip(b.run(q=q), first):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
 def test_strided_queries_and_given_outputs():
     lib = _lib()
     for seqs in (SMALL, LARGE):
