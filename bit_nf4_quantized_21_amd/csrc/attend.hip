@@ -522,19 +522,20 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
   }
 }
 
-// Joins the splits of a row: one workgroup per (token, query head).  The
-// splits' references and sums first, then their outputs, 256 / (DP / 4) splits
-// at a time, in a fixed order.
-template <int DP>
+// Joins the splits of the rows.  P groups of DP / 4 lanes work on a row, each
+// on every P-th split, 256 / (P DP / 4) rows to a workgroup; the groups meet in
+// LDS.  Few splits of many rows take P = 1 (51 000 rows in 2: 16 us, 97 with a
+// workgroup to each), many splits of few rows the whole workgroup.
+template <int DP, bool WIDE>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int tile_rows) {
-  constexpr int L = DP / 4, P = 256 / L;  // lanes of a row, splits at a time
-  __shared__ __align__(16) float4 s_acc[P][L];
-  __shared__ float s_red[2][4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.y;
+  constexpr int L = DP / 4, P = WIDE ? 256 / L : 1, R = 256 / (L * P);
+  __shared__ __align__(16) float4 s_acc[WIDE ? P : 1][L];
+  __shared__ float s_sum[WIDE ? P : 1];
+  const int c = threadIdx.x % L, part = WIDE ? threadIdx.x / L : 0, b = blockIdx.y;
   const int H = a.pool.heads, G = a.group, Hq = H * G, D = a.pool.dim;
   const Seq sq = load_seq(a, b);
-  const int e = blockIdx.x;
-  if (e >= (int64_t)sq.n * Hq) return;
+  const int e = blockIdx.x * R + (WIDE ? 0 : threadIdx.x / L);
+  if (e >= (int64_t)sq.n * Hq) return;  // the whole workgroup where it meets
   const int i = e / Hq, hq = e - i * Hq, rows = sq.n * G;
   const int row0 = (i * G + hq % G) / tile_rows * tile_rows;
   const int hi = seen_hi(a, sq, (min(rows, row0 + tile_rows) - 1) / G), lo = seen_lo(a, sq, row0 / G) & ~15;
@@ -542,45 +543,46 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int tile
   const int64_t at = (sq.first + i) * Hq + hq, step = a.tokens * Hq;
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + at;
   float top = -INFINITY;
-  for (int s = tid; s < n; s += 256) top = fmaxf(top, ml[s * step].x);
-#pragma unroll
-  for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-  if (lane == 0) s_red[0][wave] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3]));
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) top = fmaxf(top, ml[s * step].x);
   const float ref = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f;
-  for (int s = tid; s < n; s += 256) {
-    const float2 v = ml[s * step];
-    sum += v.y * __builtin_amdgcn_exp2f(v.x - ref);
-  }
-#pragma unroll
-  for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
-  if (lane == 0) s_red[1][wave] = sum;
-  const int c = tid % L, part = tid / L;
   float4 acc = make_float4(0, 0, 0, 0);
   if (4 * c < D) {
 #pragma unroll 4
     for (int s = part; s < n; s += P) {
-      const float f = __builtin_amdgcn_exp2f(ml[s * step].x - ref);
+      const float2 w = ml[s * step];
       const float4 v = *reinterpret_cast<const float4*>(a.part_o + (s * step + at) * D + 4 * c);
+      const float f = __builtin_amdgcn_exp2f(w.x - ref);
+      sum += w.y * f;
       acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
     }
   }
-  s_acc[part][c] = acc;
-  __syncthreads();
-  sum = (s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]);
-  if (tid < L && 4 * tid < D) {
+  if constexpr (WIDE) {
+    s_acc[part][c] = acc;
+    if (c == 0) s_sum[part] = sum;
+    __syncthreads();
+    if (part) return;
 #pragma unroll
     for (int p = 1; p < P; ++p) {
-      const float4 v = s_acc[p][tid];
+      const float4 v = s_acc[p][c];
       acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+      sum += s_sum[p];
     }
-    const float inv = sum == 0.0f ? 0.0f : a.unit / sum;
-    *reinterpret_cast<uint2*>(a.out + at * D + 4 * tid) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   }
-  if (tid == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+  const float inv = sum == 0.0f ? 0.0f : a.unit / sum;
+  if (4 * c < D)
+    *reinterpret_cast<uint2*>(a.out + at * D + 4 * c) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (c == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+template <int DP>
+void launch_join(const AttendArgs& a, int tile_rows, hipStream_t s) {
+  const int64_t rows = (int64_t)a.max_new * a.q.heads;
+  constexpr int R = 1024 / DP;  // rows of a workgroup when they are many
+  if (a.splits > 16) hipLaunchKernelGGL((attend_join_kernel<DP, true>), dim3((unsigned)rows, (unsigned)a.batch), dim3(256), 0, s, a, tile_rows);
+  else hipLaunchKernelGGL((attend_join_kernel<DP, false>), dim3((unsigned)((rows + R - 1) / R), (unsigned)a.batch), dim3(256), 0, s, a, tile_rows);
 }
 
 uint32_t bf16_round_host(float f) {  // finite f
@@ -607,7 +609,11 @@ Plan make_plan(const AttendProblem& p) {
   Plan r{};
   const int64_t group = p.q.heads / p.pool.heads, rows = p.max_new * group;
   r.tile = rows > 32;
-  r.tile_rows = r.tile ? kTileRows : rows > 16 && p.pool.dim <= 128 ? 32 : 16;
+  // Quantized rows are widened once per tile: 256 rows share that where there
+  // are more than 128 (the chunks below: 203 -> 188 us with int8, 447 -> 179
+  // with NF4); bf16 rows need none of it, and two smaller workgroups of a CU
+  // overlap their matrix and vector phases.
+  r.tile_rows = r.tile ? (rows > 128 && p.pool.type != kKVBF16 && p.pool.dim <= 128 ? 256 : 128) : rows > 16 && p.pool.dim <= 128 ? 32 : 16;
   r.tiles = std::max<int64_t>(1, (rows + r.tile_rows - 1) / r.tile_rows);
   // Keys that a tile can see, from a multiple of 16 on.
   int64_t span = p.max_len;
@@ -620,9 +626,11 @@ Plan make_plan(const AttendProblem& p) {
   // up to 1000 tokens, 32 heads, bf16, 16.0 us in one launch, 13.0 + 4.0 and
   // the gap in two; 64 of up to 8192, 8 heads, int8, 145 us, 134 + 12 in four
   // splits.  8 heads of 131071 NF4 keys: 43 + 4 us in 32 splits of eight waves,
-  // 44 + 5.5 in 64 of four.
-  const int64_t full = r.tile ? 512 : 128, want = r.tile ? 512 : 256;
-  int64_t splits = work >= full ? 1 : std::min((want + work - 1) / work, span / 512);
+  // 44 + 5.5 in 64 of four.  Tiles are long and uneven (a sequence's length, the
+  // causal corner), so they want twice what the chip holds at once: 4 chunks of
+  // 300 to 512 tokens over 512 to 4608, int8, 188 us whole, 162 + 16 in two.
+  const int64_t full = !r.tile ? 128 : r.tile_rows == 256 ? 512 : 1024, want = !r.tile ? 256 : full;
+  int64_t splits = work >= full ? 1 : std::min((want + work - 1) / work, span / (r.tile ? 256 : 512));
   splits = std::max<int64_t>(splits, 1);
   // Eight waves to a workgroup where each has steps enough; four for short
   // sequences (those 4 of up to 1000 tokens: 16.1 us, 17.8 with eight).
@@ -712,7 +720,7 @@ hipError_t launch_attend(const AttendProblem& p, const float table[16], void* ws
   }
   if (r.tile) {
     KernelTimer kt_("attend_tile_kernel", s);
-    launch_attend_tile(a, s);
+    launch_attend_tile(a, r.tile_rows, s);
     e = hipGetLastError();
   } else {
     KernelTimer kt_("attend_stream_kernel", s);
@@ -723,10 +731,9 @@ hipError_t launch_attend(const AttendProblem& p, const float table[16], void* ws
   }
   if (e != hipSuccess || r.splits == 1) return e;
   KernelTimer kt_("attend_join_kernel", s);
-  const dim3 grid((unsigned)((int64_t)p.max_new * p.q.heads), (unsigned)p.batch);
-  if (p.pool.dim <= 64) hipLaunchKernelGGL(attend_join_kernel<64>, grid, dim3(256), 0, s, a, r.tile_rows);
-  else if (p.pool.dim <= 128) hipLaunchKernelGGL(attend_join_kernel<128>, grid, dim3(256), 0, s, a, r.tile_rows);
-  else hipLaunchKernelGGL(attend_join_kernel<256>, grid, dim3(256), 0, s, a, r.tile_rows);
+  if (p.pool.dim <= 64) launch_join<64>(a, r.tile_rows, s);
+  else if (p.pool.dim <= 128) launch_join<128>(a, r.tile_rows, s);
+  else launch_join<256>(a, r.tile_rows, s);
   return hipGetLastError();
 }
 

@@ -124,8 +124,8 @@ __device__ __forceinline__ bf16x8 int8_to_bf16x8(uint32_t a, uint32_t b) {
 // Growth of a row's maximum (in powers of two) that its reference lets pass.
 constexpr float kSlack = 8.0f;
 
-// The tile kernel (attend_tile.hip): rows of a tile and its launch.
-constexpr int kTileRows = 128;
-void launch_attend_tile(const AttendArgs& a, hipStream_t s);
+// The tile kernel (attend_tile.hip): 128 rows to a tile, or 256 (quantized
+// caches, heads of up to 128).
+void launch_attend_tile(const AttendArgs& a, int rows, hipStream_t s);
 
 }  // namespace qlora

@@ -38,8 +38,8 @@ __device__ __forceinline__ int v_chunk(int key, int c) {
   return c ^ (DP == 64 ? ((key >> 1) & 1) << 2 : (key & 3) << 2);
 }
 
-template <int OP, int DP, bool EXACT>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(AttendArgs a) {
+template <int OP, int DP, int WAVES, bool EXACT>
+__global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_kernel(AttendArgs a) {
   constexpr bool CODES = OP == kOpINT8 || OP == kOpLevel;  // exact operands, scales on scores and weights
   constexpr int BITS = kBitsOf<OP>;
   constexpr bool ASYNC = OP == kOpBF16 && EXACT;         // rows go from memory to LDS as they are
@@ -47,7 +47,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
   constexpr int EL = BITS == 16 ? 8 : 16;                // elements per staged piece
   constexpr int PW = EL * BITS / 32;                     // its dwords
   constexpr int PR = DP / EL;                            // pieces of a row
-  constexpr int NP = kTileKeys * PR / 256;               // pieces per thread
+  constexpr int RUN = WAVES * 64 / PR;                   // keys that the waves' pieces cover at once
+  constexpr int NP = kTileKeys > RUN ? kTileKeys / RUN : 1;  // pieces per thread
+  constexpr int ROWS = 32 * WAVES;
   // Each half of the two tiles is an object of its own: the compiler waits for
   // a copy into LDS before any read that might see it.
   __shared__ __align__(16) uint16_t s_k0[kTileKeys * DP], s_v0[kTileKeys * DP];
@@ -75,9 +77,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
   const int split = id - next * a.splits, tile = a.tiles - 1 - next;
   const Seq sq = load_seq(a, b);
   if (sq.bad && tid == 0) atomicOr(a.status, kStatusIndex);
-  const int rows = sq.n * G, row0 = tile * kTileRows;
+  const int rows = sq.n * G, row0 = tile * ROWS;
   if (row0 >= rows) return;
-  const int i_first = uniform_div(row0, G), i_last = uniform_div(min(rows, row0 + kTileRows) - 1, G);
+  const int i_first = uniform_div(row0, G), i_last = uniform_div(min(rows, row0 + ROWS) - 1, G);
   const int hi = seen_hi(a, sq, i_last), lo = seen_lo(a, sq, i_first);
   const int k0 = (lo & ~15) + split * a.chunk;
   if (split > 0 && k0 >= hi) return;
@@ -85,7 +87,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
   const int full_hi = seen_hi(a, sq, i_first), full_lo = seen_lo(a, sq, i_last);
 
   const int shift = a.pool.shift, first_page = k0 >> shift, last = ((k1 - 1) >> shift) - first_page;
-  for (int p = tid; k0 < k1 && p <= last; p += 256) {
+  for (int p = tid; k0 < k1 && p <= last; p += 64 * WAVES) {
     int page = a.pages[(int64_t)b * a.width + first_page + p];
     if (page < 0 || page >= a.pool.pages) {
       atomicOr(a.status, kStatusIndex);
@@ -93,7 +95,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
     }
     s_page[p] = page;
   }
-  if (BITS == 4) {
+  if (BITS == 4 && tid < 256) {
     // A byte's two levels: a pair of bf16 (exact levels), or two fp32 values.
     uint32_t x = 0, y = 0;
 #pragma unroll
@@ -139,6 +141,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
   // keys, which lies in one page: its address is the wave's plus the lane's.
   const uint32_t row_bytes = (uint32_t)kv_row_bytes(a.pool.type, D);
   const int pc = lane % PR, wave_key = wave * (64 / PR), lane_key = lane / PR;
+  const bool stages = RUN <= kTileKeys || wave_key < kTileKeys;  // eight waves may be more than the pieces
   const uint32_t lane_off = lane_key * row_bytes + pc * (PW * 4);
   uint32_t kr[ASYNC ? 1 : NP][PW], vr[ASYNC ? 1 : NP][PW];
   float scale_k = 0.0f, scale_v = 0.0f;
@@ -148,12 +151,13 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
   auto read_pages = [&](int j0) {
 #pragma unroll
     for (int n = 0; n < NP; ++n)
-      pages[n] = s_page[min(((j0 + wave_key + (256 / PR) * n) >> shift) - first_page, last)];
+      pages[n] = s_page[min(((j0 + wave_key + RUN * n) >> shift) - first_page, last)];
   };
   auto load = [&](uint16_t* to_k, uint16_t* to_v, int j0) {
+    if (stages)
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
-      const int j = j0 + wave_key + (256 / PR) * n;
+      const int j = j0 + wave_key + RUN * n;
       const int64_t base =
           (((int64_t)__builtin_amdgcn_readfirstlane(pages[n]) * H + h) << shift) + (j & ((1 << shift) - 1));
       const uint8_t* kp = a.pool.k + base * row_bytes;
@@ -161,11 +165,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
       if constexpr (ASYNC) asm("" : "+s"(kp), "+s"(vp));  // kept in scalar registers: the lanes add 32 bits
       if constexpr (ASYNC) {
         // Straight to LDS, lane by lane: the swizzle picks the lane's source.
-        const int key = wave_key + lane_key + (256 / PR) * n;
+        const int key = wave_key + lane_key + RUN * n;
         const uint32_t ko = lane_key * row_bytes + k_chunk<DP>(key, pc) * 16;
         const uint32_t vo = lane_key * row_bytes + v_chunk<DP>(key, pc) * 16;
-        __builtin_amdgcn_global_load_lds((const gptr_t*)(kp + ko), (lptr_t*)(to_k + (wave_key + (256 / PR) * n) * DP), 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((const gptr_t*)(vp + vo), (lptr_t*)(to_v + (wave_key + (256 / PR) * n) * DP), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((const gptr_t*)(kp + ko), (lptr_t*)(to_k + (wave_key + RUN * n) * DP), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((const gptr_t*)(vp + vo), (lptr_t*)(to_v + (wave_key + RUN * n) * DP), 16, 0, 0);
       } else if (EXACT || pc * EL < D) {
         if constexpr (PW == 4) {
           const u32x4 x = *reinterpret_cast<const u32x4*>(kp + lane_off), y = *reinterpret_cast<const u32x4*>(vp + lane_off);
@@ -223,14 +227,15 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
   // (it must not reach rows that do not see its key through 0 * inf) and its
   // key is marked: the rows that see it get a NaN weight.  w: a piece of key
   // `key`, which PR lanes in a row hold.
-  auto tame = [&](uint32_t* w, int words, int buf, int key, int j0) {
+  auto tame = [&](auto& w, int buf, int key, int j0) {
     const bool any = j0 + key >= lo && j0 + key < hi;
     bool bad = false;
-    for (int e = 0; e < words; ++e) {
-      uint32_t x = any ? w[e] : 0u;
+#pragma unroll
+    for (uint32_t& v : w) {
+      uint32_t x = any ? v : 0u;
       if ((x & 0x7F80u) == 0x7F80u) { x &= 0xFFFF0000u; bad = true; }
       if ((x & 0x7F800000u) == 0x7F800000u) { x &= 0xFFFFu; bad = true; }
-      w[e] = x;
+      v = x;
     }
     const uint64_t all = __ballot(bad) >> ((lane / PR) * PR);
     if (pc == 0) s_wild[buf][key] = (all & (((uint64_t)1 << PR) - 1)) != 0;
@@ -240,13 +245,14 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
   auto store = [&](uint16_t* to_k, uint16_t* to_v, int buf, int j0) {
     if constexpr (!ASYNC) {
       const bool edge = on_edge(j0);
+      if (stages)
 #pragma unroll
       for (int n = 0; n < NP; ++n) {
-        const int key = wave_key + lane_key + (256 / PR) * n;
+        const int key = wave_key + lane_key + RUN * n;
         uint32_t x[EL / 2], y[EL / 2];
         widen(kr[n], OP == kOpLevel2 ? piece_ks[OP == kOpLevel2 ? n : 0] : 1.0f, x);
         widen(vr[n], OP == kOpLevel2 ? piece_vs[OP == kOpLevel2 ? n : 0] : 1.0f, y);
-        if (!CODES && edge) tame(y, EL / 2, buf, key, j0);
+        if (!CODES && edge) tame(y, buf, key, j0);
 #pragma unroll
         for (int c = 0; c < EL / 8; ++c) {
           const int ch = pc * (EL / 8) + c;
@@ -271,10 +277,10 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
     if (ASYNC && on_edge(j0)) {
 #pragma unroll
       for (int n = 0; n < NP; ++n) {
-        const int key = wave_key + lane_key + (256 / PR) * n;
+        const int key = wave_key + lane_key + RUN * n;
         u32x4* at = reinterpret_cast<u32x4*>(to_v + key * DP + pc * 8);
         uint32_t w[4] = {(*at)[0], (*at)[1], (*at)[2], (*at)[3]};
-        tame(w, 4, buf, key, j0);
+        tame(w, buf, key, j0);
         *at = u32x4{w[0], w[1], w[2], w[3]};
       }
       __syncthreads();
@@ -469,27 +475,34 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_tile_kernel(Att
     }
 }
 
-template <int OP, int DP>
+template <int OP, int DP, int WAVES>
 void tile_dim(const AttendArgs& a, dim3 grid, hipStream_t s) {
-  if (a.pool.dim == DP) hipLaunchKernelGGL((attend_tile_kernel<OP, DP, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((attend_tile_kernel<OP, DP, false>), grid, dim3(256), 0, s, a);
+  if (a.pool.dim == DP) hipLaunchKernelGGL((attend_tile_kernel<OP, DP, WAVES, true>), grid, dim3(64 * WAVES), 0, s, a);
+  else hipLaunchKernelGGL((attend_tile_kernel<OP, DP, WAVES, false>), grid, dim3(64 * WAVES), 0, s, a);
 }
 template <int OP>
-void tile_op(const AttendArgs& a, dim3 grid, hipStream_t s) {
-  if (a.pool.dim <= 64) tile_dim<OP, 64>(a, grid, s);
-  else if (a.pool.dim <= 128) tile_dim<OP, 128>(a, grid, s);
-  else tile_dim<OP, 256>(a, grid, s);
+void tile_op(const AttendArgs& a, int rows, dim3 grid, hipStream_t s) {
+  if constexpr (OP != kOpBF16) {
+    if (rows == 256) {
+      if (a.pool.dim <= 64) tile_dim<OP, 64, 8>(a, grid, s);
+      else tile_dim<OP, 128, 8>(a, grid, s);
+      return;
+    }
+  }
+  if (a.pool.dim <= 64) tile_dim<OP, 64, 4>(a, grid, s);
+  else if (a.pool.dim <= 128) tile_dim<OP, 128, 4>(a, grid, s);
+  else tile_dim<OP, 256, 4>(a, grid, s);
 }
 
 }  // namespace
 
-void launch_attend_tile(const AttendArgs& a, hipStream_t s) {
+void launch_attend_tile(const AttendArgs& a, int rows, hipStream_t s) {
   const int64_t total = (int64_t)a.batch * a.pool.heads * a.tiles * a.splits;
   const dim3 grid((unsigned)total);
-  if (a.pool.type == kKVBF16) tile_op<kOpBF16>(a, grid, s);
-  else if (a.pool.type == kKVINT8) tile_op<kOpINT8>(a, grid, s);
-  else if (a.pool.type == kKVNF4) tile_op<kOpLevel2>(a, grid, s);
-  else tile_op<kOpLevel>(a, grid, s);
+  if (a.pool.type == kKVBF16) tile_op<kOpBF16>(a, rows, grid, s);
+  else if (a.pool.type == kKVINT8) tile_op<kOpINT8>(a, rows, grid, s);
+  else if (a.pool.type == kKVNF4) tile_op<kOpLevel2>(a, rows, grid, s);
+  else tile_op<kOpLevel>(a, rows, grid, s);
 }
 
 }  // namespace qlora

@@ -27,15 +27,22 @@ def _heads(t, name):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, dim]")
+    n, h, d = t.shape
     st, sh, sd = t.stride()
-    if sd != 1 and t.shape[2] > 1:
+    if sd != 1 and d > 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
     # The stride of an axis of one element is never used.
-    return Heads(t.data_ptr(), st if t.shape[0] > 1 else 0, sh if t.shape[1] > 1 else 0, t.shape[1])
+    return Heads(t.data_ptr(), st if n > 1 else 0, sh if h > 1 else 0, h)
+
+
+def _new_heads(like, heads, dim):
+    """A contiguous tensor of the same tokens, and its view."""
+    t = like.new_empty((like.shape[0], heads, dim))
+    return t, Heads(t.data_ptr(), heads * dim, dim, heads)
 
 
 def _index(t, n, dtype, name):
@@ -76,21 +83,28 @@ def rope(q, k, table, positions, layout="half", inverse=False, q_out=None, k_out
     from rot on are copied.  inverse=True is the transpose: the gradient of q
     and k from those of the rotated ones.  q_out, k_out: outputs (q and k
     themselves for in place); allocated when absent.  Returns (q_out, k_out)."""
-    torch = _torch()
-    T, _, D = q.shape
+    T, hq, D = q.shape
     rows, rot = _table(table, positions, T)
-    if k is not None and (k.shape[0] != T or k.shape[2] != D):
-        raise ValueError("q and k must have the same tokens and dim")
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k is not None and k_out is None else k_out
-    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
-        raise ValueError("outputs must have their input's shape")
-    views = [_heads(q, "q"), _heads(q_out, "q_out")]
+    qv = _heads(q, "q")
+    if q_out is None:
+        q_out, qo = _new_heads(q, hq, D)
+    else:
+        qo = _heads(q_out, "q_out")
+    kv = ko = None
     if k is not None:
-        views += [_heads(k, "k"), _heads(k_out, "k_out")]
-    refs = [ctypes.byref(v) for v in views] + [None] * (4 - len(views))
-    _check(lib().qlora_rope(T, D, rot, _choice(ROPE_LAYOUTS, layout, "layout"), 1 if inverse else 0, _p(table), rows,
-                            _p(positions), *refs, _stream(stream)))
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError("q and k must have the same tokens and dim")
+        kv = _heads(k, "k")
+        if k_out is None:
+            k_out, ko = _new_heads(k, k.shape[1], D)
+        else:
+            ko = _heads(k_out, "k_out")
+        if k_out.shape != k.shape:
+            raise ValueError("outputs must have their input's shape")
+    if q_out.shape != q.shape:
+        raise ValueError("outputs must have their input's shape")
+    _check(lib().qlora_rope(T, D, rot, _choice(ROPE_LAYOUTS, layout, "layout"), 1 if inverse else 0, table.data_ptr(),
+                            rows, positions.data_ptr(), qv, qo, kv, ko, _stream(stream)))
     return q_out, k_out
 
 
@@ -146,8 +160,9 @@ def kv_write(cache, k, v, slots, table=None, positions=None, layout="half", stre
     _index(slots, T, torch.int64, "slots")
     rows, rot = (0, 0) if table is None else _table(table, positions, T)
     kh, vh = _heads(k, "k"), _heads(v, "v")
-    _check(lib().qlora_kv_write(ctypes.byref(cache._desc), T, ctypes.byref(kh), ctypes.byref(vh), _p(slots), _p(table),
-                                rows, _p(positions), rot, _choice(ROPE_LAYOUTS, layout, "layout"), _stream(stream)))
+    _check(lib().qlora_kv_write(cache._desc, T, kh, vh, slots.data_ptr(), None if table is None else table.data_ptr(),
+                                rows, None if table is None else positions.data_ptr(), rot,
+                                _choice(ROPE_LAYOUTS, layout, "layout"), _stream(stream)))
 
 
 def kv_read(cache, slots, k_out=None, v_out=None, stream=None):
@@ -156,16 +171,21 @@ def kv_read(cache, slots, k_out=None, v_out=None, stream=None):
     torch = _torch()
     T = slots.numel()
     _dev(slots, torch.int64, "slots")
-    outs = []
-    for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
-        t = torch.empty(T, cache.heads, cache.dim, dtype=torch.bfloat16, device=slots.device) if t is None else t
-        outs.append(_need(_dev(t, torch.bfloat16, nm), T * cache.heads * cache.dim, nm))
-    _check(lib().qlora_kv_read(ctypes.byref(cache._desc), T, _p(slots), _p(outs[0]), _p(outs[1]), _stream(stream)))
-    return outs[0], outs[1]
+    shape = (T, cache.heads, cache.dim)
+    if k_out is None:
+        k_out = cache.k.new_empty(shape, dtype=torch.bfloat16)
+    else:
+        _need(_dev(k_out, torch.bfloat16, "k_out"), T * cache.heads * cache.dim, "k_out")
+    if v_out is None:
+        v_out = cache.k.new_empty(shape, dtype=torch.bfloat16)
+    else:
+        _need(_dev(v_out, torch.bfloat16, "v_out"), T * cache.heads * cache.dim, "v_out")
+    _check(lib().qlora_kv_read(cache._desc, T, slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), _stream(stream)))
+    return k_out, v_out
 
 
 def attend_paged_workspace_bytes(cache, tokens, q_heads, batch, max_new, max_len, causal=True, window=0):
-    return int(lib().qlora_attend_paged_workspace_bytes(ctypes.byref(cache._desc), tokens, q_heads, batch, max_new,
+    return int(lib().qlora_attend_paged_workspace_bytes(cache._desc, tokens, q_heads, batch, max_new,
                                                         max_len, 1 if causal else 0, window))
 
 
@@ -190,19 +210,21 @@ def attend_paged(q, cache, pages, starts, lengths, max_new, max_len, scale=None,
         raise ValueError("pages must be [batch, pages_per_seq]")
     _index(starts, B + 1, torch.int32, "starts")
     _dev(lengths, torch.int32, "lengths")
-    out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device) if out is None else out
-    _need(_dev(out, torch.bfloat16, "out"), T * Hq * D, "out")
+    if out is None:
+        out = q.new_empty((T, Hq, D))
+    else:
+        _need(_dev(out, torch.bfloat16, "out"), T * Hq * D, "out")
     if lse is True:
-        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
-    elif lse is False:
+        lse = q.new_empty((T, Hq), dtype=torch.float32)
+    elif lse is False or lse is None:
         lse = None
-    if lse is not None:
+    else:
         _need(_dev(lse, torch.float32, "lse"), T * Hq, "lse")
     nbytes = attend_paged_workspace_bytes(cache, T, Hq, B, max_new, max_len, causal, window)
     workspace = _workspace(nbytes, q.device, workspace)
-    qh = _heads(q, "q")
-    _check(lib().qlora_attend_paged(ctypes.byref(cache._desc), T, ctypes.byref(qh), B, _p(pages), pages.shape[1],
-                                    _p(starts), _p(lengths), max_new, max_len, D ** -0.5 if scale is None else scale,
-                                    1 if causal else 0, window, _p(out), _p(lse), _p(workspace), nbytes,
-                                    _stream(stream)))
+    _check(lib().qlora_attend_paged(cache._desc, T, _heads(q, "q"), B, pages.data_ptr(), pages.shape[1],
+                                    starts.data_ptr(), lengths.data_ptr(), max_new, max_len,
+                                    D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
+                                    None if lse is None else lse.data_ptr(),
+                                    None if workspace is None else workspace.data_ptr(), nbytes, _stream(stream)))
     return out, lse
