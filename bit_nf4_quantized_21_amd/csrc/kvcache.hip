@@ -13,7 +13,13 @@
 // per block of 64) lets attention apply it to whole scores and weights.
 //
 // Both kernels are bound by memory: 2 bytes per element on the dense side,
-// the row's codes and 4 bytes on the other.
+// the row's codes and 4 bytes on the other.  2048 tokens of 32 heads of 128,
+// rotated and stored in NF4: 15 us (43 MB; 34 with a comparison per boundary
+// and a head per thread), read back 12 us; 4001 tokens of 8 heads, rotated, in
+// int8: 8 us, 9973 read back 16 us (61 MB).
+#include <cmath>
+#include <mutex>
+
 #include "common.hpp"
 #include "device_state.hpp"
 #include "kvcache.hpp"
@@ -26,156 +32,175 @@ namespace {
 
 constexpr float kTinyRow = 1e-30f;
 
-struct Decision4 {
-  float m[15];
-  uint64_t codes;
-  uint32_t zero_code;
+// How a level is decided: uniform bins of [-1, 1], each holding at most one
+// boundary; entry = (the boundary, 2 where there is none; the codes below and
+// above it).  kBins separates the boundaries of all three types by more than
+// an fp32 estimate of the bin can err (checked on the host), so one read and
+// one comparison give #{boundaries : y > m}.
+constexpr int kBins = 127;
+struct Bins {
+  float m[kBins];
+  uint8_t codes[kBins];
 };
 
 struct KVWriteArgs {
   KVPool pool;
   HeadsView k, v;
-  int64_t rows;  // tokens * heads * 2
+  int64_t T;
+  int32_t groups;  // head groups of a token's row set
   const int64_t* slots;
   RopeTable rope;
-  Decision4 d4;
   int* status;
 };
 
-// 8 elements of a head from element e0, widened, rotated when asked.
-template <int ROPE>
-__device__ __forceinline__ void load8(const uint16_t* p, uint32_t e0, const RopeTable& t, int64_t pos, bool rotate,
-                                      float (&v)[8]) {
-  const u32x4 w = *reinterpret_cast<const u32x4*>(p + e0);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    v[2 * q] = bf16_lo(w[q]);
-    v[2 * q + 1] = bf16_hi(w[q]);
-  }
-  if (ROPE == 0 || !rotate || e0 >= (uint32_t)t.rot) return;
-  const uint32_t half = (uint32_t)t.rot / 2;
-  if (ROPE == 1) {
-    const bool first = e0 < half;
-    const u32x4 o = *reinterpret_cast<const u32x4*>(p + (first ? e0 + half : e0 - half));
-    float cs[16];
-    rope_row8(t, pos, first ? e0 : e0 - half, 1.0f, cs);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float other = j & 1 ? bf16_hi(o[j / 2]) : bf16_lo(o[j / 2]);
-      if (first) rope_pair(v[j], other, cs[2 * j], cs[2 * j + 1]);
-      else rope_pair(other, v[j], cs[2 * j], cs[2 * j + 1]);
-    }
-  } else {
-    const float4* row = reinterpret_cast<const float4*>(t.table + pos * t.rot + e0);
-    const float4 r0 = row[0], r1 = row[1];
-    rope_pair(v[0], v[1], r0.x, r0.y);
-    rope_pair(v[2], v[3], r0.z, r0.w);
-    rope_pair(v[4], v[5], r1.x, r1.y);
-    rope_pair(v[6], v[7], r1.z, r1.w);
-  }
+// Largest of the LPR lanes of a row (LPR = 4, 8, 16), by lane exchanges inside
+// the vector unit.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
+  const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, false);
+  return y > x ? y : x;
+}
+template <int LPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+  x = dpp_max<0xB1>(x);                           // quad_perm [1,0,3,2]
+  x = dpp_max<0x4E>(x);                           // quad_perm [2,3,0,1]
+  if constexpr (LPR >= 8) x = dpp_max<0x141>(x);  // row_half_mirror
+  if constexpr (LPR >= 16) x = dpp_max<0x140>(x); // row_mirror
+  return x;
 }
 
-// LPR lanes per row, 16 elements per lane.
-template <int KT, int LPR, int ROPE>
-__global__ __launch_bounds__(256) void kv_write_kernel(KVWriteArgs a) {
+// LPR lanes per row, two pieces of 8 elements per lane: pieces that are turned
+// against each other where the keys are rotated in the half layout, neighbours
+// else.  A thread stores the same pieces of HB heads of a token, so a token's
+// rotation is read once for all of them.
+template <int KT, int LPR, int ROPE, int HB>
+__global__ __launch_bounds__(256) void kv_write_kernel(KVWriteArgs a, Bins bins) {
+  __shared__ float2 s_bin[KT == kKVNF4 ? kBins + 1 : 1];
+  if (KT == kKVNF4) {
+    const int t = threadIdx.x < kBins ? threadIdx.x : kBins - 1;
+    if (threadIdx.x <= kBins) s_bin[threadIdx.x] = make_float2(bins.m[t], __uint_as_float(bins.codes[t]));
+    __syncthreads();
+  }
   const int64_t r = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
-  if (r >= a.rows) return;  // the lanes of a row leave together
-  const uint32_t H = (uint32_t)a.pool.heads;
-  const int64_t ts = r / H;
-  const uint32_t h = (uint32_t)(r - ts * H);
+  const int64_t ts = r / a.groups;
+  const int h0 = (int)(r - ts * a.groups) * HB;
   const bool is_v = ts & 1;
   const int64_t tok = ts >> 1;
+  if (tok >= a.T) return;  // the lanes of a row leave together
+  const int H = a.pool.heads, u = threadIdx.x % LPR, D = a.pool.dim;
   const int64_t slot = a.slots[tok];
   if (slot < 0) return;
-  const int u = threadIdx.x % LPR;
   if (slot >= (a.pool.pages << a.pool.shift)) {
     if (u == 0) atomicOr(a.status, kStatusIndex);
     return;
   }
-  const HeadsView& hv = is_v ? a.v : a.k;
-  const uint16_t* p = hv.data + tok * hv.token_stride + (int64_t)h * hv.head_stride;
-  int64_t pos = 0;
-  if (ROPE && !is_v) {
-    pos = a.rope.positions[tok];
+  const bool mine = u * 16 < D;
+  const bool turn = ROPE && !is_v && u * 16 < a.rope.rot;
+  // The lane's pieces start at elements lo and hi.
+  int lo = u * 16, hi = lo + 8;
+  float cs[16];
+  if (turn) {
+    int64_t pos = a.rope.positions[tok];
     if (pos < 0 || pos >= a.rope.n) {
       if (u == 0) atomicOr(a.status, kStatusIndex);
       pos = 0;
     }
+    if (ROPE == 1) {
+      lo = u * 8;
+      hi = lo + a.rope.rot / 2;
+    }
+    rope_row8(a.rope, pos, u * 8, 1.0f, cs);
   }
-  float v[16] = {};
-  const bool mine = u * 16 < a.pool.dim;
-  if (mine) {
-    float lo[8], hi[8];
-    load8<ROPE>(p, u * 16, a.rope, pos, !is_v, lo);
-    load8<ROPE>(p, u * 16 + 8, a.rope, pos, !is_v, hi);
+  const HeadsView& hv = is_v ? a.v : a.k;
+  const uint16_t* src = hv.data + tok * hv.token_stride;
+  u32x4 x[HB], y[HB];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = lo[j];
-      v[8 + j] = hi[j];
+  for (int i = 0; i < HB; ++i) {
+    x[i] = y[i] = u32x4{0, 0, 0, 0};
+    if (mine && h0 + i < H) {
+      const uint16_t* p = src + (int64_t)(h0 + i) * hv.head_stride;
+      x[i] = *reinterpret_cast<const u32x4*>(p + lo);
+      y[i] = *reinterpret_cast<const u32x4*>(p + hi);
     }
   }
   const int64_t mask = ((int64_t)1 << a.pool.shift) - 1;
-  const int64_t row = (((slot >> a.pool.shift) * H + h) << a.pool.shift) + (slot & mask);
-  uint8_t* dst = (is_v ? a.pool.v : a.pool.k) + row * kv_row_bytes(a.pool.type, a.pool.dim);
-  if (KT == kKVBF16) {
-    if (mine) {
+  const int64_t row_bytes = kv_row_bytes(a.pool.type, D);
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        reinterpret_cast<u32x4*>(dst)[2 * u + q] =
-            u32x4{pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                  pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7])};
-    }
-    return;
-  }
-  // The row's largest magnitude, as integers: NaN > infinity > every number.
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint32_t b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-    top = b > top ? b : top;
-  }
-#pragma unroll
-  for (int off = 1; off < LPR; off <<= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)top, off, 64);
-    top = o > top ? o : top;
-  }
-  const float t = __uint_as_float(top);
-  const bool fine = t >= kTinyRow;
-  const float unit = fine ? 1.0f / t : 0.0f;
-  float* sc = (is_v ? a.pool.vs : a.pool.ks) + row;
-  if (u == 0) {
-    float s = KT == kKVINT8 ? t * (float)(1.0 / 127.0) : t;
-    if (!fine) s = 0.0f;
-    if (top >= 0x7F800000u) s = __uint_as_float(0x7FC00000u);
-    *sc = s;
-  }
-  if (!mine) return;
-  if (KT == kKVINT8) {
-    const float m = unit * 127.0f;
-    uint32_t w[4];
+  for (int i = 0; i < HB; ++i) {
+    const int h = h0 + i;
+    if (h >= H) return;
+    float v[16];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      w[q] = 0;
+      v[2 * q] = bf16_lo(x[i][q]);
+      v[2 * q + 1] = bf16_hi(x[i][q]);
+      v[8 + 2 * q] = bf16_lo(y[i][q]);
+      v[8 + 2 * q + 1] = bf16_hi(y[i][q]);
+    }
+    if (turn) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float c = rintf(v[4 * q + j] * m);
-        c = c < -127.0f ? -127.0f : c > 127.0f ? 127.0f : c;
-        w[q] |= ((uint32_t)(int)c & 0xFFu) << (8 * j);
+      for (int q = 0; q < 8; ++q) rope_pair(v[ROPE == 1 ? q : 2 * q], v[ROPE == 1 ? 8 + q : 2 * q + 1], cs[2 * q], cs[2 * q + 1]);
+    }
+    const int64_t row = (((slot >> a.pool.shift) * H + h) << a.pool.shift) + (slot & mask);
+    uint8_t* dst = (is_v ? a.pool.v : a.pool.k) + row * row_bytes;
+    if constexpr (KT == kKVBF16) {
+      if (mine) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          *reinterpret_cast<u32x4*>(dst + 2 * (q ? hi : lo)) =
+              u32x4{pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                    pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7])};
+      }
+    } else {
+      // The row's largest magnitude, as integers: NaN > infinity > every number.
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+        top = b > top ? b : top;
+      }
+      top = row_max<LPR>(top);
+      const float t = __uint_as_float(top);
+      const bool fine = t >= kTinyRow;
+      const float unit = fine ? 1.0f / t : 0.0f;
+      if (u == 0) {
+        float s = KT == kKVINT8 ? t * (float)(1.0 / 127.0) : t;
+        if (!fine) s = 0.0f;
+        if (top >= 0x7F800000u) s = __uint_as_float(0x7FC00000u);
+        (is_v ? a.pool.vs : a.pool.ks)[row] = s;
+      }
+      if constexpr (KT == kKVINT8) {
+        const float m = unit * 127.0f;
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          w[q] = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float c = __builtin_amdgcn_fmed3f(rintf(v[4 * q + j] * m), -127.0f, 127.0f);
+            w[q] |= ((uint32_t)(int)c & 0xFFu) << (8 * j);
+          }
+        }
+        if (mine) {
+          *reinterpret_cast<uint2*>(dst + lo) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2*>(dst + hi) = make_uint2(w[2], w[3]);
+        }
+      } else {
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float e = v[j] * unit;
+          // NaN and out-of-range products (a row that is no numbers) land in a bin too.
+          const int bin = (int)__builtin_amdgcn_fmed3f(__builtin_fmaf(e, 0.5f * kBins, 0.5f * kBins), 0.0f, (float)(kBins - 1));
+          const float2 d = s_bin[bin];
+          w[j / 8] |= ((__float_as_uint(d.y) >> (e > d.x ? 4 : 0)) & 15u) << (4 * (j % 8));
+        }
+        if (mine) {
+          *reinterpret_cast<uint32_t*>(dst + lo / 2) = w[0];
+          *reinterpret_cast<uint32_t*>(dst + hi / 2) = w[1];
+        }
       }
     }
-    reinterpret_cast<u32x4*>(dst)[u] = u32x4{w[0], w[1], w[2], w[3]};
-  } else {
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float y = v[j] * unit;
-      uint32_t level = 0;
-#pragma unroll
-      for (int b = 0; b < 15; ++b) level += y > a.d4.m[b] ? 1u : 0u;
-      const uint32_t c = (uint32_t)(a.d4.codes >> (4 * level)) & 15u;
-      w[j / 8] |= c << (4 * (j % 8));
-    }
-    reinterpret_cast<uint2*>(dst)[u] = make_uint2(w[0], w[1]);
   }
 }
 
@@ -240,18 +265,58 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KVReadArgs a) {
   reinterpret_cast<u32x4*>(dst)[2 * u + 1] = o[1];
 }
 
+template <int KT, int LPR, int HB>
+void write_rope(KVWriteArgs a, const Bins& bins, hipStream_t s) {
+  a.groups = (a.pool.heads + HB - 1) / HB;
+  const int64_t rows = a.T * 2 * a.groups;
+  const dim3 grid((unsigned)((rows + 256 / LPR - 1) / (256 / LPR)));
+  if (!a.rope.table) hipLaunchKernelGGL((kv_write_kernel<KT, LPR, 0, HB>), grid, dim3(256), 0, s, a, bins);
+  else if (!a.rope.interleaved) hipLaunchKernelGGL((kv_write_kernel<KT, LPR, 1, HB>), grid, dim3(256), 0, s, a, bins);
+  else hipLaunchKernelGGL((kv_write_kernel<KT, LPR, 2, HB>), grid, dim3(256), 0, s, a, bins);
+}
 template <int KT, int LPR>
-void write_rope(const KVWriteArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.rows + 256 / LPR - 1) / (256 / LPR)));
-  if (!a.rope.table) hipLaunchKernelGGL((kv_write_kernel<KT, LPR, 0>), grid, dim3(256), 0, s, a);
-  else if (!a.rope.interleaved) hipLaunchKernelGGL((kv_write_kernel<KT, LPR, 1>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((kv_write_kernel<KT, LPR, 2>), grid, dim3(256), 0, s, a);
+void write_heads(const KVWriteArgs& a, const Bins& bins, hipStream_t s) {
+  // Four heads to a thread once that leaves enough workgroups.
+  if (a.T * 2 * a.pool.heads * LPR >= 4 * 256 * 1024) write_rope<KT, LPR, 4>(a, bins, s);
+  else write_rope<KT, LPR, 1>(a, bins, s);
 }
 template <int KT>
-void write_lanes(const KVWriteArgs& a, hipStream_t s) {
-  if (a.pool.dim <= 64) write_rope<KT, 4>(a, s);
-  else if (a.pool.dim <= 128) write_rope<KT, 8>(a, s);
-  else write_rope<KT, 16>(a, s);
+void write_lanes(const KVWriteArgs& a, const Bins& bins, hipStream_t s) {
+  if (a.pool.dim <= 64) write_heads<KT, 4>(a, bins, s);
+  else if (a.pool.dim <= 128) write_heads<KT, 8>(a, bins, s);
+  else write_heads<KT, 16>(a, bins, s);
+}
+
+// The bins of a type; false if kBins does not separate its boundaries.
+bool make_kv_bins(const Midpoints& mp, Bins* out) {
+  for (int b = 0; b < kBins; ++b) {
+    const double lo = -1.0 + b * (2.0 / kBins), hi = lo + 2.0 / kBins;
+    uint32_t below = 0, inside = 0;
+    out->m[b] = 2.0f;
+    for (int j = 0; j < 15; ++j) {
+      const double m = (float)mp.m[j];  // +inf past the type's last
+      if (m < lo) ++below;
+      else if (m < hi) {
+        ++inside;
+        out->m[b] = (float)m;
+      }
+      if (std::fabs(m - lo) < 1e-5 || std::fabs(m - hi) < 1e-5) return false;
+    }
+    if (inside > 1) return false;
+    out->codes[b] = (uint8_t)(level_code(mp, below) | (level_code(mp, below + 1 < 16 ? below + 1 : 15) << 4));
+  }
+  return true;
+}
+
+// The same, built once per type.
+bool kv_bins(int type, const Midpoints& mp, Bins* out) {
+  static std::once_flag once[3];
+  static Bins bins[3];
+  static bool good[3];
+  const int i = type - kKVNF4;
+  std::call_once(once[i], [&] { good[i] = make_kv_bins(mp, &bins[i]); });
+  *out = bins[i];
+  return good[i];
 }
 
 }  // namespace
@@ -259,23 +324,21 @@ void write_lanes(const KVWriteArgs& a, hipStream_t s) {
 hipError_t launch_kv_write(const KVPool& pool, int64_t T, const HeadsView& k, const HeadsView& v,
                            const int64_t* slots, const RopeTable& rope, const Midpoints& mp, hipStream_t s) {
   KVWriteArgs a{};
+  Bins bins{};
   hipError_t e = hipSuccess;
   a.status = status_word(&e);
   if (!a.status) return e;
+  if (pool.type >= kKVNF4 && !kv_bins(pool.type, mp, &bins)) return hipErrorInvalidValue;  // no shipped type
   a.pool = pool;
   a.k = k;
   a.v = v;
-  a.rows = T * pool.heads * 2;
+  a.T = T;
   a.slots = slots;
   a.rope = rope;
-  for (int j = 0; j < 15; ++j) a.d4.m[j] = (float)mp.m[j];
-  a.d4.codes = mp.codes;
-  a.d4.zero_code = mp.zero_code;
-  if (a.rows <= 0) return hipSuccess;
   KernelTimer kt_("kv_write_kernel", s);
-  if (pool.type == kKVBF16) write_lanes<kKVBF16>(a, s);
-  else if (pool.type == kKVINT8) write_lanes<kKVINT8>(a, s);
-  else write_lanes<kKVNF4>(a, s);
+  if (pool.type == kKVBF16) write_lanes<kKVBF16>(a, bins, s);
+  else if (pool.type == kKVINT8) write_lanes<kKVINT8>(a, bins, s);
+  else write_lanes<kKVNF4>(a, bins, s);
   return hipGetLastError();
 }
 

@@ -8,7 +8,9 @@
 // The table is built once per model (fp64 angles, rounded to fp32 once), so
 // that long positions lose nothing: an fp32 product position * frequency is
 // off by position * 2^-24 radians.  The rotation itself is bound by memory:
-// 4 bytes per element of q and k and one table row per token.
+// 4 bytes per element of q and k and one table row per token (4096 tokens of
+// 104 heads of 128: 220 MB in 43 us, 5.1 TB/s; 4 tokens of 64 heads 3.5 us, a
+// launch).  16 elements to a thread, with 64 bytes of the table from the caches.
 #include <cmath>
 
 #include "common.hpp"
@@ -53,53 +55,39 @@ struct RopeArgs {
   int* status;
 };
 
-// A thread turns one unit (16 elements of the dims: 8 pairs, or 16 dims that
-// pass) of HB heads of one token, with the unit's table values read once.
-template <int HB, bool INTER>
+// A thread turns one unit of one head of a token: 16 elements, 8 pairs of them
+// or 16 dims that pass.
+template <bool INTER>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
-  const uint32_t units = (uint32_t)a.dim / 16, groups = ((uint32_t)a.heads + HB - 1) / HB;
+  const uint32_t units = (uint32_t)a.dim / 16;
   const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-  const uint64_t t64 = id / (units * groups);
-  if (t64 >= (uint64_t)a.T) return;
-  const int64_t tok = (int64_t)t64;
-  const uint32_t in_tok = (uint32_t)(id - t64 * (units * groups));
-  const uint32_t grp = in_tok / units, u = in_tok - grp * units;
-  const uint32_t turned = (uint32_t)a.t.rot / 16;
+  const int64_t tok = (int64_t)(id / (units * (uint32_t)a.heads));
+  if (tok >= a.T) return;
+  const uint32_t in_tok = (uint32_t)(id - (uint64_t)tok * (units * (uint32_t)a.heads));
+  const int h = (int)(in_tok / units);
+  const uint32_t u = in_tok - (uint32_t)h * units;
   int32_t pos = a.t.positions[tok];
   if (pos < 0 || pos >= a.t.n) {
     if (in_tok == 0) atomicOr(a.status, kStatusIndex);
     pos = 0;
   }
-  const bool turn = u < turned;
-  const uint32_t lo = !turn ? u * 16 : INTER ? u * 16 : u * 8;
-  const uint32_t hi = !turn || INTER ? lo + 8 : lo + (uint32_t)a.t.rot / 2;
-  float cs[16];
-  if (turn) rope_row8(a.t, pos, u * 8, a.sign, cs);
-  u32x4 x[HB], y[HB];
-#pragma unroll
-  for (int j = 0; j < HB; ++j) {
-    const int h = (int)(grp * HB) + j;
-    if (h < a.heads) {
-      const HeadsView& v = h < a.q_heads ? a.q : a.k;
-      const uint16_t* p = v.data + tok * v.token_stride + (int64_t)(h < a.q_heads ? h : h - a.q_heads) * v.head_stride;
-      x[j] = *reinterpret_cast<const u32x4*>(p + lo);
-      y[j] = *reinterpret_cast<const u32x4*>(p + hi);
-    }
+  const bool turn = u < (uint32_t)a.t.rot / 16;
+  const uint32_t lo = turn && !INTER ? u * 8 : u * 16, hi = turn && !INTER ? lo + (uint32_t)a.t.rot / 2 : lo + 8;
+  const bool is_q = h < a.q_heads;
+  const int64_t hh = is_q ? h : h - a.q_heads;
+  const HeadsView& from = is_q ? a.q : a.k;
+  const uint16_t* p = from.data + tok * from.token_stride + hh * from.head_stride;
+  u32x4 x = *reinterpret_cast<const u32x4*>(p + lo), y = *reinterpret_cast<const u32x4*>(p + hi);
+  if (turn) {
+    float cs[16];
+    rope_row8(a.t, pos, u * 8, a.sign, cs);
+    if (INTER) rope_inter16(x, y, cs);
+    else rope_half8(x, y, cs);
   }
-#pragma unroll
-  for (int j = 0; j < HB; ++j) {
-    const int h = (int)(grp * HB) + j;
-    if (h < a.heads) {
-      if (turn) {
-        if (INTER) rope_inter16(x[j], y[j], cs);
-        else rope_half8(x[j], y[j], cs);
-      }
-      const HeadsView& v = h < a.q_heads ? a.q_out : a.k_out;
-      uint16_t* p = v.data + tok * v.token_stride + (int64_t)(h < a.q_heads ? h : h - a.q_heads) * v.head_stride;
-      *reinterpret_cast<u32x4*>(p + lo) = x[j];
-      *reinterpret_cast<u32x4*>(p + hi) = y[j];
-    }
-  }
+  const HeadsView& to = is_q ? a.q_out : a.k_out;
+  uint16_t* o = to.data + tok * to.token_stride + hh * to.head_stride;
+  *reinterpret_cast<u32x4*>(o + lo) = x;
+  *reinterpret_cast<u32x4*>(o + hi) = y;
 }
 
 }  // namespace
@@ -133,8 +121,8 @@ hipError_t launch_rope(int64_t T, int32_t dim, const RopeTable& t, bool inverse,
   if (n <= 0) return hipSuccess;
   KernelTimer kt_("rope_kernel", s);
   const dim3 grid((unsigned)((n + 255) / 256));
-  if (t.interleaved) hipLaunchKernelGGL((rope_kernel<1, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((rope_kernel<1, false>), grid, dim3(256), 0, s, a);
+  if (t.interleaved) hipLaunchKernelGGL(rope_kernel<true>, grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(rope_kernel<false>, grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -39,9 +39,11 @@ def _heads(t, name):
     return Heads(t.data_ptr(), st if n > 1 else 0, sh if h > 1 else 0, h)
 
 
-def _new_heads(like, heads, dim):
-    """A contiguous tensor of the same tokens, and its view."""
-    t = like.new_empty((like.shape[0], heads, dim))
+def _new_heads(like):
+    """A contiguous tensor like this one, and its view."""
+    torch = _torch()
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    _, heads, dim = t.shape
     return t, Heads(t.data_ptr(), heads * dim, dim, heads)
 
 
@@ -83,11 +85,11 @@ def rope(q, k, table, positions, layout="half", inverse=False, q_out=None, k_out
     from rot on are copied.  inverse=True is the transpose: the gradient of q
     and k from those of the rotated ones.  q_out, k_out: outputs (q and k
     themselves for in place); allocated when absent.  Returns (q_out, k_out)."""
-    T, hq, D = q.shape
+    T, _, D = q.shape
     rows, rot = _table(table, positions, T)
     qv = _heads(q, "q")
     if q_out is None:
-        q_out, qo = _new_heads(q, hq, D)
+        q_out, qo = _new_heads(q)
     else:
         qo = _heads(q_out, "q_out")
     kv = ko = None
@@ -96,7 +98,7 @@ def rope(q, k, table, positions, layout="half", inverse=False, q_out=None, k_out
             raise ValueError("q and k must have the same tokens and dim")
         kv = _heads(k, "k")
         if k_out is None:
-            k_out, ko = _new_heads(k, k.shape[1], D)
+            k_out, ko = _new_heads(k)
         else:
             ko = _heads(k_out, "k_out")
         if k_out.shape != k.shape:
@@ -211,7 +213,7 @@ def attend_paged(q, cache, pages, starts, lengths, max_new, max_len, scale=None,
     _index(starts, B + 1, torch.int32, "starts")
     _dev(lengths, torch.int32, "lengths")
     if out is None:
-        out = q.new_empty((T, Hq, D))
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _need(_dev(out, torch.bfloat16, "out"), T * Hq * D, "out")
     if lse is True:
