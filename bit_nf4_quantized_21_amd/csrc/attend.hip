@@ -636,7 +636,7 @@ Plan make_plan(const AttendProblem& p) {
   // sequences (those 4 of up to 1000 tokens: 16.1 us, 17.8 with eight).
   r.waves = span / splits > 2048 && r.tile_rows == 16 && p.pool.dim <= 128 ? 8 : 4;
   r.chunk = ((span + splits - 1) / splits + 127) / 128 * 128;
-  r.chunk = std::min<int64_t>(std::max<int64_t>(r.chunk, 128), kMaxChunk);
+  r.chunk = std::min<int64_t>(std::max<int64_t>(r.chunk, 128), r.tile ? kTileChunk : kMaxChunk);
   r.splits = std::max<int64_t>(1, (span + r.chunk - 1) / r.chunk);
   return r;
 }

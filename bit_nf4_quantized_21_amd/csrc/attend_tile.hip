@@ -56,7 +56,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   __shared__ __align__(16) uint16_t s_k1[kTileKeys * DP], s_v1[kTileKeys * DP];
   __shared__ __align__(16) float s_sc[CODES ? 2 : 1][2][kTileKeys];
   __shared__ __align__(16) uint8_t s_wild[2][kTileKeys];
-  __shared__ int s_page[kMaxChunk / 16 + 1];
+  // Of each page of the split: its number, and where its rows of this head
+  // start in the codes (bytes).
+  __shared__ int s_page[kTileChunk / 16 + 1];
+  __shared__ int64_t s_at[kTileChunk / 16 + 1];
   __shared__ uint2 s_lut[BITS == 4 ? 256 : 1];
 
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h2 = lane >> 5;
@@ -94,6 +97,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
       page = 0;
     }
     s_page[p] = page;
+    s_at[p] = (((int64_t)page * H + h) << shift) * kv_row_bytes(a.pool.type, a.pool.dim);
   }
   if (BITS == 4 && tid < 256) {
     // A byte's two levels: a pair of bf16 (exact levels), or two fp32 values.
@@ -146,23 +150,21 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   uint32_t kr[ASYNC ? 1 : NP][PW], vr[ASYNC ? 1 : NP][PW];
   float scale_k = 0.0f, scale_v = 0.0f;
   float piece_ks[OP == kOpLevel2 ? NP : 1], piece_vs[OP == kOpLevel2 ? NP : 1];
-  // Pages of the pieces of the tile to load next, read one tile ahead.
-  int pages[NP];
+  // Where the pages of the pieces of the next tile start, read a tile ahead.
+  int64_t page_at[NP];
   auto read_pages = [&](int j0) {
 #pragma unroll
     for (int n = 0; n < NP; ++n)
-      pages[n] = s_page[min(((j0 + wave_key + RUN * n) >> shift) - first_page, last)];
+      page_at[n] = s_at[min(((j0 + wave_key + RUN * n) >> shift) - first_page, last)];
   };
+  const uint32_t in_page = (1u << shift) - 1;
   auto load = [&](uint16_t* to_k, uint16_t* to_v, int j0) {
     if (stages)
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
-      const int j = j0 + wave_key + RUN * n;
-      const int64_t base =
-          (((int64_t)__builtin_amdgcn_readfirstlane(pages[n]) * H + h) << shift) + (j & ((1 << shift) - 1));
-      const uint8_t* kp = a.pool.k + base * row_bytes;
-      const uint8_t* vp = a.pool.v + base * row_bytes;
-      if constexpr (ASYNC) asm("" : "+s"(kp), "+s"(vp));  // kept in scalar registers: the lanes add 32 bits
+      const uint32_t row = (uint32_t)(j0 + wave_key + RUN * n) & in_page;
+      const uint8_t* kp = a.pool.k + page_at[n] + row * row_bytes;
+      const uint8_t* vp = a.pool.v + page_at[n] + row * row_bytes;
       if constexpr (ASYNC) {
         // Straight to LDS, lane by lane: the swizzle picks the lane's source.
         const int key = wave_key + lane_key + RUN * n;
@@ -184,8 +186,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
         for (int w = 0; w < PW; ++w) kr[n][w] = vr[n][w] = 0;
       }
       if constexpr (OP == kOpLevel2) {
-        piece_ks[n] = a.pool.ks[base + lane_key];
-        piece_vs[n] = a.pool.vs[base + lane_key];
+        const int page = s_page[min(((j0 + wave_key + RUN * n) >> shift) - first_page, last)];
+        const int64_t at = (((int64_t)page * H + h) << shift) + row + lane_key;
+        piece_ks[n] = a.pool.ks[at];
+        piece_vs[n] = a.pool.vs[at];
       }
     }
     if constexpr (CODES) {
@@ -339,18 +343,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
         }
     }
     const float k2 = CODES ? 1.0f : s2;
-    const bool edge = on_edge(j0);
-    // Bounds of the keys that the lane's row sees, against the register's own
-    // place 32 c + 8 (i / 4) + i % 4.
-    const int from = my_lo - j0 - 4 * h2, to = my_hi - j0 - 4 * h2;
-    if (edge) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int at = 32 * c + 8 * (i / 4) + i % 4;
-          if (at < from || at >= to) s[c][i] = -INFINITY;
-        }
+    if (on_edge(j0)) {
       uint32_t wild[8], some = 0;
 #pragma unroll
       for (int n = 0; n < 8; ++n) some |= wild[n] = *reinterpret_cast<const uint32_t*>(&s_wild[buf][8 * n + 4 * h2]);
@@ -358,11 +351,19 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-              const int at = 32 * c + 8 * (i / 4) + i % 4;
-              if ((wild[4 * c + i / 4] >> (8 * (i % 4)) & 255u) && at >= from && at < to) s[c][i] = __uint_as_float(0x7FC00000u);
-            }
+          for (int i = 0; i < 16; ++i)
+            if (wild[4 * c + i / 4] >> (8 * (i % 4)) & 255u) s[c][i] = __uint_as_float(0x7FC00000u);
       }
+      // Bounds of the keys that the lane's row sees, against the register's own
+      // place 32 c + 8 (i / 4) + i % 4.
+      const int from = my_lo - j0 - 4 * h2, to = my_hi - j0 - 4 * h2;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int at = 32 * c + 8 * (i / 4) + i % 4;
+          if (at < from || at >= to) s[c][i] = -INFINITY;
+        }
     }
     float top = s[0][0];
 #pragma unroll
