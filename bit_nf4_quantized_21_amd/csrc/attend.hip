@@ -44,9 +44,14 @@ __device__ __forceinline__ void pack_levels(const uint2 (&w)[4], bf16x8 (&out)[N
 
 // ---------------------------------------------------------------------------
 // Streaming kernel: 16 * NQ rows of one sequence and key/value head against
-// one split of its keys.  Each of the four waves takes every fourth step of 32
-// keys straight from memory into MFMA operands, with its own running maximum
-// and sum; the waves meet once, in LDS, at the end.
+// one split of its keys.  Each of the WAVES waves takes every WAVES-th step of
+// 32 keys straight from memory into MFMA operands, with its own running maximum
+// and sum; the waves meet once, in LDS, at the end.  What bounds it: memory
+// where the cache holds 8 or 16 bits (64 sequences of up to 8192 tokens, int8:
+// 650 MB in 144 us, 4.5 TB/s; 131071 keys of 8 heads 5.2 TB/s, bf16 5.8), the
+// lookups and the instructions of a step where it holds 4 (131071 NF4 keys:
+// 143 MB in 43 us, 3.3 TB/s; Int4 37 us; int8 39 us when the rows come from the
+// caches).
 //
 // S^T = K Q^T by 16x16x32 MFMAs: lane (r = lane & 15, g = lane >> 4) loads the
 // contiguous dims [g DP/4, (g + 1) DP/4) of key r (of each 16-key block) and
@@ -668,6 +673,8 @@ void stream_rows(const AttendArgs& a, int waves, unsigned grid, hipStream_t s) {
 }  // namespace
 
 bool attend_fits(const AttendProblem& p) {
+  // Rows and (token, head) pairs are counted in 32 bits.
+  if ((int64_t)p.max_new * p.q.heads >= (int64_t(1) << 30)) return false;
   const Plan r = make_plan(p);
   const int64_t groups = (int64_t)p.batch * p.pool.heads;
   return r.tiles < (int64_t(1) << 31) && groups * r.tiles < (int64_t(1) << 31) &&

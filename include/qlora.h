@@ -504,11 +504,15 @@ int qlora_kv_read(const qlora_kv_cache* cache, int64_t T, const int64_t* slots, 
  *   lse      [tokens, q heads] fp32, or NULL.
  *   workspace  qlora_attend_paged_workspace_bytes bytes (the partial sums
  *            when the keys are split over workgroups).
- * Scores, the running maximum and sum and the output's accumulation are fp32;
- * keys and values enter the products as bf16 (int8 codes and FP4 levels are
- * exact there; NF4 and Int4 levels are rounded to bf16, their row scales are
- * not) and the weights are rounded to bf16 before the second product.
- * Deterministic: splits are joined in a fixed order.
+ * Scores, the running maximum and sum and the output's accumulation are fp32.
+ * Keys and values enter the products as bf16: bf16 rows, int8 codes and the
+ * levels of Int4 and FP4 exactly (a row's scale multiplies whole scores and
+ * weights, in fp32), NF4 as two bf16 values per level, or, in the kernel for
+ * many rows, as the product level * scale rounded to bf16.  The weights enter
+ * the second product as two bf16 values, in the kernel for many rows (more
+ * than 32 rows of max_new * q heads / cache heads) as one.
+ * max_new * q heads must be below 2^30.  Deterministic: splits are joined in a
+ * fixed order.
  */
 size_t qlora_attend_paged_workspace_bytes(const qlora_kv_cache* cache, int64_t tokens, int32_t q_heads, int32_t batch,
                                           int64_t max_new, int64_t max_len, int32_t causal, int64_t window);

@@ -389,6 +389,16 @@ def test_split_keys(seqs, hq, h, kv):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
 
 
+@pytest.mark.parametrize("n", [1, 20, 90])
+def test_nothing_stored(n):
+    for kv in ("bf16", "int8"):
+        b = Batch([(n, 0), (0, 0), (n, 0)], 4, 2, 64, kv, 16, seed=18)
+        assert b.bounds["max_len"] == 0
+        out, lse = b.run()
+        assert torch.all(out == 0) and torch.all(lse == float("-inf"))
+        b.check(out, lse)
+
+
 @pytest.mark.parametrize("scale", [-0.2, 0.0, 1.0])
 @pytest.mark.parametrize("seqs", [SMALL, LARGE], ids=["small", "large"])
 def test_scales(seqs, scale):
