@@ -7,14 +7,16 @@
 // bf16, else to registers, from where they are widened into the other half
 // before the one barrier of the step.
 //
-// What bounds it: instructions.  Per tile and wave a bf16 cache takes 32 MFMAs
-// (1024 clocks), 215 vector instructions of which 32 are exponentials, 53 LDS
-// and 60 scalar ones, and what two waves per SIMD issue of them hardly
-// overlaps: the matrix units are 40 % busy, the vector units 44 %, at the
-// 1.9 GHz that the chip then holds.  52 heads of 4096 causal rows: 269 us,
-// 830 TFLOP/s of what is seen (a dense product of 8192^3 in bf16 runs at 1258
-// here).  The scores of the next tile computed between this one's exponentials
-// gained nothing and cost 32 registers.
+// What bounds it: instructions and power.  Per tile and wave a bf16 cache takes
+// 32 MFMAs (1024 clocks), 204 vector instructions of which 32 are
+// exponentials, 53 LDS and 116 scalar ones; with two waves per SIMD the matrix
+// units are 42 % busy and the vector units about as much, at the 1.9 GHz that
+// the chip then holds (with zeros for data it runs 12 % faster).  52 heads of
+// 4096 causal rows: 269 us, 830 TFLOP/s of what is seen (a dense product of
+// 8192^3 in bf16 runs at 1258 here).  Memory is not it: all keys from one page
+// take as long.  No faster: the scores of the next tile computed between this
+// one's exponentials (32 registers more), operands read further ahead, 256 rows
+// for bf16, heads kept together on an XCD.
 //
 // S^T = K Q^T by 32x32x16 MFMAs: lane (r = lane & 31, h = lane >> 5) ends up
 // with the scores of query r against keys 8 (i / 4) + 4 h + i % 4 of each
