@@ -23,7 +23,7 @@ namespace {
 // (`lut`): an entry per byte, a bf16 pair, or for kOpLevel2 that and the pair
 // of what it misses.  (A table of 16 single codes, whose reads never meet in a
 // bank, needs twice the reads and four more instructions a pair: 131071 NF4
-// keys 54.7 us, 41 this way.)
+// keys 54.7 us, 48 with it for the keys alone, 43 this way.)
 template <int KT>
 __device__ __forceinline__ uint2 level_pair(const uint32_t* lut, uint32_t x, int q) {
   const char* p = reinterpret_cast<const char*>(lut);
@@ -102,6 +102,12 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
   id = next;
   next = uniform_div(id, a.batch);
   const int b = id - next * a.batch, split = uniform_div(next, a.tiles), tile = next - split * a.tiles;
+  // Without a window a split's first page is known before the lengths are: its
+  // pages are read with them (entries of the table past a sequence's own are
+  // read but not used).
+  const int shift = a.pool.shift, ahead = ((split * a.chunk) >> shift) + tid;
+  int early = 0;
+  if (!a.window && ahead < a.width) early = a.pages[(int64_t)b * a.width + ahead];
   const Seq sq = load_seq(a, b);
   if (sq.bad && tid == 0) atomicOr(a.status, kStatusIndex);
   const int G = a.group, rows = sq.n * G, row0 = tile * 16 * NQ;
@@ -114,9 +120,9 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
   // Steps inside [full_lo, full_hi) are seen by every row.
   const int full_hi = seen_hi(a, sq, i_first), full_lo = seen_lo(a, sq, i_last);
 
-  const int shift = a.pool.shift, first_page = k0 >> shift, last = ((k1 - 1) >> shift) - first_page;
+  const int first_page = k0 >> shift, last = ((k1 - 1) >> shift) - first_page;
   for (int p = tid; k0 < k1 && p <= last; p += 64 * WAVES) {
-    int page = a.pages[(int64_t)b * a.width + first_page + p];
+    int page = !a.window && p == tid ? early : a.pages[(int64_t)b * a.width + first_page + p];
     if (page < 0 || page >= a.pool.pages) {
       atomicOr(a.status, kStatusIndex);
       page = 0;

@@ -137,9 +137,16 @@ def _check(rc: int):
         raise QLoRAError(msg)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported by the first call that needs it."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dev(t, dtype, name):
