@@ -117,6 +117,7 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
   const int k0 = (lo & ~15) + split * a.chunk;
   if (split > 0 && k0 >= hi) return;
   const int k1 = min(hi, k0 + a.chunk);
+  const bool several = hi - (lo & ~15) > a.chunk;  // splits, that the join puts together
   // Steps inside [full_lo, full_hi) are seen by every row.
   const int full_hi = seen_hi(a, sq, i_first), full_lo = seen_lo(a, sq, i_last);
 
@@ -500,7 +501,7 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
       const int64_t at = (sq.first + i) * Hq + h * G + gh;
       const float inv = sum == 0.0f ? 0.0f : a.unit / sum;
       if (part == 0) {
-        if (a.splits > 1) {
+        if (several) {
           float* ml = a.part_ml + ((int64_t)split * a.tokens * Hq + at) * 2;
           ml[0] = top;
           ml[1] = sum;
@@ -514,7 +515,7 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
         for (int w = 0; w < WAVES; ++w)
 #pragma unroll
           for (int t = 0; t < DT; ++t) v[t] += s_o[(w * 16 + qr) * OS + part * DT + t];
-        if (a.splits > 1) {
+        if (several) {
           float* po = a.part_o + ((int64_t)split * a.tokens * Hq + at) * D + part * DT;
 #pragma unroll
           for (int t = 0; t < DT; ++t) po[t] = v[t];
@@ -536,7 +537,8 @@ __global__ __launch_bounds__(64 * WAVES) void attend_stream_kernel(AttendArgs a)
 // Joins the splits of the rows.  P groups of DP / 4 lanes work on a row, each
 // on every P-th split, 256 / (P DP / 4) rows to a workgroup; the groups meet in
 // LDS.  Few splits of many rows take P = 1 (51 000 rows in 2: 16 us, 97 with a
-// workgroup to each), many splits of few rows the whole workgroup.
+// workgroup to each), many splits of few rows the whole workgroup.  Row tiles
+// whose keys fit one split were finished by their own workgroup.
 template <int DP, bool WIDE>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int tile_rows) {
   constexpr int L = DP / 4, P = WIDE ? 256 / L : 1, R = 256 / (L * P);
@@ -550,7 +552,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int tile
   const int i = e / Hq, hq = e - i * Hq, rows = sq.n * G;
   const int row0 = (i * G + hq % G) / tile_rows * tile_rows;
   const int hi = seen_hi(a, sq, (min(rows, row0 + tile_rows) - 1) / G), lo = seen_lo(a, sq, row0 / G) & ~15;
-  const int n = hi <= lo ? 1 : (hi - lo + a.chunk - 1) / a.chunk;
+  if (hi - lo <= a.chunk) return;
+  const int n = (hi - lo + a.chunk - 1) / a.chunk;
   const int64_t at = (sq.first + i) * Hq + hq, step = a.tokens * Hq;
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + at;
   float top = -INFINITY;
@@ -639,7 +642,7 @@ Plan make_plan(const AttendProblem& p) {
   // splits.  8 heads of 131071 NF4 keys: 43 + 4 us in 32 splits of eight waves,
   // 44 + 5.5 in 64 of four.  Tiles are long and uneven (a sequence's length, the
   // causal corner), so they want twice what the chip holds at once: 4 chunks of
-  // 300 to 512 tokens over 512 to 4608, int8, 188 us whole, 162 + 16 in two.
+  // 300 to 512 tokens over 512 to 4608, int8, 188 us whole, 158 + 12 in two, 147 + 14 in three.
   const int64_t full = !r.tile ? 128 : r.tile_rows == 256 ? 512 : 1024, want = !r.tile ? 256 : full;
   int64_t splits = work >= full ? 1 : std::min((want + work - 1) / work, span / (r.tile ? 256 : 512));
   splits = std::max<int64_t>(splits, 1);

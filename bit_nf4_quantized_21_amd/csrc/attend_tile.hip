@@ -456,7 +456,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   if (!ok) return;
   const int Hq = H * G;
   const int64_t at = (sq.first + qi) * Hq + h * G + qg;
-  if (a.splits > 1) {
+  if (hi - (lo & ~15) > a.chunk) {  // the other splits' part is to come
     const int64_t to = (int64_t)split * a.tokens * Hq + at;
     if (h2 == 0) {
       a.part_ml[2 * to] = m;

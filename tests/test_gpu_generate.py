@@ -389,6 +389,23 @@ def test_split_keys(seqs, hq, h, kv):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int8", "nf4"])
+@pytest.mark.parametrize("hq,h,n", [(2, 2, 1), (2, 1, 10), (4, 1, 30), (2, 1, 150)])
+def test_split_and_whole_sequences_together(hq, h, n, kv):
+    """Sequences whose keys are cut over workgroups beside such that fit one, in any order of lengths."""
+    b = Batch([(min(n, 3), 40), (n, 2600), (n, 640), (1, 641), (n, 5200), (0, 5200), (n, max(n, 639)), (2, 0), (n, 2600)],
+              hq, h, 128, kv, 32, seed=8)
+    b.check(*b.run())
+    b.check(*b.run(causal=False), causal=False)
+
+
+@pytest.mark.parametrize("n,batch", [(1, 70), (40, 64), (40, 65)])
+def test_many_sequences(n, batch):
+    seqs = [(n, n + (37 * i) % 90) for i in range(batch)]
+    b = Batch(seqs, 2, 1, 64, "int8", 16, seed=9)
+    b.check(*b.run())
+
+
 @pytest.mark.parametrize("n", [1, 20, 90])
 def test_nothing_stored(n):
     for kv in ("bf16", "int8"):
