@@ -174,17 +174,17 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   const bool stages = RUN <= kTileKeys || wave_key < kTileKeys;  // eight waves may be more than the pieces
   const uint32_t lane_off = lane_key * row_bytes + pc * (PW * 4);
   uint32_t kr[ASYNC ? 1 : NP][PW], vr[ASYNC ? 1 : NP][PW];
-  float scale_k = 0.0f, scale_v = 0.0f;
+  float scale = 0.0f;  // of a key in the first wave, of a value in the second
   float piece_ks[OP == kOpLevel2 ? NP : 1], piece_vs[OP == kOpLevel2 ? NP : 1];
   // Where the pages of the pieces of the next tile start, read a tile ahead.
   int64_t page_at[NP];
-  auto read_pages = [&](int j0) {
+  auto read_pages = [&](int j0) __attribute__((always_inline)) {
 #pragma unroll
     for (int n = 0; n < NP; ++n)
       page_at[n] = s_at[min(((j0 + wave_key + RUN * n) >> shift) - first_page, last)];
   };
   const uint32_t in_page = (1u << shift) - 1;
-  auto load = [&](uint16_t* to_k, uint16_t* to_v, int j0) {
+  auto load = [&](uint16_t* to_k, uint16_t* to_v, int j0) __attribute__((always_inline)) {
     if (stages)
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
@@ -198,18 +198,17 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
         const uint32_t vo = lane_key * row_bytes + v_chunk<DP>(key, pc) * 16;
         __builtin_amdgcn_global_load_lds((const gptr_t*)(kp + ko), (lptr_t*)(to_k + (wave_key + RUN * n) * DP), 16, 0, 0);
         __builtin_amdgcn_global_load_lds((const gptr_t*)(vp + vo), (lptr_t*)(to_v + (wave_key + RUN * n) * DP), 16, 0, 0);
-      } else if (EXACT || pc * EL < D) {
-        if constexpr (PW == 4) {
-          const u32x4 x = *reinterpret_cast<const u32x4*>(kp + lane_off), y = *reinterpret_cast<const u32x4*>(vp + lane_off);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) { kr[n][w] = x[w]; vr[n][w] = y[w]; }
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(kp + lane_off), y = *reinterpret_cast<const uint2*>(vp + lane_off);
-          kr[n][0] = x.x; kr[n][1] = x.y; vr[n][0] = y.x; vr[n][1] = y.y;
-        }
       } else {
+        // (Whole values, assigned once: assigned on two paths, the pieces were
+        // kept in scratch memory.)
+        typedef uint32_t piece __attribute__((ext_vector_type(PW)));
+        piece x = {}, y = {};
+        if (EXACT || pc * EL < D) {
+          x = *reinterpret_cast<const piece*>(kp + lane_off);
+          y = *reinterpret_cast<const piece*>(vp + lane_off);
+        }
 #pragma unroll
-        for (int w = 0; w < PW; ++w) kr[n][w] = vr[n][w] = 0;
+        for (int w = 0; w < PW; ++w) { kr[n][w] = x[w]; vr[n][w] = y[w]; }
       }
       if constexpr (OP == kOpLevel2) {
         const int page = s_page[min(((j0 + wave_key + RUN * n) >> shift) - first_page, last)];
@@ -221,13 +220,12 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     if constexpr (CODES) {
       const int j = j0 + lane, page = s_page[min((j >> shift) - first_page, last)];
       const int64_t base = (((int64_t)page * H + h) << shift) + (j & ((1 << shift) - 1));
-      if (wave == 0) scale_k = a.pool.ks[base];
-      else if (wave == 1) scale_v = a.pool.vs[base];
+      if (wave < 2) scale = (wave ? a.pool.vs : a.pool.ks)[base];
     }
     read_pages(j0 + kTileKeys);
   };
   // A staged piece as bf16 pairs.
-  auto widen = [&](const uint32_t (&w)[PW], float sc, uint32_t (&out)[EL / 2]) {
+  auto widen = [&](const uint32_t (&w)[PW], float sc, uint32_t (&out)[EL / 2]) __attribute__((always_inline)) {
     if constexpr (OP == kOpBF16) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) out[e] = w[e];
@@ -257,7 +255,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   // (it must not reach rows that do not see its key through 0 * inf) and its
   // key is marked: the rows that see it get a NaN weight.  w: a piece of key
   // `key`, which PR lanes in a row hold.
-  auto tame = [&](auto& w, int buf, int key, int j0) {
+  auto tame = [&](auto& w, int buf, int key, int j0) __attribute__((always_inline)) {
     const bool any = j0 + key >= lo && j0 + key < hi;
     bool bad = false;
 #pragma unroll
@@ -270,9 +268,9 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     const uint64_t all = __ballot(bad) >> ((lane / PR) * PR);
     if (pc == 0) s_wild[buf][key] = (all & (((uint64_t)1 << PR) - 1)) != 0;
   };
-  auto on_edge = [&](int j0) { return j0 < full_lo || j0 + kTileKeys > full_hi; };
+  auto on_edge = [&](int j0) __attribute__((always_inline)) { return j0 < full_lo || j0 + kTileKeys > full_hi; };
   // What is left to do for a tile once its rows are here, before the barrier.
-  auto store = [&](uint16_t* to_k, uint16_t* to_v, int buf, int j0) {
+  auto store = [&](uint16_t* to_k, uint16_t* to_v, int buf, int j0) __attribute__((always_inline)) {
     if constexpr (!ASYNC) {
       const bool edge = on_edge(j0);
       if (stages)
@@ -295,11 +293,11 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     }
     if constexpr (CODES) {
       if (wave == 0) {
-        s_sc[buf][0][lane] = scale_k * s2;
+        s_sc[buf][0][lane] = scale * s2;
       } else if (wave == 1) {
         // The codes are finite; a scale that is not is treated as such a value.
-        const bool bad = (__float_as_uint(scale_v) & 0x7F800000u) == 0x7F800000u, any = j0 + lane >= lo && j0 + lane < hi;
-        s_sc[buf][1][lane] = bad && on_edge(j0) ? 0.0f : scale_v;
+        const bool bad = (__float_as_uint(scale) & 0x7F800000u) == 0x7F800000u, any = j0 + lane >= lo && j0 + lane < hi;
+        s_sc[buf][1][lane] = bad && on_edge(j0) ? 0.0f : scale;
         s_wild[buf][lane] = bad && any;
       }
     }
@@ -330,11 +328,11 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     v_at[t] = key * DP + v_chunk<DP>(key, col / 8) * 8 + (col & 7);
   }
 
-  auto compute = [&](const uint16_t* tk, const uint16_t* tv, int buf, int j0) {
+  auto compute = [&](const uint16_t* tk, const uint16_t* tv, int buf, int j0) __attribute__((always_inline)) {
     // Keys come from LDS two MFMA pairs ahead of their use.
     f32x16 s[2];
     u32x4 kf[3][2];
-    auto read_k = [&](int t) {
+    auto read_k = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) kf[t % 3][c] = *reinterpret_cast<const u32x4*>(tk + k_at[t] + 32 * c * DP);
     };
@@ -349,7 +347,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     }
     // The first values are on their way while the scores become weights.
     s16x4 vf[2][2][2];  // two dim blocks at a time
-    auto read_v = [&](int i) {
+    auto read_v = [&](int i) __attribute__((always_inline)) {
       const int n = i / (NB / 2), t0 = i % (NB / 2) * 2;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -451,7 +449,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     read_pages(k0);
     load(s_k0, s_v0, k0);
     store(s_k0, s_v0, 0, k0);
-    auto step = [&](uint16_t* k, uint16_t* v, uint16_t* next_k, uint16_t* next_v, int buf, int j0) {
+    auto step = [&](uint16_t* k, uint16_t* v, uint16_t* next_k, uint16_t* next_v, int buf, int j0) __attribute__((always_inline)) {
       const bool more = j0 + kTileKeys < k1;
       if (more) load(next_k, next_v, j0 + kTileKeys);
       if (j0 < w_hi && j0 + kTileKeys > w_lo) compute(k, v, buf, j0);
