@@ -624,7 +624,7 @@ Plan make_plan(const AttendProblem& p) {
   const int64_t group = p.q.heads / p.pool.heads, rows = p.max_new * group;
   r.tile = rows > 32;
   // Quantized rows are widened once per tile: 256 rows share that where there
-  // are more than 128 (the chunks below: 203 -> 188 us with int8, 447 -> 179
+  // are more than 128 (the chunks below: 137 -> 132 us with int8, 166 -> 135
   // with NF4); bf16 rows need none of it, and two smaller workgroups of a CU
   // overlap their matrix and vector phases.
   r.tile_rows = r.tile ? (rows > 128 && p.pool.type != kKVBF16 && p.pool.dim <= 128 ? 256 : 128) : rows > 16 && p.pool.dim <= 128 ? 32 : 16;
@@ -642,7 +642,8 @@ Plan make_plan(const AttendProblem& p) {
   // splits.  8 heads of 131071 NF4 keys: 43 + 4 us in 32 splits of eight waves,
   // 44 + 5.5 in 64 of four.  Tiles are long and uneven (a sequence's length, the
   // causal corner), so they want twice what the chip holds at once: 4 chunks of
-  // 300 to 512 tokens over 512 to 4608, int8, 185 us whole, 145 + 12 in two, 147 + 14 in three.
+  // 300 to 512 tokens over 512 to 4608, int8, 173 us whole, 132 + 12 in two,
+  // 140 + 14 in three.
   const int64_t full = !r.tile ? 128 : r.tile_rows == 256 ? 512 : 1024, want = !r.tile ? 256 : full;
   int64_t splits = work >= full ? 1 : std::min((want + work - 1) / work, span / (r.tile ? 256 : 512));
   splits = std::max<int64_t>(splits, 1);

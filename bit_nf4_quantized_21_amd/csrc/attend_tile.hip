@@ -84,7 +84,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   // start in the codes (bytes).
   __shared__ int s_page[kTileChunk / 16 + 1];
   __shared__ int64_t s_at[kTileChunk / 16 + 1];
-  __shared__ uint2 s_lut[BITS == 4 ? 256 : 1];
+  // Entries one after another: at 8 bytes each, pairs of bf16 met half of the
+  // banks (the chunks below in FP4: 151 us, so 141).
+  constexpr int LW = OP == kOpLevel ? 1 : 2;
+  __shared__ __align__(8) uint32_t s_lut[BITS == 4 ? 256 * LW : 1];
 
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h2 = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -96,7 +99,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   // keys to all of its tiles.  (Head by head, 52 heads of 4096 causal rows took
   // 20 % longer: 1.2 waves per SIMD on average, the last head's long tiles
   // alone.  Sequences as they come: 4 chunks of 300 to 512 tokens over 512 to
-  // 4608, int8, 157 us, 145 in this order.)
+  // 4608, int8, 157 us, 145 in this order (132 as it is now).)
   int id = (int)blockIdx.x, next = uniform_div(id, H);
   const int h = id - next * H;
   id = next;
@@ -134,7 +137,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
       x = (tid & 15) == e ? v : x;
       y = (tid >> 4) == e ? v : y;
     }
-    s_lut[tid] = OP == kOpLevel ? make_uint2(x | (y << 16), 0) : make_uint2(x, y);
+    if constexpr (OP == kOpLevel) s_lut[tid] = x | (y << 16);
+    else reinterpret_cast<uint2*>(s_lut)[tid] = make_uint2(x, y);
   }
 
   const int D = a.pool.dim;
@@ -239,7 +243,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
       const char* lut = reinterpret_cast<const char*>(s_lut);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const char* p = lut + lut_offset<8>(w[e / 4], e % 4);
+        const char* p = lut + lut_offset<4 * LW>(w[e / 4], e % 4);
         if constexpr (OP == kOpLevel) {
           out[e] = *reinterpret_cast<const uint32_t*>(p);
         } else {
