@@ -10,7 +10,7 @@
 // What bounds it: instructions and power.  Per tile and wave a bf16 cache takes
 // 32 MFMAs (1024 clocks), 204 vector instructions of which 32 are
 // exponentials, 53 LDS and 116 scalar ones; with two waves per SIMD the matrix
-// units are 42 % busy and the vector units about as much, at the 1.9 GHz that
+// units are 39 % busy and the vector units about as much, at the 1.9 to 2.0 GHz that
 // the chip then holds (with zeros for data it runs 12 % faster).  52 heads of
 // 4096 causal rows: 269 us, 830 TFLOP/s of what is seen (a dense product of
 // 8192^3 in bf16 runs at 1258 here).  Memory is not it: all keys from one page
