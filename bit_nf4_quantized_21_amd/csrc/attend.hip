@@ -634,18 +634,33 @@ Plan make_plan(const AttendProblem& p) {
   if (p.window > 0 && p.causal) span = std::min<int64_t>(span, (int64_t)p.window + r.tile_rows);
   span += 15;
   const int64_t work = std::max<int64_t>(1, (int64_t)p.batch * p.pool.heads * r.tiles);
-  // Splits cost a second launch and its partial sums (6 us at the least), so
-  // the keys are only split where too few workgroups would be left to fill the
-  // chip.  Streaming, 128 workgroups reach the memory's rate: 4 sequences of
-  // up to 1000 tokens, 32 heads, bf16, 16.0 us in one launch, 13.0 + 4.0 and
-  // the gap in two; 64 of up to 8192, 8 heads, int8, 145 us, 134 + 12 in four
-  // splits.  8 heads of 131071 NF4 keys: 43 + 4 us in 32 splits of eight waves,
-  // 44 + 5.5 in 64 of four.  Tiles are long and uneven (a sequence's length, the
-  // causal corner), so they want twice what the chip holds at once: 4 chunks of
-  // 300 to 512 tokens over 512 to 4608, int8, 173 us whole, 132 + 12 in two,
-  // 140 + 14 in three.
-  const int64_t full = !r.tile ? 128 : r.tile_rows == 256 ? 512 : 1024, want = !r.tile ? 256 : full;
-  int64_t splits = work >= full ? 1 : std::min((want + work - 1) / work, span / (r.tile ? 256 : 512));
+  // Splits cost a second launch and its partial sums (6 us at the least).
+  int64_t splits = 1;
+  if (r.tile) {
+    // Tiles are long and uneven (a sequence's length, the causal corner), so they
+    // want twice what the chip holds at once: 4 chunks of 300 to 512 tokens over
+    // 512 to 4608, int8, 173 us whole, 132 + 12 in two, 140 + 14 in three.
+    const int64_t full = r.tile_rows == 256 ? 512 : 1024;
+    if (work < full) splits = std::min((full + work - 1) / work, span / 256);
+  } else if (work < 128) {
+    // Streaming, one workgroup to a CU: 8 heads of 131071 NF4 keys 43 + 4 us in
+    // 32 splits of eight waves, 44 + 5.5 in 64 of four.
+    splits = std::min(256 / work, span / 512);
+  } else {
+    // A CU takes as long for two workgroups as for one twice as long (nearly), so
+    // the fullest CU's keys count, against the join: 1000 keys' time and 500 for
+    // each split's sums.  us in 1, 2, 3, 4 splits: 128 sequences and heads of 4000
+    // NF4 keys 36 27 35 30 (bf16 66 55 63 57), 145 of 7324 82 88 68 74, 320 of 4000
+    // 75 70 70 73, 512 of 500 to 4000 69 74 79 84, 128 of 200 to 1000, bf16, 16 17.
+    int64_t least = (work + 255) / 256 * span;
+    for (int64_t s = 2; s <= 4 && span / s >= 512; ++s) {
+      const int64_t keys = (work * s + 255) / 256 * (span / s) + 500 * (s + 1);
+      if (keys < least) {
+        least = keys;
+        splits = s;
+      }
+    }
+  }
   splits = std::max<int64_t>(splits, 1);
   // Eight waves to a workgroup where each has steps enough; four for short
   // sequences (those 4 of up to 1000 tokens: 16.1 us, 17.8 with eight).
