@@ -399,6 +399,14 @@ def test_split_and_whole_sequences_together(hq, h, n, kv):
     b.check(*b.run(causal=False), causal=False)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "nf4"])
+def test_a_long_context_beside_short_ones(kv):
+    """Many splits of one sequence (a workgroup joins each row), one of the others'."""
+    b = Batch([(1, 20000), (1, 5), (1, 512), (2, 700), (0, 30), (2, 1)], 4, 2, 64, kv, 128, seed=10)
+    b.check(*b.run())
+    b.check(*b.run(window=9000), window=9000)
+
+
 @pytest.mark.parametrize("n,batch", [(1, 70), (40, 64), (40, 65)])
 def test_many_sequences(n, batch):
     seqs = [(n, n + (37 * i) % 90) for i in range(batch)]
