@@ -101,16 +101,6 @@ enum Operand { kOpBF16, kOpINT8, kOpLevel, kOpLevel2 };
 template <int KT>
 constexpr int kBitsOf = KT == kOpBF16 ? 16 : KT == kOpINT8 ? 8 : 4;
 
-// SIZE times byte q of x (one instruction once compiled).  Not the inline
-// assembly of the linear layers' lookups: its writes are no vector instructions
-// to the compiler's hazard checks, and here its target may be a register that a
-// matrix instruction still reads as its addend (wrong sums now and then with
-// 256-wide heads).
-template <int SIZE>
-__device__ __forceinline__ uint32_t lut_offset(uint32_t x, int q) {
-  return ((x >> (8 * q)) & 255u) * SIZE;
-}
-
 // 8 consecutive int8 codes -> 8 bf16 (exact).
 __device__ __forceinline__ bf16x8 int8_to_bf16x8(uint32_t a, uint32_t b) {
   float f[8];

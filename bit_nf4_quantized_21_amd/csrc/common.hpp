@@ -156,63 +156,14 @@ __device__ __forceinline__ void buf_load16_to_lds(rsrc_t r, void* lds_block, uin
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)lds_block, 16, (int)off, 0, 0, 0);
 }
 
-// v_bfe_u32 with constant offset / width, kept as one instruction (the
-// compiler otherwise splits some extracts into a shift and a mask).
-template <int OFF, int W>
-__device__ __forceinline__ uint32_t bfe(uint32_t x) {
-  uint32_t r;
-  asm("v_bfe_u32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "i"(OFF), "i"(W));
-  return r;
-}
-
-// Byte q (0..3, a constant once unrolled) of x, by one v_bfe_u32.
-__device__ __forceinline__ uint32_t bfe8(uint32_t x, int q) {
-  switch (q) {
-    case 0: return bfe<0, 8>(x);
-    case 1: return bfe<8, 8>(x);
-    case 2: return bfe<16, 8>(x);
-    default: return bfe<24, 8>(x);
-  }
-}
-
-// Codebook values of the 8 codes of a dword, element e = nibble e, from the
-// 16-entry fp32 table at LDS address 0 (`lds` points there): byte q of
-// (x << 2) & 0x3C3C3C3C is 4 * code(2q), of (x >> 2) & 0x3C3C3C3C is
-// 4 * code(2q + 1), so each lookup address is one bitfield extract.
-__device__ __forceinline__ void lut8_lds0(const unsigned char* lds, uint32_t x, float (&f)[8]) {
-  const uint32_t y4 = (x << 2) & 0x3C3C3C3Cu, z4 = (x >> 2) & 0x3C3C3C3Cu;
-  f[0] = *reinterpret_cast<const float*>(lds + bfe<0, 8>(y4));
-  f[1] = *reinterpret_cast<const float*>(lds + bfe<0, 8>(z4));
-  f[2] = *reinterpret_cast<const float*>(lds + bfe<8, 8>(y4));
-  f[3] = *reinterpret_cast<const float*>(lds + bfe<8, 8>(z4));
-  f[4] = *reinterpret_cast<const float*>(lds + bfe<16, 8>(y4));
-  f[5] = *reinterpret_cast<const float*>(lds + bfe<16, 8>(z4));
-  f[6] = *reinterpret_cast<const float*>(lds + bfe<24, 8>(y4));
-  f[7] = *reinterpret_cast<const float*>(lds + bfe<24, 8>(z4));
-}
-
-// 8 * byte q of x (q = 0..3, a constant once unrolled) in one VALU
-// instruction: a shift whose source operand selects the byte (SDWA).
-template <int Q>
-__device__ __forceinline__ uint32_t byte_x8(uint32_t x) {
-  uint32_t r;
-  if constexpr (Q == 0)
-    asm("v_lshlrev_b32_sdwa %0, 3, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_0" : "=v"(r) : "v"(x));
-  else if constexpr (Q == 1)
-    asm("v_lshlrev_b32_sdwa %0, 3, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_1" : "=v"(r) : "v"(x));
-  else if constexpr (Q == 2)
-    asm("v_lshlrev_b32_sdwa %0, 3, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_2" : "=v"(r) : "v"(x));
-  else
-    asm("v_lshlrev_b32_sdwa %0, 3, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_3" : "=v"(r) : "v"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t byte_x8(uint32_t x, int q) {
-  switch (q) {
-    case 0: return byte_x8<0>(x);
-    case 1: return byte_x8<1>(x);
-    case 2: return byte_x8<2>(x);
-    default: return byte_x8<3>(x);
-  }
+// SIZE times byte q of x (q = 0..3, a constant once unrolled): once compiled a
+// shift whose source operand selects the byte (the highest one takes a shift
+// and a mask).  Left to the compiler and not written as inline assembly: the hazard checks do not see
+// into assembly, and the target may be a register that a matrix instruction
+// issued just before still reads as its addend (wrong sums now and then).
+template <int SIZE>
+__device__ __forceinline__ uint32_t lut_offset(uint32_t x, int q) {
+  return ((x >> (8 * q)) & 255u) * SIZE;
 }
 
 // Pair table of the codebook at LDS address 0: entry b (b = one code byte,
@@ -250,7 +201,7 @@ __device__ __forceinline__ void pair_table_from_arg(unsigned char* lds, const Co
 __device__ __forceinline__ void lut8_pairs(const unsigned char* lds, uint32_t x, float (&f)[8]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const float2 v = *reinterpret_cast<const float2*>(lds + byte_x8(x, q));
+    const float2 v = *reinterpret_cast<const float2*>(lds + lut_offset<8>(x, q));
     f[2 * q] = v.x;
     f[2 * q + 1] = v.y;
   }

@@ -210,7 +210,7 @@ __global__ __launch_bounds__(256, 1) void gemm_dx_kernel(DxGemmParams p, Codeboo
     if constexpr (U_ >= 0 && g_ < 32 && (3 * g_) / 2 == U_) {                                          \
       constexpr int u_ = g_ >> 2, w_ = g_ & 3, hf_ = u_ >> 2, pr_ = u_ & 3;                            \
       constexpr int rs_ = w_ >> 1, b_ = w_ & 1;                                                        \
-      const float2 v_ = *reinterpret_cast<const float2*>(smem + byte_x8(CODES[2 * pr_ + rs_], 2 * hf_ + b_)); \
+      const float2 v_ = *reinterpret_cast<const float2*>(smem + lut_offset<8>(CODES[2 * pr_ + rs_], 2 * hf_ + b_)); \
       fp[u_][4 * rs_ + 2 * b_] = v_.x;                                                                 \
       fp[u_][4 * rs_ + 2 * b_ + 1] = v_.y;                                                             \
     }                                                                                                  \

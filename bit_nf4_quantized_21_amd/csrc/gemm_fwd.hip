@@ -217,7 +217,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fwd_kernel(FwdGemmParams p, Codeb
       if (i < 8) {                                                                                    \
         XNXT[i] = *reinterpret_cast<const bf16x8*>(xs_ + i * 4096);                                  \
         const int g_ = i >> 2, q_ = i & 3;                                                            \
-        const float2 v_ = *reinterpret_cast<const float2*>(tbl + byte_x8(CA[g_][S], q_));            \
+        const float2 v_ = *reinterpret_cast<const float2*>(tbl + lut_offset<8>(CA[g_][S], q_));            \
         fp[g_][2 * q_] = v_.x;                                                                        \
         fp[g_][2 * q_ + 1] = v_.y;                                                                    \
       } else {                                                                                        \
