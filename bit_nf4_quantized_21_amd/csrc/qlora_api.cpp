@@ -537,7 +537,7 @@ int check_attend(const qlora_kv_cache* cache, bool buffers, int64_t tokens, int3
   p->tokens = tokens;
   p->q.heads = q_heads;
   p->batch = batch;
-  p->width = pages_per_seq;
+  p->width = max_len > 0 ? pages_per_seq : 0;  // nothing stored: the table may be null, no entry of it is read
   p->max_new = (int32_t)max_new;
   p->max_len = (int32_t)max_len;
   p->causal = causal;

@@ -494,7 +494,7 @@ int qlora_kv_read(const qlora_kv_cache* cache, int64_t T, const int64_t* slots, 
  *            heads a multiple of the cache's.
  *   batch    sequences;  starts [batch+1] and lengths [batch] int32 with
  *            starts[0] = 0 and starts[batch] = tokens.
- *   pages    [batch][pages_per_seq] int32.
+ *   pages    [batch][pages_per_seq] int32; may be NULL where max_len = 0.
  *   max_new, max_len  upper bounds of starts[b+1] - starts[b] and lengths[b]
  *            (the launch is sized by them; no call reads device memory on the
  *            host); a sequence beyond them is cut and reported as

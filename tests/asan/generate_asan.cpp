@@ -269,6 +269,27 @@ static void check_attend() {
   a.c.dim = 24; EXPECT(a.need() == 0);
 }
 
+// Nothing is stored: no table of pages is needed, however many pages a sequence
+// may have, and the kernels are told of no entry that they could read.
+static void check_nothing_stored() {
+  for (int64_t width : {0, 1, 4, 1000})
+    for (int64_t window : {0, 5})
+      for (int64_t n : {1, 100}) {
+        Attend a;
+        a.pages = nullptr;
+        a.width = width;
+        a.max_len = 0;
+        a.window = window;
+        a.tokens = 2 * n;
+        a.max_new = n;
+        LAUNCHED(a.run());
+        EXPECT(attended.width == 0 && attended.max_len == 0);
+        a.pages = at<int32_t>(kAddr);
+        LAUNCHED(a.run());
+        EXPECT(attended.width == 0);
+      }
+}
+
 // A query over many shapes: it answers (0 or a size), and a size is enough for
 // the call of the same shape.
 static void check_workspace() {
@@ -300,6 +321,7 @@ int main() {
   check_rope();
   check_cache();
   check_attend();
+  check_nothing_stored();
   check_workspace();
   if (failures) {
     fprintf(stderr, "%d expectation(s) failed\n", failures);
