@@ -7,7 +7,7 @@ from __future__ import annotations
 
 import ctypes
 
-from .qlora import Heads, KVCacheDesc, _check, _dev, _need, _p, _stream, _torch, _workspace, lib
+from .qlora import Heads, KVCacheDesc, _check, _dev, _empty, _need, _p, _stream, _torch, _workspace, lib
 
 KV_TYPES = {"bf16": 0, "int8": 1, "nf4": 2, "int4": 3, "fp4": 4}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3}
@@ -39,10 +39,9 @@ def _heads(t, name):
     return Heads(t.data_ptr(), st if n > 1 else 0, sh if h > 1 else 0, h)
 
 
-def _new_heads(like):
+def _new_heads(like, stream):
     """A contiguous tensor like this one, and its view."""
-    torch = _torch()
-    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    t = _empty(like.shape, like.dtype, like.device, stream)
     _, heads, dim = t.shape
     return t, Heads(t.data_ptr(), heads * dim, dim, heads)
 
@@ -60,7 +59,7 @@ def rope_table(positions, rot, base=10000.0, scaling="none", factor=1.0, origina
     that turn at least `high` times over `original` positions keep their
     frequency, those that turn at most `low` times get it divided)."""
     torch = _torch()
-    table = torch.empty(positions, rot // 2, 2, dtype=torch.float32, device=device)
+    table = _empty((positions, rot // 2, 2), torch.float32, device, stream)
     _check(lib().qlora_rope_table(positions, rot, float(base), _choice(ROPE_SCALINGS, scaling, "scaling"),
                                   float(factor), float(original), float(low), float(high), float(amplitude),
                                   _p(table), _stream(stream)))
@@ -89,7 +88,7 @@ def rope(q, k, table, positions, layout="half", inverse=False, q_out=None, k_out
     rows, rot = _table(table, positions, T)
     qv = _heads(q, "q")
     if q_out is None:
-        q_out, qo = _new_heads(q)
+        q_out, qo = _new_heads(q, stream)
     else:
         qo = _heads(q_out, "q_out")
     kv = ko = None
@@ -98,7 +97,7 @@ def rope(q, k, table, positions, layout="half", inverse=False, q_out=None, k_out
             raise ValueError("q and k must have the same tokens and dim")
         kv = _heads(k, "k")
         if k_out is None:
-            k_out, ko = _new_heads(k)
+            k_out, ko = _new_heads(k, stream)
         else:
             ko = _heads(k_out, "k_out")
         if k_out.shape != k.shape:
@@ -175,11 +174,11 @@ def kv_read(cache, slots, k_out=None, v_out=None, stream=None):
     _dev(slots, torch.int64, "slots")
     shape = (T, cache.heads, cache.dim)
     if k_out is None:
-        k_out = cache.k.new_empty(shape, dtype=torch.bfloat16)
+        k_out = _empty(shape, torch.bfloat16, cache.k.device, stream)
     else:
         _need(_dev(k_out, torch.bfloat16, "k_out"), T * cache.heads * cache.dim, "k_out")
     if v_out is None:
-        v_out = cache.k.new_empty(shape, dtype=torch.bfloat16)
+        v_out = _empty(shape, torch.bfloat16, cache.k.device, stream)
     else:
         _need(_dev(v_out, torch.bfloat16, "v_out"), T * cache.heads * cache.dim, "v_out")
     _check(lib().qlora_kv_read(cache._desc, T, slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), _stream(stream)))
@@ -213,17 +212,17 @@ def attend_paged(q, cache, pages, starts, lengths, max_new, max_len, scale=None,
     _index(starts, B + 1, torch.int32, "starts")
     _dev(lengths, torch.int32, "lengths")
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     else:
         _need(_dev(out, torch.bfloat16, "out"), T * Hq * D, "out")
     if lse is True:
-        lse = q.new_empty((T, Hq), dtype=torch.float32)
+        lse = _empty((T, Hq), torch.float32, q.device, stream)
     elif lse is False or lse is None:
         lse = None
     else:
         _need(_dev(lse, torch.float32, "lse"), T * Hq, "lse")
     nbytes = attend_paged_workspace_bytes(cache, T, Hq, B, max_new, max_len, causal, window)
-    workspace = _workspace(nbytes, q.device, workspace)
+    workspace = _workspace(nbytes, q.device, workspace, stream)
     _check(lib().qlora_attend_paged(cache._desc, T, _heads(q, "q"), B, pages.data_ptr(), pages.shape[1],
                                     starts.data_ptr(), lengths.data_ptr(), max_new, max_len,
                                     D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),

@@ -5,6 +5,12 @@ and the current HIP stream; every step of the computation runs in the
 library's kernels.  The library is loaded from this package directory and
 must have been built (python -m bit_nf4_quantized_21_amd.build); there is no
 fallback of any kind.
+
+Every call takes a `stream` (default: the current one).  What a call allocates
+itself, outputs and workspace, is safe to use and to drop on the current stream
+as on that one.  Inputs and given buffers are the caller's: work of another
+stream on them has to be waited for before the call, and they have to be kept
+(or recorded) until the call's stream has used them.
 """
 
 from __future__ import annotations
@@ -189,6 +195,25 @@ def _stream(stream=None):
     return C._cuda_getCurrentRawStream(C._cuda_getDevice())
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on `stream` (None: the current one) to write.
+
+    The allocator hands a freed block out again in the order of the stream it
+    was allocated on.  So the block comes from the call's own stream: one of the
+    current stream's could still be read by work queued there, and once dropped
+    it would be given away while the call still writes it.  The caller goes on
+    on the current stream, so the block also stays until what is queued there
+    when it is dropped has run."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    callers = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(callers)
+    return t
+
+
 def device_status(stream=None):
     """Raise QLoRAError if a kernel's bounded wait ran out since the last
     query (waits for the stream; clears the status)."""
@@ -238,8 +263,8 @@ def quantize_nf4(W, codes=None, absmax=None, stream=None, qtype="nf4"):
     _dev(W, torch.bfloat16 if bf16 else torch.float32, "W")
     n = W.numel()
     nb = (n + 63) // 64
-    codes = torch.empty(n // 2, dtype=torch.uint8, device=W.device) if codes is None else codes
-    absmax = torch.empty(nb, dtype=torch.float32, device=W.device) if absmax is None else absmax
+    codes = _empty(n // 2, torch.uint8, W.device, stream) if codes is None else codes
+    absmax = _empty(nb, torch.float32, W.device, stream) if absmax is None else absmax
     _need(_dev(codes, torch.uint8, "codes"), n // 2, "codes")
     _need(_dev(absmax, torch.float32, "absmax"), nb, "absmax")
     _check(lib().qlora_quantize_4bit(_p(W), 1 if bf16 else 0, n, 64, _qtype(qtype), _p(codes), _p(absmax),
@@ -256,9 +281,9 @@ def quantize_dq(W, qtype="nf4", codes=None, q8=None, s2=None, stream=None):
     n = W.numel()
     nb = (n + 63) // 64
     ng = (nb + 255) // 256
-    codes = torch.empty(n // 2, dtype=torch.uint8, device=W.device) if codes is None else codes
-    q8 = torch.empty(nb, dtype=torch.uint8, device=W.device) if q8 is None else q8
-    s2 = torch.empty(ng, dtype=torch.float32, device=W.device) if s2 is None else s2
+    codes = _empty(n // 2, torch.uint8, W.device, stream) if codes is None else codes
+    q8 = _empty(nb, torch.uint8, W.device, stream) if q8 is None else q8
+    s2 = _empty(ng, torch.float32, W.device, stream) if s2 is None else s2
     _need(_dev(codes, torch.uint8, "codes"), n // 2, "codes")
     _need(_dev(q8, torch.uint8, "q8"), nb, "q8")
     _need(_dev(s2, torch.float32, "s2"), ng, "s2")
@@ -273,8 +298,8 @@ def double_quant(absmax, q8=None, s2=None, stream=None):
     _dev(absmax, torch.float32, "absmax")
     nb = absmax.numel()
     ng = (nb + 255) // 256
-    q8 = torch.empty(nb, dtype=torch.uint8, device=absmax.device) if q8 is None else q8
-    s2 = torch.empty(ng, dtype=torch.float32, device=absmax.device) if s2 is None else s2
+    q8 = _empty(nb, torch.uint8, absmax.device, stream) if q8 is None else q8
+    s2 = _empty(ng, torch.float32, absmax.device, stream) if s2 is None else s2
     _dev(q8, torch.uint8, "q8")
     _dev(s2, torch.float32, "s2")
     if q8.numel() < nb or s2.numel() < ng:
@@ -292,7 +317,7 @@ def dequantize_nf4(codes, q8, s2, n, dtype=None, out=None, stream=None, qtype="n
     _dev(codes, torch.uint8, "codes")
     _dev(q8, torch.uint8, "q8")
     _dev(s2, torch.float32, "s2")
-    out = torch.empty(n, dtype=dtype, device=codes.device) if out is None else out
+    out = _empty(n, dtype, codes.device, stream) if out is None else out
     _dev(out, dtype, "out")
     _need(codes, n // 2, "codes")
     _need(q8, (n + 63) // 64, "q8")
@@ -311,9 +336,10 @@ def linear_bwd_workspace_bytes(T, K, N, r):
     return int(lib().qlora_linear_bwd_workspace_bytes(T, K, N, r))
 
 
-def _workspace(nbytes, device, ws):
+def _workspace(nbytes, device, ws, stream=None):
     """The caller's workspace if given (the library checks its size), else a
-    new one of the size the library asks for."""
+    new one of the size the library asks for, from the memory of the call's
+    stream (see _empty)."""
     torch = _torch()
     if ws is not None:
         _dev(ws, torch.uint8, "workspace")
@@ -322,7 +348,10 @@ def _workspace(nbytes, device, ws):
         return ws
     if nbytes == 0:
         return None
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def linear_fwd(X, codes, q8, s2, A, B, alpha, N, Y=None, XA=None, workspace=None, stream=None, qtype="nf4"):
@@ -339,12 +368,12 @@ def linear_fwd(X, codes, q8, s2, A, B, alpha, N, Y=None, XA=None, workspace=None
     if A.shape != (K, r) or B.shape != (r, N):
         raise ValueError("A must be [K,r] and B [r,N]")
     _weight(codes, q8, s2, N, K)
-    Y = torch.empty(T, N, dtype=torch.bfloat16, device=X.device) if Y is None else Y
-    XA = torch.empty(T, r, dtype=torch.float32, device=X.device) if XA is None else XA
+    Y = _empty((T, N), torch.bfloat16, X.device, stream) if Y is None else Y
+    XA = _empty((T, r), torch.float32, X.device, stream) if XA is None else XA
     _need(_dev(Y, torch.bfloat16, "Y"), T * N, "Y")
     _need(_dev(XA, torch.float32, "XA"), T * r, "XA")
     nbytes = linear_fwd_workspace_bytes(T, K, N, r)
-    workspace = _workspace(nbytes, X.device, workspace)
+    workspace = _workspace(nbytes, X.device, workspace, stream)
     _check(lib().qlora_linear_fwd_4bit(_qtype(qtype), _p(X), T, K, N, _p(codes), _p(q8), _p(s2), _p(A), _p(B), r,
                                        float(alpha), _p(Y), _p(XA), _p(workspace), nbytes, _stream(stream)))
     return Y, XA
@@ -408,8 +437,8 @@ def linear_fwd_grouped(layers, alpha, T, r, workspace=None, stream=None, qtype="
         _weight(codes, q8, s2, N, K)
         Y = L.get("Y")
         XA = L.get("XA")
-        Y = torch.empty(T, N, dtype=torch.bfloat16, device=X.device) if Y is None else Y
-        XA = torch.empty(T, r, dtype=torch.float32, device=X.device) if XA is None else XA
+        Y = _empty((T, N), torch.bfloat16, X.device, stream) if Y is None else Y
+        XA = _empty((T, r), torch.float32, X.device, stream) if XA is None else XA
         _need(_dev(Y, torch.bfloat16, "Y"), T * N, "Y")
         _need(_dev(XA, torch.float32, "XA"), T * r, "XA")
         descs[i] = LinearDesc(X.data_ptr(), codes.data_ptr(), q8.data_ptr(), s2.data_ptr(), A.data_ptr(),
@@ -418,7 +447,7 @@ def linear_fwd_grouped(layers, alpha, T, r, workspace=None, stream=None, qtype="
     n = len(layers)
     nbytes = int(lib().qlora_linear_fwd_grouped_workspace_bytes(n, descs, T, r))
     dev = layers[0]["X"].device if layers else "cuda"
-    workspace = _workspace(nbytes, dev, workspace)
+    workspace = _workspace(nbytes, dev, workspace, stream)
     _check(lib().qlora_linear_fwd_grouped(_qtype(qtype), n, descs, T, r, float(alpha), _p(workspace), nbytes,
                                           _stream(stream)))
     return outs
@@ -448,9 +477,9 @@ def linear_bwd_grouped(layers, alpha, T, r, workspace=None, stream=None, qtype="
         dX = L.get("dX")
         dA = L.get("dA")
         dB = L.get("dB")
-        dX = torch.empty(T, K, dtype=torch.bfloat16, device=X.device) if dX is None else dX
-        dA = torch.empty(K, r, dtype=torch.bfloat16, device=X.device) if dA is None else dA
-        dB = torch.empty(r, N, dtype=torch.bfloat16, device=X.device) if dB is None else dB
+        dX = _empty((T, K), torch.bfloat16, X.device, stream) if dX is None else dX
+        dA = _empty((K, r), torch.bfloat16, X.device, stream) if dA is None else dA
+        dB = _empty((r, N), torch.bfloat16, X.device, stream) if dB is None else dB
         for t, nm, n in ((dX, "dX", T * K), (dA, "dA", K * r), (dB, "dB", r * N)):
             _need(_dev(t, torch.bfloat16, nm), n, nm)
         descs[i] = LinearBwdDesc(dY.data_ptr(), X.data_ptr(), XA.data_ptr(), codes.data_ptr(), q8.data_ptr(),
@@ -460,7 +489,7 @@ def linear_bwd_grouped(layers, alpha, T, r, workspace=None, stream=None, qtype="
     n = len(layers)
     nbytes = int(lib().qlora_linear_bwd_grouped_workspace_bytes(n, descs, T, r))
     dev = layers[0]["X"].device if layers else "cuda"
-    workspace = _workspace(nbytes, dev, workspace)
+    workspace = _workspace(nbytes, dev, workspace, stream)
     _check(lib().qlora_linear_bwd_grouped(_qtype(qtype), n, descs, T, r, float(alpha), _p(workspace), nbytes,
                                           _stream(stream)))
     return outs
@@ -485,13 +514,13 @@ def linear_bwd(dY, X, XA, codes, q8, s2, A, B, alpha, dX=None, dA=None, dB=None,
     if A.shape != (K, r) or B.shape != (r, N) or dY.shape[0] != T or (XA is not None and XA.shape != (T, r)):
         raise ValueError("shape mismatch")
     _weight(codes, q8, s2, N, K)
-    dX = torch.empty(T, K, dtype=torch.bfloat16, device=X.device) if dX is None else dX
-    dA = torch.empty(K, r, dtype=torch.bfloat16, device=X.device) if dA is None else dA
-    dB = torch.empty(r, N, dtype=torch.bfloat16, device=X.device) if dB is None else dB
+    dX = _empty((T, K), torch.bfloat16, X.device, stream) if dX is None else dX
+    dA = _empty((K, r), torch.bfloat16, X.device, stream) if dA is None else dA
+    dB = _empty((r, N), torch.bfloat16, X.device, stream) if dB is None else dB
     for t, nm, n in ((dX, "dX", T * K), (dA, "dA", K * r), (dB, "dB", r * N)):
         _need(_dev(t, torch.bfloat16, nm), n, nm)
     nbytes = linear_bwd_workspace_bytes(T, K, N, r)
-    workspace = _workspace(nbytes, X.device, workspace)
+    workspace = _workspace(nbytes, X.device, workspace, stream)
     _check(lib().qlora_linear_bwd_4bit(_qtype(qtype), _p(dY), _p(X), _p(XA), T, K, N, _p(codes), _p(q8), _p(s2),
                                        _p(A), _p(B), r, float(alpha), _p(dX), _p(dA), _p(dB), _p(workspace), nbytes,
                                        _stream(stream)))
@@ -522,9 +551,9 @@ def load_4bit(path, device="cuda", stream=None):
     torch = _torch()
     qtype, N, K = load_4bit_info(path)
     nb = (N * K + 63) // 64
-    codes = torch.empty(N * K // 2, dtype=torch.uint8, device=device)
-    q8 = torch.empty(nb, dtype=torch.uint8, device=device)
-    s2 = torch.empty((nb + 255) // 256, dtype=torch.float32, device=device)
+    codes = _empty(N * K // 2, torch.uint8, device, stream)
+    q8 = _empty(nb, torch.uint8, device, stream)
+    s2 = _empty((nb + 255) // 256, torch.float32, device, stream)
     _check(lib().qlora_load_4bit(os.fsencode(path), _qtype(qtype), N, K, _p(codes), _p(q8), _p(s2),
                                  _stream(stream)))
     return codes, q8, s2, qtype, N, K
@@ -554,7 +583,7 @@ def adamw_step(param, master, m, v, grad, step, lr, beta1=0.9, beta2=0.999, eps=
     if grad_norm_out is not None:
         _dev(grad_norm_out, torch.float32, "grad_norm_out")
     nbytes = adamw_workspace_bytes(n)
-    workspace = _workspace(nbytes, param.device, workspace)
+    workspace = _workspace(nbytes, param.device, workspace, stream)
     _check(lib().qlora_adamw_step(n, _p(param), _p(master), _p(m), _p(v), _p(grad), int(step), float(lr),
                                   float(beta1), float(beta2), float(eps), float(weight_decay), float(max_grad_norm),
                                   _p(grad_norm_out), _p(workspace), nbytes, _stream(stream)))

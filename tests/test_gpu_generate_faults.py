@@ -5,7 +5,7 @@ import ctypes
 
 import pytest
 
-from test_gpu_generate import _i32, _lib
+from test_gpu_generate import Batch, _dev, _i32, _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,85 @@ def test_nothing_stored_needs_no_table_of_pages(n, kv):
         out.fill_(7.0)
         lse.zero_()
     lib.device_status()
+
+
+def _busy(cycles=200_000_000):
+    """Keep the current stream at work for a while."""
+    torch.cuda._sleep(cycles)
+
+
+def test_workspace_and_outputs_of_a_call_on_another_stream():
+    """A block that work queued on the current stream still has to read is not
+    taken by a call on another stream, and an output dropped on the current
+    stream is not given to the other stream's next call before that work ran."""
+    lib = _lib()
+    b = Batch([(1, 4000), (1, 1), (1, 2047)], 8, 2, 128, "int8", 64, seed=5, pad=3)
+    want, want_lse = (t.clone() for t in b.run())
+    q = _dev(b.q)
+    nbytes = lib.attend_paged_workspace_bytes(b.cache, 3, 8, 3, **b.bounds)
+    assert nbytes > 0
+    side = torch.cuda.Stream()
+    sizes = (nbytes, want.numel() * 2, want_lse.numel() * 4)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = [torch.full((n,), 3, dtype=torch.uint8, device="cuda") for n in sizes]
+    side.wait_stream(torch.cuda.current_stream())
+    _busy()
+    copies = [t.clone() for t in held]
+    del held
+    out, lse = b.run(q=q, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert all(bool((c == 3).all()) for c in copies)
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, want_lse)
+
+    torch.cuda.current_stream().wait_stream(side)
+    _busy()
+    copy = out.clone()
+    del out, lse
+    other, _ = b.run(q=-q, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(copy.view(torch.int16), want.view(torch.int16))
+    assert not torch.equal(other.view(torch.int16), want.view(torch.int16))
+
+
+def test_other_calls_on_another_stream():
+    """Rotation, cache and linear calls with stream=: what they allocate is not
+    what the current stream still reads."""
+    lib = _lib()
+    side = torch.cuda.Stream()
+    T, K, N, r = 64, 512, 512, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.randn(N, K, generator=g, device="cuda") * 0.02
+    x = torch.randn(T, K, generator=g, device="cuda").bfloat16()
+    a, bb = (torch.randn(*s, generator=g, device="cuda").bfloat16() for s in ((K, r), (r, N)))
+    heads = x.view(T, 4, 128)
+    table, pos = lib.rope_table(64, 128), _i32(range(T))
+    cache = lib.KVCache.empty(5, 4, 16, 128)
+    slots = torch.arange(T, device="cuda")
+    lib.kv_write(cache, heads, heads, slots)
+    codes, q8, s2 = lib.quantize_dq(w)
+
+    def calls(**kw):
+        codes1, q81, s21 = lib.quantize_dq(w, **kw)
+        y, xa = lib.linear_fwd(x, codes, q8, s2, a, bb, 16.0, N, **kw)
+        grads = lib.linear_bwd(y, x, xa, codes, q8, s2, a, bb, 16.0, **kw)
+        turned, _ = lib.rope(heads, None, table, pos, **kw)
+        return (codes1, q81, s21, y, xa, *grads, turned, *lib.kv_read(cache, slots, **kw), lib.rope_table(64, 128, **kw),
+                lib.dequantize_nf4(codes, q8, s2, N * K, **kw))
+
+    want = calls()
+    sizes = [t.numel() * t.element_size() for t in want]
+    sizes += [lib.linear_fwd_workspace_bytes(T, K, N, r), lib.linear_bwd_workspace_bytes(T, K, N, r)]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = [torch.full((max(1, n),), 3, dtype=torch.uint8, device="cuda") for n in sizes]
+    side.wait_stream(torch.cuda.current_stream())
+    _busy()
+    copies = [t.clone() for t in held]
+    del held
+    got = calls(stream=side)
+    torch.cuda.synchronize()
+    assert all(bool((c == 3).all()) for c in copies)
+    for t, u in zip(got, want):
+        assert torch.equal(t.view(torch.uint8), u.view(torch.uint8))

@@ -1,0 +1,61 @@
+"""Where the bindings allocate (CPU only): every tensor that a call makes for
+itself comes from the memory of the stream that the call runs on."""
+
+import ast
+import contextlib
+import os
+
+import pytest
+
+from bit_nf4_quantized_21_amd import generate, qlora
+
+torch = pytest.importorskip("torch")
+
+
+class _Stream:
+    device = "a device"
+
+
+def _trace(monkeypatch):
+    inside, events = [], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        inside.append(s)
+        yield
+        inside.pop()
+
+    class Tensor:
+        def record_stream(self, s):
+            events.append(("record", s))
+
+    def empty(*_, **__):
+        events.append(("empty", inside[-1] if inside else None))
+        return Tensor()
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: ("current", device))
+    monkeypatch.setattr(torch, "empty", empty)
+    return events
+
+
+def test_allocations_follow_the_calls_stream(monkeypatch):
+    events, s = _trace(monkeypatch), _Stream()
+    qlora._workspace(16, "cuda", None, s)
+    assert events == [("empty", s)]
+    del events[:]
+    qlora._empty((2, 3), torch.float32, "cuda", s)
+    assert events == [("empty", s), ("record", ("current", "a device"))]
+    del events[:]
+    qlora._workspace(16, "cuda", None)
+    qlora._empty((2, 3), torch.float32, "cuda", None)
+    assert events == [("empty", None)] * 2
+
+
+@pytest.mark.parametrize("module", [qlora, generate])
+def test_no_call_allocates_elsewhere(module):
+    allocators = {"empty", "empty_like", "new_empty", "zeros", "zeros_like", "new_zeros", "full", "contiguous", "clone", "to"}
+    tree = ast.parse(open(os.path.abspath(module.__file__)).read())
+    for f in ast.walk(tree):
+        if isinstance(f, ast.FunctionDef) and f.name not in ("_empty", "_workspace") and "stream" in [a.arg for a in f.args.args]:
+            used = {n.func.attr for n in ast.walk(f) if isinstance(n, ast.Call) and isinstance(n.func, ast.Attribute)}
+            assert not used & allocators, f.name
