@@ -4,7 +4,6 @@
 
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <string>
@@ -476,7 +475,9 @@ int check_heads(const qlora_heads* h, qlora::HeadsView* out) {
   if (!h) return QLORA_ERR_NULL;
   if (h->heads < 1 || h->heads > (1 << 16)) return QLORA_ERR_SHAPE;
   if (h->token_stride % 8 != 0 || h->head_stride % 8 != 0) return QLORA_ERR_ALIGN;
-  if (std::llabs(h->token_stride) > (int64_t(1) << 32) || std::llabs(h->head_stride) > (int64_t(1) << 32))
+  constexpr int64_t kMaxStride = int64_t(1) << 32;
+  if (h->token_stride > kMaxStride || h->token_stride < -kMaxStride || h->head_stride > kMaxStride ||
+      h->head_stride < -kMaxStride)
     return QLORA_ERR_SHAPE;
   if (!h->data) return QLORA_ERR_NULL;
   if (!aligned16(h->data)) return QLORA_ERR_ALIGN;
@@ -531,7 +532,7 @@ int check_attend(const qlora_kv_cache* cache, bool buffers, int64_t tokens, int3
     return QLORA_ERR_SHAPE;
   if (q_heads < 1 || q_heads > (1 << 16) || q_heads % cache->heads != 0) return QLORA_ERR_SHAPE;
   if (causal != 0 && causal != 1) return QLORA_ERR_UNSUPPORTED;
-  if (pages_per_seq < 0 || (pages_per_seq << p->pool.shift) < max_len || pages_per_seq > kMaxTokens) return QLORA_ERR_SHAPE;
+  if (pages_per_seq < 0 || pages_per_seq > kMaxTokens || (pages_per_seq << p->pool.shift) < max_len) return QLORA_ERR_SHAPE;
   if (max_new > tokens) max_new = tokens;
   if (batch > 65535) return QLORA_ERR_SHAPE;
   p->tokens = tokens;

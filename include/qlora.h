@@ -368,7 +368,7 @@ int qlora_adamw_step(int64_t n, uint16_t* param, float* master, float* m, float*
  *
  * A view of [tokens, heads, dim] bf16 values whose dims are contiguous: a
  * tensor of its own or a part of a fused q/k/v output.  Strides are in
- * elements and multiples of 8 (a head starts on 16 bytes).
+ * elements, multiples of 8 (a head starts on 16 bytes) and at most 2^32 in size.
  */
 typedef struct {
   uint16_t* data; /* read only where a call says "in" */

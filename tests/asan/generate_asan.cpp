@@ -149,6 +149,12 @@ static void check_rope() {
   a = Args(); a.q.token_stride = 255; REFUSED(a.run(), QLORA_ERR_ALIGN);
   a = Args(); a.qo.head_stride = 60; REFUSED(a.run(), QLORA_ERR_ALIGN);
   for (int32_t h : {0, -1, INT32_MIN, INT32_MAX}) { a = Args(); a.q.heads = a.qo.heads = h; REFUSED(a.run(), QLORA_ERR_SHAPE); }
+  // Strides of more than 2^32 elements, the one whose magnitude int64 cannot hold among them.
+  for (int64_t s : {INT64_MIN, -(int64_t(1) << 33), int64_t(1) << 33, INT64_MAX - 7}) {
+    a = Args(); a.q.token_stride = s; REFUSED(a.run(), QLORA_ERR_SHAPE);
+    a = Args(); a.ko.head_stride = s; REFUSED(a.run(), QLORA_ERR_SHAPE);
+  }
+  a = Args(); a.q.token_stride = -(int64_t(1) << 32); a.k.head_stride = int64_t(1) << 32; LAUNCHED(a.run());
   a = Args(); a.qo.heads = 5; REFUSED(a.run(), QLORA_ERR_SHAPE);
   a = Args(); a.ko.heads = 5; REFUSED(a.run(), QLORA_ERR_SHAPE);
 }
@@ -243,6 +249,7 @@ static void check_attend() {
   }
   a.tokens = INT64_MAX; BAD(QLORA_ERR_SHAPE);
   a.max_len = INT64_MAX; BAD(QLORA_ERR_SHAPE);
+  for (int64_t w : {INT64_MAX, int64_t(1) << 60, int64_t(1) << 59, (int64_t(1) << 30) + 1}) { a.width = w; BAD(QLORA_ERR_SHAPE); }
   a.batch = -1; BAD(QLORA_ERR_SHAPE);
   a.batch = 1 << 17; BAD(QLORA_ERR_SHAPE);
   a.max_len = 65; BAD(QLORA_ERR_SHAPE);
