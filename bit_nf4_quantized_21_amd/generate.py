@@ -41,7 +41,9 @@ def _heads(t, name):
 
 def _new_heads(like, stream):
     """A contiguous tensor like this one, and its view."""
-    t = _empty(like.shape, like.dtype, like.device, stream)
+    torch = _torch()
+    t = (torch.empty_like(like, memory_format=torch.contiguous_format) if stream is None
+         else _empty(like.shape, like.dtype, like.device, stream))
     _, heads, dim = t.shape
     return t, Heads(t.data_ptr(), heads * dim, dim, heads)
 
@@ -174,11 +176,13 @@ def kv_read(cache, slots, k_out=None, v_out=None, stream=None):
     _dev(slots, torch.int64, "slots")
     shape = (T, cache.heads, cache.dim)
     if k_out is None:
-        k_out = _empty(shape, torch.bfloat16, cache.k.device, stream)
+        k_out = (cache.k.new_empty(shape, dtype=torch.bfloat16) if stream is None
+                 else _empty(shape, torch.bfloat16, cache.k.device, stream))
     else:
         _need(_dev(k_out, torch.bfloat16, "k_out"), T * cache.heads * cache.dim, "k_out")
     if v_out is None:
-        v_out = _empty(shape, torch.bfloat16, cache.k.device, stream)
+        v_out = (cache.k.new_empty(shape, dtype=torch.bfloat16) if stream is None
+                 else _empty(shape, torch.bfloat16, cache.k.device, stream))
     else:
         _need(_dev(v_out, torch.bfloat16, "v_out"), T * cache.heads * cache.dim, "v_out")
     _check(lib().qlora_kv_read(cache._desc, T, slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), _stream(stream)))
@@ -212,11 +216,12 @@ def attend_paged(q, cache, pages, starts, lengths, max_new, max_len, scale=None,
     _index(starts, B + 1, torch.int32, "starts")
     _dev(lengths, torch.int32, "lengths")
     if out is None:
-        out = _empty(q.shape, q.dtype, q.device, stream)
+        out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
+               else _empty(q.shape, q.dtype, q.device, stream))
     else:
         _need(_dev(out, torch.bfloat16, "out"), T * Hq * D, "out")
     if lse is True:
-        lse = _empty((T, Hq), torch.float32, q.device, stream)
+        lse = q.new_empty((T, Hq), dtype=torch.float32) if stream is None else _empty((T, Hq), torch.float32, q.device, stream)
     elif lse is False or lse is None:
         lse = None
     else:

@@ -206,10 +206,10 @@ def _empty(shape, dtype, device, stream):
     when it is dropped has run."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)   # (as a tuple 0.6 us more)
     callers = torch.cuda.current_stream(stream.device)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty(*shape, dtype=dtype, device=device)
     t.record_stream(callers)
     return t
 
@@ -263,8 +263,8 @@ def quantize_nf4(W, codes=None, absmax=None, stream=None, qtype="nf4"):
     _dev(W, torch.bfloat16 if bf16 else torch.float32, "W")
     n = W.numel()
     nb = (n + 63) // 64
-    codes = _empty(n // 2, torch.uint8, W.device, stream) if codes is None else codes
-    absmax = _empty(nb, torch.float32, W.device, stream) if absmax is None else absmax
+    codes = _empty((n // 2,), torch.uint8, W.device, stream) if codes is None else codes
+    absmax = _empty((nb,), torch.float32, W.device, stream) if absmax is None else absmax
     _need(_dev(codes, torch.uint8, "codes"), n // 2, "codes")
     _need(_dev(absmax, torch.float32, "absmax"), nb, "absmax")
     _check(lib().qlora_quantize_4bit(_p(W), 1 if bf16 else 0, n, 64, _qtype(qtype), _p(codes), _p(absmax),
@@ -281,9 +281,9 @@ def quantize_dq(W, qtype="nf4", codes=None, q8=None, s2=None, stream=None):
     n = W.numel()
     nb = (n + 63) // 64
     ng = (nb + 255) // 256
-    codes = _empty(n // 2, torch.uint8, W.device, stream) if codes is None else codes
-    q8 = _empty(nb, torch.uint8, W.device, stream) if q8 is None else q8
-    s2 = _empty(ng, torch.float32, W.device, stream) if s2 is None else s2
+    codes = _empty((n // 2,), torch.uint8, W.device, stream) if codes is None else codes
+    q8 = _empty((nb,), torch.uint8, W.device, stream) if q8 is None else q8
+    s2 = _empty((ng,), torch.float32, W.device, stream) if s2 is None else s2
     _need(_dev(codes, torch.uint8, "codes"), n // 2, "codes")
     _need(_dev(q8, torch.uint8, "q8"), nb, "q8")
     _need(_dev(s2, torch.float32, "s2"), ng, "s2")
@@ -298,8 +298,8 @@ def double_quant(absmax, q8=None, s2=None, stream=None):
     _dev(absmax, torch.float32, "absmax")
     nb = absmax.numel()
     ng = (nb + 255) // 256
-    q8 = _empty(nb, torch.uint8, absmax.device, stream) if q8 is None else q8
-    s2 = _empty(ng, torch.float32, absmax.device, stream) if s2 is None else s2
+    q8 = _empty((nb,), torch.uint8, absmax.device, stream) if q8 is None else q8
+    s2 = _empty((ng,), torch.float32, absmax.device, stream) if s2 is None else s2
     _dev(q8, torch.uint8, "q8")
     _dev(s2, torch.float32, "s2")
     if q8.numel() < nb or s2.numel() < ng:
@@ -317,7 +317,7 @@ def dequantize_nf4(codes, q8, s2, n, dtype=None, out=None, stream=None, qtype="n
     _dev(codes, torch.uint8, "codes")
     _dev(q8, torch.uint8, "q8")
     _dev(s2, torch.float32, "s2")
-    out = _empty(n, dtype, codes.device, stream) if out is None else out
+    out = _empty((n,), dtype, codes.device, stream) if out is None else out
     _dev(out, dtype, "out")
     _need(codes, n // 2, "codes")
     _need(q8, (n + 63) // 64, "q8")
@@ -551,9 +551,9 @@ def load_4bit(path, device="cuda", stream=None):
     torch = _torch()
     qtype, N, K = load_4bit_info(path)
     nb = (N * K + 63) // 64
-    codes = _empty(N * K // 2, torch.uint8, device, stream)
-    q8 = _empty(nb, torch.uint8, device, stream)
-    s2 = _empty((nb + 255) // 256, torch.float32, device, stream)
+    codes = _empty((N * K // 2,), torch.uint8, device, stream)
+    q8 = _empty((nb,), torch.uint8, device, stream)
+    s2 = _empty(((nb + 255) // 256,), torch.float32, device, stream)
     _check(lib().qlora_load_4bit(os.fsencode(path), _qtype(qtype), N, K, _p(codes), _p(q8), _p(s2),
                                  _stream(stream)))
     return codes, q8, s2, qtype, N, K
