@@ -169,6 +169,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[t][i] = 0.0f;
   float m = -INFINITY, l = 0.0f;
+  uint32_t spoilt = 0;  // not 0: the row sees a value that is no number
   __syncthreads();
 
   // Piece n of a thread is chunk lane % PR of key lane / PR of a run of 64 / PR
@@ -257,8 +258,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   };
   // A value that no row sees becomes 0; one that is not finite becomes 0 too
   // (it must not reach rows that do not see its key through 0 * inf) and its
-  // key is marked: the rows that see it get a NaN weight.  w: a piece of key
-  // `key`, which PR lanes in a row hold.
+  // key is marked: the rows that see it give NaN.  w: a piece of key `key`,
+  // which PR lanes in a row hold.
   auto tame = [&](auto& w, int buf, int key, int j0) __attribute__((always_inline)) {
     const bool any = j0 + key >= lo && j0 + key < hi;
     bool bad = false;
@@ -372,19 +373,16 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     }
     const float k2 = CODES ? 1.0f : s2;
     if (on_edge(j0)) {
-      uint32_t wild[8], some = 0;
-#pragma unroll
-      for (int n = 0; n < 8; ++n) some |= wild[n] = *reinterpret_cast<const uint32_t*>(&s_wild[buf][8 * n + 4 * h2]);
-      if (__any(some != 0)) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (wild[4 * c + i / 4] >> (8 * (i % 4)) & 255u) s[c][i] = __uint_as_float(0x7FC00000u);
-      }
       // Bounds of the keys that the lane's row sees, against the register's own
       // place 32 c + 8 (i / 4) + i % 4.
       const int from = my_lo - j0 - 4 * h2, to = my_hi - j0 - 4 * h2;
+      // Values that are no numbers spoil the outputs of the rows that see them;
+      // the scores, and so the log-sum, stay.  (Rare: a loop, which needs no
+      // registers beside the scores.)
+      if (__any(reinterpret_cast<const uint32_t*>(s_wild[buf])[lane & 15] != 0))
+#pragma unroll 1
+        for (int key = 0; key < kTileKeys; ++key)
+          if (j0 + key >= my_lo && j0 + key < my_hi) spoilt |= s_wild[buf][key];
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -470,6 +468,11 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
     l = __uint_as_float(p[0]) + __uint_as_float(p[1]);
   }
+  if (spoilt)
+#pragma unroll
+    for (int t = 0; t < NB; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[t][i] = __uint_as_float(0x7FC00000u);
   if (!ok) return;
   const int Hq = H * G;
   const int64_t at = (sq.first + qi) * Hq + h * G + qg;

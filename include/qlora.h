@@ -488,7 +488,9 @@ int qlora_kv_read(const qlora_kv_cache* cache, int64_t T, const int64_t* slots, 
  *   lse = log(sum_j exp(scale * (q . k_j))).
  * A token that sees nothing (no length, or more new than stored ones) gives
  * zeros and lse = -inf.  What tokens that a row does not see hold (the end of
- * a page, a page given back) does not matter, whether finite or not.
+ * a page, a page given back) does not matter, whether finite or not.  A value
+ * that is no finite number makes the outputs of the tokens that see it no
+ * finite numbers, in its own dims at the least; lse does not depend on values.
  * Query head x uses key/value head x / (q heads / cache heads).
  *   tokens   rows of q, out and lse.  q  in: view of `tokens` tokens; its
  *            heads a multiple of the cache's.

@@ -117,3 +117,35 @@ def test_other_calls_on_another_stream():
     assert all(bool((c == 3).all()) for c in copies)
     for t, u in zip(got, want):
         assert torch.equal(t.view(torch.uint8), u.view(torch.uint8))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8", "nf4", "fp4"])
+@pytest.mark.parametrize("n,hq,h,D", [(4, 2, 1, 64), (100, 2, 1, 64), (130, 4, 2, 128), (100, 2, 2, 80)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_value_that_is_no_number_leaves_the_log_sum_alone(n, hq, h, D, kv, bad):
+    """lse is a function of the scores, so a value (or its scale) that is no
+    number must not change a bit of it, whether the key lies at the edge of what
+    the rows see or where all of them see it.  Rows that do not see the key keep
+    every bit of their outputs; those that see it are no numbers in its dim."""
+    b = Batch([(n, 900), (n, 0), (n, 701)], hq, h, D, kv, 16, seed=21)
+    first = b.run()
+    b.check(*first)
+    for kw in (dict(), dict(window=200), dict(causal=False)):
+        out, lse = b.run(**kw)
+        for key in (899, 898 - n // 2, 900 - n, 890 - n, 300):
+            page, off = int(b.table[0, key // 16]), key % 16
+            where = (page, h - 1, off, 5) if kv == "bf16" else (page, h - 1, off)
+            buffer = b.cache.v if kv == "bf16" else b.cache.v_scale
+            kept = buffer[where].clone()
+            buffer[where] = bad
+            got, got_lse = b.run(**kw)
+            buffer[where] = kept
+            assert torch.equal(got_lse.view(torch.int32), lse.view(torch.int32)), (key, kw)
+            at = torch.arange(900 - n, 900, device="cuda")
+            sees = (at >= key) if kw.get("causal", True) else torch.ones_like(at, dtype=torch.bool)
+            if "window" in kw:
+                sees &= key > at - kw["window"]
+            mine = torch.zeros(got.shape[0], hq, dtype=torch.bool, device="cuda")
+            mine[:n, hq - hq // h:] = sees[:, None]
+            assert torch.equal(got[~mine].view(torch.int16), out[~mine].view(torch.int16)), (key, kw)
+            assert not bool(torch.isfinite(got[mine][:, 5]).any()), (key, kw)
