@@ -49,7 +49,8 @@ __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int b) {
   int64_t s0 = __builtin_amdgcn_readfirstlane(a.starts[b]), s1 = __builtin_amdgcn_readfirstlane(a.starts[b + 1]);
   int64_t len = __builtin_amdgcn_readfirstlane(a.lengths[b]);
   Seq q;
-  q.bad = false;
+  // The sequences cover the tokens: a row outside of them would not be written.
+  q.bad = (b == 0 && s0 != 0) || (b == a.batch - 1 && s1 != a.tokens);
   if (s0 < 0 || s0 > a.tokens) { s0 = s0 < 0 ? 0 : a.tokens; q.bad = true; }
   if (s1 < s0 || s1 > a.tokens) { s1 = s1 < s0 ? s0 : a.tokens; q.bad = true; }
   if (s1 - s0 > a.max_new) { s1 = s0 + a.max_new; q.bad = true; }

@@ -201,7 +201,8 @@ def attend_paged(q, cache, pages, starts, lengths, max_new, max_len, scale=None,
 
     q: [tokens, q_heads, dim] bf16 (dims contiguous); pages: int32 [batch,
     pages_per_seq]; starts: int32 [batch + 1], the first new token of each
-    sequence and the end; lengths: int32 [batch], stored tokens with the new
+    sequence and the end (0 and q's tokens at both ends; padding is a last
+    sequence of length 0); lengths: int32 [batch], stored tokens with the new
     ones; max_new, max_len: host bounds of both.  scale defaults to dim**-0.5.
     out: bf16 [tokens, q_heads, dim]; lse: True, or an fp32 [tokens, q_heads]
     tensor, to have the log-sums too.  Returns (out, lse or None)."""
@@ -215,6 +216,8 @@ def attend_paged(q, cache, pages, starts, lengths, max_new, max_len, scale=None,
         raise ValueError("pages must be [batch, pages_per_seq]")
     _index(starts, B + 1, torch.int32, "starts")
     _dev(lengths, torch.int32, "lengths")
+    if T > 0 and (B == 0 or max_new == 0):
+        raise ValueError("tokens of no sequence: batch and max_new must be positive where q has tokens")
     if out is None:
         out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
                else _empty(q.shape, q.dtype, q.device, stream))

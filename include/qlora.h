@@ -495,7 +495,10 @@ int qlora_kv_read(const qlora_kv_cache* cache, int64_t T, const int64_t* slots, 
  *   tokens   rows of q, out and lse.  q  in: view of `tokens` tokens; its
  *            heads a multiple of the cache's.
  *   batch    sequences;  starts [batch+1] and lengths [batch] int32 with
- *            starts[0] = 0 and starts[batch] = tokens.
+ *            starts[0] = 0 and starts[batch] = tokens; rows outside of all
+ *            sequences are not written, and are reported as QLORA_ERR_INDEX.
+ *            (Padding rows: a last sequence of length 0, which gives zeros.)
+ *            tokens = 0, batch = 0 or max_new = 0: no-op, nothing is written.
  *   pages    [batch][pages_per_seq] int32; may be NULL where max_len = 0.
  *   max_new, max_len  upper bounds of starts[b+1] - starts[b] and lengths[b]
  *            (the launch is sized by them; no call reads device memory on the

@@ -149,3 +149,36 @@ def test_a_value_that_is_no_number_leaves_the_log_sum_alone(n, hq, h, D, kv, bad
             mine[:n, hq - hq // h:] = sees[:, None]
             assert torch.equal(got[~mine].view(torch.int16), out[~mine].view(torch.int16)), (key, kw)
             assert not bool(torch.isfinite(got[mine][:, 5]).any()), (key, kw)
+
+
+@pytest.mark.parametrize("n", [1, 20, 90])
+def test_rows_outside_of_all_sequences_are_reported(n):
+    """starts that begin after the first token or end before the last one leave
+    rows unwritten; a padding sequence of length 0 gives zeros instead."""
+    lib = _lib()
+    b = Batch([(n, n + 40), (n, n + 3), (4, 0)], 4, 2, 64, "int8", 16, seed=31)
+    out, lse = b.run()
+    b.check(out, lse)
+    assert torch.all(out[2 * n:] == 0) and torch.all(lse[2 * n:] == float("-inf"))
+    full = b.dstarts.clone()
+    for starts in ([1, n, 2 * n, 2 * n + 4], [0, n, 2 * n, 2 * n + 3], [0, n, 2 * n, 2 * n]):
+        b.dstarts = _i32(starts)
+        got, _ = b.run()
+        with pytest.raises(lib.QLoRAError, match="QLORA_ERR_INDEX"):
+            lib.device_status()
+        rows = slice(n, 2 * n)                     # a sequence that is whole keeps its results
+        assert torch.equal(got[rows].view(torch.int16), out[rows].view(torch.int16))
+    b.dstarts = full
+    b.check(*b.run())
+
+
+def test_tokens_of_no_sequence_are_refused():
+    lib = _lib()
+    b = Batch([(2, 9)], 4, 2, 64, "int8", 16, seed=32)
+    q = _dev(b.q)
+    with pytest.raises(ValueError, match="tokens of no sequence"):
+        lib.attend_paged(q, b.cache, b.pages, b.dstarts, b.lengths, max_new=0, max_len=9)
+    with pytest.raises(ValueError, match="tokens of no sequence"):
+        lib.attend_paged(q, b.cache, b.pages[:0], b.dstarts[:1], b.lengths[:0], max_new=2, max_len=9)
+    out, _ = lib.attend_paged(q[:0], b.cache, b.pages[:0], b.dstarts[:1], b.lengths[:0], max_new=0, max_len=0)
+    assert out.shape == (0, 4, 64)
