@@ -629,10 +629,11 @@ Plan make_plan(const AttendProblem& p) {
   // overlap their matrix and vector phases.
   r.tile_rows = r.tile ? (rows > 128 && p.pool.type != kKVBF16 && p.pool.dim <= 128 ? 256 : 128) : rows > 16 && p.pool.dim <= 128 ? 32 : 16;
   r.tiles = std::max<int64_t>(1, (rows + r.tile_rows - 1) / r.tile_rows);
-  // Keys that a tile can see, from a multiple of 16 on.
-  int64_t span = p.max_len;
-  if (p.window > 0 && p.causal) span = std::min<int64_t>(span, (int64_t)p.window + r.tile_rows);
-  span += 15;
+  // Keys that a tile can see (`reach`), from a multiple of 16 on where a window
+  // cuts them.
+  const bool cut = p.window > 0 && p.causal && (int64_t)p.window + r.tile_rows < p.max_len;
+  int64_t span = (cut ? (int64_t)p.window + r.tile_rows : p.max_len) + 15;
+  const int64_t reach = std::min<int64_t>(p.max_len, span);
   const int64_t work = std::max<int64_t>(1, (int64_t)p.batch * p.pool.heads * r.tiles);
   // Splits cost a second launch and its partial sums (6 us at the least).
   int64_t splits = 1;
@@ -666,8 +667,9 @@ Plan make_plan(const AttendProblem& p) {
   // sequences (those 4 of up to 1000 tokens: 16.1 us, 17.8 with eight).
   r.waves = span / splits > 2048 && r.tile_rows == 16 && p.pool.dim <= 128 ? 8 : 4;
   r.chunk = ((span + splits - 1) / splits + 127) / 128 * 128;
-  r.chunk = std::min<int64_t>(std::max<int64_t>(r.chunk, 128), r.tile ? kTileChunk : kMaxChunk);
-  r.splits = std::max<int64_t>(1, (span + r.chunk - 1) / r.chunk);
+  r.chunk = std::max<int64_t>(r.chunk, 128);
+  if (!r.tile) r.chunk = std::min<int64_t>(r.chunk, kMaxChunk);
+  r.splits = std::max<int64_t>(1, (reach + r.chunk - 1) / r.chunk);
   return r;
 }
 

@@ -8,7 +8,8 @@
 namespace qlora {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kMaxChunk = 16384, kTileChunk = 8192;  // keys of a split (streaming, tiles): bound the page lists in LDS
+constexpr int kMaxChunk = 16384;   // keys of a split (streaming): bounds its page list in LDS
+constexpr int kListKeys = 8192;    // keys that a tile workgroup's page list in LDS covers at a time
 
 struct AttendArgs {
   KVPool pool;

@@ -62,7 +62,10 @@ __device__ __forceinline__ int nth_longest(const AttendArgs& a, int n) {
   return __builtin_ctzll(__ballot(lane < a.batch && before == n));
 }
 
-template <int OP, int DP, int WAVES, bool EXACT>
+// LONG: a split has more keys than the list of pages covers, which is then
+// renewed on the way.  (One kernel for both: 0.4 % slower over 30 calls that
+// never renew it, the worst 70.1 -> 72.1 us.)
+template <int OP, int DP, int WAVES, bool EXACT, bool LONG>
 __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_kernel(AttendArgs a) {
   constexpr bool CODES = OP == kOpINT8 || OP == kOpLevel;  // exact operands, scales on scores and weights
   constexpr int BITS = kBitsOf<OP>;
@@ -80,10 +83,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   __shared__ __align__(16) uint16_t s_k1[kTileKeys * DP], s_v1[kTileKeys * DP];
   __shared__ __align__(16) float s_sc[CODES ? 2 : 1][2][kTileKeys];
   __shared__ __align__(16) uint8_t s_wild[2][kTileKeys];
-  // Of each page of the split: its number, and where its rows of this head
-  // start in the codes (bytes).
-  __shared__ int s_page[kTileChunk / 16 + 1];
-  __shared__ int64_t s_at[kTileChunk / 16 + 1];
+  // Of the pages of the next kListKeys keys: their numbers, and where their rows
+  // of this head start in the codes (bytes).
+  __shared__ int s_page[kListKeys / 16 + 1];
+  __shared__ int64_t s_at[kListKeys / 16 + 1];
   // Entries one after another: at 8 bytes each, pairs of bf16 met half of the
   // banks (the chunks below in FP4: 151 us, so 141).
   constexpr int LW = OP == kOpLevel ? 1 : 2;
@@ -118,16 +121,22 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   const int k1 = min(hi, k0 + a.chunk);
   const int full_hi = seen_hi(a, sq, i_first), full_lo = seen_lo(a, sq, i_last);
 
-  const int shift = a.pool.shift, first_page = k0 >> shift, last = ((k1 - 1) >> shift) - first_page;
-  for (int p = tid; k0 < k1 && p <= last; p += 64 * WAVES) {
-    int page = a.pages[(int64_t)b * a.width + first_page + p];
-    if (page < 0 || page >= a.pool.pages) {
-      atomicOr(a.status, kStatusIndex);
-      page = 0;
+  const int shift = a.pool.shift;
+  int first_page = 0, last = 0;  // the list's first page, and its last one as counted from there
+  auto list_pages = [&](int from, int to) __attribute__((always_inline)) {  // of keys [from, to)
+    first_page = from >> shift;
+    last = ((to - 1) >> shift) - first_page;
+    for (int p = tid; p <= last; p += 64 * WAVES) {
+      int page = a.pages[(int64_t)b * a.width + first_page + p];
+      if (page < 0 || page >= a.pool.pages) {
+        atomicOr(a.status, kStatusIndex);
+        page = 0;
+      }
+      s_page[p] = page;
+      s_at[p] = (((int64_t)page * H + h) << shift) * kv_row_bytes(a.pool.type, a.pool.dim);
     }
-    s_page[p] = page;
-    s_at[p] = (((int64_t)page * H + h) << shift) * kv_row_bytes(a.pool.type, a.pool.dim);
-  }
+  };
+  if (k0 < k1) list_pages(k0, LONG ? min(k1, k0 + kListKeys) : k1);
   if (BITS == 4 && tid < 256) {
     // A byte's two levels: a pair of bf16 (exact levels), or two fp32 values.
     uint32_t x = 0, y = 0;
@@ -447,21 +456,28 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     }
   };
 
-  if (k0 < k1) {
-    read_pages(k0);
-    load(s_k0, s_v0, k0);
-    store(s_k0, s_v0, 0, k0);
+  for (int from = k0; from < k1;) {  // as many keys as the list covers
+    const int to = LONG ? min(k1, from + kListKeys) : k1;
+    read_pages(from);
+    load(s_k0, s_v0, from);
+    store(s_k0, s_v0, 0, from);
     auto step = [&](uint16_t* k, uint16_t* v, uint16_t* next_k, uint16_t* next_v, int buf, int j0) __attribute__((always_inline)) {
-      const bool more = j0 + kTileKeys < k1;
+      const bool more = j0 + kTileKeys < to;
       if (more) load(next_k, next_v, j0 + kTileKeys);
       if (j0 < w_hi && j0 + kTileKeys > w_lo) compute(k, v, buf, j0);
       if (more) store(next_k, next_v, buf ^ 1, j0 + kTileKeys);
       return more;
     };
-    for (int j0 = k0;; j0 += 2 * kTileKeys) {
+    for (int j0 = from;; j0 += 2 * kTileKeys) {
       if (!step(s_k0, s_v0, s_k1, s_v1, 0, j0)) break;
       if (!step(s_k1, s_v1, s_k0, s_v0, 1, j0 + kTileKeys)) break;
     }
+    from = to;
+    if (!LONG || from >= k1) break;
+    // No wave has read the list since the last barrier; past the next one all
+    // are done with the tiles.
+    list_pages(from, min(k1, from + kListKeys));
+    __syncthreads();
   }
 
   {
@@ -507,10 +523,15 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     }
 }
 
+template <int OP, int DP, int WAVES, bool LONG>
+void tile_long(const AttendArgs& a, dim3 grid, hipStream_t s) {
+  if (a.pool.dim == DP) hipLaunchKernelGGL((attend_tile_kernel<OP, DP, WAVES, true, LONG>), grid, dim3(64 * WAVES), 0, s, a);
+  else hipLaunchKernelGGL((attend_tile_kernel<OP, DP, WAVES, false, LONG>), grid, dim3(64 * WAVES), 0, s, a);
+}
 template <int OP, int DP, int WAVES>
 void tile_dim(const AttendArgs& a, dim3 grid, hipStream_t s) {
-  if (a.pool.dim == DP) hipLaunchKernelGGL((attend_tile_kernel<OP, DP, WAVES, true>), grid, dim3(64 * WAVES), 0, s, a);
-  else hipLaunchKernelGGL((attend_tile_kernel<OP, DP, WAVES, false>), grid, dim3(64 * WAVES), 0, s, a);
+  if (a.chunk > kListKeys) tile_long<OP, DP, WAVES, true>(a, grid, s);
+  else tile_long<OP, DP, WAVES, false>(a, grid, s);
 }
 template <int OP>
 void tile_op(const AttendArgs& a, int rows, dim3 grid, hipStream_t s) {

@@ -507,8 +507,13 @@ int qlora_kv_read(const qlora_kv_cache* cache, int64_t T, const int64_t* slots, 
  *            max_len <= 2^30.
  *   out      [tokens, q heads, dim] bf16.
  *   lse      [tokens, q heads] fp32, or NULL.
- *   workspace  qlora_attend_paged_workspace_bytes bytes (the partial sums
- *            when the keys are split over workgroups).
+ *   workspace  qlora_attend_paged_workspace_bytes bytes: the partial sums
+ *            when the keys are split over workgroups, which they are where the
+ *            rows alone would not fill the chip.  With more than 32 rows of
+ *            max_new * q heads / cache heads at most 2^18 * (dim + 2) * 4
+ *            bytes (136 MB at dim 128) and 256, however long the sequences;
+ *            with fewer, max_len / 16384 splits or a few to fill the chip,
+ *            each tokens * q heads * (dim + 2) * 4 bytes.
  * Scores, the running maximum and sum and the output's accumulation are fp32.
  * Keys and values enter the products as bf16: bf16 rows, int8 codes and the
  * levels of Int4 and FP4 exactly (a row's scale multiplies whole scores and

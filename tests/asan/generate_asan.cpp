@@ -323,6 +323,55 @@ static void check_workspace() {
                 }
 }
 
+// Keys are split for the sake of parallel work alone: not because they are many,
+// and never into splits that no row reaches.  So a prompt that fills the chip
+// needs no workspace at any length, and what the kernel for many rows (more than
+// 32 per key/value head) needs has a bound that no length enters: the splits of
+// fewer row tiles than the chip holds (1024 of 128 rows, or 512 of 256), at most
+// twice as many in all, each row's sums in fp32.
+static void check_workspace_growth() {
+  for (int64_t n : {4096, 8177, 8178, 8192, 16384, 32768, 131072}) {
+    for (int32_t type : {QLORA_KV_BF16, QLORA_KV_INT8, QLORA_KV_NF4}) {
+      Attend a;
+      a.c = cache(type, 52, 128);
+      a.q = heads(52);
+      a.batch = 1;
+      a.tokens = a.max_new = a.max_len = n;
+      EXPECT(a.need() == 0);
+      a.c = cache(type, 8, 128);
+      a.q = heads(64);
+      if (n >= 16384) EXPECT(a.need() == 0);
+    }
+  }
+  for (int32_t type = 0; type < 5; ++type)
+    for (int32_t dim : {16, 64, 128, 256})
+      for (int32_t group : {1, 8})
+        for (int32_t h : {1, 8, 52})
+          for (int64_t batch : {1, 4, 64})
+            for (int64_t n : {40, 129, 4096, 20000})
+              for (int64_t len : {20000, 131072, 1 << 20, 1 << 30})
+                for (int64_t window : {0, 700, 100000}) {
+                  Attend a;
+                  a.c = cache(type, h, dim);
+                  a.q = heads(h * group);
+                  a.batch = (int32_t)batch;
+                  a.tokens = batch * n;
+                  a.max_new = n;
+                  a.max_len = len;
+                  a.window = window;
+                  EXPECT(a.need() <= (size_t)2 * 1024 * 128 * (dim + 2) * 4 + 256);
+                }
+  // One split of 16384 keys for few rows, where there is work enough.
+  Attend a;
+  a.c = cache(QLORA_KV_BF16, 8, 128);
+  a.q = heads(64);
+  a.batch = 256;
+  a.tokens = 256;
+  a.max_new = 1;
+  a.max_len = 16384;
+  EXPECT(a.need() == 0);
+}
+
 int main() {
   check_rope_table();
   check_rope();
@@ -330,6 +379,7 @@ int main() {
   check_attend();
   check_nothing_stored();
   check_workspace();
+  check_workspace_growth();
   if (failures) {
     fprintf(stderr, "%d expectation(s) failed\n", failures);
     return 1;

@@ -3,9 +3,11 @@ mended code."""
 
 import ctypes
 
+import numpy as np
 import pytest
 
-from test_gpu_generate import Batch, _dev, _i32, _lib
+from oracle import attention as at
+from test_gpu_generate import Batch, _dev, _host, _i32, _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -182,3 +184,40 @@ def test_tokens_of_no_sequence_are_refused():
         lib.attend_paged(q, b.cache, b.pages[:0], b.dstarts[:1], b.lengths[:0], max_new=2, max_len=9)
     out, _ = lib.attend_paged(q[:0], b.cache, b.pages[:0], b.dstarts[:1], b.lengths[:0], max_new=0, max_len=0)
     assert out.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("kv,n,D", [("bf16", 40, 64), ("bf16", 40, 80), ("int8", 40, 64), ("int8", 130, 64), ("nf4", 130, 128),
+                                    ("fp4", 33, 48)])
+def test_keys_past_a_list_of_pages(kv, n, D):
+    """Row tiles that fill the chip walk all keys of a sequence, past what their
+    list of pages holds at a time (8192 keys), once and more than once, and to
+    lengths around its end; nothing is split, so there is no workspace."""
+    lib = _lib()
+    long = [8176, 8177, 8192, 8193, 8257, 17000]
+    h, batch = (8 if n <= 128 else 4), 128
+    seqs = [(n, m) for m in long] + [(n, n + 7 * i) for i in range(batch - len(long))]
+    b = Batch(seqs, h, h, D, kv, 16, seed=40)
+    assert lib.attend_paged_workspace_bytes(b.cache, n * batch, h, batch, **b.bounds) == 0
+    few = range(len(long), batch - 3)               # the oracle takes its time: the long ones and three short ones
+    b.check(*b.run(), skip=few)
+    b.check(*b.run(window=8400), window=8400, skip=few)
+
+
+def test_a_long_prompt_needs_no_workspace():
+    """One prompt of 9000 tokens and 52 heads: rows at its ends and in between against the oracle's."""
+    lib = _lib()
+    n, h, D, page = 9000, 52, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn(n, h, D, generator=g, device="cuda").bfloat16() for _ in range(3))
+    pages = -(-n // page)
+    cache = lib.KVCache.empty(pages, h, page, D, kv_type="bf16")
+    lib.kv_write(cache, k, v, torch.arange(n, device="cuda"))
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None].contiguous()
+    assert lib.attend_paged_workspace_bytes(cache, n, h, 1, n, n) == 0
+    out, lse = lib.attend_paged(q, cache, table, _i32([0, n]), _i32([n]), max_new=n, max_len=n, lse=True)
+    for i in (0, 63, 127, 128, 4500, 8191, 8192, 8300, 8999):
+        ref, rl, mass = at.attend(_host(q[i:i + 1]), _host(k[:i + 1]), _host(v[:i + 1]), D ** -0.5)
+        # The weights' rounding to bf16 and the output's; scores in fp32 (sum |q k| below 100 of the scale here).
+        assert np.all(np.abs(_host(out[i:i + 1]) - ref) <= mass * (2.0 ** -8 + 2.0 ** -13) + 2.0 ** -8 * np.abs(ref))
+        assert np.all(np.abs(lse[i:i + 1].cpu().numpy() - rl) <= 2.0 ** -14)
+    lib.device_status()
