@@ -591,12 +591,17 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int tile
   if (c == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
+// The join's workgroups of a sequence: one to a row where the splits are many.
+int64_t join_groups(const AttendProblem& p, int64_t splits) {
+  const int64_t rows = (int64_t)p.max_new * p.q.heads, per = splits > 16 ? 1 : p.pool.dim <= 64 ? 16 : p.pool.dim <= 128 ? 8 : 4;
+  return (rows + per - 1) / per;
+}
+
 template <int DP>
-void launch_join(const AttendArgs& a, int tile_rows, hipStream_t s) {
-  const int64_t rows = (int64_t)a.max_new * a.q.heads;
-  constexpr int R = 1024 / DP;  // rows of a workgroup when they are many
-  if (a.splits > 16) hipLaunchKernelGGL((attend_join_kernel<DP, true>), dim3((unsigned)rows, (unsigned)a.batch), dim3(256), 0, s, a, tile_rows);
-  else hipLaunchKernelGGL((attend_join_kernel<DP, false>), dim3((unsigned)((rows + R - 1) / R), (unsigned)a.batch), dim3(256), 0, s, a, tile_rows);
+void launch_join(const AttendArgs& a, unsigned groups, int tile_rows, hipStream_t s) {
+  const dim3 grid(groups, (unsigned)a.batch);
+  if (a.splits > 16) hipLaunchKernelGGL((attend_join_kernel<DP, true>), grid, dim3(256), 0, s, a, tile_rows);
+  else hipLaunchKernelGGL((attend_join_kernel<DP, false>), grid, dim3(256), 0, s, a, tile_rows);
 }
 
 uint32_t bf16_round_host(float f) {  // finite f
@@ -703,9 +708,9 @@ bool attend_fits(const AttendProblem& p) {
   // Rows and (token, head) pairs are counted in 32 bits.
   if ((int64_t)p.max_new * p.q.heads >= (int64_t(1) << 30)) return false;
   const Plan r = make_plan(p);
-  const int64_t groups = (int64_t)p.batch * p.pool.heads;
-  return r.tiles < (int64_t(1) << 31) && groups * r.tiles < (int64_t(1) << 31) &&
-         groups * r.tiles * r.splits < (int64_t(1) << 31);
+  const int64_t groups = (int64_t)p.batch * p.pool.heads, threads = 64 * (r.tile ? r.tile_rows / 32 : r.waves);
+  if (r.tiles > INT32_MAX || groups * r.tiles > INT32_MAX || !grid_fits(groups * r.tiles * r.splits * threads)) return false;
+  return r.splits == 1 || grid_fits(join_groups(p, r.splits) * 256);
 }
 
 size_t attend_workspace_bytes(const AttendProblem& p) {
@@ -765,9 +770,10 @@ hipError_t launch_attend(const AttendProblem& p, const float table[16], void* ws
   }
   if (e != hipSuccess || r.splits == 1) return e;
   KernelTimer kt_("attend_join_kernel", s);
-  if (p.pool.dim <= 64) launch_join<64>(a, r.tile_rows, s);
-  else if (p.pool.dim <= 128) launch_join<128>(a, r.tile_rows, s);
-  else launch_join<256>(a, r.tile_rows, s);
+  const unsigned groups = (unsigned)join_groups(p, r.splits);
+  if (p.pool.dim <= 64) launch_join<64>(a, groups, r.tile_rows, s);
+  else if (p.pool.dim <= 128) launch_join<128>(a, groups, r.tile_rows, s);
+  else launch_join<256>(a, groups, r.tile_rows, s);
   return hipGetLastError();
 }
 

@@ -276,14 +276,14 @@ void write_rope(KVWriteArgs a, const Bins& bins, hipStream_t s) {
 }
 template <int KT, int LPR>
 void write_heads(const KVWriteArgs& a, const Bins& bins, hipStream_t s) {
-  // Four heads to a thread once that leaves enough workgroups.
-  if (a.T * 2 * a.pool.heads * LPR >= 4 * 256 * 1024) write_rope<KT, LPR, 4>(a, bins, s);
+  if (kv_write_heads(a.T, a.pool.heads, a.pool.dim) == 4) write_rope<KT, LPR, 4>(a, bins, s);
   else write_rope<KT, LPR, 1>(a, bins, s);
 }
 template <int KT>
 void write_lanes(const KVWriteArgs& a, const Bins& bins, hipStream_t s) {
-  if (a.pool.dim <= 64) write_heads<KT, 4>(a, bins, s);
-  else if (a.pool.dim <= 128) write_heads<KT, 8>(a, bins, s);
+  const int lanes = kv_write_lanes(a.pool.dim);
+  if (lanes == 4) write_heads<KT, 4>(a, bins, s);
+  else if (lanes == 8) write_heads<KT, 8>(a, bins, s);
   else write_heads<KT, 16>(a, bins, s);
 }
 
@@ -349,7 +349,7 @@ hipError_t launch_kv_read(const KVPool& pool, int64_t T, const int64_t* slots, u
   a.status = status_word(&e);
   if (!a.status) return e;
   a.pool = pool;
-  a.units = T * pool.heads * 2 * (pool.dim / 16);
+  a.units = kv_read_threads(T, pool.heads, pool.dim);
   a.slots = slots;
   a.k = k;
   a.v = v;

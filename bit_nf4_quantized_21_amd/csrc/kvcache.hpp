@@ -36,6 +36,26 @@ __host__ __device__ __forceinline__ int64_t kv_row_bytes(int type, int dim) {
   return type == kKVBF16 ? 2 * dim : type == kKVINT8 ? dim : dim / 2;
 }
 
+// A launch counts its threads in 32 bits along an axis: one of more comes back
+// as an error, or silently as what is left of the count.  `threads` in whole
+// workgroups of up to 512 stays below that.
+inline bool grid_fits(int64_t threads) { return threads <= (int64_t(1) << 32) - 512; }
+// Threads of the rotation, of its table, and of the cache's two kernels (see
+// their launchers).
+inline int64_t rope_threads(int64_t tokens, int64_t heads, int32_t dim) { return tokens * heads * (dim / 16); }
+inline int64_t rope_table_threads(int64_t positions, int32_t rot) { return positions * (rot / 2); }
+inline int kv_write_lanes(int32_t dim) { return dim <= 64 ? 4 : dim <= 128 ? 8 : 16; }  // of a row
+inline int64_t kv_read_threads(int64_t tokens, int64_t heads, int32_t dim) { return tokens * heads * 2 * (dim / 16); }
+// Heads that a thread of the cache write takes: four once that leaves enough
+// workgroups.
+inline int kv_write_heads(int64_t tokens, int64_t heads, int32_t dim) {
+  return tokens * 2 * heads * kv_write_lanes(dim) >= 4 * 256 * 1024 ? 4 : 1;
+}
+inline int64_t kv_write_threads(int64_t tokens, int64_t heads, int32_t dim) {
+  const int n = kv_write_heads(tokens, heads, dim);
+  return tokens * 2 * ((heads + n - 1) / n) * kv_write_lanes(dim);
+}
+
 // A cos/sin table and the positions that pick its rows; table = null: no
 // rotation.
 struct RopeTable {

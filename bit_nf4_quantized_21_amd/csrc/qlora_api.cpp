@@ -465,8 +465,8 @@ int qlora_linear_bwd(const uint16_t* dY, const uint16_t* X, const float* XA, int
 }
 
 namespace {
-// Extents up to here keep every row number and byte count inside int64; the
-// calls bound what their grids count in 32 bits.
+// Extents up to here keep every row number and byte count inside int64; what a
+// launch counts in 32 bits is bounded by grid_fits and attend_fits.
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 
 int check_dim(int32_t dim) { return dim >= 16 && dim <= 256 && dim % 16 == 0 ? QLORA_OK : QLORA_ERR_UNSUPPORTED; }
@@ -558,6 +558,7 @@ int qlora_rope_table(int64_t positions, int32_t rot, double base, int32_t scalin
                                       !(high > low) || !std::isfinite(high)))
     return QLORA_ERR_UNSUPPORTED;
   if (positions < 0 || positions > kMaxTokens) return QLORA_ERR_SHAPE;
+  if (!qlora::grid_fits(qlora::rope_table_threads(positions, rot))) return QLORA_ERR_SHAPE;
   if (positions == 0) return QLORA_OK;
   if (!table) return QLORA_ERR_NULL;
   if (!aligned16(table)) return QLORA_ERR_ALIGN;
@@ -582,7 +583,7 @@ int qlora_rope(int64_t T, int32_t dim, int32_t rot, int32_t interleaved, int32_t
     if ((st = check_heads(k, &ki)) != QLORA_OK || (st = check_heads(k_out, &ko)) != QLORA_OK) return st;
     if (ko.heads != ki.heads) return QLORA_ERR_SHAPE;
   }
-  if (T * (int64_t)(qi.heads + ki.heads) > (int64_t(1) << 33)) return QLORA_ERR_SHAPE;
+  if (!qlora::grid_fits(qlora::rope_threads(T, (int64_t)qi.heads + ki.heads, dim))) return QLORA_ERR_SHAPE;
   return hip_status(qlora::launch_rope(T, dim, t, inverse != 0, qi, qo, ki, ko, (hipStream_t)stream));
 }
 
@@ -596,7 +597,8 @@ int qlora_kv_write(const qlora_kv_cache* cache, int64_t T, const qlora_heads* k,
   if (st != QLORA_OK) return st;
   qlora::HeadsView kv{}, vv{};
   if ((st = check_heads(k, &kv)) != QLORA_OK || (st = check_heads(v, &vv)) != QLORA_OK) return st;
-  if (kv.heads != pool.heads || vv.heads != pool.heads || T * (int64_t)pool.heads > (int64_t(1) << 32))
+  if (kv.heads != pool.heads || vv.heads != pool.heads ||
+      !qlora::grid_fits(qlora::kv_write_threads(T, pool.heads, pool.dim)))
     return QLORA_ERR_SHAPE;
   if (!slots) return QLORA_ERR_NULL;
   if (reinterpret_cast<uintptr_t>(slots) & 7u) return QLORA_ERR_ALIGN;
@@ -615,7 +617,7 @@ int qlora_kv_read(const qlora_kv_cache* cache, int64_t T, const int64_t* slots, 
   qlora::KVPool pool{};
   const int st = check_cache(cache, true, &pool);
   if (st != QLORA_OK) return st;
-  if (T * (int64_t)pool.heads > (int64_t(1) << 32)) return QLORA_ERR_SHAPE;
+  if (!qlora::grid_fits(qlora::kv_read_threads(T, pool.heads, pool.dim))) return QLORA_ERR_SHAPE;
   if (!slots || !k || !v) return QLORA_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(slots) & 7u) || !aligned16(k) || !aligned16(v)) return QLORA_ERR_ALIGN;
   const TypeTables* tt = cache_tables(pool.type);

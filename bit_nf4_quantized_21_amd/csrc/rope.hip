@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
 }  // namespace
 
 hipError_t launch_rope_table(const RopeTableArgs& a, float* table, hipStream_t s) {
-  const int64_t n = a.n * (a.rot / 2);
+  const int64_t n = rope_table_threads(a.n, a.rot);
   if (n <= 0) return hipSuccess;
   KernelTimer kt_("rope_table_kernel", s);
   hipLaunchKernelGGL(rope_table_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a,
@@ -117,7 +117,7 @@ hipError_t launch_rope(int64_t T, int32_t dim, const RopeTable& t, bool inverse,
   a.q_out = q_out;
   a.k = k;
   a.k_out = k_out;
-  const int64_t n = T * a.heads * (dim / 16);
+  const int64_t n = rope_threads(T, a.heads, dim);
   if (n <= 0) return hipSuccess;
   KernelTimer kt_("rope_kernel", s);
   const dim3 grid((unsigned)((n + 255) / 256));

@@ -365,6 +365,10 @@ int qlora_adamw_step(int64_t n, uint16_t* param, float* master, float* m, float*
  * lengths) are checked by the kernels: one out of range never causes an
  * access out of bounds, it sets a bit that qlora_device_status returns as
  * QLORA_ERR_INDEX, and the results of that call are then unreliable.
+ * A call whose launch would take 2^32 threads or more is refused as
+ * QLORA_ERR_SHAPE: a thread turns or reads back 16 elements and stores 16 of
+ * four heads; attention takes 256 or 512 to each sequence, key/value head, row
+ * tile and split.
  *
  * A view of [tokens, heads, dim] bf16 values whose dims are contiguous: a
  * tensor of its own or a part of a fused q/k/v output.  Strides are in

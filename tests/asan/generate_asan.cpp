@@ -372,6 +372,54 @@ static void check_workspace_growth() {
   EXPECT(a.need() == 0);
 }
 
+// Launches of 2^32 threads and more lose the upper bits of their count: refused.
+static void check_grid_limits() {
+  EXPECT(qlora_rope_table(int64_t(1) << 30, 16, 1e4, 0, 1, 0, 1, 32, 1, at<float>(kAddr), nullptr) == QLORA_ERR_SHAPE);
+  LAUNCHED(qlora_rope_table((int64_t(1) << 29) - 64, 16, 1e4, 0, 1, 0, 1, 32, 1, at<float>(kAddr), nullptr));
+  REFUSED(qlora_rope_table(int64_t(1) << 26, 128, 1e4, 0, 1, 0, 1, 32, 1, at<float>(kAddr), nullptr), QLORA_ERR_SHAPE);
+  const qlora_heads h8 = heads(8, 1024, 128), h2 = heads(2, 1024, 128);
+  auto rope = [&](int64_t T) {
+    return qlora_rope(T, 128, 128, 0, 0, at<float>(kAddr), 8, at<int32_t>(kAddr), &h8, &h8, &h8, &h8, nullptr);
+  };
+  REFUSED(rope(int64_t(1) << 25), QLORA_ERR_SHAPE);         // 16 heads of 8 units
+  REFUSED(rope((int64_t(1) << 25) + 5), QLORA_ERR_SHAPE);
+  LAUNCHED(rope((int64_t(1) << 25) - 4));
+  qlora_kv_cache c = cache(QLORA_KV_NF4, 2, 128);
+  auto write = [&](int64_t T) {
+    return qlora_kv_write(&c, T, &h2, &h2, at<int64_t>(kAddr), nullptr, 0, nullptr, 0, 0, nullptr);
+  };
+  auto read = [&](int64_t T) {
+    return qlora_kv_read(&c, T, at<int64_t>(kAddr), at<uint16_t>(kAddr), at<uint16_t>(kAddr), nullptr);
+  };
+  REFUSED(write(int64_t(1) << 28), QLORA_ERR_SHAPE);        // keys and values, one group of heads, 8 lanes
+  REFUSED(write(int64_t(1) << 30), QLORA_ERR_SHAPE);
+  LAUNCHED(write((int64_t(1) << 28) - 32));
+  REFUSED(read(int64_t(1) << 27), QLORA_ERR_SHAPE);         // keys and values of 2 heads, 8 units
+  REFUSED(read((int64_t(1) << 27) + 1), QLORA_ERR_SHAPE);
+  LAUNCHED(read((int64_t(1) << 27) - 16));
+  Attend a;
+  a.c = cache(QLORA_KV_BF16, 256, 64);
+  a.q = heads(256);
+  a.batch = 65535;
+  a.tokens = 65535;
+  a.max_new = 1;
+  LAUNCHED(a.run());                                        // 65535 * 256 workgroups of 256
+  a.c.heads = a.q.heads = 512;
+  REFUSED(a.run(), QLORA_ERR_SHAPE);
+  a.max_new = 16;                                           // as many workgroups, of more rows
+  a.tokens = 65535 * 16;
+  REFUSED(a.run(), QLORA_ERR_SHAPE);
+  a.c = cache(QLORA_KV_INT8, 128, 64);                      // 256-row tiles take 512 threads
+  a.q = heads(128);
+  a.max_new = 200;
+  a.tokens = 65535 * 200;
+  a.max_len = 64;
+  LAUNCHED(a.run());
+  a.max_new = 300;
+  a.tokens = 65535 * 300;
+  REFUSED(a.run(), QLORA_ERR_SHAPE);
+}
+
 int main() {
   check_rope_table();
   check_rope();
@@ -380,6 +428,7 @@ int main() {
   check_nothing_stored();
   check_workspace();
   check_workspace_growth();
+  check_grid_limits();
   if (failures) {
     fprintf(stderr, "%d expectation(s) failed\n", failures);
     return 1;
