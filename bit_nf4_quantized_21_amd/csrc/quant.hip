@@ -18,6 +18,7 @@
 // The double quantizer gives each group of 256 constants to one wavefront;
 // the fused quantizer gives each group of 256 blocks to one workgroup and
 // keeps the absmax values on chip.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -452,20 +453,30 @@ BinTables make_bins(const Midpoints& mp, int nbins) {
   return t;
 }
 
+// Weights (or constants) of a launch: threads are counted in 32 bits, so larger
+// problems take several launches, cut where every group of constants ends.
+constexpr int64_t kLaunchMax = int64_t(1) << 33;
+template <typename F>
+void in_pieces(int64_t n, F launch) {
+  for (int64_t at = 0; at < n; at += kLaunchMax) launch(at, std::min(n - at, kLaunchMax));
+}
+
 template <typename T>
 hipError_t launch_quantize_t(void (*binned_kernel)(const T*, int64_t, uint8_t*, float*, Midpoints, BinTables),
                              const T* W,
                              int64_t n, uint8_t* codes, float* absmax, const Midpoints& mp, const char* name,
                              hipStream_t s) {
-  const int64_t nb = (n + kBlock - 1) / kBlock;
   constexpr int G = kQGroupBlocks;
-  const int64_t grid = (nb + 16 * G - 1) / (16 * G);
   const int nbins = choose_bins(mp);
   const BinTables bins = nbins ? make_bins(mp, nbins) : BinTables{};
   if (bins.nbins == 0) return hipErrorInvalidValue;
   {
     KernelTimer kt_(name, s);
-    hipLaunchKernelGGL(binned_kernel, dim3((unsigned)grid), dim3(256), 0, s, W, n, codes, absmax, mp, bins);
+    in_pieces(n, [&](int64_t at, int64_t m) {
+      const int64_t nb = (m + kBlock - 1) / kBlock, grid = (nb + 16 * G - 1) / (16 * G);
+      hipLaunchKernelGGL(binned_kernel, dim3((unsigned)grid), dim3(256), 0, s, W + at, m, codes + at / 2,
+                         absmax + at / kBlock, mp, bins);
+    });
   }
   return hipGetLastError();
 }
@@ -475,14 +486,16 @@ hipError_t launch_quantize_dq_t(void (*binned_kernel)(const T*, int64_t, uint8_t
                                                       BinTables),
                                 const T* W, int64_t n, uint8_t* codes, uint8_t* q8, float* s2, const Midpoints& mp,
                                 const char* name, hipStream_t s) {
-  const int64_t nb = (n + kBlock - 1) / kBlock;
-  const int64_t grid = (nb + kBlock2 - 1) / kBlock2;
   const int nbins = choose_bins(mp);
   const BinTables bins = nbins ? make_bins(mp, nbins) : BinTables{};
   if (bins.nbins == 0) return hipErrorInvalidValue;
   {
     KernelTimer kt_(name, s);
-    hipLaunchKernelGGL(binned_kernel, dim3((unsigned)grid), dim3(256), 0, s, W, n, codes, q8, s2, mp, bins);
+    in_pieces(n, [&](int64_t at, int64_t m) {
+      const int64_t nb = (m + kBlock - 1) / kBlock, grid = (nb + kBlock2 - 1) / kBlock2;
+      hipLaunchKernelGGL(binned_kernel, dim3((unsigned)grid), dim3(256), 0, s, W + at, m, codes + at / 2,
+                         q8 + at / kBlock, s2 + at / (kBlock * kBlock2), mp, bins);
+    });
   }
   return hipGetLastError();
 }
@@ -508,23 +521,27 @@ hipError_t launch_quantize_dq(const void* W, bool bf16, int64_t n, uint8_t* code
 }
 
 hipError_t launch_double_quant(const float* absmax, int64_t nb, uint8_t* q8, float* s2, hipStream_t s) {
-  const int64_t ng = (nb + kBlock2 - 1) / kBlock2;
-  const int64_t grid = (ng + 3) / 4;
   {
     KernelTimer kt_("double_quant_kernel", s);
-    hipLaunchKernelGGL(double_quant_kernel, dim3((unsigned)grid), dim3(256), 0, s, absmax, nb, q8, s2);
+    in_pieces(nb, [&](int64_t at, int64_t m) {
+      const int64_t ng = (m + kBlock2 - 1) / kBlock2, grid = (ng + 3) / 4;
+      hipLaunchKernelGGL(double_quant_kernel, dim3((unsigned)grid), dim3(256), 0, s, absmax + at, m, q8 + at,
+                         s2 + at / kBlock2);
+    });
   }
   return hipGetLastError();
 }
 
 hipError_t launch_dequantize(const uint8_t* codes, const uint8_t* q8, const float* s2, int64_t n,
                              int out_bf16, void* out, const Codebook& cb, hipStream_t s) {
-  const int64_t groups = (n + 7) / 8;
-  const int64_t grid = (groups + 255) / 256;
   {
     KernelTimer kt_("dequantize_kernel", s);
-    hipLaunchKernelGGL(dequantize_kernel, dim3((unsigned)grid), dim3(256), 0, s, codes, q8, s2, n, out_bf16,
-                     out, cb);
+    in_pieces(n, [&](int64_t at, int64_t m) {
+      const int64_t grid = ((m + 7) / 8 + 255) / 256;
+      hipLaunchKernelGGL(dequantize_kernel, dim3((unsigned)grid), dim3(256), 0, s, codes + at / 2, q8 + at / kBlock,
+                         s2 + at / (kBlock * kBlock2), m, out_bf16,
+                         static_cast<void*>(static_cast<char*>(out) + at * (out_bf16 ? 2 : 4)), cb);
+    });
   }
   return hipGetLastError();
 }
