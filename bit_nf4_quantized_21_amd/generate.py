@@ -52,6 +52,18 @@ def _index(t, n, dtype, name):
     return _need(_dev(t, dtype, name), n, name)
 
 
+def _given(t, shape, dtype, name):
+    """A given output: it holds what is written, and where it has the output's
+    axes they are in its order (rows of a longer buffer, not [heads, tokens, dim])."""
+    n = 1
+    for x in shape:
+        n *= x
+    _need(_dev(t, dtype, name), n, name)
+    if t.dim() == len(shape) and tuple(t.shape[1:]) != tuple(shape[1:]):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
 def rope_table(positions, rot, base=10000.0, scaling="none", factor=1.0, original=0, low=1.0, high=32.0,
                amplitude=1.0, device="cuda", stream=None):
     """Table of rotations, fp32 [positions, rot/2, 2] (see qlora_rope_table).
@@ -179,12 +191,12 @@ def kv_read(cache, slots, k_out=None, v_out=None, stream=None):
         k_out = (cache.k.new_empty(shape, dtype=torch.bfloat16) if stream is None
                  else _empty(shape, torch.bfloat16, cache.k.device, stream))
     else:
-        _need(_dev(k_out, torch.bfloat16, "k_out"), T * cache.heads * cache.dim, "k_out")
+        _given(k_out, shape, torch.bfloat16, "k_out")
     if v_out is None:
         v_out = (cache.k.new_empty(shape, dtype=torch.bfloat16) if stream is None
                  else _empty(shape, torch.bfloat16, cache.k.device, stream))
     else:
-        _need(_dev(v_out, torch.bfloat16, "v_out"), T * cache.heads * cache.dim, "v_out")
+        _given(v_out, shape, torch.bfloat16, "v_out")
     _check(lib().qlora_kv_read(cache._desc, T, slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), _stream(stream)))
     return k_out, v_out
 
@@ -222,13 +234,13 @@ def attend_paged(q, cache, pages, starts, lengths, max_new, max_len, scale=None,
         out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
                else _empty(q.shape, q.dtype, q.device, stream))
     else:
-        _need(_dev(out, torch.bfloat16, "out"), T * Hq * D, "out")
+        _given(out, (T, Hq, D), torch.bfloat16, "out")
     if lse is True:
         lse = q.new_empty((T, Hq), dtype=torch.float32) if stream is None else _empty((T, Hq), torch.float32, q.device, stream)
     elif lse is False or lse is None:
         lse = None
     else:
-        _need(_dev(lse, torch.float32, "lse"), T * Hq, "lse")
+        _given(lse, (T, Hq), torch.float32, "lse")
     nbytes = attend_paged_workspace_bytes(cache, T, Hq, B, max_new, max_len, causal, window)
     workspace = _workspace(nbytes, q.device, workspace, stream)
     _check(lib().qlora_attend_paged(cache._desc, T, _heads(q, "q"), B, pages.data_ptr(), pages.shape[1],

@@ -215,8 +215,9 @@ def _empty(shape, dtype, device, stream):
 
 
 def device_status(stream=None):
-    """Raise QLoRAError if a kernel's bounded wait ran out since the last
-    query (waits for the stream; clears the status)."""
+    """Raise QLoRAError if since the last query a kernel's bounded wait ran out or
+    a kernel met an index out of range in device memory (a page, slot, position,
+    length or start); waits for the stream and clears the status."""
     _check(lib().qlora_device_status(_stream(stream)))
 
 

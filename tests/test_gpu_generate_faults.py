@@ -221,3 +221,33 @@ def test_a_long_prompt_needs_no_workspace():
         assert np.all(np.abs(_host(out[i:i + 1]) - ref) <= mass * (2.0 ** -8 + 2.0 ** -13) + 2.0 ** -8 * np.abs(ref))
         assert np.all(np.abs(lse[i:i + 1].cpu().numpy() - rl) <= 2.0 ** -14)
     lib.device_status()
+
+
+def test_given_outputs_of_another_shape_are_refused():
+    """A buffer with the output's axes in another order would be filled as if
+    they were its own; longer and flat ones hold the rows in order."""
+    lib = _lib()
+    b = Batch([(3, 20), (2, 9)], 4, 2, 64, "int8", 16, seed=33)
+    want, want_lse = b.run()
+    bf16, f32 = dict(dtype=torch.bfloat16, device="cuda"), dict(dtype=torch.float32, device="cuda")
+    for shape in ((4, 5, 64), (5, 64, 4), (10, 2, 64)):
+        with pytest.raises(ValueError, match="out must be"):
+            b.run(out=torch.empty(shape, **bf16))
+    with pytest.raises(ValueError, match="lse must be"):
+        b.run(lse=torch.empty((4, 5), **f32))
+    with pytest.raises(ValueError, match="elements"):
+        b.run(out=torch.empty((4, 4, 64), **bf16))
+    for shape in ((5, 4, 64), (7, 4, 64), (5, 256), (2000,)):
+        out, lse = torch.empty(shape, **bf16), torch.empty(shape[:1] + (4,), **f32)
+        b.run(out=out, lse=lse)
+        assert torch.equal(out.view(-1)[:1280].view(torch.int16), want.view(-1).view(torch.int16))
+        assert torch.equal(lse.view(-1)[:20], want_lse.view(-1))
+    slots = torch.arange(6, device="cuda")
+    k, v = lib.kv_read(b.cache, slots)
+    with pytest.raises(ValueError, match="k_out must be"):
+        lib.kv_read(b.cache, slots, k_out=torch.empty((2, 6, 64), **bf16))
+    with pytest.raises(ValueError, match="v_out must be"):
+        lib.kv_read(b.cache, slots, v_out=torch.empty((64, 6, 2), **bf16))
+    longer = torch.empty((9, 2, 64), **bf16)
+    lib.kv_read(b.cache, slots, k_out=longer, v_out=torch.empty(6 * 128, **bf16))
+    assert torch.equal(longer[:6].view(torch.int16), k.view(torch.int16))
