@@ -50,8 +50,8 @@ __device__ __forceinline__ void pack_levels(const uint2 (&w)[4], bf16x8 (&out)[N
 // where the cache holds 8 or 16 bits (64 sequences of up to 8192 tokens, int8:
 // 650 MB in 144 us, 4.5 TB/s; 131071 keys of 8 heads 5.2 TB/s, bf16 5.8), the
 // lookups and the instructions of a step where it holds 4 (131071 NF4 keys:
-// 143 MB in 43 us, 3.3 TB/s; Int4 37 us; int8 39 us when the rows come from the
-// caches).
+// 143 MB in 42 us, 3.4 TB/s; Int4 37 us; int8 39 us when the rows come from the
+// caches; the join of 5 us is not in these).
 //
 // S^T = K Q^T by 16x16x32 MFMAs: lane (r = lane & 15, g = lane >> 4) loads the
 // contiguous dims [g DP/4, (g + 1) DP/4) of key r (of each 16-key block) and
@@ -629,9 +629,13 @@ Plan make_plan(const AttendProblem& p) {
   const int64_t group = p.q.heads / p.pool.heads, rows = p.max_new * group;
   r.tile = rows > 32;
   // Quantized rows are widened once per tile: 256 rows share that where there
-  // are more than 128 (the chunks below: 137 -> 132 us with int8, 166 -> 135
-  // with NF4); bf16 rows need none of it, and two smaller workgroups of a CU
-  // overlap their matrix and vector phases.
+  // are more than 128; bf16 rows need none of it, and two smaller workgroups of a
+  // CU overlap their matrix and vector phases.  us with 128 and 256 rows, 4
+  // sequences of n tokens over 2048, 32 heads: n = 129 int8 69 64, NF4 71 61, FP4
+  // 73 67; 200: 68 71, 74 72, 75 76; 250: 74 77, 78 78, 79 82; 300: 99 98, 105
+  // 100, 109 106; 500: 115 111, 125 112, 125 115.  Where there are few workgroups
+  // the larger tiles lose: 33 tokens of 64 heads over 8192 keys of 8, int8 40
+  // 54, NF4 44 56.
   r.tile_rows = r.tile ? (rows > 128 && p.pool.type != kKVBF16 && p.pool.dim <= 128 ? 256 : 128) : rows > 16 && p.pool.dim <= 128 ? 32 : 16;
   r.tiles = std::max<int64_t>(1, (rows + r.tile_rows - 1) / r.tile_rows);
   // Keys that a tile can see (`reach`), from a multiple of 16 on where a window

@@ -258,7 +258,9 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
           out[e] = *reinterpret_cast<const uint32_t*>(p);
         } else {
           // Rounded as the product level * scale: the scales differ from row
-          // to row, so the roundings do too and average out over the keys.
+          // to row, so the roundings do too and average out over the keys (512
+          // rows over 2048: off by 3.3e-3 of the norm, with exact levels 2.3e-3).
+          // Two values each would double the MFMAs of both products.
           const float2 f = *reinterpret_cast<const float2*>(p);
           out[e] = pack_bf16x2(f.x * sc, f.y * sc);
         }
@@ -438,7 +440,12 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     }
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      // The weights enter the second product as bf16, their sum stays fp32.
+      // The weights enter the second product as one bf16 value each (after the
+      // row's scale, where the rows are codes), their sum stays fp32.  As two,
+      // like in the kernel for few rows, outputs are as good as their own
+      // rounding (1.6e-3 of the norm, against 2.0e-3 to 2.4e-3 this way), but
+      // the second product's MFMAs double: 52 heads of 4096 rows 276 -> 357 us,
+      // 4 chunks of 512 over 4096, 32 heads, int8 190 -> 231, NF4 184 -> 226.
       float p[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) p[e] = s[n / 2][8 * (n % 2) + e];

@@ -12,11 +12,16 @@
 // it reads back as NaN instead of as a finite row.  One scale per row (not
 // per block of 64) lets attention apply it to whole scores and weights.
 //
-// Both kernels are bound by memory: 2 bytes per element on the dense side,
-// the row's codes and 4 bytes on the other.  2048 tokens of 32 heads of 128,
-// rotated and stored in NF4: 15 us (43 MB; 34 with a comparison per boundary
-// and a head per thread), read back 12 us; 4001 tokens of 8 heads, rotated, in
-// int8: 8 us, 9973 read back 16 us (61 MB).
+// Both kernels move 2 bytes per element on the dense side, the row's codes and
+// 4 bytes on the other.  Reading back and 8 and 16 bits are bound by memory:
+// 4096 tokens of 32 heads of 128 read back from bf16 in 25 us (5.3 TB/s), int8
+// 21 (4.9), NF4 20 (4.2), stored as bf16 34 (3.9, in scattered rows of 256
+// bytes), int8 27 (3.7).  A 4-bit write is bound by its vector instructions:
+// 2048 such tokens, rotated and stored in NF4, 15 us (43 MB; 34 with a
+// comparison per boundary and a head per thread) issue 4.9 M of them, which take
+// 19 k of the 31 k clocks that the kernel runs beyond an empty launch; its
+// lookups and their conflicts take 3 k.  4001 tokens of 8
+// heads, rotated, in int8: 8 us, 9973 read back 15 us (61 MB).
 #include <cmath>
 #include <mutex>
 
