@@ -631,11 +631,11 @@ Plan make_plan(const AttendProblem& p) {
   // Quantized rows are widened once per tile: 256 rows share that where there
   // are more than 128; bf16 rows need none of it, and two smaller workgroups of a
   // CU overlap their matrix and vector phases.  us with 128 and 256 rows, 4
-  // sequences of n tokens over 2048, 32 heads: n = 129 int8 69 64, NF4 71 61, FP4
-  // 73 67; 200: 68 71, 74 72, 75 76; 250: 74 77, 78 78, 79 82; 300: 99 98, 105
-  // 100, 109 106; 500: 115 111, 125 112, 125 115.  Where there are few workgroups
+  // sequences of n tokens over 2048, 32 heads: n = 129 int8 69 64, NF4 78 69, FP4
+  // 73 67; 200: 68 71, 77 76, 75 76; 250: 74 77, 81 83, 79 82; 300: 99 98, 110
+  // 106, 109 106; 500: 115 111, 128 116, 125 115.  Where there are few workgroups
   // the larger tiles lose: 33 tokens of 64 heads over 8192 keys of 8, int8 40
-  // 54, NF4 44 56.
+  // 54, NF4 47 60.
   r.tile_rows = r.tile ? (rows > 128 && p.pool.type != kKVBF16 && p.pool.dim <= 128 ? 256 : 128) : rows > 16 && p.pool.dim <= 128 ? 32 : 16;
   r.tiles = std::max<int64_t>(1, (rows + r.tile_rows - 1) / r.tile_rows);
   // Keys that a tile can see (`reach`), from a multiple of 16 on where a window

@@ -98,7 +98,7 @@ __device__ __forceinline__ float sum_groups(float x) {
 // 2^-8, the same way in every row, which a sum over 10^5 keys does not average
 // out (7 % of such an output's norm, measured); it enters as the sum of two
 // bf16 values (2^-16), each with its own MFMA, or in the tile kernel as the
-// rounded product with its row's scale.
+// product with its row's scale, rounded to fp16.
 enum Operand { kOpBF16, kOpINT8, kOpLevel, kOpLevel2 };
 template <int KT>
 constexpr int kBitsOf = KT == kOpBF16 ? 16 : KT == kOpINT8 ? 8 : 4;

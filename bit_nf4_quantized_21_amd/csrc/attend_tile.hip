@@ -32,6 +32,8 @@ namespace qlora {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(1))) void gptr_t;
 typedef __attribute__((address_space(3))) void lptr_t;
@@ -47,6 +49,33 @@ __device__ __forceinline__ int k_chunk(int key, int c) {
 template <int DP>
 __device__ __forceinline__ int v_chunk(int key, int c) {
   return c ^ (DP == 64 ? ((key >> 1) & 1) << 2 : (key & 3) << 2);
+}
+
+// Two fp32 as fp16, rounded to nearest even.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
+template <bool HALF>
+__device__ __forceinline__ f32x16 mfma_tile(bf16x8 a, bf16x8 b, f32x16 c) {
+  if constexpr (HALF) return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else return mfma32(a, b, c);
+}
+
+// Scales of magnitudes in [2^-5, 2^6) are used as they are, and so are 0 and what
+// is no finite number; others as part * 2^power with 1 <= |part| < 2, but power >=
+// -90.
+__device__ __forceinline__ bool usual_scales(float a, float b) {
+  return fmaxf(fabsf(a), fabsf(b)) < 64.0f && fminf(fabsf(a), fabsf(b)) >= 0.03125f;
+}
+struct SplitScale {
+  float part;
+  int power;
+};
+__device__ __forceinline__ SplitScale split_scale(float s) {
+  const int e = (int)(__float_as_uint(s) >> 23 & 255u) - 127;
+  const int power = usual_scales(s, s) || e == 128 || s == 0.0f ? 0 : max(e, -90);
+  return {ldexpf(s, -power), power};
 }
 
 // The sequence with the n-th largest length; of more than a wave holds, the
@@ -68,6 +97,20 @@ __device__ __forceinline__ int nth_longest(const AttendArgs& a, int n) {
 template <int OP, int DP, int WAVES, bool EXACT, bool LONG>
 __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_kernel(AttendArgs a) {
   constexpr bool CODES = OP == kOpINT8 || OP == kOpLevel;  // exact operands, scales on scores and weights
+  // NF4: fp16 operands, 8 times finer than bf16 (which left outputs off by 3.3e-3
+  // of the norm; now 1.75e-3, of which 1.66e-3 is their own rounding).  They are
+  // kept in range by powers of two: of a query's largest element, which goes to
+  // its scores, and of scales beyond the usual, of which a key's
+  // goes to its scores and a value's into the exponent of its weights.  The
+  // running maximum is then that of score + power, so the weights are in range
+  // for the values that they multiply, row by row, and their sum takes the power
+  // out again.  Weights are kept 2^UP higher, up to 2^15, so the least is 2^-35 of
+  // the largest: with usual scales what 10^5 keys lose by it stays below a bf16 unit
+  // of the output, whatever they hold.  (NF4 chunks and prompts take 5 to 8 % longer
+  // than with bf16 operands, half of it for the choice between scales: 4 chunks of
+  // 512 over 4096, 32 heads, 182 -> 193 us, 8192 tokens of a prompt 611 -> 652.)
+  constexpr bool HALF = OP == kOpLevel2;
+  constexpr float SLACK = HALF ? 4.0f : kSlack, UP = 15.0f - SLACK;
   constexpr int BITS = kBitsOf<OP>;
   constexpr bool ASYNC = OP == kOpBF16 && EXACT;         // rows go from memory to LDS as they are
   constexpr int NT = DP / 16, NB = DP / 32;
@@ -82,6 +125,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   __shared__ __align__(16) uint16_t s_k0[kTileKeys * DP], s_v0[kTileKeys * DP];
   __shared__ __align__(16) uint16_t s_k1[kTileKeys * DP], s_v1[kTileKeys * DP];
   __shared__ __align__(16) float s_sc[CODES ? 2 : 1][2][kTileKeys];
+  // HALF: the powers of each key's and value's scale (a byte each), and whether
+  // a wave staged one that is not 0.
+  __shared__ uint32_t s_power[HALF ? 2 : 1][HALF ? kTileKeys : 1];
+  __shared__ __align__(8) uint8_t s_odd[2][8];
   __shared__ __align__(16) uint8_t s_wild[2][kTileKeys];
   // Of the pages of the next kListKeys keys: their numbers, and where their rows
   // of this head start in the codes (bytes).
@@ -161,8 +208,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   const int wi_first = uniform_div(min(wrow, rows - 1), G), wi_last = uniform_div(min(rows, wrow + 32) - 1, G);
   const int w_lo = seen_lo(a, sq, wi_first), w_hi = wave_rows ? seen_hi(a, sq, wi_last) : 0;
   bf16x8 q[NT];
+  float row_scale = s2;  // HALF: of the row's scores
   {
     const uint16_t* p = a.q.data + (sq.first + qi) * a.q.token_stride + (int64_t)(h * G + qg) * a.q.head_stride;
+    uint32_t top = 0;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int d = t * 16 + h2 * 8;
@@ -170,6 +219,21 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
       if (ok && (EXACT || d < D)) w = *reinterpret_cast<const u32x4*>(p + d);
       w ^= flip;
       q[t] = as_bf16x8(w);
+      if constexpr (HALF)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
+    }
+    if constexpr (HALF) {
+      const auto x = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+      const int e = (int)(max(x[0], x[1]) >> 7), power = e == 255 ? 0 : max(e, 1) - 127;
+      row_scale = ldexpf(s2, power);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        u32x4 w = __builtin_bit_cast(u32x4, q[t]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(ldexpf(bf16_lo(w[e]), -power), ldexpf(bf16_hi(w[e]), -power));
+        q[t] = as_bf16x8(w);
+      }
     }
   }
   f32x16 o[NB];
@@ -257,12 +321,11 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
         if constexpr (OP == kOpLevel) {
           out[e] = *reinterpret_cast<const uint32_t*>(p);
         } else {
-          // Rounded as the product level * scale: the scales differ from row
-          // to row, so the roundings do too and average out over the keys (512
-          // rows over 2048: off by 3.3e-3 of the norm, with exact levels 2.3e-3).
-          // Two values each would double the MFMAs of both products.
+          // Rounded as the product of the level and the scale's part: that
+          // differs from row to row, so the roundings do too and average out
+          // over the keys.
           const float2 f = *reinterpret_cast<const float2*>(p);
-          out[e] = pack_bf16x2(f.x * sc, f.y * sc);
+          out[e] = pack_f16x2(f.x * sc, f.y * sc);
         }
       }
     }
@@ -276,9 +339,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     bool bad = false;
 #pragma unroll
     for (uint32_t& v : w) {
+      constexpr uint32_t EXPO = HALF ? 0x7C00u : 0x7F80u;
       uint32_t x = any ? v : 0u;
-      if ((x & 0x7F80u) == 0x7F80u) { x &= 0xFFFF0000u; bad = true; }
-      if ((x & 0x7F800000u) == 0x7F800000u) { x &= 0xFFFFu; bad = true; }
+      if ((x & EXPO) == EXPO) { x &= 0xFFFF0000u; bad = true; }
+      if ((x & EXPO << 16) == EXPO << 16) { x &= 0xFFFFu; bad = true; }
       v = x;
     }
     const uint64_t all = __ballot(bad) >> ((lane / PR) * PR);
@@ -287,6 +351,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   auto on_edge = [&](int j0) __attribute__((always_inline)) { return j0 < full_lo || j0 + kTileKeys > full_hi; };
   // What is left to do for a tile once its rows are here, before the barrier.
   auto store = [&](uint16_t* to_k, uint16_t* to_v, int buf, int j0) __attribute__((always_inline)) {
+    bool odd = false;
     if constexpr (!ASYNC) {
       const bool edge = on_edge(j0);
       if (stages)
@@ -294,8 +359,22 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
       for (int n = 0; n < NP; ++n) {
         const int key = wave_key + lane_key + RUN * n;
         uint32_t x[EL / 2], y[EL / 2];
-        widen(kr[n], OP == kOpLevel2 ? piece_ks[OP == kOpLevel2 ? n : 0] : 1.0f, x);
-        widen(vr[n], OP == kOpLevel2 ? piece_vs[OP == kOpLevel2 ? n : 0] : 1.0f, y);
+        float ks = 1.0f, vs = 1.0f;
+        if constexpr (HALF) {
+          ks = piece_ks[n];
+          vs = piece_vs[n];
+          uint32_t powers = 0;
+          if (__builtin_expect(__any(!usual_scales(ks, vs)), 0)) {
+            const SplitScale sk = split_scale(ks), sv = split_scale(vs);
+            ks = sk.part;
+            vs = sv.part;
+            powers = (sk.power & 0xFF) | (sv.power & 0xFF) << 8;
+            odd |= powers && j0 + key >= lo && j0 + key < hi;
+          }
+          if (pc == 0) s_power[buf][key] = powers;
+        }
+        widen(kr[n], ks, x);
+        widen(vr[n], vs, y);
         if (!CODES && edge) tame(y, buf, key, j0);
 #pragma unroll
         for (int c = 0; c < EL / 8; ++c) {
@@ -306,6 +385,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
               u32x4{y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]};
         }
       }
+    }
+    if constexpr (HALF) {
+      odd = __any(odd);
+      if (lane == 0) s_odd[buf][wave] = odd;
     }
     if constexpr (CODES) {
       if (wave == 0) {
@@ -344,7 +427,15 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     v_at[t] = key * DP + v_chunk<DP>(key, col / 8) * 8 + (col & 7);
   }
 
+  // What the exponents are taken relative to, for a maximum m.  (From 2^23 on m - UP
+  // is rounded by more than fp16 has room for; a score's own rounding is 1 there.)
+  auto reference = [&](float m) __attribute__((always_inline)) {
+    if constexpr (HALF) return m == -INFINITY ? 0.0f : fabsf(m) < 8388608.0f ? m - UP : m;
+    return m == -INFINITY ? 0.0f : m;
+  };
   auto compute = [&](const uint16_t* tk, const uint16_t* tv, int buf, int j0) __attribute__((always_inline)) {
+    uint64_t odd_waves = 0;
+    if constexpr (HALF) odd_waves = *reinterpret_cast<const uint64_t*>(s_odd[buf]);
     // Keys come from LDS two MFMA pairs ahead of their use.
     f32x16 s[2];
     u32x4 kf[3][2];
@@ -359,7 +450,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
       if (t + 2 < NT) read_k(t + 2);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) s[c] = mfma32(as_bf16x8(kf[t % 3][c]), q[t], t ? s[c] : f32x16{});
+      for (int c = 0; c < 2; ++c) s[c] = mfma_tile<HALF>(as_bf16x8(kf[t % 3][c]), q[t], t ? s[c] : f32x16{});
     }
     // The first values are on their way while the scores become weights.
     s16x4 vf[2][2][2];  // two dim blocks at a time
@@ -382,7 +473,22 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
           s[c][4 * i] *= f.x; s[c][4 * i + 1] *= f.y; s[c][4 * i + 2] *= f.z; s[c][4 * i + 3] *= f.w;
         }
     }
-    const float k2 = CODES ? 1.0f : s2;
+    // Score * k2 + power is what the exponent is taken of.
+    float k2 = CODES ? 1.0f : HALF ? row_scale : s2;
+    bool odd = false;
+    if constexpr (HALF) {
+      odd = __builtin_amdgcn_readfirstlane((uint32_t)odd_waves | (WAVES > 4 ? (uint32_t)(odd_waves >> 32) : 0u)) != 0;
+      if (__builtin_expect(odd, 0)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int power = (int)s_power[buf][32 * c + 8 * (i / 4) + i % 4 + 4 * h2];
+            s[c][i] = __builtin_fmaf(ldexpf(s[c][i], (int8_t)power), k2, (float)(int8_t)(power >> 8));
+          }
+        k2 = 1.0f;
+      }
+    }
     if (on_edge(j0)) {
       // Bounds of the keys that the lane's row sees, against the register's own
       // place 32 c + 8 (i / 4) + i % 4.
@@ -411,15 +517,15 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
       const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
       top = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])) * k2;
     }
-    if (__any(top > m + kSlack)) {
+    if (__any(top > m + SLACK)) {
       top = fmaxf(top, m);
-      const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+      const float f = top == -INFINITY ? 1.0f : m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(reference(m) - reference(top));
       l *= f;
 #pragma unroll
       for (int t = 0; t < NB; ++t) o[t] *= f;
       m = top;
     }
-    const float ref = m == -INFINITY ? 0.0f : m;
+    const float ref = reference(m);
     float sum = 0.0f;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
@@ -428,6 +534,14 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
         s[c][i] = __builtin_amdgcn_exp2f(CODES ? s[c][i] - ref : __builtin_fmaf(s[c][i], k2, -ref));
         sum += s[c][i];
       }
+    if (HALF && __builtin_expect(odd, 0)) {
+      sum = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          sum += ldexpf(s[c][i], -(int8_t)(s_power[buf][32 * c + 8 * (i / 4) + i % 4 + 4 * h2] >> 8));
+    }
     l += sum;
     if constexpr (CODES) {
 #pragma unroll
@@ -440,16 +554,17 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
     }
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      // The weights enter the second product as one bf16 value each (after the
-      // row's scale, where the rows are codes), their sum stays fp32.  As two,
-      // like in the kernel for few rows, outputs are as good as their own
-      // rounding (1.6e-3 of the norm, against 2.0e-3 to 2.4e-3 this way), but
-      // the second product's MFMAs double: 52 heads of 4096 rows 276 -> 357 us,
-      // 4 chunks of 512 over 4096, 32 heads, int8 190 -> 231, NF4 184 -> 226.
+      // The weights enter the second product as one bf16 (or fp16) value each,
+      // after the row's scale where the rows are codes; their sum stays fp32.
+      // As two bf16 values, like in the kernel for few rows, outputs are as good
+      // as their own rounding (1.6e-3 of the norm, against 2.0e-3 to 2.4e-3 this
+      // way), but the second product's MFMAs double: 52 heads of 4096 rows 276 ->
+      // 357 us, 4 chunks of 512 over 4096, 32 heads, int8 190 -> 231.
       float p[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) p[e] = s[n / 2][8 * (n % 2) + e];
-      const bf16x8 pb = to_bf16x8(p);
+      const bf16x8 pb = HALF ? as_bf16x8(pack_f16x2(p[0], p[1]), pack_f16x2(p[2], p[3]), pack_f16x2(p[4], p[5]), pack_f16x2(p[6], p[7]))
+                             : to_bf16x8(p);
 #pragma unroll
       for (int t = 0; t < NB; ++t) {
         const int i = (n * NB + t) / 2;
@@ -458,7 +573,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
           __builtin_amdgcn_sched_barrier(0);
         }
         const uint2 x = __builtin_bit_cast(uint2, vf[i % 2][t % 2][0]), y = __builtin_bit_cast(uint2, vf[i % 2][t % 2][1]);
-        o[t] = mfma32(as_bf16x8(x.x, x.y, y.x, y.y), pb, o[t]);
+        o[t] = mfma_tile<HALF>(as_bf16x8(x.x, x.y, y.x, y.y), pb, o[t]);
       }
     }
   };
@@ -497,6 +612,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[t][i] = __uint_as_float(0x7FC00000u);
   if (!ok) return;
+  if (HALF && m != -INFINITY) m = reference(m);  // what the sums are relative to
   const int Hq = H * G;
   const int64_t at = (sq.first + qi) * Hq + h * G + qg;
   if (hi - (lo & ~15) > a.chunk) {  // the other splits' part is to come

@@ -522,13 +522,15 @@ int qlora_kv_read(const qlora_kv_cache* cache, int64_t T, const int64_t* slots, 
  * Keys and values enter the products as bf16: bf16 rows, int8 codes and the
  * levels of Int4 and FP4 exactly (a row's scale multiplies whole scores and
  * weights, in fp32), NF4 as two bf16 values per level, or, in the kernel for
- * many rows, as the product level * scale rounded to bf16.  The weights enter
- * the second product as two bf16 values, in the kernel for many rows (more
- * than 32 rows of max_new * q heads / cache heads) as one.  So with few rows an
- * output is off by little more than its own rounding (1.6e-3 of the norm), with
- * many by 2.0e-3 to 2.4e-3, NF4 3.3e-3.
+ * many rows (more than 32 rows of max_new * q heads / cache heads), as the
+ * product level * scale rounded to fp16, beside a power of two.  The weights
+ * enter the second product as two bf16 values, in the kernel for many rows as
+ * one, with NF4 as one fp16 value.  So with few rows an output is off by little
+ * more than its own rounding (1.6e-3 of the norm), with many by 2.0e-3 to 2.4e-3,
+ * with NF4 1.75e-3.
  * The weights are not normalized before the second product and stay below 2^8:
- * values of 2^120 / (keys seen) and more may overflow to infinity.
+ * values of 2^120 / (keys seen) and more may overflow to infinity (not with NF4
+ * and many rows).
  * max_new * q heads must be below 2^30.  Deterministic: splits are joined in a
  * fixed order.
  */

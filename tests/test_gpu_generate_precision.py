@@ -7,8 +7,9 @@ import pytest
 
 import attention_bounds as bounds
 from oracle import attention as at
+from oracle import nf4
 from oracle.compare import ulp_bf16
-from test_gpu_generate import Batch, _host, _lib
+from test_gpu_generate import Batch, _dev, _host, _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +74,71 @@ def test_a_long_context_by_its_norm():
         # 32 splits of 8 waves: 13 steps to a wave, four matrix instructions to a step, each up to 8 additions.
         off = np.linalg.norm(out[0, x] - ref[0, x]) / np.linalg.norm(ref[0, x])
         assert off <= bounds.norm_factor("nf4", ratio, 512), (x, off)
+
+
+def _many(kv, n, m, hq, h, D, seed):
+    b = Batch([(n, m)], hq, h, D, kv, 16, seed=seed)
+    assert n * hq // h > 32                              # the kernel for many rows
+    return b
+
+
+@pytest.mark.parametrize("kv", at.KV_TYPES)
+@pytest.mark.parametrize("n,m,hq,h,D", [(100, 300, 2, 1, 64), (200, 1100, 4, 4, 128), (70, 700, 8, 2, 80), (150, 900, 2, 2, 256)])
+def test_many_rows_by_their_norm(n, m, hq, h, D, kv):
+    """The roundings of weights, keys and values are as good as independent of each other and of the outputs' own, so the
+    squares of their norms add up.  Rounding a number of b significant bits leaves on average 2^-b / sqrt(3) times 0.7 of it
+    (mantissas are spread over [1, 2)): the outputs' own is known; a weight in bf16 adds as much again (so sqrt(2), 1.5 with
+    its spread), while fp16 weights, keys and values (NF4) add 3 times an 8th of it, squared: 1.02, 1.2 with all else."""
+    b = _many(kv, n, m, hq, h, D, 60)
+    out, lse = b.run()
+    b.check(out, lse)
+    ref, _, _ = at.attend(b.q, b.k[0], b.v[0], D ** -0.5)
+    own = np.linalg.norm(nf4.bf16_round(ref.astype(np.float32)) - ref)
+    off = np.linalg.norm(_host(out) - ref)
+    assert off <= (1.2 if kv == "nf4" else 1.5) * own, off / own
+
+
+@pytest.mark.parametrize("kv", ["nf4", "int8", "bf16", "fp4"])
+@pytest.mark.parametrize("n,m", [(2, 300), (100, 300), (140, 1100)])
+@pytest.mark.parametrize("what", ["values", "keys", "queries", "all", "zeros", "huge values", "tiny values", "large scores"])
+def test_rows_of_every_size(what, n, m, kv):
+    """Scales from 2^-90 to 2^100, side by side: no operand may leave its range, and what a row sees most of decides how
+    exact it is, not what is largest."""
+    lib = _lib()
+    b = _many(kv, n, m, 4, 1, 64, 61) if n > 8 else Batch([(n, m)], 4, 1, 64, kv, 16, seed=61)
+    rng = np.random.Generator(np.random.PCG64(62))
+
+    def sizes(rows, lo, hi):
+        return np.exp2(rng.integers(lo, hi + 1, rows)).astype(np.float32)[:, None, None]
+    k, v = (nf4.bf16_round(rng.normal(size=(m, 1, 64)).astype(np.float32)) for _ in range(2))
+    if what in ("values", "all"):
+        v = v * sizes(m, -60, 40)
+    if what in ("keys", "all"):
+        k = k * sizes(m, -80, 2)
+    if what in ("queries", "all"):
+        b.q = nf4.bf16_round(b.q * sizes(n, -70, 3))
+    if what == "zeros":
+        k[rng.random(m) < 0.3] = 0
+        v[rng.random(m) < 0.3] = 0
+    if what == "huge values":
+        v = v * sizes(m, 80, 96)
+    if what == "tiny values":
+        v = v * sizes(m, -92, -80)
+    if what == "large scores":
+        k, b.q = k * np.float32(2.0 ** 14), nf4.bf16_round(b.q * np.float32(2.0 ** 12))
+    k, v = nf4.bf16_round(k.astype(np.float32)), nf4.bf16_round(v.astype(np.float32))
+    j = np.arange(m)
+    lib.kv_write(b.cache, _dev(k), _dev(v), torch.tensor(b.table[0, j // 16] * 16 + j % 16).cuda())
+    b.k, b.v = ([x] if kv == "bf16" else [at.stored_values(*at.quantize_rows(x, kv), kv)] for x in (k, v))
+    for kw in (dict(), dict(window=90), dict(causal=False)):
+        out, lse = b.run(**kw)
+        assert bool(torch.isfinite(out).all())
+        if what != "large scores":
+            b.check(out, lse, **kw)
+        else:                                            # a score's own rounding exceeds 1: one key takes all
+            hit = np.zeros(out.shape[0], bool)
+            o = _host(out)
+            for x in range(4):
+                near = np.abs(o[:, x, None] - b.v[0][None, :, 0]).max(-1) <= 2.0 ** -7 * np.abs(b.v[0][None, :, 0]).max(-1)
+                hit |= near.any(1)
+            assert hit.mean() > 0.9
