@@ -62,19 +62,19 @@ __device__ __forceinline__ f32x16 mfma_tile(bf16x8 a, bf16x8 b, f32x16 c) {
   else return mfma32(a, b, c);
 }
 
-// Scales of magnitudes in [2^-5, 2^6) are used as they are, and so are 0 and what
-// is no finite number; others as part * 2^power with 1 <= |part| < 2, but power >=
-// -90.
-__device__ __forceinline__ bool usual_scales(float a, float b) {
-  return fmaxf(fabsf(a), fabsf(b)) < 64.0f && fminf(fabsf(a), fabsf(b)) >= 0.03125f;
-}
+// Usual scales, used as they are: keys' from 2^-10 and below 2^15 (fp16 holds their
+// rows), values' from 2^-5 and below 2^6 (close enough to each other for fp16
+// weights).  So are 0 and what is no finite number; others are split as part *
+// 2^power with 1 <= |part| < 2, but power >= -90.
+__device__ __forceinline__ bool usual_key(float s) { return fabsf(s) >= 0.0009765625f && fabsf(s) < 32768.0f; }
+__device__ __forceinline__ bool usual_value(float s) { return fabsf(s) >= 0.03125f && fabsf(s) < 64.0f; }
 struct SplitScale {
   float part;
   int power;
 };
-__device__ __forceinline__ SplitScale split_scale(float s) {
+__device__ __forceinline__ SplitScale split_scale(float s, bool usual) {
   const int e = (int)(__float_as_uint(s) >> 23 & 255u) - 127;
-  const int power = usual_scales(s, s) || e == 128 || s == 0.0f ? 0 : max(e, -90);
+  const int power = usual || e == 128 || s == 0.0f ? 0 : max(e, -90);
   return {ldexpf(s, -power), power};
 }
 
@@ -108,7 +108,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
   // the largest: with usual scales what 10^5 keys lose by it stays below a bf16 unit
   // of the output, whatever they hold.  (NF4 chunks and prompts take 5 to 8 % longer
   // than with bf16 operands, half of it for the choice between scales: 4 chunks of
-  // 512 over 4096, 32 heads, 182 -> 193 us, 8192 tokens of a prompt 611 -> 652.)
+  // 512 over 4096, 32 heads, 182 -> 193 us, 244 where the scales are not the usual
+  // ones; 8192 tokens of a prompt 611 -> 652.)
   constexpr bool HALF = OP == kOpLevel2;
   constexpr float SLACK = HALF ? 4.0f : kSlack, UP = 15.0f - SLACK;
   constexpr int BITS = kBitsOf<OP>;
@@ -364,8 +365,9 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attend_tile_ker
           ks = piece_ks[n];
           vs = piece_vs[n];
           uint32_t powers = 0;
-          if (__builtin_expect(__any(!usual_scales(ks, vs)), 0)) {
-            const SplitScale sk = split_scale(ks), sv = split_scale(vs);
+          const bool k_fine = usual_key(ks), v_fine = usual_value(vs);
+          if (__builtin_expect(__any(!k_fine || !v_fine), 0)) {
+            const SplitScale sk = split_scale(ks, k_fine), sv = split_scale(vs, v_fine);
             ks = sk.part;
             vs = sv.part;
             powers = (sk.power & 0xFF) | (sv.power & 0xFF) << 8;
