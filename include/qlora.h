@@ -529,8 +529,9 @@ int qlora_kv_read(const qlora_kv_cache* cache, int64_t T, const int64_t* slots, 
  * more than its own rounding (1.6e-3 of the norm), with many by 2.0e-3 to 2.4e-3,
  * with NF4 1.75e-3.
  * The weights are not normalized before the second product and stay below 2^8:
- * values of 2^120 / (keys seen) and more may overflow to infinity (not with NF4
- * and many rows).
+ * values of 2^120 / (keys seen) and more may overflow to infinity.  With NF4 and
+ * many rows they may not, but weights below 2^-36 of a row's largest (of weight *
+ * scale where the scales are far apart) count as nothing there.
  * max_new * q heads must be below 2^30.  Deterministic: splits are joined in a
  * fixed order.
  */
