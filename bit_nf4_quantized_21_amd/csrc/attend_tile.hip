@@ -2,7 +2,7 @@
 // chunks of prompts, and single tokens of large head groups.
 //
 // A workgroup of four or eight waves owns 32 rows per wave and walks the keys
-// in tiles of 64 that it holds in LDS as bf16, two tiles deep: the next tile's
+// in tiles of 64 that it holds in LDS as bf16 (NF4: fp16), two tiles deep: the next tile's
 // rows are on their way while this one is used, straight to LDS where they are
 // bf16, else to registers, from where they are widened into the other half
 // before the one barrier of the step.
