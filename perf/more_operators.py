@@ -107,8 +107,9 @@ def work(case):
         return {"bytes": one["bytes"] + 2 * T * (K + N) + adapters, "flops": 8 * T * N * K + 12 * T * r * (K + N)}
     if case["op"] == "loss":
         T, K, V = (case[k] for k in "TKV")
-        return {"bytes": 2 * K * (T + V) + 16 * T + (2 * T * K if case["grad"] else 0),
-                "flops": (4 if case["grad"] else 2) * T * K * V}
+        learned = T - int(T * case["ignored"])  # the others' rows of X are not needed
+        return {"bytes": 2 * K * (learned + V) + 16 * T + (2 * T * K if case["grad"] else 0),
+                "flops": (4 if case["grad"] else 2) * learned * K * V}
     n = sum(_lengths(case))
     return {"bytes": n * ((4 if case["source"] == "float32" else 2) + 2), "flops": 3 * n}
 
@@ -244,7 +245,7 @@ def _plain_loss(s):
     lse = top + torch.log(torch.exp(z - top).sum(1, keepdim=True))
     loss = torch.where(real, (lse - z.gather(1, at))[:, 0], 0.0)
     count = real.sum().clamp(min=1)
-    out = {"loss": loss, "lse": lse[:, 0], "mean": (loss.double().sum() / count).float().view(1)}
+    out = {"loss": loss, "lse": torch.where(real, lse[:, 0], 0.0), "mean": (loss.double().sum() / count).float().view(1)}
     if s["grad"]:
         z = z.sub_(lse).exp_()
         z.scatter_add_(1, at, torch.full_like(lse, -1.0))
@@ -285,8 +286,9 @@ def run(state):
         if s["grad"]:
             out["dX"] = dX
         return out
-    norm = lib.clip_grads(s["grads"], s["max_norm"], out=s["out"])
-    return {"norm": norm, "out": s["flat"]}
+    if "set" not in s:  # the gradients keep their places from step to step
+        s["set"] = lib.GradSet(s["grads"], s["out"])
+    return {"norm": lib.clip_grads(s["set"], s["max_norm"]), "out": s["flat"]}
 
 
 # ---------------------------------------------------------------- 64 bits
@@ -313,7 +315,7 @@ def _exact_loss(s):
     t, n = s["targets"], s["targets"].shape[0]
     real = t >= 0
     out = {"loss": torch.zeros(n, dtype=torch.float64, device="cuda"),
-           "lse": torch.empty(n, dtype=torch.float64, device="cuda")}
+           "lse": torch.zeros(n, dtype=torch.float64, device="cuda")}
     dX = torch.zeros(s["X"].shape, dtype=torch.float64, device="cuda")
     w = s["W"].double()
     count = max(int(real.sum()), 1)
@@ -321,8 +323,9 @@ def _exact_loss(s):
         rows = slice(i, min(i + 1024, n))
         x, mine = s["X"][rows].double(), real[rows]
         logp = x @ w.t()
-        out["lse"][rows] = torch.logsumexp(logp, 1)
-        logp -= out["lse"][rows, None]
+        lse = torch.logsumexp(logp, 1)
+        out["lse"][rows] = torch.where(mine, lse, 0.0)  # tokens that are not learned have none
+        logp -= lse[:, None]
         at = t[rows].clamp(min=0)[:, None]
         out["loss"][rows] = torch.where(mine, -logp.gather(1, at)[:, 0], 0.0)
         if s["grad"]:
