@@ -9,3 +9,7 @@ from .qlora import (  # noqa: F401
 from .generate import (  # noqa: F401
     KV_TYPES, KVCache, attend_paged, attend_paged_workspace_bytes, kv_read, kv_write, rope, rope_table,
 )
+from .train import (  # noqa: F401
+    ACTS, GradSet, clip_grads, clip_grads_workspace_bytes, gated_bwd, gated_bwd_workspace_bytes, gated_fwd,
+    gated_fwd_workspace_bytes, head_loss, head_loss_workspace_bytes,
+)

@@ -56,6 +56,8 @@ struct FwdGemmParams {
   int tiles_n, tiles_m;  // filled by the launcher
   FwdGemmProblem prob[kGemmBatchMax];  // the batch (filled by the launcher for a single problem)
   int batch, tiles_per;  // problems, tiles per problem
+  uint16_t* saved;       // gated pair: [2][T][N] multipliers of the backward, or null
+  int act;               // gated pair: activation
 };
 
 struct DxGemmParams {
@@ -83,7 +85,8 @@ struct DxGemmParams {
 struct GemvPlan {
   int grid, nparts, ks;
 };
-GemvPlan gemv_plan(int64_t N, int64_t K, int64_t T, int32_t r);
+// `sets` > 1: as many linears' partials share a workgroup's LDS.
+GemvPlan gemv_plan(int64_t N, int64_t K, int64_t T, int32_t r, int sets = 1);
 
 // A group of small-token forwards served by one XA-partial launch and one
 // GEMV launch (T <= 16, shared T, r and s).  The launcher fills nparts, ks,
@@ -112,15 +115,26 @@ struct GemvGroupT {
   int count;
   int T, r, RP;          // RP = r rounded up to 64
   float s;
+  uint16_t* saved;       // gated pair: [2][T][N] multipliers of the backward, or null
+  int act;               // gated pair: activation
 };
 using GemvGroup = GemvGroupT<kGemvGroupMax>;
 hipError_t launch_gemv_group(GemvGroup g, const Codebook& cb, hipStream_t s);
+// A gated pair: L[0] is the gate, whose Y takes the block's output, L[1] the up
+// linear of the same shape and input.
+hipError_t launch_gemv_pair(GemvGroupT<2> g, const Codebook& cb, hipStream_t s);
 
 hipError_t launch_gemm_fwd(const FwdGemmParams& p, const Codebook& cb, hipStream_t s);
 // Batched launches: p.prob[0 .. p.batch) are filled by the caller (the
 // single-problem pointers of p are ignored); shapes, r and s are shared.
 hipError_t launch_gemm_fwd_batched(const FwdGemmParams& p, const Codebook& cb, hipStream_t s);
 hipError_t launch_gemm_dx_batched(const DxGemmParams& p, const Codebook& cb, hipStream_t s);
+// A gated pair: prob[0] is the gate, whose Y takes the block's output, prob[1]
+// the up linear of the same shape and input.
+hipError_t launch_gemm_fwd_pair(const FwdGemmParams& p, const Codebook& cb, hipStream_t s);
+// The sum of two linears' input gradients, written to prob[0].dX: one
+// contraction over both linears' rows.
+hipError_t launch_gemm_dx_pair(const DxGemmParams& p, const Codebook& cb, hipStream_t s);
 hipError_t launch_gemv_fwd(const FwdGemmParams& p, const Codebook& cb, hipStream_t s);
 hipError_t launch_gemm_dx(const DxGemmParams& p, const Codebook& cb, hipStream_t s);
 
@@ -128,5 +142,7 @@ hipError_t launch_gemm_dx(const DxGemmParams& p, const Codebook& cb, hipStream_t
 // sized from these).
 SplitPlan dx_plan(int64_t T, int64_t K, int64_t N, int batch = 1);
 SplitPlan fwd_plan(int64_t T, int64_t K, int64_t N, int batch = 1);
+SplitPlan dx_pair_plan(int64_t T, int64_t K, int64_t N);
+SplitPlan fwd_pair_plan(int64_t T, int64_t K, int64_t N);
 
 }  // namespace qlora

@@ -38,6 +38,10 @@
 //    token-tile-major tiles, so the dY rows of a token tile are fetched into
 //    that XCD's L2 once and re-read there by every k-tile (measured faster
 //    than k-tile-major, which shares the code columns instead).
+//
+// PAIR: the sum of two linears' input gradients (the gate and up linears of a
+// gated feed-forward block, which share their input): the contraction runs
+// over the rows of the first, then of the second, into the same accumulators.
 #include "common.hpp"
 #include "timing.hpp"
 #include "gemm.hpp"
@@ -72,6 +76,7 @@ __device__ __forceinline__ uint32_t swz(int row, int chunk) {
 
 }  // namespace
 
+template <bool PAIR>
 __global__ __launch_bounds__(256, 1) void gemm_dx_kernel(DxGemmParams p, Codebook cb) {
   __shared__ __align__(1024) unsigned char smem[kSmem];
   // Raw code tiles of two steps, each its own object so the compiler can
@@ -88,7 +93,6 @@ __global__ __launch_bounds__(256, 1) void gemm_dx_kernel(DxGemmParams p, Codeboo
   const int tile_g = __builtin_amdgcn_readfirstlane(it.tile), sidx = __builtin_amdgcn_readfirstlane(it.sidx);
   const int bat = __builtin_amdgcn_readfirstlane(tile_g / p.tiles_per);
   const int tile = tile_g - bat * p.tiles_per;
-  const DxGemmProblem& P = p.prob[bat];
   // Workgroup-uniform values kept in scalar registers (the buffer views
   // built from them must be uniform).
   const int tk = __builtin_amdgcn_readfirstlane(tile % p.tiles_k);
@@ -102,8 +106,15 @@ __global__ __launch_bounds__(256, 1) void gemm_dx_kernel(DxGemmParams p, Codeboo
   const int64_t k0 = (int64_t)tk * kTileK, t0 = (int64_t)tt * kTileT;
   const int64_t K2 = K / 2, bpr = K / 64;
   const int nsteps = (int)((N + 63) / 64);
-  const int jbeg = __builtin_amdgcn_readfirstlane(it.kbeg), jend = __builtin_amdgcn_readfirstlane(it.kend);
-  (void)nsteps;
+  const int ibeg = __builtin_amdgcn_readfirstlane(it.kbeg), iend = __builtin_amdgcn_readfirstlane(it.kend);
+
+  f32x16 acc[4][4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.0f;
 
   // dY staging: lane -> rows xr + 32 i of the tile, 16-byte chunk xc.
   const int xc = tid & 7, xr = tid >> 3;
@@ -115,6 +126,15 @@ __global__ __launch_bounds__(256, 1) void gemm_dx_kernel(DxGemmParams p, Codeboo
   const int64_t skb = k0 / 64 + sb;
   const bool sval = 64 * skb < K;
 
+  // MFMA operand r of a substep s: r < 4 the dY rows 128 wt + 32 r (B), else
+  // the W' rows 128 wk + 32 (r - 4) (A); lane half h takes n 8 (2s + h) ..
+  auto read_op = [&](int wbase, int dbase, int s, int r) -> bf16x8 {
+    return r < 4 ? *reinterpret_cast<const bf16x8*>(smem + dbase + swz(128 * wt + 32 * r + l32, 2 * s + h))
+                 : *reinterpret_cast<const bf16x8*>(smem + wbase + swz(128 * wk + 32 * (r - 4) + l32, 2 * s + h));
+  };
+  // Steps of this slice over one weight's rows (PAIR: the first weight's steps
+  // come before the second's).
+  auto contract = [&](const DxGemmProblem& P, int jbeg, int jend) __attribute__((always_inline)) {
   // Buffer views: loads past the end return zero.  Codes of rows n >= N
   // read zero and their scales are zero, so those W' rows vanish; k past K
   // has zero scales too.  dY rows are viewed from this tile's first row.
@@ -167,21 +187,6 @@ __global__ __launch_bounds__(256, 1) void gemm_dx_kernel(DxGemmParams p, Codeboo
   auto write_col = [&](int base, int hf, int c, const uint32_t(&col)[4]) {
     *reinterpret_cast<u32x4*>(smem + base + swz(8 * kq + 4 * hf + c, rg)) = u32x4{col[0], col[1], col[2], col[3]};
   };
-  // MFMA operand r of a substep s: r < 4 the dY rows 128 wt + 32 r (B), else
-  // the W' rows 128 wk + 32 (r - 4) (A); lane half h takes n 8 (2s + h) ..
-  auto read_op = [&](int wbase, int dbase, int s, int r) -> bf16x8 {
-    return r < 4 ? *reinterpret_cast<const bf16x8*>(smem + dbase + swz(128 * wt + 32 * r + l32, 2 * s + h))
-                 : *reinterpret_cast<const bf16x8*>(smem + wbase + swz(128 * wk + 32 * (r - 4) + l32, 2 * s + h));
-  };
-
-  f32x16 acc[4][4];
-#pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.0f;
-
   uint32_t cA[8], cB[8];    // codes of two steps, alternating
   u32x4 dyr[8];             // dY rows of the next step
   uint32_t qv[2];           // q8 / s2 loaded one step before their scale is stored
@@ -324,6 +329,22 @@ __global__ __launch_bounds__(256, 1) void gemm_dx_kernel(DxGemmParams p, Codeboo
 #undef QLORA_DX_STEP
 #undef QLORA_DX_SLICE
 #undef QLORA_DX_DECODE_SLOT
+  };
+  if constexpr (PAIR) {
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {
+      const int lo = ibeg - w * nsteps, hi = iend - w * nsteps;
+      const int jbeg = lo < 0 ? 0 : lo, jend = hi < nsteps ? hi : nsteps;
+      if (jbeg >= jend) continue;  // uniform
+      contract(p.prob[w], jbeg, jend);
+      // What was copied for steps past the end has landed before the next
+      // weight's codes are copied there.
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+    }
+  } else {
+    contract(p.prob[bat], ibeg, iend);
+  }
   __syncthreads();  // every wave is done with the buffers
 
   // Adapter term: A[k][j] (rows k) against the hi and lo rows of s G
@@ -334,6 +355,9 @@ __global__ __launch_bounds__(256, 1) void gemm_dx_kernel(DxGemmParams p, Codeboo
   // zero through an out-of-range offset.
   const int r = p.r;
   if (sidx == 0) {
+#pragma unroll 1
+  for (int w = 0; w < (PAIR ? 2 : 1); ++w) {
+    const DxGemmProblem& P = p.prob[PAIR ? w : bat];
     const rsrc_t ra = make_rsrc(P.A + k0 * r, (K - k0) * r * 2);
     const rsrc_t rgh = make_rsrc(P.Gh + t0 * p.RP, (T - t0) * p.RP * 2);
     const rsrc_t rgl = make_rsrc(P.Gl + t0 * p.RP, (T - t0) * p.RP * 2);
@@ -372,6 +396,7 @@ __global__ __launch_bounds__(256, 1) void gemm_dx_kernel(DxGemmParams p, Codeboo
       }
     }
   }
+  }
 
   if (it.S > 1 && !splitk_combine(acc, p.slots + (int64_t)it.ordinal * it.S * kSplitSlotFloats,
                                   p.counters + it.ordinal, p.counters + p.plan.nsplit() + it.ordinal, it.S, sidx,
@@ -398,17 +423,36 @@ __global__ __launch_bounds__(256, 1) void gemm_dx_kernel(DxGemmParams p, Codeboo
       }
   }
   __syncthreads();
+  uint16_t* const out = p.prob[bat].dX;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
     const int idx = 256 * i + tid, row = idx >> 5, c = idx & 31;
     const int64_t t = t0 + row, k = k0 + 8 * c;
     const u32x4 v = *reinterpret_cast<const u32x4*>(smem + row * 512 + ((c ^ (row & 31)) << 4));
-    if (t < T && k < K) *reinterpret_cast<u32x4*>(P.dX + t * K + k) = v;  // K % 64 == 0: chunks whole
+    if (t < T && k < K) *reinterpret_cast<u32x4*>(out + t * K + k) = v;  // K % 64 == 0: chunks whole
   }
 }
 
 SplitPlan dx_plan(int64_t T, int64_t K, int64_t N, int batch) {
   return make_split_plan((int64_t)batch * ((K + kTileK - 1) / kTileK) * ((T + kTileT - 1) / kTileT), (N + 63) / 64);
+}
+
+SplitPlan dx_pair_plan(int64_t T, int64_t K, int64_t N) {
+  return make_split_plan(((K + kTileK - 1) / kTileK) * ((T + kTileT - 1) / kTileT), 2 * ((N + 63) / 64));
+}
+
+hipError_t launch_gemm_dx_pair(const DxGemmParams& p0, const Codebook& cb, hipStream_t s) {
+  DxGemmParams p = p0;
+  p.batch = 1;
+  p.tiles_k = (int)((p.K + kTileK - 1) / kTileK);
+  p.tiles_t = (int)((p.T + kTileT - 1) / kTileT);
+  p.tiles_per = p.tiles_k * p.tiles_t;
+  p.plan = dx_pair_plan(p.T, p.K, p.N);
+  {
+    KernelTimer kt_("gated_gemm_dx_kernel", s);
+    hipLaunchKernelGGL(gemm_dx_kernel<true>, dim3(8 * p.plan.items), dim3(256), 0, s, p, cb);
+  }
+  return hipGetLastError();
 }
 
 hipError_t launch_gemm_dx(const DxGemmParams& p0, const Codebook& cb, hipStream_t s) {
@@ -426,7 +470,7 @@ hipError_t launch_gemm_dx_batched(const DxGemmParams& p0, const Codebook& cb, hi
   p.plan = dx_plan(p.T, p.K, p.N, p.batch);
   {
     KernelTimer kt_("gemm_dx_kernel", s);
-    hipLaunchKernelGGL(gemm_dx_kernel, dim3(8 * p.plan.items), dim3(256), 0, s, p, cb);
+    hipLaunchKernelGGL(gemm_dx_kernel<false>, dim3(8 * p.plan.items), dim3(256), 0, s, p, cb);
   }
   return hipGetLastError();
 }

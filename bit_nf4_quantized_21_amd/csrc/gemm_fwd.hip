@@ -41,7 +41,14 @@
 //  * Workgroup order is XCD-aware: each XCD works through a contiguous run of
 //    token-tile-major tiles, so an X tile is fetched into an XCD's L2 once and
 //    re-read from there by every n-tile.
+//
+// PAIR: the two linears of a gated feed-forward block (gate and up) in one
+// tile of 128 features x 256 tokens: each wave's two row groups are the same
+// 32 features of the gate's and of the up's weight, so both sums of an output
+// meet in one lane, and H = act(G) U (and the multipliers that the backward
+// needs) is computed from the fp32 sums; neither G nor U is written.
 #include "common.hpp"
+#include "gated.hpp"
 #include "gemm.hpp"
 #include "splitk.hpp"
 #include "timing.hpp"
@@ -55,7 +62,10 @@ constexpr int kStageBytes = kTileM * 128;  // one X stage: 256 rows x 64 bf16
 constexpr int kLutBytes = 4096;            // pair table at 0, codebook at 2048, split ticket at 2112
 }  // namespace
 
+template <bool PAIR>
 __global__ __launch_bounds__(256, 1) void gemm_fwd_kernel(FwdGemmParams p, Codebook cb) {
+  constexpr int NSET = PAIR ? 2 : 1;                 // weights of a tile
+  constexpr int TILE_N = PAIR ? kTileN / 2 : kTileN;  // features of a tile
   // LDS: the codebook pair table (with the 16-entry codebook and the split
   // ticket after it) and four X stages, each its own object so the compiler
   // can tell a stage being filled by buffer-to-LDS loads from the ones read.
@@ -89,7 +99,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fwd_kernel(FwdGemmParams p, Codeb
   // (LDS addresses of the buffer-to-LDS copies, M0) in scalar registers.
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, ml = lane & 31, h = lane >> 5;
   const int64_t T = p.T, K = p.K, N = p.N;
-  const int64_t n0 = (int64_t)tn * kTileN, m0 = (int64_t)tm * kTileM;
+  const int64_t n0 = (int64_t)tn * TILE_N, m0 = (int64_t)tm * kTileM;
   const int64_t K2 = K / 2, bpr = K / 64;
   const int nk = (int)(K / 64);
   const int kbeg = __builtin_amdgcn_readfirstlane(it.kbeg), kend = __builtin_amdgcn_readfirstlane(it.kend);
@@ -97,15 +107,20 @@ __global__ __launch_bounds__(256, 1) void gemm_fwd_kernel(FwdGemmParams p, Codeb
 
   // Buffer views of this tile's rows: reads past the last row return zero.
   const rsrc_t rx = make_rsrc(P.X + m0 * K, (T - m0) * K * 2);
-  const rsrc_t rc = make_rsrc(P.codes + n0 * K2, (N - n0) * K2);
-  const rsrc_t rq = make_rsrc(P.q8 + n0 * bpr, (N - n0) * bpr);
-  const rsrc_t rs = make_rsrc(P.s2, ((N * bpr + 255) / 256) * 4);
+  rsrc_t rcs[NSET], rqs[NSET], rss[NSET];
+#pragma unroll
+  for (int w = 0; w < NSET; ++w) {
+    const FwdGemmProblem& Pw = PAIR ? p.prob[w] : P;
+    rcs[w] = make_rsrc(Pw.codes + n0 * K2, (N - n0) * K2);
+    rqs[w] = make_rsrc(Pw.q8 + n0 * bpr, (N - n0) * bpr);
+    rss[w] = make_rsrc(Pw.s2, ((N * bpr + 255) / 256) * 4);
+  }
 
   int nl[2];
   bool nval[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    nl[g] = 64 * wave + 32 * g + ml;
+    nl[g] = PAIR ? 32 * wave + ml : 64 * wave + 32 * g + ml;
     nval[g] = n0 + nl[g] < N;
   }
 
@@ -123,21 +138,21 @@ __global__ __launch_bounds__(256, 1) void gemm_fwd_kernel(FwdGemmParams p, Codeb
   auto load_w_part = [&](int kb, u32x4(&c)[2], uint32_t(&q)[2], float(&sv)[2], int part) {
     const int g = part / 3;
     if (part % 3 == 0) {
-      c[g] = buf_load16(rc, (uint32_t)(nl[g] * K2 + kb * 32 + 16 * h));
+      c[g] = buf_load16(rcs[g * (NSET - 1)], (uint32_t)(nl[g] * K2 + kb * 32 + 16 * h));
     } else if (part % 3 == 1) {
-      q[g] = buf_load1(rq, (uint32_t)(nl[g] * bpr + kb));
+      q[g] = buf_load1(rqs[g * (NSET - 1)], (uint32_t)(nl[g] * bpr + kb));
     } else {
       const int64_t b = (n0 + nl[g]) * bpr + kb;
-      sv[g] = __uint_as_float(buf_load4(rs, (uint32_t)((b >> 8) * 4)));
+      sv[g] = __uint_as_float(buf_load4(rss[g * (NSET - 1)], (uint32_t)((b >> 8) * 4)));
     }
   };
   auto load_w = [&](int kb, u32x4(&c)[2], uint32_t(&q)[2], float(&sv)[2]) {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      c[g] = buf_load16(rc, (uint32_t)(nl[g] * K2 + kb * 32 + 16 * h));
-      q[g] = buf_load1(rq, (uint32_t)(nl[g] * bpr + kb));
+      c[g] = buf_load16(rcs[g * (NSET - 1)], (uint32_t)(nl[g] * K2 + kb * 32 + 16 * h));
+      q[g] = buf_load1(rqs[g * (NSET - 1)], (uint32_t)(nl[g] * bpr + kb));
       const int64_t b = (n0 + nl[g]) * bpr + kb;
-      sv[g] = __uint_as_float(buf_load4(rs, (uint32_t)((b >> 8) * 4)));
+      sv[g] = __uint_as_float(buf_load4(rss[g * (NSET - 1)], (uint32_t)((b >> 8) * 4)));
     }
   };
   auto lut8 = [&](uint32_t x, float(&f)[8]) { lut8_pairs(tbl, x, f); };
@@ -292,9 +307,12 @@ __global__ __launch_bounds__(256, 1) void gemm_fwd_kernel(FwdGemmParams p, Codeb
   // registers; the hi / lo tiles are copied by buffer-to-LDS loads straight
   // into the swizzled X-stage layout.
   if (sidx == 0) {
+#pragma unroll
+  for (int w = 0; w < NSET; ++w) {
+    const FwdGemmProblem& Pw = PAIR ? p.prob[w] : P;
     const int r = p.r;
-    const rsrc_t rh = make_rsrc(P.XAh + m0 * p.RP, (T - m0) * p.RP * 2);
-    const rsrc_t rl = make_rsrc(P.XAl + m0 * p.RP, (T - m0) * p.RP * 2);
+    const rsrc_t rh = make_rsrc(Pw.XAh + m0 * p.RP, (T - m0) * p.RP * 2);
+    const rsrc_t rl = make_rsrc(Pw.XAl + m0 * p.RP, (T - m0) * p.RP * 2);
     const int bjg = tid & 7, bng = tid >> 3;  // lane's 8 j and 8 n of the B tile
     const int64_t bn = n0 + 8 * bng;
     const int drow = lane >> 3, dphys = lane & 7;
@@ -303,7 +321,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fwd_kernel(FwdGemmParams p, Codeb
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int j = jb + 8 * bjg + i;
-        brow[i] = (j < r && bn < N) ? *reinterpret_cast<const u32x4*>(P.B + (int64_t)j * N + bn)
+        brow[i] = (j < r && bn < N) ? *reinterpret_cast<const u32x4*>(Pw.B + (int64_t)j * N + bn)
                                     : u32x4{0u, 0u, 0u, 0u};
       }
       __syncthreads();  // every wave is done with the stages
@@ -330,18 +348,20 @@ __global__ __launch_bounds__(256, 1) void gemm_fwd_kernel(FwdGemmParams p, Codeb
         bf16x8 aop[2];
 #pragma unroll
         for (int g = 0; g < 2; ++g)
-          aop[g] = *reinterpret_cast<const bf16x8*>(xring[0] + (64 * wave + 32 * g + ml) * 128 + (((4 * h + s) ^ sw) << 4));
+          aop[g] = *reinterpret_cast<const bf16x8*>(xring[0] + nl[g] * 128 + (((4 * h + s) ^ sw) << 4));
         read_x(1, s, xa);
         read_x(2, s, xb);
 #pragma unroll
         for (int mi = 0; mi < 8; ++mi)
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
+            if (PAIR && g != w) continue;
             acc[g][mi] = mfma32(aop[g], xa[mi], acc[g][mi]);
             acc[g][mi] = mfma32(aop[g], xb[mi], acc[g][mi]);
           }
       }
     }
+  }
   }
 
   if (it.S > 1) {
@@ -350,6 +370,56 @@ __global__ __launch_bounds__(256, 1) void gemm_fwd_kernel(FwdGemmParams p, Codeb
                         p.counters + p.plan.nsplit() + it.ordinal,
                         it.S, sidx, reinterpret_cast<int*>(tbl + 2112), p.status))
       return;
+  }
+
+  if constexpr (PAIR) {
+    // A lane holds G and U of token 32 mi + ml and features 32 wave + 8 q4 + 4 h
+    // + (0..3).  H, then P1, then P2 go through LDS as bf16 / 16-bit tiles of
+    // [256 tokens][128 features], 16-byte chunks XOR-ed with the row, so that 16
+    // lanes store one row of 256 bytes.
+    auto store_tile = [&](int half, uint16_t* out) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int idx = 256 * i + tid, row = idx >> 4, c = idx & 15;
+        const int64_t m = m0 + row, n = n0 + 8 * c;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(xring[2 * half + (i >> 3)] + (row & 127) * 256 + ((c ^ (row & 15)) << 4));
+        if (m < T && n < N) *reinterpret_cast<u32x4*>(out + m * N + n) = v;
+      }
+    };
+    auto put = [&](int half, int mi, int q4, uint32_t lo, uint32_t hi) {
+      const int row = 32 * (mi & 3) + ml, c = 4 * wave + q4;
+      *reinterpret_cast<uint2*>(xring[2 * half + (mi >> 2)] + row * 256 + ((c ^ (row & 15)) << 4) + 8 * h) = make_uint2(lo, hi);
+    };
+    const bool save = p.saved != nullptr;
+    uint32_t p2[8][4][2];
+    __syncthreads();  // every wave is done with the stages
+#pragma unroll
+    for (int mi = 0; mi < 8; ++mi)
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        GatedValues v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = gated_values(p.act, acc[0][mi][4 * q4 + e], acc[1][mi][4 * q4 + e]);
+        put(0, mi, q4, pack_bf16x2(v[0].h, v[1].h), pack_bf16x2(v[2].h, v[3].h));
+        if (save) {
+          put(1, mi, q4, multiplier_bits(v[0].p1) | multiplier_bits(v[1].p1) << 16,
+              multiplier_bits(v[2].p1) | multiplier_bits(v[3].p1) << 16);
+          p2[mi][q4][0] = multiplier_bits(v[0].p2) | multiplier_bits(v[1].p2) << 16;
+          p2[mi][q4][1] = multiplier_bits(v[2].p2) | multiplier_bits(v[3].p2) << 16;
+        }
+      }
+    __syncthreads();
+    store_tile(0, P.Y);
+    if (!save) return;
+    store_tile(1, p.saved);
+    __syncthreads();
+#pragma unroll
+    for (int mi = 0; mi < 8; ++mi)
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) put(0, mi, q4, p2[mi][q4][0], p2[mi][q4][1]);
+    __syncthreads();
+    store_tile(0, p.saved + T * N);
+    return;
   }
 
   // Y through LDS: D[n][m] of a 32x32 tile gives lane (ml, h) token
@@ -387,6 +457,24 @@ SplitPlan fwd_plan(int64_t T, int64_t K, int64_t N, int batch) {
   return make_split_plan((int64_t)batch * ((N + kTileN - 1) / kTileN) * ((T + kTileM - 1) / kTileM), K / 64);
 }
 
+SplitPlan fwd_pair_plan(int64_t T, int64_t K, int64_t N) {
+  return make_split_plan(((N + kTileN / 2 - 1) / (kTileN / 2)) * ((T + kTileM - 1) / kTileM), K / 64);
+}
+
+hipError_t launch_gemm_fwd_pair(const FwdGemmParams& p0, const Codebook& cb, hipStream_t s) {
+  FwdGemmParams p = p0;
+  p.batch = 1;
+  p.tiles_n = (int)((p.N + kTileN / 2 - 1) / (kTileN / 2));
+  p.tiles_m = (int)((p.T + kTileM - 1) / kTileM);
+  p.tiles_per = p.tiles_n * p.tiles_m;
+  p.plan = fwd_pair_plan(p.T, p.K, p.N);
+  {
+    KernelTimer kt_("gated_gemm_fwd_kernel", s);
+    hipLaunchKernelGGL(gemm_fwd_kernel<true>, dim3(8 * p.plan.items), dim3(256), 0, s, p, cb);
+  }
+  return hipGetLastError();
+}
+
 hipError_t launch_gemm_fwd(const FwdGemmParams& p0, const Codebook& cb, hipStream_t s) {
   FwdGemmParams p = p0;
   p.batch = 1;
@@ -402,7 +490,7 @@ hipError_t launch_gemm_fwd_batched(const FwdGemmParams& p0, const Codebook& cb, 
   p.plan = fwd_plan(p.T, p.K, p.N, p.batch);
   {
     KernelTimer kt_("gemm_fwd_kernel", s);
-    hipLaunchKernelGGL(gemm_fwd_kernel, dim3(8 * p.plan.items), dim3(256), 0, s, p, cb);
+    hipLaunchKernelGGL(gemm_fwd_kernel<false>, dim3(8 * p.plan.items), dim3(256), 0, s, p, cb);
   }
   return hipGetLastError();
 }

@@ -28,7 +28,12 @@
 // layer at once): each linear owns a contiguous range of workgroups, so the
 // launch and ramp are paid once for the whole group and the weight streams
 // of all its linears overlap.  A single linear is a group of one.
+//
+// PAIR: the gate and up linears of a gated feed-forward block.  A workgroup's
+// row groups alternate between the same 16 features of the two weights, so
+// both sums of an output end in one workgroup, which writes H = act(G) U.
 #include "common.hpp"
+#include "gated.hpp"
 #include "timing.hpp"
 #include "gemm.hpp"
 
@@ -147,34 +152,42 @@ struct ChunkRegs {
 // groups put more weight bytes in flight per wave (4 KiB per chunk at
 // RG = 4) and share each X load among more rows; the launcher picks RG so
 // the grid still fills the GPU.
-template <int RG, int NMAX>
+template <int RG, int NMAX, bool PAIR = false>
 __global__ __launch_bounds__(kThreads) void gemv_fwd_kernel(GemvGroupT<NMAX> G, Codebook cb) {
   constexpr int ROWS = 16 * RG;
+  constexpr int NSET = PAIR ? 2 : 1;
+  constexpr int FEAT = ROWS / NSET;  // features of a workgroup
+  static_assert(!PAIR || (NMAX == 2 && RG % 2 == 0), "a pair's row groups alternate");
   static_assert(kWaves * ROWS * 17 * 4 <= kPartLdsBytes, "wave sums fit the partial area");
   int li = 0;
 #pragma unroll
   for (int j = 1; j < NMAX; ++j)
-    if (j < G.count && (int)blockIdx.x >= G.L[j].wg_begin) li = j;
+    if (!PAIR && j < G.count && (int)blockIdx.x >= G.L[j].wg_begin) li = j;
   const GemvLinear& p = G.L[li];
   const int bid = (int)blockIdx.x - p.wg_begin;  // workgroup of this linear
   __shared__ __align__(4096) unsigned char tbl[2048];    // codebook pair table at LDS address 0
   // XA partials [nparts][T][RP] (copied in at the start); after they are
   // summed, the waves' partial outputs [kWaves][ROWS][17].
   __shared__ __align__(16) float ps[kPartLdsBytes / 4];
-  __shared__ __align__(16) float xa_s[16][kXaPitch];       // XA[t][j]
-  __shared__ __align__(16) uint16_t b_s[kMaxR * ROWS];     // B[j][n0 + nn] at j * ROWS + nn
+  __shared__ __align__(16) float xa_s[NSET][16][kXaPitch];      // XA[t][j]
+  __shared__ __align__(16) uint16_t b_s[NSET][kMaxR * FEAT];    // B[j][n0 + nn] at j * FEAT + nn
 
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int l16 = lane & 15, g = lane >> 4;
   const int64_t T = G.T, K = p.K, N = p.N;
   const int r = G.r, RP = G.RP;
-  const int64_t n0 = (int64_t)bid * ROWS;
+  const int64_t n0 = (int64_t)bid * FEAT;
   const int64_t K2 = K / 2, bpr = K / 64;
 
   const int64_t nchunk = (K + 127) / 128;
-  const rsrc_t rc = make_rsrc(p.codes, N * K2);
-  const rsrc_t rq = make_rsrc(p.q8, N * bpr);
-  const rsrc_t rs = make_rsrc(p.s2, ((N * bpr + 255) / 256) * 4);
+  rsrc_t rc[NSET], rq[NSET], rs[NSET];
+#pragma unroll
+  for (int w = 0; w < NSET; ++w) {
+    const GemvLinear& pw = PAIR ? G.L[w] : p;
+    rc[w] = make_rsrc(pw.codes, N * K2);
+    rq[w] = make_rsrc(pw.q8, N * bpr);
+    rs[w] = make_rsrc(pw.s2, ((N * bpr + 255) / 256) * 4);
+  }
   const rsrc_t rx = make_rsrc(p.X, T * K * 2);
   // This wave's chunks are c = wave + 8 m, m < nmine.
   const int nmine = nchunk > wave ? (int)((nchunk - wave + kWaves - 1) / kWaves) : 0;
@@ -189,11 +202,12 @@ __global__ __launch_bounds__(kThreads) void gemv_fwd_kernel(GemvGroupT<NMAX> G, 
     const bool kv = m < nmine && k0 < K;  // K % 64 == 0: a 32-k group is whole or absent
 #pragma unroll
     for (int rg = 0; rg < RG; ++rg) {
-      const int64_t n = n0 + 16 * rg + l16;
-      R.c[rg] = buf_load16(rc, off_if(kv, (uint32_t)(n * K2 + k0 / 2)));
+      const int64_t n = n0 + 16 * (rg / NSET) + l16;
+      const int w = rg % NSET;
+      R.c[rg] = buf_load16(rc[w], off_if(kv, (uint32_t)(n * K2 + k0 / 2)));
       const int64_t b = n * bpr + k0 / 64;
-      R.q[rg] = buf_load1(rq, off_if(kv, (uint32_t)b));
-      R.s2[rg] = __uint_as_float(buf_load4(rs, off_if(kv, (uint32_t)((b >> 8) * 4))));
+      R.q[rg] = buf_load1(rq[w], off_if(kv, (uint32_t)b));
+      R.s2[rg] = __uint_as_float(buf_load4(rs[w], off_if(kv, (uint32_t)((b >> 8) * 4))));
     }
     // Lanes of padding tokens (l16 >= T) read past the X view: zero, and no
     // memory traffic (an exec-masked load would cost more than this).
@@ -205,19 +219,22 @@ __global__ __launch_bounds__(kThreads) void gemv_fwd_kernel(GemvGroupT<NMAX> G, 
   // First the XA partials and the workgroup's B slice, copied straight into
   // LDS by buffer-to-LDS loads (no registers held; bytes past either view
   // read zero), then the codebook pair table, then the weight stream.
+  constexpr int kPartSet = kPartLdsBytes / 4 / NSET;  // floats of one linear's partials
   const int nvals = (int)T * RP, nparts = p.nparts;
-  {
-    const rsrc_t rp = make_rsrc(p.P, (int64_t)nparts * nvals * 4);
+#pragma unroll
+  for (int w = 0; w < NSET; ++w) {
+    const GemvLinear& pw = PAIR ? G.L[w] : p;
+    const rsrc_t rp = make_rsrc(pw.P, (int64_t)nparts * nvals * 4);
     const int units = (nparts * nvals * 4 + 15) / 16;
     for (int u0 = wave * 64; u0 < units; u0 += kThreads)
-      buf_load16_to_lds(rp, reinterpret_cast<unsigned char*>(ps) + u0 * 16, (uint32_t)((u0 + lane) * 16));
+      buf_load16_to_lds(rp, reinterpret_cast<unsigned char*>(ps + w * kPartSet) + u0 * 16, (uint32_t)((u0 + lane) * 16));
     // B row j, 16-byte unit cu of the workgroup's ROWS columns; rows j >= r
     // read zero.
-    const rsrc_t rb = make_rsrc(p.B, (int64_t)r * N * 2);
-    constexpr int kUnitsPerRow = ROWS / 8;
+    const rsrc_t rb = make_rsrc(pw.B, (int64_t)r * N * 2);
+    constexpr int kUnitsPerRow = FEAT / 8;
     for (int u0 = wave * 64; u0 < r * kUnitsPerRow; u0 += kThreads) {
       const int u = u0 + lane, j = u / kUnitsPerRow, cu = u % kUnitsPerRow;
-      buf_load16_to_lds(rb, reinterpret_cast<unsigned char*>(b_s) + u0 * 16,
+      buf_load16_to_lds(rb, reinterpret_cast<unsigned char*>(b_s[w]) + u0 * 16,
                         off_if(u < r * kUnitsPerRow, (uint32_t)(((int64_t)j * N + n0 + 8 * cu) * 2)));
     }
   }
@@ -260,15 +277,18 @@ __global__ __launch_bounds__(kThreads) void gemv_fwd_kernel(GemvGroupT<NMAX> G, 
   // also returns it.
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's copies into LDS
   __syncthreads();
-  for (int v = tid; v < nvals; v += kThreads) {
-    float x = ps[v];
-    for (int b = 1; b < nparts; ++b) x += ps[b * nvals + v];
-    const int t = v / RP, jj = v % RP;
-    if (jj < r) {
-      xa_s[t][jj] = x;
-      if (bid == 0) p.XA[t * r + jj] = x;
+#pragma unroll
+  for (int w = 0; w < NSET; ++w)
+    for (int v = tid; v < nvals; v += kThreads) {
+      const float* const part = ps + w * kPartSet;
+      float x = part[v];
+      for (int b = 1; b < nparts; ++b) x += part[b * nvals + v];
+      const int t = v / RP, jj = v % RP;
+      if (jj < r) {
+        xa_s[w][t][jj] = x;
+        if (bid == 0) (PAIR ? G.L[w] : p).XA[t * r + jj] = x;
+      }
     }
-  }
   __syncthreads();  // the partials are consumed: their area takes the wave sums
   // D[n][t]: lane holds column t = l16 and rows 16 rg + 4g + i.
   float* const red = ps;
@@ -278,42 +298,58 @@ __global__ __launch_bounds__(kThreads) void gemv_fwd_kernel(GemvGroupT<NMAX> G, 
     for (int i = 0; i < 4; ++i) red[(wave * ROWS + 16 * rg + 4 * g + i) * 17 + l16] = acc[rg][i];
   __syncthreads();
 
-  for (int o = tid; o < (int)T * ROWS; o += kThreads) {
-    const int t = o / ROWS, nn = o % ROWS;
+  for (int o = tid; o < (int)T * FEAT; o += kThreads) {
+    const int t = o / FEAT, nn = o % FEAT;
     if (n0 + nn < N) {
-      float y = 0.0f;
+      float ys[NSET];
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) y += red[(w * ROWS + nn) * 17 + t];
-      // s XA[t] . B[:, n]: r % 8 == 0; two interleaved sums, added at the end.
-      float lo0 = 0.0f, lo1 = 0.0f;
-      for (int j = 0; j < r; j += 8) {
-        const float4 a0 = *reinterpret_cast<const float4*>(&xa_s[t][j]);
-        const float4 a1 = *reinterpret_cast<const float4*>(&xa_s[t][j + 4]);
-        const uint16_t* bj = b_s + j * ROWS + nn;
-        lo0 += a0.x * bf16_to_f32(bj[0 * ROWS]);
-        lo1 += a0.y * bf16_to_f32(bj[1 * ROWS]);
-        lo0 += a0.z * bf16_to_f32(bj[2 * ROWS]);
-        lo1 += a0.w * bf16_to_f32(bj[3 * ROWS]);
-        lo0 += a1.x * bf16_to_f32(bj[4 * ROWS]);
-        lo1 += a1.y * bf16_to_f32(bj[5 * ROWS]);
-        lo0 += a1.z * bf16_to_f32(bj[6 * ROWS]);
-        lo1 += a1.w * bf16_to_f32(bj[7 * ROWS]);
+      for (int set = 0; set < NSET; ++set) {
+        const int row = PAIR ? 32 * (nn / 16) + 16 * set + nn % 16 : nn;
+        float y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) y += red[(w * ROWS + row) * 17 + t];
+        // s XA[t] . B[:, n]: r % 8 == 0; two interleaved sums, added at the end.
+        float lo0 = 0.0f, lo1 = 0.0f;
+        for (int j = 0; j < r; j += 8) {
+          const float4 a0 = *reinterpret_cast<const float4*>(&xa_s[set][t][j]);
+          const float4 a1 = *reinterpret_cast<const float4*>(&xa_s[set][t][j + 4]);
+          const uint16_t* bj = b_s[set] + j * FEAT + nn;
+          lo0 += a0.x * bf16_to_f32(bj[0 * FEAT]);
+          lo1 += a0.y * bf16_to_f32(bj[1 * FEAT]);
+          lo0 += a0.z * bf16_to_f32(bj[2 * FEAT]);
+          lo1 += a0.w * bf16_to_f32(bj[3 * FEAT]);
+          lo0 += a1.x * bf16_to_f32(bj[4 * FEAT]);
+          lo1 += a1.y * bf16_to_f32(bj[5 * FEAT]);
+          lo0 += a1.z * bf16_to_f32(bj[6 * FEAT]);
+          lo1 += a1.w * bf16_to_f32(bj[7 * FEAT]);
+        }
+        const float lo = lo0 + lo1;
+        y += G.s * lo;
+        ys[set] = y;
       }
-      const float lo = lo0 + lo1;
-      y += G.s * lo;
-      const uint32_t v = pack_bf16x2(y, 0.0f);
-      p.Y[(int64_t)t * N + n0 + nn] = (uint16_t)(v & 0xFFFF);
+      const int64_t at = (int64_t)t * N + n0 + nn;
+      if constexpr (PAIR) {
+        const GatedValues v = gated_values(G.act, ys[0], ys[1]);
+        p.Y[at] = (uint16_t)(pack_bf16x2(v.h, 0.0f) & 0xFFFF);
+        if (G.saved) {
+          G.saved[at] = (uint16_t)multiplier_bits(v.p1);
+          G.saved[T * N + at] = (uint16_t)multiplier_bits(v.p2);
+        }
+      } else {
+        const uint32_t v = pack_bf16x2(ys[0], 0.0f);
+        p.Y[at] = (uint16_t)(v & 0xFFFF);
+      }
     }
   }
 }
 
-GemvPlan gemv_plan(int64_t N, int64_t K, int64_t T, int32_t r) {
+GemvPlan gemv_plan(int64_t N, int64_t K, int64_t T, int32_t r, int sets) {
   GemvPlan g{};
   g.grid = (int)((N + kRowsPerWG - 1) / kRowsPerWG);
   const int64_t RP = (r + 63) / 64 * 64;
   int64_t np = (K + 127) / 128;  // slices of at least 128 k
   // the partials of all slices must fit the GEMV's LDS area
-  int64_t cap = (int64_t)(kPartLdsBytes / 4) / (T * RP);
+  int64_t cap = (int64_t)(kPartLdsBytes / 4 / sets) / (T * RP);
   if (cap > kMaxParts) cap = kMaxParts;
   if (np > cap) np = cap;
   if (np < 1) np = 1;
@@ -384,6 +420,33 @@ hipError_t launch_gemv_group(GemvGroup g, const Codebook& cb, hipStream_t s) {
     return launch_gemv_kernels(g1, parts, wg, RG, cb, s);
   }
   return launch_gemv_kernels(g, parts, wg, RG, cb, s);
+}
+
+hipError_t launch_gemv_pair(GemvGroupT<2> g, const Codebook& cb, hipStream_t s) {
+  // Row groups per workgroup as in launch_gemv_group; two at least, one of
+  // each weight.
+  GemvLinear& a = g.L[0];
+  const int RG = (a.N + 31) / 32 >= 1024 ? 4 : 2;
+  const GemvPlan pl = gemv_plan(a.N, a.K, g.T, g.r, 2);
+  for (int i = 0; i < 2; ++i) {
+    g.L[i].nparts = pl.nparts;
+    g.L[i].ks = pl.ks;
+    g.L[i].wg_begin = 0;
+    g.L[i].part_begin = i * pl.nparts;
+  }
+  {
+    KernelTimer kt_("xa_partial_kernel", s);
+    hipLaunchKernelGGL(xa_partial_kernel<2>, dim3(2 * pl.nparts), dim3(512), 0, s, g);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  {
+    KernelTimer kt_("gated_gemv_kernel", s);
+    const int feat = 8 * RG, wg = (int)((a.N + feat - 1) / feat);
+    if (RG == 4) hipLaunchKernelGGL((gemv_fwd_kernel<4, 2, true>), dim3(wg), dim3(kThreads), 0, s, g, cb);
+    else hipLaunchKernelGGL((gemv_fwd_kernel<2, 2, true>), dim3(wg), dim3(kThreads), 0, s, g, cb);
+  }
+  return hipGetLastError();
 }
 
 hipError_t launch_gemv_fwd(const FwdGemmParams& p, const Codebook& cb, hipStream_t s) {

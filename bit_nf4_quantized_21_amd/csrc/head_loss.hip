@@ -1,0 +1,673 @@
+// Softmax cross entropy of tokens over a large vocabulary, with its gradient,
+// without keeping the logits (gfx950, bf16 MFMA 32x32x16).
+//
+//   z_j = x . w_j,  loss = log sum_j exp(z_j) - z_t,
+//   dx = g (sum_{j != t} p_j w_j  -  (1 - p_t) w_t),   p = softmax(z)
+//
+// x: a token's last hidden state, W [V,K] the head, which is frozen as every
+// base weight of a model trained by adapters, so it gets no gradient.
+//
+// Two matrix products, not three: the exponentials are taken relative to a
+// reference that is known before the logits are, so the first product writes
+// exp(z_j - ref) in bf16 at once and the second multiplies it by W; what the
+// sum and its scale are is applied to the result.  The reference is the
+// target's own logit (one dot product per token).  Tiles whose largest logit
+// is more than kLift above it take their own maximum and are reported; a
+// small kernel then brings their rows to one reference again.  So a step
+// costs 4 T K V operations where a loss and a later gradient that recomputes
+// the logits would cost 6, and the target's term is left out of the
+// exponentials: its weight 1 - p_t is the sum of the others, which keeps its
+// digits for tokens that are nearly certain.
+//
+// The vocabulary is taken in pieces whose exponentials fit kPieceBytes, and
+// tokens in blocks of kBlockTokens.  Tokens whose target is negative are not
+// learned: the others are listed first, and only they are multiplied.
+//
+// Exponentials enter the second product as bf16, so dx is off by 1.7e-3 (half
+// a bf16 step, root mean square) of the sum of p_j w_j beside its own rounding;
+// logits, sums and the products' accumulation are fp32.
+#include "common.hpp"
+#include "device_state.hpp"
+#include "timing.hpp"
+#include "train.hpp"
+
+namespace qlora {
+
+namespace {
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int64_t kBlockTokens = 4096;
+constexpr int64_t kPieceBytes = int64_t(64) << 20;
+constexpr float kLift = 40.0f;       // e^40 leaves e^48 of fp32's range for sums and weights
+constexpr float kLog2e = 1.4426950408889634f;
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+
+// Everything a step needs, by value.
+struct Loss {
+  HeadLossArgs a;
+  int32_t* list;    // [T] tokens that are learned, ascending
+  int32_t* count;   // [1] their number
+  float* tz;        // [block] the target's logit
+  float* ref;       // [block] what the exponentials are relative to
+  int32_t* lifted;  // [block] the largest logit of a lifted tile, as an ordered integer
+  int32_t* flags;   // [blocks * pieces] whether any tile of the piece was lifted
+  float2* stats;    // [block][nstat] (reference, sum) of each row and stretch of kStat columns
+  uint16_t* P;      // [block][piece] exponentials
+  float* acc;       // [slabs][block][K] sum of exponentials times W
+  int64_t block;    // tokens of a block
+  int64_t piece;    // columns of a piece, a multiple of 256
+  int32_t pieces;
+  int32_t nstat;
+  int32_t slabs;    // at most
+  int* status;
+};
+
+// Floats as integers in the same order (finite ones and infinities).
+__device__ __forceinline__ int32_t ordered(float x) {
+  const int32_t i = (int32_t)__float_as_uint(x);
+  return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float from_ordered(int32_t i) { return __uint_as_float((uint32_t)(i ^ ((i >> 31) & 0x7FFFFFFF))); }
+constexpr int32_t kNotLifted = INT32_MIN;
+
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// Rows of block b that are learned.
+__device__ __forceinline__ int rows_of(const Loss& L, int64_t b) {
+  const int64_t left = (int64_t)__builtin_amdgcn_readfirstlane(*L.count) - b * L.block;
+  return left < 0 ? 0 : left < L.block ? (int)left : (int)L.block;
+}
+}  // namespace
+
+// The learned tokens in ascending order, their number, and zeroed flags.  One
+// workgroup: the targets are 8 bytes a token.
+__global__ __launch_bounds__(1024) void head_select_kernel(Loss L, int nflags) {
+  __shared__ int wave_n[16];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  for (int i = tid; i < nflags; i += 1024) L.flags[i] = 0;
+  int base = 0;
+  bool bad = false;
+  for (int64_t t0 = 0; t0 < L.a.T; t0 += 1024) {
+    const int64_t t = t0 + tid;
+    const int64_t y = t < L.a.T ? L.a.targets[t] : -1;
+    bad |= y >= L.a.V;
+    const bool on = y >= 0 && y < L.a.V;
+    const uint64_t m = __ballot(on);
+    __syncthreads();
+    if (lane == 0) wave_n[wave] = __popcll(m);
+    __syncthreads();
+    int before = base, all = 0;
+    for (int w = 0; w < 16; ++w) {
+      before += w < wave ? wave_n[w] : 0;
+      all += wave_n[w];
+    }
+    if (on) L.list[before + __popcll(m & ((1ull << lane) - 1))] = (int32_t)t;
+    base += all;
+  }
+  if (bad) atomicOr(L.status, kStatusIndex);
+  if (tid == 0) *L.count = base;
+}
+
+// The target's logit of each learned token of a block: one wave per token.
+__global__ __launch_bounds__(256) void head_target_kernel(Loss L, int b) {
+  const int i = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (i >= rows_of(L, b)) return;
+  const int64_t K = L.a.K, t = L.list[b * L.block + i];
+  const uint16_t* x = L.a.X + t * K;
+  const uint16_t* w = L.a.W + L.a.targets[t] * K;
+  float sum = 0.0f;
+  for (int64_t k = lane * 8; k < K; k += 512) {
+    const u32x4 xv = *reinterpret_cast<const u32x4*>(x + k), wv = *reinterpret_cast<const u32x4*>(w + k);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum += bf16_lo(xv[q]) * bf16_lo(wv[q]) + bf16_hi(xv[q]) * bf16_hi(wv[q]);
+  }
+#pragma unroll
+  for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  if (lane == 0) {
+    L.tz[i] = sum;
+    L.ref[i] = sum;
+    L.lifted[i] = kNotLifted;
+  }
+}
+
+// Tile shapes of the two products by the tokens of a tile.
+template <int BT>
+struct Shape;
+template <>
+struct Shape<256> {
+  static constexpr int kWaves = 8, BV = 256, WV = 2, WT = 4;    // logits: vocabulary rows, waves along them and tokens
+  static constexpr int BK = 256, GT = 2, GK = 4;                // gradient: columns of W, waves along tokens and them
+};
+template <>
+struct Shape<64> {
+  static constexpr int kWaves = 4, BV = 128, WV = 4, WT = 1;
+  static constexpr int BK = 128, GT = 1, GK = 4;
+};
+
+// First product: the logits of BT tokens and BV vocabulary rows, and of them
+// the sums of exponentials (one per token and wave) and, for the gradient, the
+// exponentials themselves.
+template <int BT, bool GRAD>
+__global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_logits_kernel(Loss L, int b, int pc) {
+  using S = Shape<BT>;
+  constexpr int NW = S::kWaves, BV = S::BV, A = BV / S::WV / 32, B = BT / S::WT / 32;
+  constexpr int kStage = (BV + BT) * 128;
+  __shared__ __align__(1024) unsigned char st0[kStage], st1[kStage];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int l32 = lane & 31, h = lane >> 5, wv = wave % S::WV, wt = wave / S::WV;
+  const int rows = rows_of(L, b);
+  const int tiles_t = (rows + BT - 1) / BT;
+  const int64_t K = L.a.K, V = L.a.V;
+  const int64_t c0 = (int64_t)pc * L.piece, c1 = c0 + L.piece < V ? c0 + L.piece : V;
+  const int tiles_v = (int)((c1 - c0 + BV - 1) / BV);
+  // The grid is sized for whole blocks; XCD x (workgroup b runs on b % 8)
+  // takes a run of tiles, token tiles innermost.
+  const int tiles = tiles_t * tiles_v, per = (tiles + 7) / 8;
+  const int at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || at >= tiles) return;
+  const int tt = __builtin_amdgcn_readfirstlane(at % tiles_t), tv = __builtin_amdgcn_readfirstlane(at / tiles_t);
+  const int64_t v0 = c0 + (int64_t)tv * BV;
+  const int r0 = tt * BT;
+
+  const rsrc_t rw = make_rsrc(L.a.W + v0 * K, (V - v0) * K * 2);
+  const rsrc_t rx = make_rsrc(L.a.X, L.a.T * K * 2);
+
+  // Staging: rows of 64 values (128 bytes), eight rows to an instruction; the
+  // 16-byte chunk index is XOR-ed with bits 1..3 of the row.
+  constexpr int NA = BV / 8 / NW, NB = BT / 8 / NW;
+  const int dr = lane >> 3, dc = lane & 7;
+  uint32_t ao[NA], bo[NB];
+#pragma unroll
+  for (int i = 0; i < NA; ++i) {
+    const int row = wave * (BV / NW) + 8 * i + dr;
+    ao[i] = (uint32_t)(row * K * 2 + ((dc ^ ((row >> 1) & 7)) << 4));
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int row = wave * (BT / NW) + 8 * i + dr;
+    const bool ok = r0 + row < rows;
+    const int64_t t = ok ? L.list[b * L.block + r0 + row] : 0;
+    bo[i] = ok ? (uint32_t)(t * K * 2 + ((dc ^ ((row >> 1) & 7)) << 4)) : kOffNone;
+  }
+  auto load = [&](unsigned char* st, int kb) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i) buf_load16_to_lds(rw, st + (wave * (BV / NW) + 8 * i) * 128, ao[i] + kb * 128);
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      buf_load16_to_lds(rx, st + (BV + wave * (BT / NW) + 8 * i) * 128, bo[i] + kb * 128);
+  };
+  f32x16 acc[A][B];
+#pragma unroll
+  for (int a = 0; a < A; ++a)
+#pragma unroll
+    for (int c = 0; c < B; ++c)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][c][e] = 0.0f;
+  const int sw = (l32 >> 1) & 7;
+  auto compute = [&](const unsigned char* st) {
+    const unsigned char* pa = st + (wv * (BV / S::WV) + l32) * 128;
+    const unsigned char* pb = st + (BV + wt * (BT / S::WT) + l32) * 128;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int ch = ((2 * s + h) ^ sw) << 4;
+      bf16x8 av[A], bv[B];
+#pragma unroll
+      for (int a = 0; a < A; ++a) av[a] = *reinterpret_cast<const bf16x8*>(pa + a * 4096 + ch);
+#pragma unroll
+      for (int c = 0; c < B; ++c) bv[c] = *reinterpret_cast<const bf16x8*>(pb + c * 4096 + ch);
+#pragma unroll
+      for (int a = 0; a < A; ++a)
+#pragma unroll
+        for (int c = 0; c < B; ++c) acc[a][c] = mfma32(av[a], bv[c], acc[a][c]);
+    }
+  };
+  const int nk = (int)(K / 64);
+  load(st0, 0);
+  for (int kb = 0; kb < nk; kb += 2) {
+    __syncthreads();  // step kb's rows have landed, st1 is free
+    if (kb + 1 < nk) load(st1, kb + 1);
+    compute(st0);
+    if (kb + 1 < nk) {
+      __syncthreads();
+      if (kb + 2 < nk) load(st0, kb + 2);
+      compute(st1);
+    }
+  }
+
+  // Lane (l32, h) holds of token 32 c + l32 the logits of rows 8 (e / 4) + 4 h
+  // + e % 4 of each 32-row block a.
+  const int nv = (int)(c1 - v0 < BV ? c1 - v0 : BV);  // rows that exist
+  if (GRAD) __syncthreads();                           // the stages take the exponentials
+#pragma unroll
+  for (int c = 0; c < B; ++c) {
+    const int rt = r0 + wt * (BT / S::WT) + 32 * c + l32;
+    const bool ok = rt < rows;
+    const int64_t t = ok ? L.list[b * L.block + rt] : 0;
+    const int64_t y = L.a.targets[t] - v0;               // the target's row of this tile, if there
+    const int own = y >= 0 && y < BV ? (int)y : -1;
+    const float base = ok ? L.ref[rt] : 0.0f;
+    float m = -INFINITY;
+#pragma unroll
+    for (int a = 0; a < A; ++a)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int v = wv * (BV / S::WV) + 32 * a + 8 * (e / 4) + 4 * h + e % 4;
+        if (v >= nv || v == own) acc[a][c][e] = -INFINITY;
+        m = fmaxf(m, acc[a][c][e]);
+      }
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    const bool lift = ok && m - base > kLift;
+    const float ref = lift ? m : base;
+    if (GRAD && lift && h == 0) {
+      atomicMax(L.lifted + rt, ordered(m));
+      atomicOr(L.flags + b * L.pieces + pc, 1);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int a = 0; a < A; ++a)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        acc[a][c][e] = exp_of(acc[a][c][e] - ref);
+        sum += acc[a][c][e];
+      }
+    sum += __shfl_xor(sum, 32, 64);
+    const int64_t stat = (v0 + wv * (BV / S::WV)) / (BV / S::WV);
+    if (ok && h == 0 && stat < L.nstat) L.stats[(int64_t)rt * L.nstat + stat] = make_float2(ref, sum);
+    if constexpr (GRAD) {
+      unsigned char* const row = (wt * (BT / S::WT) + 32 * c < BT / 2 ? st0 : st1) +
+                                 ((wt * (BT / S::WT) + 32 * c + l32) % (BT / 2)) * (BV * 2);
+#pragma unroll
+      for (int a = 0; a < A; ++a)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int ch = wv * (BV / S::WV / 8) + 4 * a + q;
+          *reinterpret_cast<uint2*>(row + ((ch ^ (l32 & (BV / 8 - 1))) << 4) + 8 * h) =
+              make_uint2(pack_bf16x2(acc[a][c][4 * q], acc[a][c][4 * q + 1]),
+                         pack_bf16x2(acc[a][c][4 * q + 2], acc[a][c][4 * q + 3]));
+        }
+    }
+  }
+  if constexpr (GRAD) {
+    __syncthreads();
+    constexpr int CH = BV / 8;  // 16-byte chunks of a row
+#pragma unroll
+    for (int i = 0; i < BT * CH / (64 * NW); ++i) {
+      const int idx = 64 * NW * i + tid, row = idx / CH, ch = idx % CH;
+      const unsigned char* p = (row < BT / 2 ? st0 : st1) + (row % (BT / 2)) * (BV * 2) + ((ch ^ (row & 31 & (CH - 1))) << 4);
+      if (r0 + row < rows)
+        *reinterpret_cast<u32x4*>(L.P + (int64_t)(r0 + row) * L.piece + (v0 - c0) + 8 * ch) =
+            *reinterpret_cast<const u32x4*>(p);
+    }
+  }
+}
+
+// Rows of a piece with a lifted tile: every stretch of exponentials and what
+// was summed before are brought to the row's new reference.
+__global__ __launch_bounds__(256) void head_lift_kernel(Loss L, int b, int pc, int stretch, int nslabs) {
+  if (L.flags[b * L.pieces + pc] == 0) return;
+  const int64_t K = L.a.K, c0 = (int64_t)pc * L.piece, c1 = c0 + L.piece < L.a.V ? c0 + L.piece : L.a.V;
+  const int rows = rows_of(L, b);
+  for (int i = blockIdx.x; i < rows; i += gridDim.x) {
+    const int32_t o = L.lifted[i];
+    const float old = L.ref[i], now = from_ordered(o);
+    __syncthreads();  // everyone has read them
+    if (o == kNotLifted || !(now > old)) continue;
+    for (int64_t c = c0 + threadIdx.x * 8; c < c1; c += 256 * 8) {
+      const float f = exp_of(L.stats[(int64_t)i * L.nstat + c / stretch].x - now);
+      u32x4* p = reinterpret_cast<u32x4*>(L.P + (int64_t)i * L.piece + (c - c0));
+      u32x4 v = *p;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = pack_bf16x2(bf16_lo(v[q]) * f, bf16_hi(v[q]) * f);
+      *p = v;
+    }
+    if (pc > 0) {
+      const float f = exp_of(old - now);
+      for (int s = 0; s < nslabs; ++s)
+        for (int64_t k = threadIdx.x; k < K; k += 256) L.acc[((int64_t)s * L.block + i) * K + k] *= f;
+    }
+    if (threadIdx.x == 0) {
+      L.ref[i] = now;
+      L.lifted[i] = kNotLifted;
+    }
+  }
+}
+
+// Second product: acc[row][k] += sum over the piece of P[row][v] W[v][k].  The
+// contraction is cut into slabs where the tiles alone would not fill the chip.
+template <int BT>
+__global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_grad_kernel(Loss L, int b, int pc, int nslabs) {
+  using S = Shape<BT>;
+  constexpr int NW = S::kWaves, BK = S::BK, A = BT / S::GT / 32, B = BK / S::GK / 32;
+  constexpr int kStage = BT * 128 + 64 * BK * 2;
+  __shared__ __align__(1024) unsigned char st0[kStage], st1[kStage];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int l32 = lane & 31, h = lane >> 5, wk = wave % S::GK, wt = wave / S::GK;
+  const int rows = rows_of(L, b);
+  const int tiles_t = (rows + BT - 1) / BT;
+  const int64_t K = L.a.K, V = L.a.V;
+  const int64_t c0 = (int64_t)pc * L.piece, c1 = c0 + L.piece < V ? c0 + L.piece : V;
+  const int tiles_k = (int)((K + BK - 1) / BK);
+  const int tiles = tiles_t * tiles_k * nslabs, per = (tiles + 7) / 8;
+  const int at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || at >= tiles) return;
+  const int tt = __builtin_amdgcn_readfirstlane(at % tiles_t);
+  const int tk = __builtin_amdgcn_readfirstlane(at / tiles_t % tiles_k);
+  const int sl = __builtin_amdgcn_readfirstlane(at / tiles_t / tiles_k);
+  const int r0 = tt * BT;
+  const int64_t k0 = (int64_t)tk * BK;
+  // This slab's steps of 64 rows of W.
+  const int steps = (int)((c1 - c0 + 63) / 64), each = (steps + nslabs - 1) / nslabs;
+  const int sbeg = sl * each < steps ? sl * each : steps, send = sbeg + each < steps ? sbeg + each : steps;
+
+  const rsrc_t rp = make_rsrc(L.P + (int64_t)r0 * L.piece, (rows - r0) * L.piece * 2);
+  constexpr int NP = BT / 8 / NW, ND = 64 * BK * 2 / 1024 / NW;  // instructions of a wave
+  constexpr int WCH = BK / 8;                                     // 16-byte chunks of a row of the W tile
+  uint32_t po[NP], wo[ND];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int row = wave * (BT / NW) + 8 * i + (lane >> 3);
+    po[i] = (uint32_t)(row * L.piece * 2 + (((lane & 7) ^ ((row >> 1) & 7)) << 4));
+  }
+#pragma unroll
+  for (int i = 0; i < ND; ++i) {
+    const int unit = (wave * ND + i) * 64 + lane, v = unit / WCH, ch = (unit % WCH) ^ ((v & 3) << 2);
+    wo[i] = (uint32_t)((v * K + 8 * ch) * 2);
+  }
+  auto load = [&](unsigned char* st, int sb) {
+    const int64_t v = c0 + (int64_t)sb * 64;
+    const rsrc_t rw = make_rsrc(L.a.W + v * K + k0, ((V - v) * K - k0) * 2);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) buf_load16_to_lds(rp, st + (wave * (BT / NW) + 8 * i) * 128, po[i] + sb * 128);
+#pragma unroll
+    for (int i = 0; i < ND; ++i) buf_load16_to_lds(rw, st + BT * 128 + (wave * ND + i) * 1024, wo[i]);
+  };
+  f32x16 acc[A][B];
+#pragma unroll
+  for (int a = 0; a < A; ++a)
+#pragma unroll
+    for (int c = 0; c < B; ++c)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][c][e] = 0.0f;
+  const int sw = (l32 >> 1) & 7;
+  // Of W's rows the lane names row (lane & 15) / 4 of four and four columns to
+  // a transposing read, and gets its own column of the four rows.
+  const int tr_row = 8 * h + ((lane & 15) >> 2), tr_col = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  auto compute = [&](const unsigned char* st) {
+    const unsigned char* pa = st + (wt * (BT / S::GT) + l32) * 128;
+    const unsigned char* pw = st + BT * 128;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      bf16x8 av[A], bv[B];
+#pragma unroll
+      for (int a = 0; a < A; ++a) av[a] = *reinterpret_cast<const bf16x8*>(pa + a * 4096 + (((2 * s + h) ^ sw) << 4));
+#pragma unroll
+      for (int c = 0; c < B; ++c) {
+        s16x4 part[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int v = 16 * s + 4 * e + tr_row, col = wk * (BK / S::GK) + 32 * c + tr_col;
+          part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_s16x4*)(pw + v * BK * 2 + (((col >> 3) ^ ((v & 3) << 2)) << 4) + (col & 7) * 2));
+        }
+        const uint2 lo = __builtin_bit_cast(uint2, part[0]), hi = __builtin_bit_cast(uint2, part[1]);
+        bv[c] = as_bf16x8(lo.x, lo.y, hi.x, hi.y);
+      }
+#pragma unroll
+      for (int a = 0; a < A; ++a)
+#pragma unroll
+        for (int c = 0; c < B; ++c) acc[a][c] = mfma32(av[a], bv[c], acc[a][c]);
+    }
+  };
+  if (sbeg < send) load(st0, sbeg);
+  for (int sb = sbeg; sb < send; sb += 2) {
+    __syncthreads();
+    if (sb + 1 < send) load(st1, sb + 1);
+    compute(st0);
+    if (sb + 1 < send) {
+      __syncthreads();
+      if (sb + 2 < send) load(st0, sb + 2);
+      compute(st1);
+    }
+  }
+  // Lane (l32, h) holds column 32 c + l32 of rows 8 (e / 4) + 4 h + e % 4.
+  float* const out = L.acc + (int64_t)sl * L.block * K;
+#pragma unroll
+  for (int a = 0; a < A; ++a)
+#pragma unroll
+    for (int c = 0; c < B; ++c) {
+      const int64_t k = k0 + wk * (BK / S::GK) + 32 * c + l32;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int row = r0 + wt * (BT / S::GT) + 32 * a + 8 * (e / 4) + 4 * h + e % 4;
+        if (row < rows && k < K) {
+          float* p = out + (int64_t)row * K + k;
+          *p = pc > 0 ? *p + acc[a][c][e] : acc[a][c][e];
+        }
+      }
+    }
+}
+
+// A learned token's loss, and the row of its gradient.
+__global__ __launch_bounds__(256) void head_finish_kernel(Loss L, int b, int nslabs) {
+  __shared__ float red[4];
+  const int i = blockIdx.x, tid = threadIdx.x;
+  if (i >= rows_of(L, b)) return;
+  const int64_t K = L.a.K, t = L.list[b * L.block + i];
+  const float tz = L.tz[i];
+  // The row's last reference, or a later one of a loss without gradient.
+  float ref = L.ref[i];
+  for (int j = tid; j < L.nstat; j += 256) ref = fmaxf(ref, L.stats[(int64_t)i * L.nstat + j].x);
+#pragma unroll
+  for (int off = 32; off; off >>= 1) ref = fmaxf(ref, __shfl_xor(ref, off, 64));
+  if ((tid & 63) == 0) red[tid >> 6] = ref;
+  __syncthreads();
+  ref = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  __syncthreads();
+  float sum = 0.0f;
+  for (int j = tid; j < L.nstat; j += 256) {
+    const float2 s = L.stats[(int64_t)i * L.nstat + j];
+    sum += s.y * exp_of(s.x - ref);
+  }
+#pragma unroll
+  for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  if ((tid & 63) == 0) red[tid >> 6] = sum;
+  __syncthreads();
+  const float rest = red[0] + red[1] + red[2] + red[3];
+  const float own = exp_of(tz - ref), total = rest + own;
+  if (tid == 0) {
+    const float loss = ref == tz ? log1pf(rest) : (ref - tz) + logf(total);
+    L.a.loss[t] = loss;
+    L.a.lse[t] = tz + loss;
+  }
+  if (!L.a.dX) return;
+  const float g = L.a.dloss ? L.a.dloss[t] : 1.0f / (float)*L.count;
+  const float up = g / total, down = g * (rest / total);
+  const uint16_t* w = L.a.W + L.a.targets[t] * K;
+  for (int64_t k = tid * 8; k < K; k += 2048) {
+    float v[8] = {};
+    for (int s = 0; s < nslabs; ++s) {
+      const float4* p = reinterpret_cast<const float4*>(L.acc + ((int64_t)s * L.block + i) * K + k);
+      const float4 x = p[0], y = p[1];
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    const u32x4 wv = *reinterpret_cast<const u32x4*>(w + k);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[2 * q] = v[2 * q] * up - down * bf16_lo(wv[q]);
+      v[2 * q + 1] = v[2 * q + 1] * up - down * bf16_hi(wv[q]);
+    }
+    *reinterpret_cast<bf16x8*>(L.a.dX + t * K + k) = to_bf16x8(v);
+  }
+}
+
+// What tokens that are not learned get: zeros.
+__global__ __launch_bounds__(256) void head_rest_kernel(Loss L) {
+  for (int64_t t = blockIdx.x; t < L.a.T; t += gridDim.x) {
+    const int64_t y = L.a.targets[t];
+    if (y >= 0 && y < L.a.V) continue;
+    if (threadIdx.x == 0) {
+      L.a.loss[t] = 0.0f;
+      L.a.lse[t] = 0.0f;
+    }
+    if (L.a.dX)
+      for (int64_t k = threadIdx.x * 8; k < L.a.K; k += 2048)
+        *reinterpret_cast<u32x4*>(L.a.dX + t * L.a.K + k) = u32x4{0u, 0u, 0u, 0u};
+  }
+}
+
+__global__ void head_zero_kernel(float* mean) {
+  if (threadIdx.x == 0) *mean = 0.0f;
+}
+
+// The mean over the learned tokens (0 if there are none), summed in fp64.
+__global__ __launch_bounds__(256) void head_mean_kernel(Loss L) {
+  __shared__ double red[4];
+  double x = 0.0;
+  const int n = *L.count;
+  for (int i = threadIdx.x; i < n; i += 256) x += (double)L.a.loss[L.list[i]];
+#pragma unroll
+  for (int off = 32; off; off >>= 1) x += __shfl_xor(x, off, 64);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+  __syncthreads();
+  if (threadIdx.x == 0) *L.a.mean = n > 0 ? (float)((red[0] + red[1] + red[2] + red[3]) / n) : 0.0f;
+}
+
+namespace {
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+bool small_tiles(int64_t T) { return T <= 64; }
+
+// Slabs of the second product: as many as fill the 256 compute units.
+int slabs_of(int64_t rows, int64_t K, int64_t piece) {
+  const int64_t bt = small_tiles(rows) ? 64 : 256, bk = small_tiles(rows) ? 128 : 256;
+  const int64_t tiles = cdiv(rows, bt) * cdiv(K, bk);
+  int64_t s = 256 / tiles;
+  const int64_t most = cdiv(piece, 512);  // at least eight steps each
+  if (s > most) s = most;
+  if (s > 16) s = 16;
+  return s < 1 ? 1 : (int)s;
+}
+
+struct Layout {
+  Loss L;
+  int64_t blocks;
+  int stretch;  // columns of one sum
+  size_t total;
+};
+Layout layout(const HeadLossArgs& a, bool grad, char* ws) {
+  Layout l{};
+  Loss& L = l.L;
+  L.a = a;
+  const int64_t T = a.T, K = a.K, V = a.V;
+  const bool small = small_tiles(T);
+  L.block = T < kBlockTokens ? T : kBlockTokens;
+  l.blocks = cdiv(T, L.block);
+  int64_t piece = kPieceBytes / (2 * L.block) / 256 * 256;
+  if (!grad || piece > round_up(V, 256)) piece = round_up(V, 256);
+  L.piece = piece;
+  L.pieces = (int32_t)cdiv(V, piece);
+  l.stretch = small ? 32 : 128;
+  L.nstat = (int32_t)cdiv(V, l.stretch);
+  L.slabs = slabs_of(L.block, K, piece);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* p = ws + at;
+    at += align256(bytes);
+    return p;
+  };
+  L.list = reinterpret_cast<int32_t*>(take((size_t)T * 4));
+  L.count = reinterpret_cast<int32_t*>(take(4));
+  L.flags = reinterpret_cast<int32_t*>(take((size_t)l.blocks * L.pieces * 4));
+  L.tz = reinterpret_cast<float*>(take((size_t)L.block * 4));
+  L.ref = reinterpret_cast<float*>(take((size_t)L.block * 4));
+  L.lifted = reinterpret_cast<int32_t*>(take((size_t)L.block * 4));
+  L.stats = reinterpret_cast<float2*>(take((size_t)L.block * L.nstat * 8));
+  if (grad) {
+    L.P = reinterpret_cast<uint16_t*>(take((size_t)L.block * piece * 2));
+    L.acc = reinterpret_cast<float*>(take((size_t)L.slabs * L.block * K * 4));
+  }
+  l.total = at;
+  return l;
+}
+
+template <int BT>
+hipError_t launch_block(const Layout& l, int b, hipStream_t s) {
+  using S = Shape<BT>;
+  const Loss& L = l.L;
+  const int tiles_t = (int)cdiv(L.block, BT);
+  const bool grad = L.a.dX != nullptr;
+  {
+    KernelTimer kt_("head_target_kernel", s);
+    hipLaunchKernelGGL(head_target_kernel, dim3((unsigned)cdiv(L.block, 4)), dim3(256), 0, s, L, b);
+  }
+  for (int pc = 0; pc < L.pieces; ++pc) {
+    const int64_t c0 = pc * L.piece, n = L.a.V - c0 < L.piece ? L.a.V - c0 : L.piece;
+    const unsigned grid = 8 * (unsigned)cdiv(tiles_t * cdiv(n, S::BV), 8);
+    {
+      KernelTimer kt_("head_logits_kernel", s);
+      if (grad) hipLaunchKernelGGL((head_logits_kernel<BT, true>), dim3(grid), dim3(64 * S::kWaves), 0, s, L, b, pc);
+      else hipLaunchKernelGGL((head_logits_kernel<BT, false>), dim3(grid), dim3(64 * S::kWaves), 0, s, L, b, pc);
+    }
+    if (!grad) continue;
+    {
+      KernelTimer kt_("head_lift_kernel", s);
+      hipLaunchKernelGGL(head_lift_kernel, dim3(256), dim3(256), 0, s, L, b, pc, l.stretch, L.slabs);
+    }
+    {
+      KernelTimer kt_("head_grad_kernel", s);
+      const unsigned g2 = 8 * (unsigned)cdiv((int64_t)tiles_t * cdiv(L.a.K, S::BK) * L.slabs, 8);
+      hipLaunchKernelGGL((head_grad_kernel<BT>), dim3(g2), dim3(64 * S::kWaves), 0, s, L, b, pc, L.slabs);
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  {
+    KernelTimer kt_("head_finish_kernel", s);
+    hipLaunchKernelGGL(head_finish_kernel, dim3((unsigned)L.block), dim3(256), 0, s, L, b, L.slabs);
+  }
+  return hipGetLastError();
+}
+}  // namespace
+
+size_t head_loss_workspace_bytes(int64_t T, int64_t K, int64_t V, bool grad) {
+  if (T <= 0) return 0;
+  HeadLossArgs a{};
+  a.T = T;
+  a.K = K;
+  a.V = V;
+  return layout(a, grad, nullptr).total;
+}
+
+hipError_t launch_head_loss(const HeadLossArgs& a, void* ws, hipStream_t s) {
+  if (a.T == 0) {
+    hipLaunchKernelGGL(head_zero_kernel, dim3(1), dim3(64), 0, s, a.mean);
+    return hipGetLastError();
+  }
+  Layout l = layout(a, a.dX != nullptr, static_cast<char*>(ws));
+  hipError_t e = hipSuccess;
+  l.L.status = status_word(&e);
+  if (!l.L.status) return e;
+  {
+    KernelTimer kt_("head_select_kernel", s);
+    hipLaunchKernelGGL(head_select_kernel, dim3(1), dim3(1024), 0, s, l.L, (int)(l.blocks * l.L.pieces));
+  }
+  for (int b = 0; b < l.blocks; ++b) {
+    e = small_tiles(a.T) ? launch_block<64>(l, b, s) : launch_block<256>(l, b, s);
+    if (e != hipSuccess) return e;
+  }
+  {
+    KernelTimer kt_("head_rest_kernel", s);
+    hipLaunchKernelGGL(head_rest_kernel, dim3((unsigned)(a.T < 1024 ? a.T : 1024)), dim3(256), 0, s, l.L);
+  }
+  {
+    KernelTimer kt_("head_mean_kernel", s);
+    hipLaunchKernelGGL(head_mean_kernel, dim3(1), dim3(256), 0, s, l.L);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace qlora

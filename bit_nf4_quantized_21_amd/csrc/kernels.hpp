@@ -80,6 +80,39 @@ hipError_t launch_linear_fwd_grouped(int count, const GroupedLinear* L, int64_t 
 hipError_t launch_linear_bwd(const LinearArgs& a, const Codebook& cb, const uint16_t* dY, const uint16_t* X,
                              const float* XA, uint16_t* dX, uint16_t* dA, uint16_t* dB, void* ws, hipStream_t s);
 
+// The gated feed-forward block: H = act(G) U with G and U the outputs of the
+// adapted linears `gate` and `up` (their Y is not used), and its backward.
+// `saved` [2][T][N]: the multipliers that the forward keeps for the backward.
+struct GatedWeight {
+  const uint8_t* codes;
+  const uint8_t* q8;
+  const float* s2;
+  const uint16_t* A;
+  const uint16_t* B;
+};
+struct GatedArgs {
+  int64_t T, K, N;
+  int32_t r;
+  float s;  // alpha / r
+  GatedWeight w[2];  // gate, up
+};
+size_t gated_fwd_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t r);
+size_t gated_bwd_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t r);
+// True if every operand and workspace region fits the kernels' 32-bit views.
+bool gated_views_fit(int64_t T, int64_t K, int64_t N, int32_t r);
+// XA [2][T][r] fp32 out.
+hipError_t launch_gated_fwd(const GatedArgs& a, int act, const Codebook& cb, const uint16_t* X, uint16_t* H,
+                            uint16_t* saved, float* XA, void* ws, hipStream_t s);
+struct GatedGrads {
+  uint16_t* dX;
+  uint16_t* dA[2];
+  uint16_t* dB[2];
+};
+hipError_t launch_gated_bwd(const GatedArgs& a, const Codebook& cb, const uint16_t* dH, const uint16_t* X,
+                            const uint16_t* saved, const float* XA, const GatedGrads& g, void* ws, hipStream_t s);
+hipError_t launch_gated_slopes(const uint16_t* dH, const uint16_t* saved, uint16_t* dG, uint16_t* dU, int64_t n,
+                               hipStream_t s);
+
 // AdamW update of a flat adapter buffer (optim.hip); `ws` holds the fp64
 // norm partials when clipping or the norm is asked for.
 size_t adamw_workspace_bytes(int64_t n);

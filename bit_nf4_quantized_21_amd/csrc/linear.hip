@@ -197,11 +197,12 @@ struct FwdBatchLayout {
   size_t p, xah, slots, counters, total;
   SplitPlan g;
 };
-FwdBatchLayout fwd_batch_layout(int64_t T, int64_t K, int64_t N, int32_t r, int count) {
+// `pair`: two linears whose outputs are the two sides of one gated tile.
+FwdBatchLayout fwd_batch_layout(int64_t T, int64_t K, int64_t N, int32_t r, int count, bool pair = false) {
   FwdBatchLayout l{};
   l.p = align256((size_t)cdiv(K, row_chunk(T, K, count)) * T * rpad(r) * sizeof(float));
   l.xah = align256((size_t)T * rpad(r) * sizeof(uint16_t));
-  l.g = fwd_plan(T, K, N, count);
+  l.g = pair ? fwd_pair_plan(T, K, N) : fwd_plan(T, K, N, count);
   l.slots = l.g.S > 1 ? align256((size_t)l.g.nsplit() * l.g.S * kSplitSlotFloats * sizeof(float)) : 0;
   l.counters = align256((size_t)(l.g.nsplit() > 0 ? 2 * l.g.nsplit() : 1) * sizeof(int));
   // per problem: rowdot partials and the hi / lo rows of s XA
@@ -212,7 +213,8 @@ struct BwdBatchLayout {
   size_t pg, g, planes, ptok_b, ptok_a, per, slots, counters, total;
   SplitPlan d;
 };
-BwdBatchLayout bwd_batch_layout(int64_t T, int64_t K, int64_t N, int32_t r, int count) {
+// `pair`: two linears whose input gradients are summed.
+BwdBatchLayout bwd_batch_layout(int64_t T, int64_t K, int64_t N, int32_t r, int count, bool pair = false) {
   BwdBatchLayout l{};
   const BwdLayout b = bwd_layout(T, K, N, r, count);
   l.pg = b.pg;
@@ -220,7 +222,7 @@ BwdBatchLayout bwd_batch_layout(int64_t T, int64_t K, int64_t N, int32_t r, int 
   l.planes = b.planes;
   l.ptok_b = b.ptok_b;
   l.ptok_a = b.ptok_a;
-  l.d = dx_plan(T, K, N, count);
+  l.d = pair ? dx_pair_plan(T, K, N) : dx_plan(T, K, N, count);
   l.slots = l.d.S > 1 ? align256((size_t)l.d.nsplit() * l.d.S * kSplitSlotFloats * sizeof(float)) : 0;
   l.counters = align256((size_t)(l.d.nsplit() > 0 ? 2 * l.d.nsplit() : 1) * sizeof(int));
   // per problem: rowdot partials, hi / lo rows of s G, four tokdot planes
@@ -240,10 +242,16 @@ size_t bwd_batch_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t r, int
   return bwd_batch_layout(T, K, N, r, count).total;
 }
 
+// What a gated pair adds to a batch of two.
+struct GatedExtra {
+  int act;
+  uint16_t* saved;
+};
+
 hipError_t launch_linear_fwd_batch(int count, const GroupedLinear* L, int64_t T, int32_t r, float s,
-                                   const Codebook& cb, void* ws, hipStream_t st) {
+                                   const Codebook& cb, void* ws, hipStream_t st, const GatedExtra* gated = nullptr) {
   const int64_t K = L[0].K, N = L[0].N;
-  const FwdBatchLayout l = fwd_batch_layout(T, K, N, r, count);
+  const FwdBatchLayout l = fwd_batch_layout(T, K, N, r, count, gated != nullptr);
   char* w = reinterpret_cast<char*>(ws);
   char* w2 = w + (size_t)count * (l.p + 2 * l.xah);
   int* counters = reinterpret_cast<int*>(w2 + l.slots);
@@ -282,11 +290,17 @@ hipError_t launch_linear_fwd_batch(int count, const GroupedLinear* L, int64_t T,
   p.RP = (int)rpad(r);
   p.slots = reinterpret_cast<float*>(w2);
   p.counters = counters;
+  if (gated) {
+    p.act = gated->act;
+    p.saved = gated->saved;
+    return launch_gemm_fwd_pair(p, cb, st);
+  }
   return launch_gemm_fwd_batched(p, cb, st);
 }
 
+// `pair`: L[0].dX takes the sum of both linears' input gradients.
 hipError_t launch_linear_bwd_batch(int count, const GroupedLinearBwd* L, int64_t T, int32_t r, float s,
-                                   const Codebook& cb, void* ws, hipStream_t st) {
+                                   const Codebook& cb, void* ws, hipStream_t st, bool pair = false) {
   const int64_t K = L[0].K, N = L[0].N;
   if (T == 0) {
     for (int i = 0; i < count; ++i) {
@@ -297,7 +311,7 @@ hipError_t launch_linear_bwd_batch(int count, const GroupedLinearBwd* L, int64_t
     }
     return hipSuccess;
   }
-  const BwdBatchLayout l = bwd_batch_layout(T, K, N, r, count);
+  const BwdBatchLayout l = bwd_batch_layout(T, K, N, r, count, pair);
   char* w = reinterpret_cast<char*>(ws);
   char* w3 = w + (size_t)count * l.per;
   int* counters = reinterpret_cast<int*>(w3 + l.slots);
@@ -371,7 +385,7 @@ hipError_t launch_linear_bwd_batch(int count, const GroupedLinearBwd* L, int64_t
   p.RP = (int)rpad(r);
   p.slots = reinterpret_cast<float*>(w3);
   p.counters = counters;
-  return launch_gemm_dx_batched(p, cb, st);
+  return pair ? launch_gemm_dx_pair(p, cb, st) : launch_gemm_dx_batched(p, cb, st);
 }
 
 // Runs of consecutive linears with the same K and N, at most kGemmBatchMax
@@ -455,6 +469,125 @@ hipError_t launch_linear_fwd_grouped(int count, const GroupedLinear* L, int64_t 
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+// ---------------------------------------------------------------------------
+// The gated feed-forward block.
+// Forward, T <= 16: XA partials of both linears, then one GEMV whose workgroups
+// hold rows of both weights; T > 16: one launch of each rowdot kernel for both,
+// then one GEMM whose tiles hold both sides.  Backward: dG and dU from dH and
+// the kept multipliers, then the rank-r products of both linears in one launch
+// each, and one GEMM that contracts over both weights' rows.
+// ---------------------------------------------------------------------------
+namespace {
+size_t gated_gemv_partials(int64_t T, int64_t K, int64_t N, int32_t r) {
+  return align256((size_t)gemv_plan(N, K, T, r, 2).nparts * T * rpad(r) * sizeof(float));
+}
+// Backward: dG and dU, XA recomputed where the caller did not keep it (with
+// its rowdot partials), then the batch's own workspace.
+struct GatedBwdLayout {
+  size_t d, xa, pxa, batch, total;
+};
+GatedBwdLayout gated_bwd_layout(int64_t T, int64_t K, int64_t N, int32_t r) {
+  GatedBwdLayout l{};
+  l.d = align256((size_t)T * N * sizeof(uint16_t));
+  l.xa = align256((size_t)T * r * sizeof(float));
+  l.pxa = align256((size_t)cdiv(K, row_chunk(T, K, 2)) * T * rpad(r) * sizeof(float));
+  l.batch = bwd_batch_layout(T, K, N, r, 2, true).total;
+  l.total = 2 * (l.d + l.xa + l.pxa) + l.batch;
+  return l;
+}
+}  // namespace
+
+size_t gated_fwd_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t r) {
+  if (T <= 0) return 0;
+  return T <= kGemvMaxT ? 2 * gated_gemv_partials(T, K, N, r) : fwd_batch_layout(T, K, N, r, 2, true).total;
+}
+
+size_t gated_bwd_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t r) {
+  return T <= 0 ? 0 : gated_bwd_layout(T, K, N, r).total;
+}
+
+bool gated_views_fit(int64_t T, int64_t K, int64_t N, int32_t r) {
+  if (!linear_views_fit(T, K, N, r)) return false;
+  if (T <= 0) return true;
+  const int64_t lim = 0x7FFFFFFF;
+  const FwdBatchLayout f = fwd_batch_layout(T, K, N, r, 2, true);
+  const BwdBatchLayout b = bwd_batch_layout(T, K, N, r, 2, true);
+  const size_t regions[] = {f.p, f.xah, f.slots, b.pg, b.g, b.planes, b.ptok_b, b.ptok_a, b.slots,
+                            (size_t)cdiv(K, row_chunk(T, K, 2)) * (size_t)(T * rpad(r)) * sizeof(float)};
+  for (size_t x : regions)
+    if (x > (size_t)lim) return false;
+  return true;
+}
+
+hipError_t launch_gated_fwd(const GatedArgs& a, int act, const Codebook& cb, const uint16_t* X, uint16_t* H,
+                            uint16_t* saved, float* XA, void* ws, hipStream_t s) {
+  if (a.T == 0) return hipSuccess;
+  if (a.T <= kGemvMaxT) {
+    GemvGroupT<2> g{};
+    g.count = 2;
+    g.T = (int)a.T;
+    g.r = a.r;
+    g.RP = (int)rpad(a.r);
+    g.s = a.s;
+    g.saved = saved;
+    g.act = act;
+    for (int i = 0; i < 2; ++i) {
+      GemvLinear& L = g.L[i];
+      L.X = X;
+      L.codes = a.w[i].codes;
+      L.q8 = a.w[i].q8;
+      L.s2 = a.w[i].s2;
+      L.A = a.w[i].A;
+      L.B = a.w[i].B;
+      L.Y = H;
+      L.XA = XA + i * a.T * a.r;
+      L.P = reinterpret_cast<float*>(static_cast<char*>(ws) + i * gated_gemv_partials(a.T, a.K, a.N, a.r));
+      L.K = a.K;
+      L.N = a.N;
+    }
+    return launch_gemv_pair(g, cb, s);
+  }
+  GroupedLinear L[2];
+  for (int i = 0; i < 2; ++i)
+    L[i] = GroupedLinear{X, a.w[i].codes, a.w[i].q8, a.w[i].s2, a.w[i].A, a.w[i].B, H, XA + i * a.T * a.r, a.K, a.N};
+  const GatedExtra x{act, saved};
+  return launch_linear_fwd_batch(2, L, a.T, a.r, a.s, cb, ws, s, &x);
+}
+
+hipError_t launch_gated_bwd(const GatedArgs& a, const Codebook& cb, const uint16_t* dH, const uint16_t* X,
+                            const uint16_t* saved, const float* XA, const GatedGrads& g, void* ws, hipStream_t s) {
+  GroupedLinearBwd L[2];
+  if (a.T == 0) {
+    for (int i = 0; i < 2; ++i)
+      L[i] = GroupedLinearBwd{nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+                              g.dA[i], g.dB[i], a.K, a.N};
+    return launch_linear_bwd_batch(2, L, 0, a.r, a.s, cb, ws, s, true);
+  }
+  const GatedBwdLayout l = gated_bwd_layout(a.T, a.K, a.N, a.r);
+  char* w = static_cast<char*>(ws);
+  uint16_t* d[2] = {reinterpret_cast<uint16_t*>(w), reinterpret_cast<uint16_t*>(w + l.d)};
+  w += 2 * l.d;
+  if (!XA) {
+    // Not kept (gradient checkpointing): recomputed from X and A.
+    const uint16_t* Ms[2] = {X, X};
+    const uint16_t* Vs[2] = {a.w[0].A, a.w[1].A};
+    float* Ps[2] = {reinterpret_cast<float*>(w + 2 * l.xa), reinterpret_cast<float*>(w + 2 * l.xa + l.pxa)};
+    RowdotOut os[2] = {};
+    for (int i = 0; i < 2; ++i) os[i].f32 = reinterpret_cast<float*>(w + i * l.xa);
+    hipError_t e = launch_rowdot_batch(2, Ms, Vs, /*v_lr=*/true, Ps, os, a.T, a.K, a.r, row_chunk(a.T, a.K, 2), s);
+    if (e != hipSuccess) return e;
+  }
+  const float* xa[2];
+  for (int i = 0; i < 2; ++i) xa[i] = XA ? XA + i * a.T * a.r : reinterpret_cast<const float*>(w + i * l.xa);
+  w += 2 * (l.xa + l.pxa);
+  hipError_t e = launch_gated_slopes(dH, saved, d[0], d[1], a.T * a.N, s);
+  if (e != hipSuccess) return e;
+  for (int i = 0; i < 2; ++i)
+    L[i] = GroupedLinearBwd{d[i], X, xa[i], a.w[i].codes, a.w[i].q8, a.w[i].s2, a.w[i].A, a.w[i].B, g.dX,
+                            g.dA[i], g.dB[i], a.K, a.N};
+  return launch_linear_bwd_batch(2, L, a.T, a.r, a.s, cb, w, s, true);
 }
 
 hipError_t launch_linear_bwd(const LinearArgs& a, const Codebook& cb, const uint16_t* dY, const uint16_t* X,

@@ -2,10 +2,12 @@
 // validation, the codebook, and dispatch to the gfx950 kernels.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -17,6 +19,7 @@
 #include "kvcache.hpp"
 #include "storage.hpp"
 #include "timing.hpp"
+#include "train.hpp"
 
 namespace {
 
@@ -131,7 +134,7 @@ const char* qlora_status_string(int status) {
     case QLORA_ERR_DEVICE:
       return "QLORA_ERR_DEVICE: a kernel's bounded wait ran out; results since the last status query are unreliable";
     case QLORA_ERR_INDEX:
-      return "QLORA_ERR_INDEX: a page, slot, position, length or start was out of range; results since the last "
+      return "QLORA_ERR_INDEX: a page, slot, position, length, start or target was out of range; results since the last "
              "status query are unreliable";
     default: return "unknown qlora_status";
   }
@@ -462,6 +465,174 @@ int qlora_linear_bwd(const uint16_t* dY, const uint16_t* X, const float* XA, int
                      size_t workspace_bytes, void* stream) {
   return qlora_linear_bwd_4bit(qlora::kQNF4, dY, X, XA, T, K, N, codes, q8, s2, A, B, r, alpha, dX, dA, dB, workspace,
                                workspace_bytes, stream);
+}
+
+namespace {
+int check_gated(const qlora_adapted_weight* w, qlora::GatedWeight* out) {
+  if (!w) return QLORA_ERR_NULL;
+  if (!w->codes || !w->q8 || !w->s2 || !w->A || !w->B) return QLORA_ERR_NULL;
+  if (!aligned16(w->codes) || !aligned16(w->q8) || !aligned16(w->s2) || !aligned16(w->A) || !aligned16(w->B))
+    return QLORA_ERR_ALIGN;
+  *out = qlora::GatedWeight{w->codes, w->q8, w->s2, w->A, w->B};
+  return QLORA_OK;
+}
+int check_gated_shape(int64_t T, int64_t K, int64_t N, int32_t r) {
+  const int st = check_linear_shape(T, K, N, r);
+  if (st != QLORA_OK) return st;
+  return qlora::gated_views_fit(T, K, N, r) ? QLORA_OK : QLORA_ERR_SHAPE;
+}
+}  // namespace
+
+size_t qlora_gated_fwd_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t r) {
+  return check_gated_shape(T, K, N, r) == QLORA_OK ? qlora::gated_fwd_workspace_bytes(T, K, N, r) : 0;
+}
+
+size_t qlora_gated_bwd_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t r) {
+  return check_gated_shape(T, K, N, r) == QLORA_OK ? qlora::gated_bwd_workspace_bytes(T, K, N, r) : 0;
+}
+
+int qlora_gated_fwd(int32_t qtype, int32_t act, const uint16_t* X, int64_t T, int64_t K, int64_t N,
+                    const qlora_adapted_weight* gate, const qlora_adapted_weight* up, int32_t r, float alpha,
+                    uint16_t* H, uint16_t* saved, float* XA, void* workspace, size_t workspace_bytes, void* stream) {
+  const TypeTables* tt = type_tables(qtype);
+  if (!tt || act < QLORA_ACT_SILU || act > QLORA_ACT_GELU_TANH) return QLORA_ERR_UNSUPPORTED;
+  int st = check_gated_shape(T, K, N, r);
+  if (st != QLORA_OK) return st;
+  if (T == 0) return QLORA_OK;
+  qlora::GatedArgs a{T, K, N, r, (float)(alpha / (float)r), {}};
+  if ((st = check_gated(gate, &a.w[0])) != QLORA_OK || (st = check_gated(up, &a.w[1])) != QLORA_OK) return st;
+  if (!X || !H || !XA) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(H) || !aligned16(saved) || !aligned16(XA)) return QLORA_ERR_ALIGN;
+  const size_t need = qlora::gated_fwd_workspace_bytes(T, K, N, r);
+  if (!workspace || workspace_bytes < need) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
+  return hip_status(qlora::launch_gated_fwd(a, act, tt->cb, X, H, saved, XA, workspace, (hipStream_t)stream));
+}
+
+int qlora_gated_bwd(int32_t qtype, const uint16_t* dH, const uint16_t* X, const uint16_t* saved, const float* XA,
+                    int64_t T, int64_t K, int64_t N, const qlora_adapted_weight* gate,
+                    const qlora_adapted_weight* up, int32_t r, float alpha, uint16_t* dX, uint16_t* dA_gate,
+                    uint16_t* dB_gate, uint16_t* dA_up, uint16_t* dB_up, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  const TypeTables* tt = type_tables(qtype);
+  if (!tt) return QLORA_ERR_UNSUPPORTED;
+  int st = check_gated_shape(T, K, N, r);
+  if (st != QLORA_OK) return st;
+  if (!dA_gate || !dB_gate || !dA_up || !dB_up) return QLORA_ERR_NULL;
+  if (!aligned16(dA_gate) || !aligned16(dB_gate) || !aligned16(dA_up) || !aligned16(dB_up)) return QLORA_ERR_ALIGN;
+  qlora::GatedArgs a{T, K, N, r, (float)(alpha / (float)r), {}};
+  const qlora::GatedGrads g{dX, {dA_gate, dA_up}, {dB_gate, dB_up}};
+  if (T > 0) {
+    if ((st = check_gated(gate, &a.w[0])) != QLORA_OK || (st = check_gated(up, &a.w[1])) != QLORA_OK) return st;
+    if (!dH || !X || !saved || !dX) return QLORA_ERR_NULL;  // XA may be NULL
+    if (!aligned16(dH) || !aligned16(X) || !aligned16(saved) || !aligned16(XA) || !aligned16(dX))
+      return QLORA_ERR_ALIGN;
+    const size_t need = qlora::gated_bwd_workspace_bytes(T, K, N, r);
+    if (!workspace || workspace_bytes < need) return QLORA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
+  }
+  return hip_status(qlora::launch_gated_bwd(a, tt->cb, dH, X, saved, XA, g, workspace, (hipStream_t)stream));
+}
+
+namespace {
+int check_head(int64_t T, int64_t K, int64_t V) {
+  if (T < 0 || K < 64 || K > (int64_t(1) << 20) || K % 64 != 0 || V < 1 || V > INT32_MAX) return QLORA_ERR_SHAPE;
+  if (T > INT32_MAX || T * K * 2 > INT32_MAX || T * ((V + 31) / 32) > INT32_MAX) return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+}  // namespace
+
+size_t qlora_head_loss_workspace_bytes(int64_t T, int64_t K, int64_t V, int32_t with_grad) {
+  return check_head(T, K, V) == QLORA_OK ? qlora::head_loss_workspace_bytes(T, K, V, with_grad != 0) : 0;
+}
+
+int qlora_head_loss(const uint16_t* X, int64_t T, int64_t K, const uint16_t* W, int64_t V, const int64_t* targets,
+                    const float* dloss, float* loss, float* lse, float* mean, uint16_t* dX, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  const int st = check_head(T, K, V);
+  if (st != QLORA_OK) return st;
+  if (!mean) return QLORA_ERR_NULL;
+  if (!aligned16(mean)) return QLORA_ERR_ALIGN;
+  if (T > 0) {
+    if (!X || !W || !targets || !loss || !lse) return QLORA_ERR_NULL;
+    if (!aligned16(X) || !aligned16(W) || !aligned16(targets) || !aligned16(dloss) || !aligned16(loss) ||
+        !aligned16(lse) || !aligned16(dX))
+      return QLORA_ERR_ALIGN;
+    const size_t need = qlora::head_loss_workspace_bytes(T, K, V, dX != nullptr);
+    if (!workspace || workspace_bytes < need) return QLORA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
+  }
+  const qlora::HeadLossArgs a{X, W, targets, dloss, T, K, V, loss, lse, mean, dX};
+  return hip_status(qlora::launch_head_loss(a, workspace, (hipStream_t)stream));
+}
+
+namespace {
+// Whether any output overlaps another tensor (an output that is its own
+// gradient counts once).
+bool outputs_overlap(const std::vector<qlora::GradTensor>& g) {
+  struct Span {
+    uintptr_t begin, end;
+    bool out;
+  };
+  std::vector<Span> spans;
+  spans.reserve(2 * g.size());
+  for (const qlora::GradTensor& t : g) {
+    if (t.n == 0) continue;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(t.grad), b = reinterpret_cast<uintptr_t>(t.out);
+    if (t.out) spans.push_back(Span{b, b + (uintptr_t)t.n * (t.out_wide ? 4 : 2), true});
+    if (!t.out || a != b) spans.push_back(Span{a, a + (uintptr_t)t.n * (t.wide ? 4 : 2), false});
+  }
+  const auto before = [](const Span& x, const Span& y) { return x.begin < y.begin; };
+  if (!std::is_sorted(spans.begin(), spans.end(), before)) std::sort(spans.begin(), spans.end(), before);
+  uintptr_t outs = 0, all = 0;  // the furthest ends so far
+  for (const Span& s : spans) {
+    if (s.begin < (s.out ? all : outs)) return true;
+    all = std::max(all, s.end);
+    if (s.out) outs = std::max(outs, s.end);
+  }
+  return false;
+}
+}  // namespace
+
+size_t qlora_clip_grads_workspace_bytes(int32_t count) {
+  return count < 0 || count > 65536 ? 0 : qlora::clip_grads_workspace_bytes(count);
+}
+
+int qlora_clip_grads(int32_t count, const qlora_grad* grads, float max_norm, float* norm_out, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (count < 0 || count > 65536) return QLORA_ERR_SHAPE;
+  if (std::isnan(max_norm)) return QLORA_ERR_UNSUPPORTED;
+  if (count > 0 && !grads) return QLORA_ERR_NULL;
+  const bool clip = max_norm > 0.0f;
+  std::vector<qlora::GradTensor> g;
+  try {
+    g.reserve((size_t)count);
+    int64_t total = 0;
+    for (int i = 0; i < count; ++i) {
+      const qlora_grad& x = grads[i];
+      if (x.n < 0 || x.n > (int64_t(1) << 40)) return QLORA_ERR_SHAPE;
+      if (x.type != QLORA_GRAD_BF16 && x.type != QLORA_GRAD_FP32) return QLORA_ERR_UNSUPPORTED;
+      if (x.out_type != QLORA_GRAD_BF16 && x.out_type != QLORA_GRAD_FP32) return QLORA_ERR_UNSUPPORTED;
+      const bool wide = x.type == QLORA_GRAD_FP32, out_wide = x.out_type == QLORA_GRAD_FP32;
+      if (x.n == 0) continue;
+      total += x.n;
+      if (total > (int64_t(1) << 44)) return QLORA_ERR_SHAPE;
+      if (!x.grad) return QLORA_ERR_NULL;
+      if (reinterpret_cast<uintptr_t>(x.grad) % (wide ? 4 : 2)) return QLORA_ERR_ALIGN;
+      void* const out = clip ? x.out : nullptr;
+      if (reinterpret_cast<uintptr_t>(out) % (out_wide ? 4 : 2)) return QLORA_ERR_ALIGN;
+      if (out == x.grad && wide != out_wide) return QLORA_ERR_SHAPE;
+      g.push_back(qlora::GradTensor{x.grad, out, x.n, wide, out_wide});
+    }
+    if (clip && outputs_overlap(g)) return QLORA_ERR_SHAPE;
+  } catch (const std::bad_alloc&) {
+    return QLORA_ERR_WORKSPACE;  // host memory for the list
+  }
+  if (norm_out && !aligned16(norm_out)) return QLORA_ERR_ALIGN;
+  if (!workspace || workspace_bytes < qlora::clip_grads_workspace_bytes(count)) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
+  return hip_status(qlora::launch_clip_grads((int)g.size(), g.data(), max_norm, norm_out, workspace,
+                                             (hipStream_t)stream));
 }
 
 namespace {

@@ -53,6 +53,19 @@ class KVCacheDesc(ctypes.Structure):
                 ("heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("page_size", ctypes.c_int32)]
 
 
+class AdaptedWeight(ctypes.Structure):
+    """qlora_adapted_weight: a stored 4-bit weight with its adapter (device pointers)."""
+    _fields_ = [("codes", ctypes.c_void_p), ("q8", ctypes.c_void_p), ("s2", ctypes.c_void_p), ("A", ctypes.c_void_p),
+                ("B", ctypes.c_void_p)]
+
+
+class Grad(ctypes.Structure):
+    """qlora_grad: a gradient and where its clipped values go (device pointers)."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("out_type", ctypes.c_int32)]
+
+
+_c_weight, _c_grads = ctypes.POINTER(AdaptedWeight), ctypes.POINTER(Grad)
 _c_d, _c_heads, _c_cache = ctypes.c_double, ctypes.POINTER(Heads), ctypes.POINTER(KVCacheDesc)
 
 _SIGNATURES = {
@@ -98,6 +111,17 @@ _SIGNATURES = {
     "qlora_attend_paged_workspace_bytes": (_c_sz, [_c_cache, _c_i64, _c_i32, _c_i32, _c_i64, _c_i64, _c_i32, _c_i64]),
     "qlora_attend_paged": (ctypes.c_int, [_c_cache, _c_i64, _c_heads, _c_i32, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i64,
                                           _c_f, _c_i32, _c_i64, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "qlora_gated_fwd_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i32]),
+    "qlora_gated_bwd_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i32]),
+    "qlora_gated_fwd": (ctypes.c_int, [_c_i32, _c_i32, _c_p, _c_i64, _c_i64, _c_i64, _c_weight, _c_weight, _c_i32, _c_f,
+                                       _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "qlora_gated_bwd": (ctypes.c_int, [_c_i32, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_weight, _c_weight,
+                                       _c_i32, _c_f, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "qlora_head_loss_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i32]),
+    "qlora_head_loss": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
+                                       _c_sz, _c_p]),
+    "qlora_clip_grads_workspace_bytes": (_c_sz, [_c_i32]),
+    "qlora_clip_grads": (ctypes.c_int, [_c_i32, _c_grads, _c_f, _c_p, _c_p, _c_sz, _c_p]),
     "qlora_timing_enable": (None, [ctypes.c_int]),
     "qlora_timing_read": (ctypes.c_int, [ctypes.c_char_p, _c_sz]),
     "qlora_nf4_codebook": (None, [ctypes.POINTER(ctypes.c_float)]),

@@ -56,8 +56,8 @@ typedef enum {
   QLORA_ERR_DEVICE = -7,      /* a kernel's bounded wait ran out (reported by qlora_device_status) */
   QLORA_ERR_SCRATCH = -8,     /* the problem needs more than the no-allocation entry point's scratch */
   QLORA_ERR_IO = -9,          /* a file is missing, unreadable, malformed, or of another type or shape */
-  QLORA_ERR_INDEX = -10       /* a page, slot, position, length or start in device memory was out of range (reported
-                                 by qlora_device_status) */
+  QLORA_ERR_INDEX = -10       /* a page, slot, position, length, start or target in device memory was out of range
+                                 (reported by qlora_device_status) */
 } qlora_status;
 
 /*
@@ -357,6 +357,138 @@ int qlora_adamw_step(int64_t n, uint16_t* param, float* master, float* m, float*
                      void* stream);
 
 /*
+ * The gated feed-forward block's first half (the gate and up linears of a
+ * LLaMA block, their activation and product; QLoRA project page, technical
+ * architecture: every linear of the transformer carries an adapter) in one
+ * kernel:
+ *     G = X Wg'^T + s (X Ag) Bg,   U = X Wu'^T + s (X Au) Bu,
+ *     H = act(G) * U               (from the fp32 sums, rounded to bf16 once)
+ * with W' and s as in qlora_linear_fwd; neither G nor U is stored.
+ *   act    QLORA_ACT_SILU       g / (1 + e^-g)
+ *          QLORA_ACT_GELU       g Phi(g) = g (1 + erf(g / sqrt 2)) / 2
+ *          QLORA_ACT_GELU_TANH  g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2
+ *   gate, up  the two weights [N,K] of type qtype with their adapters A [K,r],
+ *          B [r,N]; layouts, sizes and size limits as in qlora_linear_fwd.
+ *   X      [T,K] bf16, T >= 0 (0 = no-op).
+ *   H      [T,N] bf16 out.
+ *   saved  [2][T][N] 16-bit out, or NULL when no backward follows: what
+ *          qlora_gated_bwd multiplies by, act'(G) U and act(G), with 10
+ *          significant bits from 2^-30 up to 2^33 (multiples of 2^-39 below,
+ *          infinite from there on).
+ *   XA     [2][T][r] fp32 out: X Ag and X Au, for the backward.
+ *   workspace of at least qlora_gated_fwd_workspace_bytes(T,K,N,r) bytes.
+ * T <= 16 streams both 4-bit weights (decoding); more tokens take the
+ * dequantize-into-MFMA GEMM.  Deterministic.
+ */
+typedef enum { QLORA_ACT_SILU = 0, QLORA_ACT_GELU = 1, QLORA_ACT_GELU_TANH = 2 } qlora_act;
+typedef struct {
+  const uint8_t* codes;
+  const uint8_t* q8;
+  const float* s2;
+  const uint16_t* A;
+  const uint16_t* B;
+} qlora_adapted_weight;
+size_t qlora_gated_fwd_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t r);
+int qlora_gated_fwd(int32_t qtype, int32_t act, const uint16_t* X, int64_t T, int64_t K, int64_t N,
+                    const qlora_adapted_weight* gate, const qlora_adapted_weight* up, int32_t r, float alpha,
+                    uint16_t* H, uint16_t* saved, float* XA, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its backward (the frozen weights get no gradient):
+ *     dG = dH * act'(G) U,   dU = dH * act(G)      (bf16, from `saved`)
+ *     dX  = dG Wg' + s (dG Bg^T) Ag^T + dU Wu' + s (dU Bu^T) Au^T
+ *     dAg = s X^T (dG Bg^T),  dBg = s (X Ag)^T dG,  and the same for up.
+ * The two sides of dX are summed in fp32 inside one kernel.
+ *   dH [T,N] bf16; X, gate, up, r, alpha as in the forward; saved and XA what
+ *   the forward wrote for them.  XA may be NULL: it is then recomputed from X
+ *   and A (equal to the forward's for T > 16, within fp32 accumulation order
+ *   for T <= 16).  saved is needed; where it was not kept (gradient
+ *   checkpointing) qlora_gated_fwd recomputes it.
+ *   dX [T,K], dA_gate, dA_up [K,r], dB_gate, dB_up [r,N] bf16 are overwritten.
+ *   T = 0 is allowed: dX is empty, the others are set to zero.
+ *   workspace of at least qlora_gated_bwd_workspace_bytes(T,K,N,r) bytes.
+ * dG and dU enter the matrix products as bf16, so the results are off by the
+ * square root of two times their own rounding (2.4e-3 of the norm).
+ * Deterministic.
+ */
+size_t qlora_gated_bwd_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t r);
+int qlora_gated_bwd(int32_t qtype, const uint16_t* dH, const uint16_t* X, const uint16_t* saved, const float* XA,
+                    int64_t T, int64_t K, int64_t N, const qlora_adapted_weight* gate,
+                    const qlora_adapted_weight* up, int32_t r, float alpha, uint16_t* dX, uint16_t* dA_gate,
+                    uint16_t* dB_gate, uint16_t* dA_up, uint16_t* dB_up, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/*
+ * Softmax cross entropy over a vocabulary, and its gradient, without keeping
+ * the logits (the loss that instruction finetuning minimizes; the head is a
+ * base weight and gets no gradient):
+ *     z_j = x . w_j,   lse = log sum_j exp(z_j),   loss = lse - z_target,
+ *     dX = g (sum_{j != target} p_j w_j - (1 - p_target) w_target),
+ *     p = softmax(z).
+ *   X        [T,K] bf16, the tokens' last hidden states.
+ *   W        [V,K] bf16, the head.
+ *   targets  [T] int64: the token to predict, below V; a negative one (padding,
+ *            a prompt) is not learned: its loss, lse and row of dX are zero.
+ *            (One of V or more counts as not learned and is reported by
+ *            qlora_device_status as QLORA_ERR_INDEX.)
+ *   dloss    [T] fp32: the gradient g of each token's loss, or NULL: that of
+ *            the mean, 1 / (learned tokens).
+ *   loss, lse  [T] fp32 out.
+ *   mean     [1] fp32 out: the mean loss of the learned tokens, 0 if there are
+ *            none.
+ *   dX       [T,K] bf16 out, or NULL when no gradient is wanted.
+ *   T >= 0 (0: mean is set to 0), K a multiple of 64 in [64, 2^20], V >= 1;
+ *   T*K*2 bytes below 2^31, T * ceil(V / 32) below 2^31.
+ *   workspace  qlora_head_loss_workspace_bytes(T,K,V,dX != NULL) bytes: with a
+ *            gradient at most 64 MB of exponentials (of a piece of the
+ *            vocabulary and 4096 tokens), 4096 K 4 bytes or 64 MB of sums, and
+ *            8 bytes for every 128 (T <= 64: 32) logits of 4096 tokens.
+ * Only learned tokens are multiplied.  Logits and sums are fp32.  The
+ * exponentials, relative to the target's, enter the product with W as bf16, so
+ * dX is off by at most the square root of two times its own rounding; the
+ * target's weight 1 - p is the sum of the others', so it keeps its digits for
+ * tokens that are nearly certain.  Deterministic.
+ */
+size_t qlora_head_loss_workspace_bytes(int64_t T, int64_t K, int64_t V, int32_t with_grad);
+int qlora_head_loss(const uint16_t* X, int64_t T, int64_t K, const uint16_t* W, int64_t V, const int64_t* targets,
+                    const float* dloss, float* loss, float* lse, float* mean, uint16_t* dX, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * Global norm of many gradients, and clipping (QLoRA project page, challenges:
+ * gradient clipping keeps training stable), where the gradients of a model's
+ * adapters are tensors of their own:
+ *     |g| = sqrt(sum of all values' squares)           (fp64, in a fixed order)
+ *     out = c g,   c = min(1, max_norm / (|g| + 1e-6)).
+ *   grads      host array of `count` descriptors (0 <= count <= 65536):
+ *     grad     n values (n >= 0), bf16 or fp32 (type), aligned to its elements
+ *              (on 16 bytes it is read eight values at a time).
+ *     out      where the clipped values go, of out_type: `grad` itself (same
+ *              type, in place), other memory (for instance a view of the flat
+ *              bf16 buffer that qlora_adamw_step reads), or NULL: the tensor
+ *              counts for the norm only.
+ *              No output may overlap another output or gradient
+ *              (QLORA_ERR_SHAPE).
+ *   max_norm   <= 0: only the norm is computed, no output is written.
+ *   norm_out   [1] fp32 out: |g|, or NULL.
+ *   workspace of at least qlora_clip_grads_workspace_bytes(count) bytes.
+ * A norm that is infinite or no number gives outputs accordingly (0 times an
+ * infinity, or NaN everywhere), as the formula says.  In place, values are left
+ * as they are where c = 1.
+ */
+typedef enum { QLORA_GRAD_BF16 = 0, QLORA_GRAD_FP32 = 1 } qlora_grad_type;
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t n;
+  int32_t type;
+  int32_t out_type;
+} qlora_grad;
+size_t qlora_clip_grads_workspace_bytes(int32_t count);
+int qlora_clip_grads(int32_t count, const qlora_grad* grads, float max_norm, float* norm_out, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
  * The attention side of generation with a quantized model (QLoRA project
  * page, inference features: 4-bit inference and batched generation): rotary
  * positions between the q/k/v linears and the cache, a paged key/value cache
@@ -621,7 +753,7 @@ int qlora_last_hip_error(void);
  * bound ever ran out, the finishing workgroup sets a status bit on the
  * device and stores an incomplete sum.  This call waits for `stream`,
  * returns QLORA_ERR_DEVICE if that bit is set, QLORA_ERR_INDEX if a kernel of
- * the attention side met an index out of range (the outputs of the calls since
+ * the attention side or of the loss met an index out of range (the outputs of the calls since
  * the previous query are then unreliable) and clears the bits; QLORA_OK
  * otherwise, or QLORA_ERR_HIP if the wait or the read failed.  Host-blocking.
  */
