@@ -31,6 +31,8 @@
 #include "timing.hpp"
 #include "train.hpp"
 
+#include <type_traits>
+
 namespace qlora {
 
 namespace {
@@ -38,7 +40,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int64_t kBlockTokens = 4096;
-constexpr int64_t kPieceBytes = int64_t(64) << 20;
+constexpr int64_t kPieceBytes = int64_t(128) << 20;
 constexpr float kLift = 40.0f;       // e^40 leaves e^48 of fp32's range for sums and weights
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -50,18 +52,18 @@ struct Loss {
   HeadLossArgs a;
   int32_t* list;    // [T] tokens that are learned, ascending
   int32_t* count;   // [1] their number
-  float* tz;        // [block] the target's logit
-  float* ref;       // [block] what the exponentials are relative to
-  int32_t* lifted;  // [block] the largest logit of a lifted tile, as an ordered integer
+  float* tz;        // [T] the target's logit
+  float* ref;       // [T] what the token's exponentials are relative to
+  int32_t* lifted;  // [T] the largest logit of a lifted tile, as an ordered integer
   int32_t* flags;   // [blocks * pieces] whether any tile of the piece was lifted
   float2* stats;    // [block][nstat] (reference, sum) of each row and stretch of kStat columns
-  uint16_t* P;      // [block][piece] exponentials
-  float* acc;       // [slabs][block][K] sum of exponentials times W
+  uint16_t* P;      // [block][pitch] exponentials
+  float* acc;       // [slabs][rows][K] sum of exponentials times W
   int64_t block;    // tokens of a block
   int64_t piece;    // columns of a piece, a multiple of 256
+  int64_t pitch;    // of P
   int32_t pieces;
   int32_t nstat;
-  int32_t slabs;    // at most
   int* status;
 };
 
@@ -82,54 +84,70 @@ __device__ __forceinline__ int rows_of(const Loss& L, int64_t b) {
 }
 }  // namespace
 
-// The learned tokens in ascending order, their number, and zeroed flags.  One
-// workgroup: the targets are 8 bytes a token.
-__global__ __launch_bounds__(1024) void head_select_kernel(Loss L, int nflags) {
+// The first workgroup lists the learned tokens in ascending order and clears the
+// flags; the others take four tokens each: the target's logit of a learned one,
+// zeros for what the others get.
+__global__ __launch_bounds__(1024) void head_begin_kernel(Loss L, int nflags) {
   __shared__ int wave_n[16];
+  __shared__ float part[16];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  for (int i = tid; i < nflags; i += 1024) L.flags[i] = 0;
-  int base = 0;
-  bool bad = false;
-  for (int64_t t0 = 0; t0 < L.a.T; t0 += 1024) {
-    const int64_t t = t0 + tid;
-    const int64_t y = t < L.a.T ? L.a.targets[t] : -1;
-    bad |= y >= L.a.V;
-    const bool on = y >= 0 && y < L.a.V;
-    const uint64_t m = __ballot(on);
-    __syncthreads();
-    if (lane == 0) wave_n[wave] = __popcll(m);
-    __syncthreads();
-    int before = base, all = 0;
-    for (int w = 0; w < 16; ++w) {
-      before += w < wave ? wave_n[w] : 0;
-      all += wave_n[w];
+  const int64_t T = L.a.T, K = L.a.K;
+  if (blockIdx.x == 0) {
+    for (int i = tid; i < nflags; i += 1024) L.flags[i] = 0;
+    int base = 0;
+    bool bad = false;
+    for (int64_t t0 = 0; t0 < T; t0 += 1024) {
+      const int64_t t = t0 + tid;
+      const int64_t y = t < T ? L.a.targets[t] : -1;
+      bad |= y >= L.a.V;
+      const bool on = y >= 0 && y < L.a.V;
+      const uint64_t m = __ballot(on);
+      __syncthreads();
+      if (lane == 0) wave_n[wave] = __popcll(m);
+      __syncthreads();
+      int before = base, all = 0;
+      for (int w = 0; w < 16; ++w) {
+        before += w < wave ? wave_n[w] : 0;
+        all += wave_n[w];
+      }
+      if (on) L.list[before + __popcll(m & ((1ull << lane) - 1))] = (int32_t)t;
+      base += all;
     }
-    if (on) L.list[before + __popcll(m & ((1ull << lane) - 1))] = (int32_t)t;
-    base += all;
+    if (bad) atomicOr(L.status, kStatusIndex);
+    if (tid == 0) *L.count = base;
+    return;
   }
-  if (bad) atomicOr(L.status, kStatusIndex);
-  if (tid == 0) *L.count = base;
-}
-
-// The target's logit of each learned token of a block: one wave per token.
-__global__ __launch_bounds__(256) void head_target_kernel(Loss L, int b) {
-  const int i = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (i >= rows_of(L, b)) return;
-  const int64_t K = L.a.K, t = L.list[b * L.block + i];
-  const uint16_t* x = L.a.X + t * K;
-  const uint16_t* w = L.a.W + L.a.targets[t] * K;
+  const int64_t t = (int64_t)(blockIdx.x - 1) * 4 + (wave >> 2);
+  const int64_t y = t < T ? L.a.targets[t] : -1;
+  const bool on = y >= 0 && y < L.a.V;
+  const int at = (wave & 3) * 64 + lane;
   float sum = 0.0f;
-  for (int64_t k = lane * 8; k < K; k += 512) {
-    const u32x4 xv = *reinterpret_cast<const u32x4*>(x + k), wv = *reinterpret_cast<const u32x4*>(w + k);
+  if (on) {
+    const uint16_t* x = L.a.X + t * K;
+    const uint16_t* w = L.a.W + y * K;
+#pragma unroll 4
+    for (int64_t k = at * 8; k < K; k += 2048) {
+      const u32x4 xv = *reinterpret_cast<const u32x4*>(x + k), wv = *reinterpret_cast<const u32x4*>(w + k);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) sum += bf16_lo(xv[q]) * bf16_lo(wv[q]) + bf16_hi(xv[q]) * bf16_hi(wv[q]);
+      for (int q = 0; q < 4; ++q) sum += bf16_lo(xv[q]) * bf16_lo(wv[q]) + bf16_hi(xv[q]) * bf16_hi(wv[q]);
+    }
+  } else if (t < T) {
+    if (at == 0) {
+      L.a.loss[t] = 0.0f;
+      L.a.lse[t] = 0.0f;
+    }
+    if (L.a.dX)
+      for (int64_t k = at * 8; k < K; k += 2048) *reinterpret_cast<u32x4*>(L.a.dX + t * K + k) = u32x4{0u, 0u, 0u, 0u};
   }
 #pragma unroll
   for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
-  if (lane == 0) {
-    L.tz[i] = sum;
-    L.ref[i] = sum;
-    L.lifted[i] = kNotLifted;
+  if (lane == 0) part[wave] = sum;
+  __syncthreads();
+  if (on && at == 0) {
+    const float z = part[wave] + part[wave + 1] + part[wave + 2] + part[wave + 3];
+    L.tz[t] = z;
+    L.ref[t] = z;
+    L.lifted[t] = kNotLifted;
   }
 }
 
@@ -147,31 +165,92 @@ struct Shape<64> {
   static constexpr int BK = 128, GT = 1, GK = 4;
 };
 
-// First product: the logits of BT tokens and BV vocabulary rows, and of them
-// the sums of exponentials (one per token and wave) and, for the gradient, the
-// exponentials themselves.
-template <int BT, bool GRAD>
-__global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_logits_kernel(Loss L, int b, int pc) {
-  using S = Shape<BT>;
-  constexpr int NW = S::kWaves, BV = S::BV, A = BV / S::WV / 32, B = BT / S::WT / 32;
-  constexpr int kStage = (BV + BT) * 128;
-  __shared__ __align__(1024) unsigned char st0[kStage], st1[kStage];
+// Tile n of tiles_t x others: groups of four token tiles, within one the others
+// in order, so that the 32 tiles that an XCD holds at a time are four by eight
+// and share their operands through its L2.
+struct TileAt {
+  int t, other;
+};
+__device__ __forceinline__ TileAt tile_at(int n, int tiles_t, int others) {
+  const int g = n / (4 * others), in = n - g * 4 * others;
+  const int wide = tiles_t - 4 * g < 4 ? tiles_t - 4 * g : 4;
+  return TileAt{__builtin_amdgcn_readfirstlane(4 * g + in % wide), __builtin_amdgcn_readfirstlane(in / wide)};
+}
+
+// Slabs of the second product's contraction: as many as its tiles leave of the
+// 256 compute units, of eight steps at least.
+template <int BT>
+__host__ __device__ __forceinline__ int slabs_of(int64_t rows, int64_t K, int64_t piece) {
+  constexpr int BK = Shape<BT>::BK;
+  const int64_t tiles = ((rows + BT - 1) / BT) * ((K + BK - 1) / BK);
+  int64_t s = tiles > 0 ? 256 / tiles : 1;
+  const int64_t most = piece / 512;
+  if (s > most) s = most;
+  if (s > 16) s = 16;
+  return s < 1 ? 1 : (int)s;
+}
+
+// The main loop of both products: a workgroup's steps of 64 contracted values
+// through two stages of LDS.  A step is four substeps of A x B MFMAs; beside
+// each MFMA goes a fixed share of the other work, fenced so that it stays there:
+// the operands of the next substep are read from LDS, and in the last substep,
+// once every wave has read the stage for the last time (the barrier before it),
+// the rows of two steps further on are sent for into it.  They are waited for at
+// the next step's barrier, a whole step later.
+//   load(stage, step, i)  load i of L of a step's rows (past the last: nothing)
+//   read(stage, s, i)     LDS read i of R of substep s
+//   mma(s, a, c)          MFMA of operands a and c
+template <int A, int B, int R, int L, class Load, class Read, class Mma>
+__device__ __forceinline__ void pipeline(int nk, Load load, Read read, Mma mma) {
+  constexpr int N = A * B;
+  auto wait = []() __attribute__((always_inline)) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < L; ++i) load(0, 0, i);
+#pragma unroll
+  for (int i = 0; i < L; ++i) load(1, 1, i);
+  wait();
+#pragma unroll
+  for (int i = 0; i < R; ++i) read(0, 0, i);
+  __builtin_amdgcn_sched_barrier(0);
+  auto step = [&](auto stage, int kb) __attribute__((always_inline)) {
+    constexpr int cur = decltype(stage)::value;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (s == 3) wait();
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        mma(s, i / B, i % B);
+#pragma unroll
+        for (int r = i * R / N; r < (i + 1) * R / N; ++r) read(s < 3 ? cur : 1 - cur, (s + 1) & 3, r);
+        if (s == 3)
+#pragma unroll
+          for (int l = i * L / N; l < (i + 1) * L / N; ++l) load(cur, kb + 2, l);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+  int kb = 0;
+  for (; kb + 2 <= nk; kb += 2) {
+    step(std::integral_constant<int, 0>{}, kb);
+    step(std::integral_constant<int, 1>{}, kb + 1);
+  }
+  if (kb < nk) step(std::integral_constant<int, 0>{}, kb);
+  wait();  // the stages are free
+}
+
+// First product, one tile: the logits of BT tokens and BV vocabulary rows, and
+// of them the sums of exponentials (one per token and wave) and, for the
+// gradient, the exponentials themselves.
+template <int BT, int NW, int BV, int WV, int WT, bool GRAD>
+__device__ __forceinline__ void logits_tile(const Loss& L, int b, int pc, int rows, int r0, int64_t v0,
+                                            unsigned char* st0, unsigned char* st1) {
+  constexpr int A = BV / WV / 32, B = BT / WT / 32;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int l32 = lane & 31, h = lane >> 5, wv = wave % S::WV, wt = wave / S::WV;
-  const int rows = rows_of(L, b);
-  const int tiles_t = (rows + BT - 1) / BT;
+  const int l32 = lane & 31, h = lane >> 5, wv = wave % WV, wt = wave / WV;
   const int64_t K = L.a.K, V = L.a.V;
   const int64_t c0 = (int64_t)pc * L.piece, c1 = c0 + L.piece < V ? c0 + L.piece : V;
-  const int tiles_v = (int)((c1 - c0 + BV - 1) / BV);
-  // The grid is sized for whole blocks; XCD x (workgroup b runs on b % 8)
-  // takes a run of tiles, token tiles innermost.
-  const int tiles = tiles_t * tiles_v, per = (tiles + 7) / 8;
-  const int at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= per || at >= tiles) return;
-  const int tt = __builtin_amdgcn_readfirstlane(at % tiles_t), tv = __builtin_amdgcn_readfirstlane(at / tiles_t);
-  const int64_t v0 = c0 + (int64_t)tv * BV;
-  const int r0 = tt * BT;
-
   const rsrc_t rw = make_rsrc(L.a.W + v0 * K, (V - v0) * K * 2);
   const rsrc_t rx = make_rsrc(L.a.X, L.a.T * K * 2);
 
@@ -192,12 +271,13 @@ __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_logits_kernel(Los
     const int64_t t = ok ? L.list[b * L.block + r0 + row] : 0;
     bo[i] = ok ? (uint32_t)(t * K * 2 + ((dc ^ ((row >> 1) & 7)) << 4)) : kOffNone;
   }
-  auto load = [&](unsigned char* st, int kb) {
-#pragma unroll
-    for (int i = 0; i < NA; ++i) buf_load16_to_lds(rw, st + (wave * (BV / NW) + 8 * i) * 128, ao[i] + kb * 128);
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-      buf_load16_to_lds(rx, st + (BV + wave * (BT / NW) + 8 * i) * 128, bo[i] + kb * 128);
+  // Load i of step kb's rows (past the last step: nothing is read).
+  const int nk = (int)(K / 64);
+  unsigned char* const ring[2] = {st0, st1};
+  auto load = [&](int stage, int kb, int i) __attribute__((always_inline)) {
+    const uint32_t at_k = kb < nk ? (uint32_t)kb * 128 : kOffNone;
+    if (i < NA) buf_load16_to_lds(rw, ring[stage] + (wave * (BV / NW) + 8 * i) * 128, ao[i] + at_k);
+    else buf_load16_to_lds(rx, ring[stage] + (BV + wave * (BT / NW) + 8 * (i - NA)) * 128, bo[i - NA] + at_k);
   };
   f32x16 acc[A][B];
 #pragma unroll
@@ -207,83 +287,72 @@ __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_logits_kernel(Los
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[a][c][e] = 0.0f;
   const int sw = (l32 >> 1) & 7;
-  auto compute = [&](const unsigned char* st) {
-    const unsigned char* pa = st + (wv * (BV / S::WV) + l32) * 128;
-    const unsigned char* pb = st + (BV + wt * (BT / S::WT) + l32) * 128;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int ch = ((2 * s + h) ^ sw) << 4;
-      bf16x8 av[A], bv[B];
-#pragma unroll
-      for (int a = 0; a < A; ++a) av[a] = *reinterpret_cast<const bf16x8*>(pa + a * 4096 + ch);
-#pragma unroll
-      for (int c = 0; c < B; ++c) bv[c] = *reinterpret_cast<const bf16x8*>(pb + c * 4096 + ch);
-#pragma unroll
-      for (int a = 0; a < A; ++a)
-#pragma unroll
-        for (int c = 0; c < B; ++c) acc[a][c] = mfma32(av[a], bv[c], acc[a][c]);
-    }
+  bf16x8 oa[2][A], ob[2][B];  // operands of two substeps
+  // Operand i of substep s: i < B tokens, else vocabulary rows.
+  auto read = [&](int stage, int s, int i) __attribute__((always_inline)) {
+    const int ch = ((2 * s + h) ^ sw) << 4;
+    if (i < B) ob[s & 1][i] = *reinterpret_cast<const bf16x8*>(ring[stage] + (BV + wt * (BT / WT) + 32 * i + l32) * 128 + ch);
+    else oa[s & 1][i - B] = *reinterpret_cast<const bf16x8*>(ring[stage] + (wv * (BV / WV) + 32 * (i - B) + l32) * 128 + ch);
   };
-  const int nk = (int)(K / 64);
-  load(st0, 0);
-  for (int kb = 0; kb < nk; kb += 2) {
-    __syncthreads();  // step kb's rows have landed, st1 is free
-    if (kb + 1 < nk) load(st1, kb + 1);
-    compute(st0);
-    if (kb + 1 < nk) {
-      __syncthreads();
-      if (kb + 2 < nk) load(st0, kb + 2);
-      compute(st1);
-    }
-  }
+  pipeline<A, B, A + B, NA + NB>(
+      nk, load, read,
+      [&](int s, int a, int c) __attribute__((always_inline)) { acc[a][c] = mfma32(oa[s & 1][a], ob[s & 1][c], acc[a][c]); });
 
   // Lane (l32, h) holds of token 32 c + l32 the logits of rows 8 (e / 4) + 4 h
   // + e % 4 of each 32-row block a.
   const int nv = (int)(c1 - v0 < BV ? c1 - v0 : BV);  // rows that exist
-  if (GRAD) __syncthreads();                           // the stages take the exponentials
 #pragma unroll
   for (int c = 0; c < B; ++c) {
-    const int rt = r0 + wt * (BT / S::WT) + 32 * c + l32;
+    const int rt = r0 + wt * (BT / WT) + 32 * c + l32;
     const bool ok = rt < rows;
     const int64_t t = ok ? L.list[b * L.block + rt] : 0;
-    const int64_t y = L.a.targets[t] - v0;               // the target's row of this tile, if there
+    const int64_t y = ok ? L.a.targets[t] - v0 : -1;     // the target's row of this tile, if there
     const int own = y >= 0 && y < BV ? (int)y : -1;
-    const float base = ok ? L.ref[rt] : 0.0f;
+    const float base = ok ? L.ref[t] : 0.0f;
+    // The target and rows past the last count as nothing; few tiles hold any.
+    if (nv < BV || __ballot(own >= 0)) {
+#pragma unroll
+      for (int a = 0; a < A; ++a)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int v = wv * (BV / WV) + 32 * a + 8 * (e / 4) + 4 * h + e % 4;
+          if (v >= nv || v == own) acc[a][c][e] = -INFINITY;
+        }
+    }
     float m = -INFINITY;
 #pragma unroll
     for (int a = 0; a < A; ++a)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int v = wv * (BV / S::WV) + 32 * a + 8 * (e / 4) + 4 * h + e % 4;
-        if (v >= nv || v == own) acc[a][c][e] = -INFINITY;
-        m = fmaxf(m, acc[a][c][e]);
-      }
+      for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[a][c][e]);
     m = fmaxf(m, __shfl_xor(m, 32, 64));
     const bool lift = ok && m - base > kLift;
     const float ref = lift ? m : base;
     if (GRAD && lift && h == 0) {
-      atomicMax(L.lifted + rt, ordered(m));
+      atomicMax(L.lifted + t, ordered(m));
       atomicOr(L.flags + b * L.pieces + pc, 1);
     }
+    // (One rounding of ref log2 e for all of a token's exponentials: as if ref
+    // were off by half its last bit.)
+    const float ref2 = ref * kLog2e;
     float sum = 0.0f;
 #pragma unroll
     for (int a = 0; a < A; ++a)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        acc[a][c][e] = exp_of(acc[a][c][e] - ref);
+        acc[a][c][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[a][c][e], kLog2e, -ref2));
         sum += acc[a][c][e];
       }
     sum += __shfl_xor(sum, 32, 64);
-    const int64_t stat = (v0 + wv * (BV / S::WV)) / (BV / S::WV);
+    const int64_t stat = (v0 + wv * (BV / WV)) / (BV / WV);
     if (ok && h == 0 && stat < L.nstat) L.stats[(int64_t)rt * L.nstat + stat] = make_float2(ref, sum);
     if constexpr (GRAD) {
-      unsigned char* const row = (wt * (BT / S::WT) + 32 * c < BT / 2 ? st0 : st1) +
-                                 ((wt * (BT / S::WT) + 32 * c + l32) % (BT / 2)) * (BV * 2);
+      unsigned char* const row = (wt * (BT / WT) + 32 * c < BT / 2 ? st0 : st1) +
+                                 ((wt * (BT / WT) + 32 * c + l32) % (BT / 2)) * (BV * 2);
 #pragma unroll
       for (int a = 0; a < A; ++a)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int ch = wv * (BV / S::WV / 8) + 4 * a + q;
+          const int ch = wv * (BV / WV / 8) + 4 * a + q;
           *reinterpret_cast<uint2*>(row + ((ch ^ (l32 & (BV / 8 - 1))) << 4) + 8 * h) =
               make_uint2(pack_bf16x2(acc[a][c][4 * q], acc[a][c][4 * q + 1]),
                          pack_bf16x2(acc[a][c][4 * q + 2], acc[a][c][4 * q + 3]));
@@ -298,26 +367,60 @@ __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_logits_kernel(Los
       const int idx = 64 * NW * i + tid, row = idx / CH, ch = idx % CH;
       const unsigned char* p = (row < BT / 2 ? st0 : st1) + (row % (BT / 2)) * (BV * 2) + ((ch ^ (row & 31 & (CH - 1))) << 4);
       if (r0 + row < rows)
-        *reinterpret_cast<u32x4*>(L.P + (int64_t)(r0 + row) * L.piece + (v0 - c0) + 8 * ch) =
+        *reinterpret_cast<u32x4*>(L.P + (int64_t)(r0 + row) * L.pitch + (v0 - c0) + 8 * ch) =
             *reinterpret_cast<const u32x4*>(p);
     }
   }
 }
 
+// First product.  The grid is sized for whole blocks and the tiles are counted
+// here; XCD x (workgroup b runs on b % 8) takes a run of them.  Where they would
+// leave a last round of the 256 compute units half empty or emptier, that round
+// takes tiles of half as many vocabulary rows.
+template <int BT, bool GRAD>
+__global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_logits_kernel(Loss L, int b, int pc) {
+  using S = Shape<BT>;
+  constexpr int BV = S::BV;
+  __shared__ __align__(1024) unsigned char st0[(BV + BT) * 128], st1[(BV + BT) * 128];
+  const int rows = rows_of(L, b);
+  const int64_t c0 = (int64_t)pc * L.piece, c1 = c0 + L.piece < L.a.V ? c0 + L.piece : L.a.V;
+  const int tiles_t = (rows + BT - 1) / BT, tiles_v = (int)((c1 - c0 + BV - 1) / BV), tiles = tiles_t * tiles_v;
+  const int rest = tiles % 256;
+  const bool halves = BT == 256 && rest > 0 && rest <= 128;
+  const int whole = halves ? tiles - rest : tiles, per = (whole + 7) / 8;
+  const int xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
+  if (local < per) {
+    const int n = xcd * per + local;
+    if (n >= whole) return;
+    const TileAt at = tile_at(n, tiles_t, tiles_v);
+    logits_tile<BT, S::kWaves, BV, S::WV, S::WT, GRAD>(L, b, pc, rows, at.t * BT, c0 + (int64_t)at.other * BV, st0, st1);
+  } else if constexpr (BT == 256) {
+    const int per2 = (2 * rest + 7) / 8, n = xcd * per2 + local - per;
+    if (!halves || local - per >= per2 || n >= 2 * rest) return;
+    const TileAt at = tile_at(whole + n / 2, tiles_t, tiles_v);
+    const int64_t v0 = c0 + (int64_t)at.other * BV + (n & 1) * (BV / 2);
+    if (v0 >= c1) return;
+    logits_tile<BT, 8, BV / 2, 1, 8, GRAD>(L, b, pc, rows, at.t * BT, v0, st0, st1);
+  }
+}
+
 // Rows of a piece with a lifted tile: every stretch of exponentials and what
 // was summed before are brought to the row's new reference.
-__global__ __launch_bounds__(256) void head_lift_kernel(Loss L, int b, int pc, int stretch, int nslabs) {
+template <int BT>
+__global__ __launch_bounds__(256) void head_lift_kernel(Loss L, int b, int pc) {
   if (L.flags[b * L.pieces + pc] == 0) return;
+  constexpr int kStretch = Shape<BT>::BV / Shape<BT>::WV;
   const int64_t K = L.a.K, c0 = (int64_t)pc * L.piece, c1 = c0 + L.piece < L.a.V ? c0 + L.piece : L.a.V;
-  const int rows = rows_of(L, b);
+  const int rows = rows_of(L, b), nslabs = slabs_of<BT>(rows, K, L.piece);
   for (int i = blockIdx.x; i < rows; i += gridDim.x) {
-    const int32_t o = L.lifted[i];
-    const float old = L.ref[i], now = from_ordered(o);
+    const int64_t t = L.list[b * L.block + i];
+    const int32_t o = L.lifted[t];
+    const float old = L.ref[t], now = from_ordered(o);
     __syncthreads();  // everyone has read them
     if (o == kNotLifted || !(now > old)) continue;
     for (int64_t c = c0 + threadIdx.x * 8; c < c1; c += 256 * 8) {
-      const float f = exp_of(L.stats[(int64_t)i * L.nstat + c / stretch].x - now);
-      u32x4* p = reinterpret_cast<u32x4*>(L.P + (int64_t)i * L.piece + (c - c0));
+      const float f = exp_of(L.stats[(int64_t)i * L.nstat + c / kStretch].x - now);
+      u32x4* p = reinterpret_cast<u32x4*>(L.P + (int64_t)i * L.pitch + (c - c0));
       u32x4 v = *p;
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = pack_bf16x2(bf16_lo(v[q]) * f, bf16_hi(v[q]) * f);
@@ -326,11 +429,11 @@ __global__ __launch_bounds__(256) void head_lift_kernel(Loss L, int b, int pc, i
     if (pc > 0) {
       const float f = exp_of(old - now);
       for (int s = 0; s < nslabs; ++s)
-        for (int64_t k = threadIdx.x; k < K; k += 256) L.acc[((int64_t)s * L.block + i) * K + k] *= f;
+        for (int64_t k = threadIdx.x; k < K; k += 256) L.acc[((int64_t)s * rows + i) * K + k] *= f;
     }
     if (threadIdx.x == 0) {
-      L.ref[i] = now;
-      L.lifted[i] = kNotLifted;
+      L.ref[t] = now;
+      L.lifted[t] = kNotLifted;
     }
   }
 }
@@ -338,7 +441,7 @@ __global__ __launch_bounds__(256) void head_lift_kernel(Loss L, int b, int pc, i
 // Second product: acc[row][k] += sum over the piece of P[row][v] W[v][k].  The
 // contraction is cut into slabs where the tiles alone would not fill the chip.
 template <int BT>
-__global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_grad_kernel(Loss L, int b, int pc, int nslabs) {
+__global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_grad_kernel(Loss L, int b, int pc) {
   using S = Shape<BT>;
   constexpr int NW = S::kWaves, BK = S::BK, A = BT / S::GT / 32, B = BK / S::GK / 32;
   constexpr int kStage = BT * 128 + 64 * BK * 2;
@@ -350,39 +453,45 @@ __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_grad_kernel(Loss 
   const int64_t K = L.a.K, V = L.a.V;
   const int64_t c0 = (int64_t)pc * L.piece, c1 = c0 + L.piece < V ? c0 + L.piece : V;
   const int tiles_k = (int)((K + BK - 1) / BK);
-  const int tiles = tiles_t * tiles_k * nslabs, per = (tiles + 7) / 8;
-  const int at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= per || at >= tiles) return;
-  const int tt = __builtin_amdgcn_readfirstlane(at % tiles_t);
-  const int tk = __builtin_amdgcn_readfirstlane(at / tiles_t % tiles_k);
-  const int sl = __builtin_amdgcn_readfirstlane(at / tiles_t / tiles_k);
-  const int r0 = tt * BT;
-  const int64_t k0 = (int64_t)tk * BK;
+  const int nslabs = __builtin_amdgcn_readfirstlane(slabs_of<BT>(rows, K, L.piece));
+  const int whole = tiles_t * tiles_k, tiles = whole * nslabs, per = (tiles + 7) / 8;
+  const int n = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || n >= tiles) return;
+  const int sl = __builtin_amdgcn_readfirstlane(n / whole);
+  const TileAt at = tile_at(n - sl * whole, tiles_t, tiles_k);
+  const int r0 = at.t * BT;
+  const int64_t k0 = (int64_t)at.other * BK;
   // This slab's steps of 64 rows of W.
   const int steps = (int)((c1 - c0 + 63) / 64), each = (steps + nslabs - 1) / nslabs;
   const int sbeg = sl * each < steps ? sl * each : steps, send = sbeg + each < steps ? sbeg + each : steps;
 
-  const rsrc_t rp = make_rsrc(L.P + (int64_t)r0 * L.piece, (rows - r0) * L.piece * 2);
+  const rsrc_t rp = make_rsrc(L.P + (int64_t)r0 * L.pitch, (rows - r0) * L.pitch * 2);
   constexpr int NP = BT / 8 / NW, ND = 64 * BK * 2 / 1024 / NW;  // instructions of a wave
   constexpr int WCH = BK / 8;                                     // 16-byte chunks of a row of the W tile
   uint32_t po[NP], wo[ND];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int row = wave * (BT / NW) + 8 * i + (lane >> 3);
-    po[i] = (uint32_t)(row * L.piece * 2 + (((lane & 7) ^ ((row >> 1) & 7)) << 4));
+    po[i] = (uint32_t)(row * L.pitch * 2 + (((lane & 7) ^ ((row >> 1) & 7)) << 4));
   }
 #pragma unroll
   for (int i = 0; i < ND; ++i) {
     const int unit = (wave * ND + i) * 64 + lane, v = unit / WCH, ch = (unit % WCH) ^ ((v & 3) << 2);
     wo[i] = (uint32_t)((v * K + 8 * ch) * 2);
   }
-  auto load = [&](unsigned char* st, int sb) {
-    const int64_t v = c0 + (int64_t)sb * 64;
-    const rsrc_t rw = make_rsrc(L.a.W + v * K + k0, ((V - v) * K - k0) * 2);
-#pragma unroll
-    for (int i = 0; i < NP; ++i) buf_load16_to_lds(rp, st + (wave * (BT / NW) + 8 * i) * 128, po[i] + sb * 128);
-#pragma unroll
-    for (int i = 0; i < ND; ++i) buf_load16_to_lds(rw, st + BT * 128 + (wave * ND + i) * 1024, wo[i]);
+  const int nk = send - sbeg;
+  unsigned char* const ring[2] = {st0, st1};
+  auto load = [&](int stage, int step, int i) __attribute__((always_inline)) {
+    const int sb = sbeg + step;
+    if (i < NP) {
+      buf_load16_to_lds(rp, ring[stage] + (wave * (BT / NW) + 8 * i) * 128, po[i] + (step < nk ? (uint32_t)sb * 128 : kOffNone));
+    } else {
+      // W's rows from this step's first on, in a view of their own: a piece of
+      // them can be larger than one.
+      const int64_t v = c0 + (int64_t)sb * 64;
+      const rsrc_t rw = make_rsrc(L.a.W + v * K + k0, step < nk ? ((V - v) * K - k0) * 2 : 0);
+      buf_load16_to_lds(rw, ring[stage] + BT * 128 + (wave * ND + i - NP) * 1024, wo[i - NP]);
+    }
   };
   f32x16 acc[A][B];
 #pragma unroll
@@ -395,45 +504,27 @@ __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_grad_kernel(Loss 
   // Of W's rows the lane names row (lane & 15) / 4 of four and four columns to
   // a transposing read, and gets its own column of the four rows.
   const int tr_row = 8 * h + ((lane & 15) >> 2), tr_col = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-  auto compute = [&](const unsigned char* st) {
-    const unsigned char* pa = st + (wt * (BT / S::GT) + l32) * 128;
-    const unsigned char* pw = st + BT * 128;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      bf16x8 av[A], bv[B];
-#pragma unroll
-      for (int a = 0; a < A; ++a) av[a] = *reinterpret_cast<const bf16x8*>(pa + a * 4096 + (((2 * s + h) ^ sw) << 4));
-#pragma unroll
-      for (int c = 0; c < B; ++c) {
-        s16x4 part[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int v = 16 * s + 4 * e + tr_row, col = wk * (BK / S::GK) + 32 * c + tr_col;
-          part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s16x4*)(pw + v * BK * 2 + (((col >> 3) ^ ((v & 3) << 2)) << 4) + (col & 7) * 2));
-        }
-        const uint2 lo = __builtin_bit_cast(uint2, part[0]), hi = __builtin_bit_cast(uint2, part[1]);
-        bv[c] = as_bf16x8(lo.x, lo.y, hi.x, hi.y);
-      }
-#pragma unroll
-      for (int a = 0; a < A; ++a)
-#pragma unroll
-        for (int c = 0; c < B; ++c) acc[a][c] = mfma32(av[a], bv[c], acc[a][c]);
+  bf16x8 oa[2][A];
+  s16x4 ob[2][B][2];
+  // Operand i of substep s: i < 2 B half of eight rows of W, else tokens.
+  auto read = [&](int stage, int s, int i) __attribute__((always_inline)) {
+    if (i < 2 * B) {
+      const int e = i & 1, c = i >> 1;
+      const int v = 16 * s + 4 * e + tr_row, col = wk * (BK / S::GK) + 32 * c + tr_col;
+      ob[s & 1][c][e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4*)(ring[stage] + BT * 128 + v * BK * 2 + (((col >> 3) ^ ((v & 3) << 2)) << 4) + (col & 7) * 2));
+    } else {
+      oa[s & 1][i - 2 * B] = *reinterpret_cast<const bf16x8*>(
+          ring[stage] + (wt * (BT / S::GT) + 32 * (i - 2 * B) + l32) * 128 + (((2 * s + h) ^ sw) << 4));
     }
   };
-  if (sbeg < send) load(st0, sbeg);
-  for (int sb = sbeg; sb < send; sb += 2) {
-    __syncthreads();
-    if (sb + 1 < send) load(st1, sb + 1);
-    compute(st0);
-    if (sb + 1 < send) {
-      __syncthreads();
-      if (sb + 2 < send) load(st0, sb + 2);
-      compute(st1);
-    }
-  }
+  pipeline<A, B, A + 2 * B, NP + ND>(
+      nk, load, read, [&](int s, int a, int c) __attribute__((always_inline)) {
+        const uint2 lo = __builtin_bit_cast(uint2, ob[s & 1][c][0]), hi = __builtin_bit_cast(uint2, ob[s & 1][c][1]);
+        acc[a][c] = mfma32(oa[s & 1][a], as_bf16x8(lo.x, lo.y, hi.x, hi.y), acc[a][c]);
+      });
   // Lane (l32, h) holds column 32 c + l32 of rows 8 (e / 4) + 4 h + e % 4.
-  float* const out = L.acc + (int64_t)sl * L.block * K;
+  float* const out = L.acc + (int64_t)sl * rows * K;
 #pragma unroll
   for (int a = 0; a < A; ++a)
 #pragma unroll
@@ -451,14 +542,16 @@ __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_grad_kernel(Loss 
 }
 
 // A learned token's loss, and the row of its gradient.
-__global__ __launch_bounds__(256) void head_finish_kernel(Loss L, int b, int nslabs) {
+template <int BT>
+__global__ __launch_bounds__(256) void head_finish_kernel(Loss L, int b) {
   __shared__ float red[4];
-  const int i = blockIdx.x, tid = threadIdx.x;
-  if (i >= rows_of(L, b)) return;
+  const int i = blockIdx.x, tid = threadIdx.x, rows = rows_of(L, b);
+  if (i >= rows) return;
   const int64_t K = L.a.K, t = L.list[b * L.block + i];
-  const float tz = L.tz[i];
+  const int nslabs = slabs_of<BT>(rows, K, L.piece);
+  const float tz = L.tz[t];
   // The row's last reference, or a later one of a loss without gradient.
-  float ref = L.ref[i];
+  float ref = L.ref[t];
   for (int j = tid; j < L.nstat; j += 256) ref = fmaxf(ref, L.stats[(int64_t)i * L.nstat + j].x);
 #pragma unroll
   for (int off = 32; off; off >>= 1) ref = fmaxf(ref, __shfl_xor(ref, off, 64));
@@ -489,7 +582,7 @@ __global__ __launch_bounds__(256) void head_finish_kernel(Loss L, int b, int nsl
   for (int64_t k = tid * 8; k < K; k += 2048) {
     float v[8] = {};
     for (int s = 0; s < nslabs; ++s) {
-      const float4* p = reinterpret_cast<const float4*>(L.acc + ((int64_t)s * L.block + i) * K + k);
+      const float4* p = reinterpret_cast<const float4*>(L.acc + ((int64_t)s * rows + i) * K + k);
       const float4 x = p[0], y = p[1];
       v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
       v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
@@ -501,21 +594,6 @@ __global__ __launch_bounds__(256) void head_finish_kernel(Loss L, int b, int nsl
       v[2 * q + 1] = v[2 * q + 1] * up - down * bf16_hi(wv[q]);
     }
     *reinterpret_cast<bf16x8*>(L.a.dX + t * K + k) = to_bf16x8(v);
-  }
-}
-
-// What tokens that are not learned get: zeros.
-__global__ __launch_bounds__(256) void head_rest_kernel(Loss L) {
-  for (int64_t t = blockIdx.x; t < L.a.T; t += gridDim.x) {
-    const int64_t y = L.a.targets[t];
-    if (y >= 0 && y < L.a.V) continue;
-    if (threadIdx.x == 0) {
-      L.a.loss[t] = 0.0f;
-      L.a.lse[t] = 0.0f;
-    }
-    if (L.a.dX)
-      for (int64_t k = threadIdx.x * 8; k < L.a.K; k += 2048)
-        *reinterpret_cast<u32x4*>(L.a.dX + t * L.a.K + k) = u32x4{0u, 0u, 0u, 0u};
   }
 }
 
@@ -541,21 +619,9 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 bool small_tiles(int64_t T) { return T <= 64; }
 
-// Slabs of the second product: as many as fill the 256 compute units.
-int slabs_of(int64_t rows, int64_t K, int64_t piece) {
-  const int64_t bt = small_tiles(rows) ? 64 : 256, bk = small_tiles(rows) ? 128 : 256;
-  const int64_t tiles = cdiv(rows, bt) * cdiv(K, bk);
-  int64_t s = 256 / tiles;
-  const int64_t most = cdiv(piece, 512);  // at least eight steps each
-  if (s > most) s = most;
-  if (s > 16) s = 16;
-  return s < 1 ? 1 : (int)s;
-}
-
 struct Layout {
   Loss L;
   int64_t blocks;
-  int stretch;  // columns of one sum
   size_t total;
 };
 Layout layout(const HeadLossArgs& a, bool grad, char* ws) {
@@ -570,9 +636,9 @@ Layout layout(const HeadLossArgs& a, bool grad, char* ws) {
   if (!grad || piece > round_up(V, 256)) piece = round_up(V, 256);
   L.piece = piece;
   L.pieces = (int32_t)cdiv(V, piece);
-  l.stretch = small ? 32 : 128;
-  L.nstat = (int32_t)cdiv(V, l.stretch);
-  L.slabs = slabs_of(L.block, K, piece);
+  L.nstat = (int32_t)cdiv(V, small ? 32 : 128);
+  // Rows of P a power of two apart would meet in the same memory channels.
+  L.pitch = piece + (piece % 2048 == 0 ? 128 : 0);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     char* p = ws + at;
@@ -582,13 +648,18 @@ Layout layout(const HeadLossArgs& a, bool grad, char* ws) {
   L.list = reinterpret_cast<int32_t*>(take((size_t)T * 4));
   L.count = reinterpret_cast<int32_t*>(take(4));
   L.flags = reinterpret_cast<int32_t*>(take((size_t)l.blocks * L.pieces * 4));
-  L.tz = reinterpret_cast<float*>(take((size_t)L.block * 4));
-  L.ref = reinterpret_cast<float*>(take((size_t)L.block * 4));
-  L.lifted = reinterpret_cast<int32_t*>(take((size_t)L.block * 4));
+  L.tz = reinterpret_cast<float*>(take((size_t)T * 4));
+  L.ref = reinterpret_cast<float*>(take((size_t)T * 4));
+  L.lifted = reinterpret_cast<int32_t*>(take((size_t)T * 4));
   L.stats = reinterpret_cast<float2*>(take((size_t)L.block * L.nstat * 8));
   if (grad) {
-    L.P = reinterpret_cast<uint16_t*>(take((size_t)L.block * piece * 2));
-    L.acc = reinterpret_cast<float*>(take((size_t)L.slabs * L.block * K * 4));
+    L.P = reinterpret_cast<uint16_t*>(take((size_t)L.block * L.pitch * 2));
+    // Slabs and rows are counted on the device: at most 256 tiles if there are
+    // several slabs, of at most 16 times the block's rows.
+    int64_t sums = small ? 256 * 64 * 128 : 256 * 256 * 256;
+    if (sums > 16 * L.block * K) sums = 16 * L.block * K;
+    if (sums < L.block * K) sums = L.block * K;
+    L.acc = reinterpret_cast<float*>(take((size_t)sums * 4));
   }
   l.total = at;
   return l;
@@ -600,13 +671,10 @@ hipError_t launch_block(const Layout& l, int b, hipStream_t s) {
   const Loss& L = l.L;
   const int tiles_t = (int)cdiv(L.block, BT);
   const bool grad = L.a.dX != nullptr;
-  {
-    KernelTimer kt_("head_target_kernel", s);
-    hipLaunchKernelGGL(head_target_kernel, dim3((unsigned)cdiv(L.block, 4)), dim3(256), 0, s, L, b);
-  }
   for (int pc = 0; pc < L.pieces; ++pc) {
     const int64_t c0 = pc * L.piece, n = L.a.V - c0 < L.piece ? L.a.V - c0 : L.piece;
-    const unsigned grid = 8 * (unsigned)cdiv(tiles_t * cdiv(n, S::BV), 8);
+    // (Half tiles of a last round: at most 256 more workgroups.)
+    const unsigned grid = 8 * (unsigned)cdiv(tiles_t * cdiv(n, S::BV), 8) + (BT == 256 ? 256 : 0);
     {
       KernelTimer kt_("head_logits_kernel", s);
       if (grad) hipLaunchKernelGGL((head_logits_kernel<BT, true>), dim3(grid), dim3(64 * S::kWaves), 0, s, L, b, pc);
@@ -615,19 +683,19 @@ hipError_t launch_block(const Layout& l, int b, hipStream_t s) {
     if (!grad) continue;
     {
       KernelTimer kt_("head_lift_kernel", s);
-      hipLaunchKernelGGL(head_lift_kernel, dim3(256), dim3(256), 0, s, L, b, pc, l.stretch, L.slabs);
+      hipLaunchKernelGGL(head_lift_kernel<BT>, dim3(256), dim3(256), 0, s, L, b, pc);
     }
     {
       KernelTimer kt_("head_grad_kernel", s);
-      const unsigned g2 = 8 * (unsigned)cdiv((int64_t)tiles_t * cdiv(L.a.K, S::BK) * L.slabs, 8);
-      hipLaunchKernelGGL((head_grad_kernel<BT>), dim3(g2), dim3(64 * S::kWaves), 0, s, L, b, pc, L.slabs);
+      const unsigned g2 = 8 * (unsigned)cdiv((int64_t)tiles_t * cdiv(L.a.K, S::BK), 8);
+      hipLaunchKernelGGL((head_grad_kernel<BT>), dim3(g2 > 256 ? g2 : 256), dim3(64 * S::kWaves), 0, s, L, b, pc);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   {
     KernelTimer kt_("head_finish_kernel", s);
-    hipLaunchKernelGGL(head_finish_kernel, dim3((unsigned)L.block), dim3(256), 0, s, L, b, L.slabs);
+    hipLaunchKernelGGL(head_finish_kernel<BT>, dim3((unsigned)L.block), dim3(256), 0, s, L, b);
   }
   return hipGetLastError();
 }
@@ -652,16 +720,13 @@ hipError_t launch_head_loss(const HeadLossArgs& a, void* ws, hipStream_t s) {
   l.L.status = status_word(&e);
   if (!l.L.status) return e;
   {
-    KernelTimer kt_("head_select_kernel", s);
-    hipLaunchKernelGGL(head_select_kernel, dim3(1), dim3(1024), 0, s, l.L, (int)(l.blocks * l.L.pieces));
+    KernelTimer kt_("head_begin_kernel", s);
+    hipLaunchKernelGGL(head_begin_kernel, dim3((unsigned)(1 + cdiv(a.T, 4))), dim3(1024), 0, s, l.L,
+                       (int)(l.blocks * l.L.pieces));
   }
   for (int b = 0; b < l.blocks; ++b) {
     e = small_tiles(a.T) ? launch_block<64>(l, b, s) : launch_block<256>(l, b, s);
     if (e != hipSuccess) return e;
-  }
-  {
-    KernelTimer kt_("head_rest_kernel", s);
-    hipLaunchKernelGGL(head_rest_kernel, dim3((unsigned)(a.T < 1024 ? a.T : 1024)), dim3(256), 0, s, l.L);
   }
   {
     KernelTimer kt_("head_mean_kernel", s);

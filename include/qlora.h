@@ -440,7 +440,7 @@ int qlora_gated_bwd(int32_t qtype, const uint16_t* dH, const uint16_t* X, const 
  *   T >= 0 (0: mean is set to 0), K a multiple of 64 in [64, 2^20], V >= 1;
  *   T*K*2 bytes below 2^31, T * ceil(V / 32) below 2^31.
  *   workspace  qlora_head_loss_workspace_bytes(T,K,V,dX != NULL) bytes: with a
- *            gradient at most 64 MB of exponentials (of a piece of the
+ *            gradient at most 128 MB of exponentials (of a piece of the
  *            vocabulary and 4096 tokens), 4096 K 4 bytes or 64 MB of sums, and
  *            8 bytes for every 128 (T <= 64: 32) logits of 4096 tokens.
  * Only learned tokens are multiplied.  Logits and sums are fp32.  The

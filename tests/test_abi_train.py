@@ -92,7 +92,7 @@ def test_head_loss_workspace(L):
     # Without a gradient: sums and lists; with one, no more than is said, however many tokens.
     assert f(4096, 4096, 128000, 0) < 8 * 4096 * 1000 + (1 << 20)
     for T, K, V in ((4096, 4096, 128000), (16384, 4096, 128000), (512, 8192, 32000), (65, 64, 1 << 20)):
-        assert f(T, K, V, 1) < (64 << 20) + max(4 * 4096 * K, 64 << 20) + 8 * min(T, 4096) * (V // 128 + 1) + 4 * T + (1 << 20)
+        assert f(T, K, V, 1) < (130 << 20) + max(4 * 4096 * K, 64 << 20) + 8 * min(T, 4096) * (V // 128 + 1) + 16 * T + (1 << 20)
 
 
 def G(*entries):
