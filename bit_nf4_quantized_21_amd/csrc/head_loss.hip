@@ -191,61 +191,89 @@ __host__ __device__ __forceinline__ int slabs_of(int64_t rows, int64_t K, int64_
 }
 
 // The main loop of both products: a workgroup's steps of 64 contracted values
-// through two stages of LDS.  A step is four substeps of A x B MFMAs; beside
+// through LDS, W in three stages and the other operand, which is smaller and
+// comes from the caches, in two.  A step is four substeps of A x B MFMAs; beside
 // each MFMA goes a fixed share of the other work, fenced so that it stays there:
 // the operands of the next substep are read from LDS, and in the last substep,
-// once every wave has read the stage for the last time (the barrier before it),
-// the rows of two steps further on are sent for into it.  They are waited for at
-// the next step's barrier, a whole step later.
-//   load(stage, step, i)  load i of L of a step's rows (past the last: nothing)
-//   read(stage, s, i)     LDS read i of R of substep s
-//   mma(s, a, c)          MFMA of operands a and c
-template <int A, int B, int R, int L, class Load, class Read, class Mma>
-__device__ __forceinline__ void pipeline(int nk, Load load, Read read, Mma mma) {
-  constexpr int N = A * B;
-  auto wait = []() __attribute__((always_inline)) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  };
+// once every wave has read this step's stages for the last time (the barrier
+// before it), what comes next is sent for into them.  W is on its way for two
+// steps and the other operand for one, before the barrier at which a wave waits
+// for all but its last loads of W.  (W in two stages: 235 for 218 us where it
+// comes from memory, 512 tokens of 8192 over 32000 words.)
+//   load_o(stage, step, i)  load i of LO of a step's rows (past the last: nothing)
+//   load_w(stage, step, i)  the same of W, i of LW
+//   read(o, w, s, i)        LDS read i of R of substep s, from stages o and w
+//   mma(s, a, c)            MFMA of operands a and c
+template <int A, int B, int R, int LO, int LW, class LoadO, class LoadW, class Read, class Mma>
+__device__ __forceinline__ void pipeline(int nk, LoadO load_o, LoadW load_w, Read read, Mma mma) {
+  constexpr int N = A * B, L = LO + LW;
 #pragma unroll
-  for (int i = 0; i < L; ++i) load(0, 0, i);
+  for (int st = 0; st < 2; ++st) {
 #pragma unroll
-  for (int i = 0; i < L; ++i) load(1, 1, i);
-  wait();
+    for (int i = 0; i < LO; ++i) load_o(st, st, i);
 #pragma unroll
-  for (int i = 0; i < R; ++i) read(0, 0, i);
+    for (int i = 0; i < LW; ++i) load_w(st, st, i);
+  }
+#pragma unroll
+  for (int i = 0; i < LW; ++i) load_w(2, 2, i);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(L + LW) : "memory");
+#pragma unroll
+  for (int i = 0; i < R; ++i) read(0, 0, 0, i);
   __builtin_amdgcn_sched_barrier(0);
-  auto step = [&](auto stage, int kb) __attribute__((always_inline)) {
-    constexpr int cur = decltype(stage)::value;
+  auto step = [&](auto phase, int kb) __attribute__((always_inline)) {
+    constexpr int o = decltype(phase)::value % 2, w = decltype(phase)::value % 3;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      if (s == 3) wait();
+      if (s == 3) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LW) : "memory");
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         mma(s, i / B, i % B);
 #pragma unroll
-        for (int r = i * R / N; r < (i + 1) * R / N; ++r) read(s < 3 ? cur : 1 - cur, (s + 1) & 3, r);
+        for (int r = i * R / N; r < (i + 1) * R / N; ++r) read(s < 3 ? o : 1 - o, s < 3 ? w : (w + 1) % 3, (s + 1) & 3, r);
         if (s == 3)
 #pragma unroll
-          for (int l = i * L / N; l < (i + 1) * L / N; ++l) load(cur, kb + 2, l);
+          for (int l = i * L / N; l < (i + 1) * L / N; ++l) {
+            if (l < LO) load_o(o, kb + 2, l);
+            else load_w(w, kb + 3, l - LO);
+          }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
   int kb = 0;
-  for (; kb + 2 <= nk; kb += 2) {
+  for (; kb + 6 <= nk; kb += 6) {
     step(std::integral_constant<int, 0>{}, kb);
     step(std::integral_constant<int, 1>{}, kb + 1);
+    step(std::integral_constant<int, 2>{}, kb + 2);
+    step(std::integral_constant<int, 3>{}, kb + 3);
+    step(std::integral_constant<int, 4>{}, kb + 4);
+    step(std::integral_constant<int, 5>{}, kb + 5);
   }
   if (kb < nk) step(std::integral_constant<int, 0>{}, kb);
-  wait();  // the stages are free
+  if (kb + 1 < nk) step(std::integral_constant<int, 1>{}, kb + 1);
+  if (kb + 2 < nk) step(std::integral_constant<int, 2>{}, kb + 2);
+  if (kb + 3 < nk) step(std::integral_constant<int, 3>{}, kb + 3);
+  if (kb + 4 < nk) step(std::integral_constant<int, 4>{}, kb + 4);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the stages are free
 }
+
+// The stages of a kernel in LDS, each an object of its own, so that the compiler
+// can tell one being filled from those being read.
+struct Stages {
+  unsigned char* w[3];
+  unsigned char* o[2];
+  // Where 64 rows of what is staged on the way out go.
+  __device__ __forceinline__ unsigned char* area(int q) const {
+    return q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : o[0];
+  }
+};
 
 // First product, one tile: the logits of BT tokens and BV vocabulary rows, and
 // of them the sums of exponentials (one per token and wave) and, for the
 // gradient, the exponentials themselves.
 template <int BT, int NW, int BV, int WV, int WT, bool GRAD>
 __device__ __forceinline__ void logits_tile(const Loss& L, int b, int pc, int rows, int r0, int64_t v0,
-                                            unsigned char* st0, unsigned char* st1) {
+                                            const Stages& st) {
   constexpr int A = BV / WV / 32, B = BT / WT / 32;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int l32 = lane & 31, h = lane >> 5, wv = wave % WV, wt = wave / WV;
@@ -271,13 +299,12 @@ __device__ __forceinline__ void logits_tile(const Loss& L, int b, int pc, int ro
     const int64_t t = ok ? L.list[b * L.block + r0 + row] : 0;
     bo[i] = ok ? (uint32_t)(t * K * 2 + ((dc ^ ((row >> 1) & 7)) << 4)) : kOffNone;
   }
-  // Load i of step kb's rows (past the last step: nothing is read).
   const int nk = (int)(K / 64);
-  unsigned char* const ring[2] = {st0, st1};
-  auto load = [&](int stage, int kb, int i) __attribute__((always_inline)) {
-    const uint32_t at_k = kb < nk ? (uint32_t)kb * 128 : kOffNone;
-    if (i < NA) buf_load16_to_lds(rw, ring[stage] + (wave * (BV / NW) + 8 * i) * 128, ao[i] + at_k);
-    else buf_load16_to_lds(rx, ring[stage] + (BV + wave * (BT / NW) + 8 * (i - NA)) * 128, bo[i - NA] + at_k);
+  auto load_w = [&](int stage, int kb, int i) __attribute__((always_inline)) {
+    buf_load16_to_lds(rw, st.w[stage] + (wave * (BV / NW) + 8 * i) * 128, ao[i] + (kb < nk ? (uint32_t)kb * 128 : kOffNone));
+  };
+  auto load_x = [&](int stage, int kb, int i) __attribute__((always_inline)) {
+    buf_load16_to_lds(rx, st.o[stage] + (wave * (BT / NW) + 8 * i) * 128, bo[i] + (kb < nk ? (uint32_t)kb * 128 : kOffNone));
   };
   f32x16 acc[A][B];
 #pragma unroll
@@ -289,13 +316,13 @@ __device__ __forceinline__ void logits_tile(const Loss& L, int b, int pc, int ro
   const int sw = (l32 >> 1) & 7;
   bf16x8 oa[2][A], ob[2][B];  // operands of two substeps
   // Operand i of substep s: i < B tokens, else vocabulary rows.
-  auto read = [&](int stage, int s, int i) __attribute__((always_inline)) {
+  auto read = [&](int o, int w, int s, int i) __attribute__((always_inline)) {
     const int ch = ((2 * s + h) ^ sw) << 4;
-    if (i < B) ob[s & 1][i] = *reinterpret_cast<const bf16x8*>(ring[stage] + (BV + wt * (BT / WT) + 32 * i + l32) * 128 + ch);
-    else oa[s & 1][i - B] = *reinterpret_cast<const bf16x8*>(ring[stage] + (wv * (BV / WV) + 32 * (i - B) + l32) * 128 + ch);
+    if (i < B) ob[s & 1][i] = *reinterpret_cast<const bf16x8*>(st.o[o] + (wt * (BT / WT) + 32 * i + l32) * 128 + ch);
+    else oa[s & 1][i - B] = *reinterpret_cast<const bf16x8*>(st.w[w] + (wv * (BV / WV) + 32 * (i - B) + l32) * 128 + ch);
   };
-  pipeline<A, B, A + B, NA + NB>(
-      nk, load, read,
+  pipeline<A, B, A + B, NB, NA>(
+      nk, load_x, load_w, read,
       [&](int s, int a, int c) __attribute__((always_inline)) { acc[a][c] = mfma32(oa[s & 1][a], ob[s & 1][c], acc[a][c]); });
 
   // Lane (l32, h) holds of token 32 c + l32 the logits of rows 8 (e / 4) + 4 h
@@ -346,8 +373,8 @@ __device__ __forceinline__ void logits_tile(const Loss& L, int b, int pc, int ro
     const int64_t stat = (v0 + wv * (BV / WV)) / (BV / WV);
     if (ok && h == 0 && stat < L.nstat) L.stats[(int64_t)rt * L.nstat + stat] = make_float2(ref, sum);
     if constexpr (GRAD) {
-      unsigned char* const row = (wt * (BT / WT) + 32 * c < BT / 2 ? st0 : st1) +
-                                 ((wt * (BT / WT) + 32 * c + l32) % (BT / 2)) * (BV * 2);
+      const int tr = wt * (BT / WT) + 32 * c + l32;
+      unsigned char* const row = st.area(tr / 64) + tr % 64 * (BV * 2);
 #pragma unroll
       for (int a = 0; a < A; ++a)
 #pragma unroll
@@ -365,7 +392,7 @@ __device__ __forceinline__ void logits_tile(const Loss& L, int b, int pc, int ro
 #pragma unroll
     for (int i = 0; i < BT * CH / (64 * NW); ++i) {
       const int idx = 64 * NW * i + tid, row = idx / CH, ch = idx % CH;
-      const unsigned char* p = (row < BT / 2 ? st0 : st1) + (row % (BT / 2)) * (BV * 2) + ((ch ^ (row & 31 & (CH - 1))) << 4);
+      const unsigned char* p = st.area(row / 64) + row % 64 * (BV * 2) + ((ch ^ (row & 31 & (CH - 1))) << 4);
       if (r0 + row < rows)
         *reinterpret_cast<u32x4*>(L.P + (int64_t)(r0 + row) * L.pitch + (v0 - c0) + 8 * ch) =
             *reinterpret_cast<const u32x4*>(p);
@@ -381,7 +408,9 @@ template <int BT, bool GRAD>
 __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_logits_kernel(Loss L, int b, int pc) {
   using S = Shape<BT>;
   constexpr int BV = S::BV;
-  __shared__ __align__(1024) unsigned char st0[(BV + BT) * 128], st1[(BV + BT) * 128];
+  __shared__ __align__(1024) unsigned char w0[BV * 128], w1[BV * 128], w2[BV * 128], x0[BT * 128], x1[BT * 128];
+  const Stages st{{w0, w1, w2}, {x0, x1}};
+  static_assert(BT == 64 || (BT == 256 && BV <= BT), "64 rows on the way out fit a stage");
   const int rows = rows_of(L, b);
   const int64_t c0 = (int64_t)pc * L.piece, c1 = c0 + L.piece < L.a.V ? c0 + L.piece : L.a.V;
   const int tiles_t = (rows + BT - 1) / BT, tiles_v = (int)((c1 - c0 + BV - 1) / BV), tiles = tiles_t * tiles_v;
@@ -393,14 +422,14 @@ __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_logits_kernel(Los
     const int n = xcd * per + local;
     if (n >= whole) return;
     const TileAt at = tile_at(n, tiles_t, tiles_v);
-    logits_tile<BT, S::kWaves, BV, S::WV, S::WT, GRAD>(L, b, pc, rows, at.t * BT, c0 + (int64_t)at.other * BV, st0, st1);
+    logits_tile<BT, S::kWaves, BV, S::WV, S::WT, GRAD>(L, b, pc, rows, at.t * BT, c0 + (int64_t)at.other * BV, st);
   } else if constexpr (BT == 256) {
     const int per2 = (2 * rest + 7) / 8, n = xcd * per2 + local - per;
     if (!halves || local - per >= per2 || n >= 2 * rest) return;
     const TileAt at = tile_at(whole + n / 2, tiles_t, tiles_v);
     const int64_t v0 = c0 + (int64_t)at.other * BV + (n & 1) * (BV / 2);
     if (v0 >= c1) return;
-    logits_tile<BT, 8, BV / 2, 1, 8, GRAD>(L, b, pc, rows, at.t * BT, v0, st0, st1);
+    logits_tile<BT, 8, BV / 2, 1, 8, GRAD>(L, b, pc, rows, at.t * BT, v0, st);
   }
 }
 
@@ -444,8 +473,8 @@ template <int BT>
 __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_grad_kernel(Loss L, int b, int pc) {
   using S = Shape<BT>;
   constexpr int NW = S::kWaves, BK = S::BK, A = BT / S::GT / 32, B = BK / S::GK / 32;
-  constexpr int kStage = BT * 128 + 64 * BK * 2;
-  __shared__ __align__(1024) unsigned char st0[kStage], st1[kStage];
+  __shared__ __align__(1024) unsigned char w0[BK * 128], w1[BK * 128], w2[BK * 128], p0[BT * 128], p1[BT * 128];
+  const Stages st{{w0, w1, w2}, {p0, p1}};
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int l32 = lane & 31, h = lane >> 5, wk = wave % S::GK, wt = wave / S::GK;
   const int rows = rows_of(L, b);
@@ -480,18 +509,16 @@ __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_grad_kernel(Loss 
     wo[i] = (uint32_t)((v * K + 8 * ch) * 2);
   }
   const int nk = send - sbeg;
-  unsigned char* const ring[2] = {st0, st1};
-  auto load = [&](int stage, int step, int i) __attribute__((always_inline)) {
-    const int sb = sbeg + step;
-    if (i < NP) {
-      buf_load16_to_lds(rp, ring[stage] + (wave * (BT / NW) + 8 * i) * 128, po[i] + (step < nk ? (uint32_t)sb * 128 : kOffNone));
-    } else {
-      // W's rows from this step's first on, in a view of their own: a piece of
-      // them can be larger than one.
-      const int64_t v = c0 + (int64_t)sb * 64;
-      const rsrc_t rw = make_rsrc(L.a.W + v * K + k0, step < nk ? ((V - v) * K - k0) * 2 : 0);
-      buf_load16_to_lds(rw, ring[stage] + BT * 128 + (wave * ND + i - NP) * 1024, wo[i - NP]);
-    }
+  auto load_p = [&](int stage, int step, int i) __attribute__((always_inline)) {
+    buf_load16_to_lds(rp, st.o[stage] + (wave * (BT / NW) + 8 * i) * 128,
+                      po[i] + (step < nk ? (uint32_t)(sbeg + step) * 128 : kOffNone));
+  };
+  // W's rows from a step's first on, in a view of their own: a piece of them can
+  // be larger than one.
+  auto load_w = [&](int stage, int step, int i) __attribute__((always_inline)) {
+    const int64_t v = c0 + (int64_t)(sbeg + step) * 64;
+    const rsrc_t rw = make_rsrc(L.a.W + v * K + k0, step < nk ? ((V - v) * K - k0) * 2 : 0);
+    buf_load16_to_lds(rw, st.w[stage] + (wave * ND + i) * 1024, wo[i]);
   };
   f32x16 acc[A][B];
 #pragma unroll
@@ -507,19 +534,19 @@ __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_grad_kernel(Loss 
   bf16x8 oa[2][A];
   s16x4 ob[2][B][2];
   // Operand i of substep s: i < 2 B half of eight rows of W, else tokens.
-  auto read = [&](int stage, int s, int i) __attribute__((always_inline)) {
+  auto read = [&](int o, int w, int s, int i) __attribute__((always_inline)) {
     if (i < 2 * B) {
       const int e = i & 1, c = i >> 1;
       const int v = 16 * s + 4 * e + tr_row, col = wk * (BK / S::GK) + 32 * c + tr_col;
       ob[s & 1][c][e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_s16x4*)(ring[stage] + BT * 128 + v * BK * 2 + (((col >> 3) ^ ((v & 3) << 2)) << 4) + (col & 7) * 2));
+          (lds_s16x4*)(st.w[w] + v * BK * 2 + (((col >> 3) ^ ((v & 3) << 2)) << 4) + (col & 7) * 2));
     } else {
       oa[s & 1][i - 2 * B] = *reinterpret_cast<const bf16x8*>(
-          ring[stage] + (wt * (BT / S::GT) + 32 * (i - 2 * B) + l32) * 128 + (((2 * s + h) ^ sw) << 4));
+          st.o[o] + (wt * (BT / S::GT) + 32 * (i - 2 * B) + l32) * 128 + (((2 * s + h) ^ sw) << 4));
     }
   };
-  pipeline<A, B, A + 2 * B, NP + ND>(
-      nk, load, read, [&](int s, int a, int c) __attribute__((always_inline)) {
+  pipeline<A, B, A + 2 * B, NP, ND>(
+      nk, load_p, load_w, read, [&](int s, int a, int c) __attribute__((always_inline)) {
         const uint2 lo = __builtin_bit_cast(uint2, ob[s & 1][c][0]), hi = __builtin_bit_cast(uint2, ob[s & 1][c][1]);
         acc[a][c] = mfma32(oa[s & 1][a], as_bf16x8(lo.x, lo.y, hi.x, hi.y), acc[a][c]);
       });
