@@ -53,6 +53,8 @@
 #include "splitk.hpp"
 #include "timing.hpp"
 
+#include <type_traits>
+
 namespace qlora {
 
 namespace {
@@ -391,34 +393,41 @@ __global__ __launch_bounds__(256, 1) void gemm_fwd_kernel(FwdGemmParams p, Codeb
       *reinterpret_cast<uint2*>(xring[2 * half + (mi >> 2)] + row * 256 + ((c ^ (row & 15)) << 4) + 8 * h) = make_uint2(lo, hi);
     };
     const bool save = p.saved != nullptr;
-    uint32_t p2[8][4][2];
     __syncthreads();  // every wave is done with the stages
+    // One straight run of code per activation: a choice between them at each of
+    // the 128 pairs cost 20 us a tile.
+    auto emit = [&](auto kind) __attribute__((always_inline)) {
+      uint32_t p2[8][4][2];
 #pragma unroll
-    for (int mi = 0; mi < 8; ++mi)
+      for (int mi = 0; mi < 8; ++mi)
 #pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) {
-        GatedValues v[4];
+        for (int q4 = 0; q4 < 4; ++q4) {
+          GatedValues v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = gated_values(p.act, acc[0][mi][4 * q4 + e], acc[1][mi][4 * q4 + e]);
-        put(0, mi, q4, pack_bf16x2(v[0].h, v[1].h), pack_bf16x2(v[2].h, v[3].h));
-        if (save) {
-          put(1, mi, q4, multiplier_bits(v[0].p1) | multiplier_bits(v[1].p1) << 16,
-              multiplier_bits(v[2].p1) | multiplier_bits(v[3].p1) << 16);
-          p2[mi][q4][0] = multiplier_bits(v[0].p2) | multiplier_bits(v[1].p2) << 16;
-          p2[mi][q4][1] = multiplier_bits(v[2].p2) | multiplier_bits(v[3].p2) << 16;
+          for (int e = 0; e < 4; ++e)
+            v[e] = gated_values<decltype(kind)::value>(acc[0][mi][4 * q4 + e], acc[1][mi][4 * q4 + e]);
+          put(0, mi, q4, pack_bf16x2(v[0].h, v[1].h), pack_bf16x2(v[2].h, v[3].h));
+          if (save) {
+            put(1, mi, q4, multiplier_pair(v[0].p1, v[1].p1), multiplier_pair(v[2].p1, v[3].p1));
+            p2[mi][q4][0] = multiplier_pair(v[0].p2, v[1].p2);
+            p2[mi][q4][1] = multiplier_pair(v[2].p2, v[3].p2);
+          }
         }
-      }
-    __syncthreads();
-    store_tile(0, P.Y);
-    if (!save) return;
-    store_tile(1, p.saved);
-    __syncthreads();
+      __syncthreads();
+      store_tile(0, P.Y);
+      if (!save) return;
+      store_tile(1, p.saved);
+      __syncthreads();
 #pragma unroll
-    for (int mi = 0; mi < 8; ++mi)
+      for (int mi = 0; mi < 8; ++mi)
 #pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) put(0, mi, q4, p2[mi][q4][0], p2[mi][q4][1]);
-    __syncthreads();
-    store_tile(0, p.saved + T * N);
+        for (int q4 = 0; q4 < 4; ++q4) put(0, mi, q4, p2[mi][q4][0], p2[mi][q4][1]);
+      __syncthreads();
+      store_tile(0, p.saved + T * N);
+    };
+    if (p.act == kActSilu) emit(std::integral_constant<int, kActSilu>{});
+    else if (p.act == kActGelu) emit(std::integral_constant<int, kActGelu>{});
+    else emit(std::integral_constant<int, kActGeluTanh>{});
     return;
   }
 

@@ -332,8 +332,8 @@ __global__ __launch_bounds__(kThreads) void gemv_fwd_kernel(GemvGroupT<NMAX> G, 
         const GatedValues v = gated_values(G.act, ys[0], ys[1]);
         p.Y[at] = (uint16_t)(pack_bf16x2(v.h, 0.0f) & 0xFFFF);
         if (G.saved) {
-          G.saved[at] = (uint16_t)multiplier_bits(v.p1);
-          G.saved[T * N + at] = (uint16_t)multiplier_bits(v.p2);
+          G.saved[at] = (uint16_t)(multiplier_top(v.p1) >> 16);
+          G.saved[T * N + at] = (uint16_t)(multiplier_top(v.p2) >> 16);
         }
       } else {
         const uint32_t v = pack_bf16x2(ys[0], 0.0f);

@@ -93,9 +93,9 @@ def clip(grads, max_norm):
 
 def multiplier(x):
     """A kept multiplier: 10 significant bits from 2^-30 to 2^33, multiples of
-    2^-39 below, infinite from there on (ties to even)."""
+    2^-39 below, infinite from there on (ties away from zero)."""
     x = np.asarray(x, dtype=np.float64)
     _, e = np.frexp(np.abs(x))                     # |x| in [2^(e-1), 2^e)
     unit = np.ldexp(1.0, np.maximum(e - 10, -39))
-    y = np.round(x / unit) * unit
+    y = np.copysign(np.floor(np.abs(x) / unit + 0.5) * unit, x)
     return np.where(np.abs(y) >= 2.0 ** 33 - 2.0 ** 23, np.copysign(np.inf, x), y)

@@ -113,9 +113,10 @@ def test_clip():
 def test_multiplier():
     m = train.multiplier
     assert m(1.0) == 1.0 and m(-1.5) == -1.5 and m(0.0) == 0.0
-    assert m(1 + 2.0 ** -9) == 1 + 2.0 ** -9 and m(1 + 2.0 ** -10) == 1.0       # a tie, to even
+    assert m(1 + 2.0 ** -9) == 1 + 2.0 ** -9 and m(1 + 2.0 ** -10) == 1 + 2.0 ** -9    # a tie, away from zero
+    assert m(1 + 1.9 * 2.0 ** -11) == 1.0 and m(-1 - 2.0 ** -10) == -1 - 2.0 ** -9
     assert m(1 + 3 * 2.0 ** -10) == 1 + 2.0 ** -8                               # the next one
-    assert m(2.0 ** -39) == 2.0 ** -39 and m(2.0 ** -40) == 0.0 and m(3 * 2.0 ** -40) == 2.0 ** -38
+    assert m(2.0 ** -39) == 2.0 ** -39 and m(2.0 ** -40) == 2.0 ** -39 and m(2.0 ** -41) == 0.0
     assert m(2.0 ** 33) == np.inf and m(-2.0 ** 40) == -np.inf and m(2.0 ** 32) == 2.0 ** 32
     assert m(2.0 ** 33 - 2.0 ** 24) == 2.0 ** 33 - 2.0 ** 24 and m(2.0 ** 33 - 2.0 ** 23) == np.inf
     x = RNG.normal(size=1000) * 10.0 ** RNG.uniform(-8, 9, 1000)
