@@ -438,7 +438,7 @@ SplitPlan dx_plan(int64_t T, int64_t K, int64_t N, int batch) {
 }
 
 SplitPlan dx_pair_plan(int64_t T, int64_t K, int64_t N) {
-  return make_split_plan(((K + kTileK - 1) / kTileK) * ((T + kTileT - 1) / kTileT), 2 * ((N + 63) / 64));
+  return make_pair_plan(((K + kTileK - 1) / kTileK) * ((T + kTileT - 1) / kTileT), 2 * ((N + 63) / 64));
 }
 
 hipError_t launch_gemm_dx_pair(const DxGemmParams& p0, const Codebook& cb, hipStream_t s) {

@@ -467,7 +467,7 @@ SplitPlan fwd_plan(int64_t T, int64_t K, int64_t N, int batch) {
 }
 
 SplitPlan fwd_pair_plan(int64_t T, int64_t K, int64_t N) {
-  return make_split_plan(((N + kTileN / 2 - 1) / (kTileN / 2)) * ((T + kTileM - 1) / kTileM), K / 64);
+  return make_pair_plan(((N + kTileN / 2 - 1) / (kTileN / 2)) * ((T + kTileM - 1) / kTileM), K / 64);
 }
 
 hipError_t launch_gemm_fwd_pair(const FwdGemmParams& p0, const Codebook& cb, hipStream_t s) {

@@ -165,6 +165,20 @@ inline SplitPlan make_split_plan(int64_t tiles, int64_t steps) {
   return pl;
 }
 
+// The plan of a gated pair's GEMMs: split only where that leaves a workgroup more
+// than 15 steps less to do, since the hand-off costs as much (257 tokens x 776
+// features, forward, in one slice and in four: K = 1024 45.8 and 49.2 us, K = 1536
+// 54.0 and 51.9, K = 4096 95.7 and 62.4).
+inline SplitPlan make_pair_plan(int64_t tiles, int64_t steps) {
+  SplitPlan pl = make_split_plan(tiles, steps);
+  if (pl.S > 1 && pl.steps - pl.steps_per <= 15) {
+    pl.S = 1;
+    pl.full = pl.items = pl.tx;
+    pl.steps_per = pl.steps;
+  }
+  return pl;
+}
+
 struct TileItem {
   int tile;     // tile index, or -1: nothing to do
   int sidx;     // slice

@@ -177,6 +177,7 @@ class GradSet:
             device = g.device
             self.descs[i] = Grad(g.data_ptr(), o.data_ptr(), g.numel(), *kinds)
         self.device = device
+        self.workspace_bytes = clip_grads_workspace_bytes(len(self.grads))
 
     def __len__(self):
         return len(self.grads)
@@ -198,7 +199,7 @@ def clip_grads(grads, max_norm, out=None, norm=None, workspace=None, stream=None
         grads = GradSet(grads, out)
     device = grads.device if len(grads) else "cuda"
     norm = _empty((1,), torch.float32, device, stream) if norm is None else _given(norm, (1,), torch.float32, "norm")
-    nbytes = clip_grads_workspace_bytes(len(grads))
+    nbytes = grads.workspace_bytes
     workspace = _workspace(nbytes, device, workspace, stream)
     _check(lib().qlora_clip_grads(len(grads), grads.descs, float(max_norm), _p(norm), _p(workspace), nbytes,
                                   _stream(stream)))
