@@ -668,7 +668,7 @@ Layout layout(const HeadLossArgs& a, bool grad, char* ws) {
   L.pitch = piece + (piece % 2048 == 0 ? 128 : 0);
   size_t at = 0;
   auto take = [&](size_t bytes) {
-    char* p = ws + at;
+    char* p = ws ? ws + at : nullptr;  // (sizes alone are asked for without one)
     at += align256(bytes);
     return p;
   };

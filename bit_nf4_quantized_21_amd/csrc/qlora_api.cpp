@@ -536,8 +536,10 @@ int qlora_gated_bwd(int32_t qtype, const uint16_t* dH, const uint16_t* X, const 
 
 namespace {
 int check_head(int64_t T, int64_t K, int64_t V) {
-  if (T < 0 || K < 64 || K > (int64_t(1) << 20) || K % 64 != 0 || V < 1 || V > INT32_MAX) return QLORA_ERR_SHAPE;
-  if (T > INT32_MAX || T * K * 2 > INT32_MAX || T * ((V + 31) / 32) > INT32_MAX) return QLORA_ERR_SHAPE;
+  // (Up to these no launch has 2^32 threads.)
+  if (T < 0 || T > (int64_t(1) << 23) || V < 1 || V > (int64_t(1) << 30)) return QLORA_ERR_SHAPE;
+  if (K < 64 || K > (int64_t(1) << 20) || K % 64 != 0) return QLORA_ERR_SHAPE;
+  if (T * K * 2 > INT32_MAX || T * ((V + 31) / 32) > INT32_MAX) return QLORA_ERR_SHAPE;
   return QLORA_OK;
 }
 }  // namespace

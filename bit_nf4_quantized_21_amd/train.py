@@ -15,6 +15,16 @@ from .qlora import (AdaptedWeight, Grad, _check, _dev, _empty, _need, _p, _qtype
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 
+def _together(device, **tensors):
+    """All of a call's tensors are on one GPU, and that is the current one (whose
+    status word and stream the call uses)."""
+    if device.index != _torch()._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on {device}, which is not the current device")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
 def _adapted(w, K, name):
     """qlora_adapted_weight of a dict of codes, q8, s2, A [K,r] and B [r,N], and its N and r."""
     torch = _torch()
@@ -25,12 +35,15 @@ def _adapted(w, K, name):
                      for k, t in (("codes", torch.uint8), ("q8", torch.uint8), ("s2", torch.float32)))
     N, r = B.shape[1], A.shape[1]
     _weight(codes, q8, s2, N, K)
+    _together(A.device, B=B, codes=codes, q8=q8, s2=s2)
     return AdaptedWeight(codes.data_ptr(), q8.data_ptr(), s2.data_ptr(), A.data_ptr(), B.data_ptr()), N, r
 
 
-def _pair(gate, up, K):
+def _pair(gate, up, X):
+    K = X.shape[1]
     g, N, r = _adapted(gate, K, "gate")
     u, N2, r2 = _adapted(up, K, "up")
+    _together(X.device, gate=gate["A"], up=up["A"])
     if (N, r) != (N2, r2):
         raise ValueError("gate and up must have the same features and rank")
     return g, u, N, r
@@ -62,7 +75,7 @@ def gated_fwd(X, gate, up, alpha, act="silu", save=False, H=None, saved=None, XA
     None, XA f32 [2,T,r])."""
     torch = _torch()
     T, K = _matrix(X, "X").shape
-    g, u, N, r = _pair(gate, up, K)
+    g, u, N, r = _pair(gate, up, X)
     code = _choice(ACTS, act, "act")
     H = _empty((T, N), torch.bfloat16, X.device, stream) if H is None else _given(H, (T, N), torch.bfloat16, "H")
     if saved is not None:
@@ -73,6 +86,7 @@ def gated_fwd(X, gate, up, alpha, act="silu", save=False, H=None, saved=None, XA
         XA = _empty((2, T, r), torch.float32, X.device, stream)
     else:
         _given(XA, (2, T, r), torch.float32, "XA")
+    _together(X.device, H=H, saved=saved, XA=XA, workspace=workspace)
     nbytes = gated_fwd_workspace_bytes(T, K, N, r)
     workspace = _workspace(nbytes, X.device, workspace, stream)
     _check(lib().qlora_gated_fwd(_qtype(qtype), code, _p(X), T, K, N, ctypes.byref(g), ctypes.byref(u), r, float(alpha),
@@ -86,7 +100,7 @@ def gated_bwd(dH, X, saved, XA, gate, up, alpha, dX=None, dA_gate=None, dB_gate=
     Returns (dX bf16 [T,K], dA_gate, dB_gate, dA_up, dB_up)."""
     torch = _torch()
     T, K = _matrix(X, "X").shape
-    g, u, N, r = _pair(gate, up, K)
+    g, u, N, r = _pair(gate, up, X)
     if tuple(_matrix(dH, "dH").shape) != (T, N):
         raise ValueError("dH must be [T,N]")
     _given(saved, (2, T, N), torch.int16, "saved")
@@ -97,6 +111,8 @@ def gated_bwd(dH, X, saved, XA, gate, up, alpha, dX=None, dA_gate=None, dB_gate=
                            (dA_up, (K, r), "dA_up"), (dB_up, (r, N), "dB_up")):
         outs.append(_empty(shape, torch.bfloat16, X.device, stream) if t is None
                     else _given(t, shape, torch.bfloat16, name))
+    _together(X.device, dH=dH, saved=saved, XA=XA, dX=dX, dA_gate=dA_gate, dB_gate=dB_gate, dA_up=dA_up, dB_up=dB_up,
+              workspace=workspace)
     nbytes = gated_bwd_workspace_bytes(T, K, N, r)
     workspace = _workspace(nbytes, X.device, workspace, stream)
     _check(lib().qlora_gated_bwd(_qtype(qtype), _p(dH), _p(X), _p(saved), _p(XA), T, K, N, ctypes.byref(g),
@@ -136,6 +152,7 @@ def head_loss(X, W, targets, dloss=None, grad=True, loss=None, lse=None, mean=No
         _given(dX, (T, K), torch.bfloat16, "dX")
     elif grad:
         dX = _empty((T, K), torch.bfloat16, X.device, stream)
+    _together(X.device, W=W, targets=targets, dloss=dloss, loss=loss, lse=lse, mean=mean, dX=dX, workspace=workspace)
     nbytes = head_loss_workspace_bytes(T, K, V, grad)
     workspace = _workspace(nbytes, X.device, workspace, stream)
     _check(lib().qlora_head_loss(_p(X), T, K, _p(W), V, _p(targets), _p(dloss), _p(loss), _p(lse), _p(mean), _p(dX),
@@ -198,6 +215,8 @@ def clip_grads(grads, max_norm, out=None, norm=None, workspace=None, stream=None
     else:
         grads = GradSet(grads, out)
     device = grads.device if len(grads) else "cuda"
+    if len(grads):
+        _together(device, norm=norm, workspace=workspace)
     norm = _empty((1,), torch.float32, device, stream) if norm is None else _given(norm, (1,), torch.float32, "norm")
     nbytes = grads.workspace_bytes
     workspace = _workspace(nbytes, device, workspace, stream)

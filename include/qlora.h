@@ -407,6 +407,7 @@ int qlora_gated_fwd(int32_t qtype, int32_t act, const uint16_t* X, int64_t T, in
  *   dX [T,K], dA_gate, dA_up [K,r], dB_gate, dB_up [r,N] bf16 are overwritten.
  *   T = 0 is allowed: dX is empty, the others are set to zero.
  *   workspace of at least qlora_gated_bwd_workspace_bytes(T,K,N,r) bytes.
+ * Outputs must not overlap inputs or each other.
  * dG and dU enter the matrix products as bf16, so the results are off by the
  * square root of two times their own rounding (2.4e-3 of the norm).
  * Deterministic.
@@ -437,8 +438,9 @@ int qlora_gated_bwd(int32_t qtype, const uint16_t* dH, const uint16_t* X, const 
  *   mean     [1] fp32 out: the mean loss of the learned tokens, 0 if there are
  *            none.
  *   dX       [T,K] bf16 out, or NULL when no gradient is wanted.
- *   T >= 0 (0: mean is set to 0), K a multiple of 64 in [64, 2^20], V >= 1;
- *   T*K*2 bytes below 2^31, T * ceil(V / 32) below 2^31.
+ *   0 <= T <= 2^23 (0: mean is set to 0), K a multiple of 64 in [64, 2^20],
+ *   1 <= V <= 2^30; T*K*2 bytes below 2^31, T * ceil(V / 32) below 2^31.
+ *   Outputs must not overlap inputs.
  *   workspace  qlora_head_loss_workspace_bytes(T,K,V,dX != NULL) bytes: with a
  *            gradient at most 128 MB of exponentials (of a piece of the
  *            vocabulary and 4096 tokens), 4096 K 4 bytes or 64 MB of sums, and

@@ -72,7 +72,7 @@ def test_head_loss(L):
     def f(X=P, T=5, K=128, w=P, V=1000, targets=P, dloss=None, loss=P, lse=P, mean=P, dX=P, ws=P, wsb=1 << 33):
         return L.qlora_head_loss(X, T, K, w, V, targets, dloss, loss, lse, mean, dX, ws, wsb, None)
     assert f(T=-1) == ESHAPE and f(K=32) == ESHAPE and f(K=100) == ESHAPE and f(K=(1 << 20) + 64) == ESHAPE
-    assert f(V=0) == ESHAPE and f(V=1 << 31) == ESHAPE
+    assert f(V=0) == ESHAPE and f(V=(1 << 30) + 1) == ESHAPE and f(T=(1 << 23) + 1, K=64, V=10) == ESHAPE
     assert f(T=1 << 23) == ESHAPE                              # T*K*2 = 2^31
     assert f(T=1 << 20, K=64, V=1 << 20) == ESHAPE             # too many sums
     for name in ("X", "w", "targets", "loss", "lse", "mean"):
