@@ -193,8 +193,9 @@ __host__ __device__ __forceinline__ int slabs_of(int64_t rows, int64_t K, int64_
 // The main loop of both products: a workgroup's steps of 64 contracted values
 // through LDS, W in three stages and the other operand, which is smaller and
 // comes from the caches, in two.  A step is four substeps of A x B MFMAs; beside
-// each MFMA goes a fixed share of the other work, fenced so that it stays there:
-// the operands of the next substep are read from LDS, and in the last substep,
+// each MFMA goes a fixed share of the other work, fenced so that it stays in its
+// substep (FENCED: beside its MFMA; the transposing reads of the second product
+// are 2 % faster where the compiler places them): the operands of the next substep are read from LDS, and in the last substep,
 // once every wave has read this step's stages for the last time (the barrier
 // before it), what comes next is sent for into them.  W is on its way for two
 // steps and the other operand for one, before the barrier at which a wave waits
@@ -204,7 +205,7 @@ __host__ __device__ __forceinline__ int slabs_of(int64_t rows, int64_t K, int64_
 //   load_w(stage, step, i)  the same of W, i of LW
 //   read(o, w, s, i)        LDS read i of R of substep s, from stages o and w
 //   mma(s, a, c)            MFMA of operands a and c
-template <int A, int B, int R, int LO, int LW, class LoadO, class LoadW, class Read, class Mma>
+template <int A, int B, int R, int LO, int LW, bool FENCED, class LoadO, class LoadW, class Read, class Mma>
 __device__ __forceinline__ void pipeline(int nk, LoadO load_o, LoadW load_w, Read read, Mma mma) {
   constexpr int N = A * B, L = LO + LW;
 #pragma unroll
@@ -236,7 +237,7 @@ __device__ __forceinline__ void pipeline(int nk, LoadO load_o, LoadW load_w, Rea
             if (l < LO) load_o(o, kb + 2, l);
             else load_w(w, kb + 3, l - LO);
           }
-        __builtin_amdgcn_sched_barrier(0);
+        if (FENCED || i == N - 1) __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
@@ -321,7 +322,7 @@ __device__ __forceinline__ void logits_tile(const Loss& L, int b, int pc, int ro
     if (i < B) ob[s & 1][i] = *reinterpret_cast<const bf16x8*>(st.o[o] + (wt * (BT / WT) + 32 * i + l32) * 128 + ch);
     else oa[s & 1][i - B] = *reinterpret_cast<const bf16x8*>(st.w[w] + (wv * (BV / WV) + 32 * (i - B) + l32) * 128 + ch);
   };
-  pipeline<A, B, A + B, NB, NA>(
+  pipeline<A, B, A + B, NB, NA, true>(
       nk, load_x, load_w, read,
       [&](int s, int a, int c) __attribute__((always_inline)) { acc[a][c] = mfma32(oa[s & 1][a], ob[s & 1][c], acc[a][c]); });
 
@@ -545,7 +546,7 @@ __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_grad_kernel(Loss 
           st.o[o] + (wt * (BT / S::GT) + 32 * (i - 2 * B) + l32) * 128 + (((2 * s + h) ^ sw) << 4));
     }
   };
-  pipeline<A, B, A + 2 * B, NP, ND>(
+  pipeline<A, B, A + 2 * B, NP, ND, false>(
       nk, load_p, load_w, read, [&](int s, int a, int c) __attribute__((always_inline)) {
         const uint2 lo = __builtin_bit_cast(uint2, ob[s & 1][c][0]), hi = __builtin_bit_cast(uint2, ob[s & 1][c][1]);
         acc[a][c] = mfma32(oa[s & 1][a], as_bf16x8(lo.x, lo.y, hi.x, hi.y), acc[a][c]);
@@ -606,13 +607,22 @@ __global__ __launch_bounds__(256) void head_finish_kernel(Loss L, int b) {
   const float g = L.a.dloss ? L.a.dloss[t] : 1.0f / (float)*L.count;
   const float up = g / total, down = g * (rest / total);
   const uint16_t* w = L.a.W + L.a.targets[t] * K;
+  // The row of every slab, four on their way at a time (past the last: zeros).
+  const int64_t apart = (int64_t)rows * K;
+  const rsrc_t sums = make_rsrc(L.acc + (int64_t)i * K, ((nslabs - 1) * apart + K) * 4);
   for (int64_t k = tid * 8; k < K; k += 2048) {
     float v[8] = {};
-    for (int s = 0; s < nslabs; ++s) {
-      const float4* p = reinterpret_cast<const float4*>(L.acc + ((int64_t)s * rows + i) * K + k);
-      const float4 x = p[0], y = p[1];
-      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    for (int s0 = 0; s0 < nslabs; s0 += 4) {
+      u32x4 x[4][2];
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          x[s][e] = buf_load16(sums, off_if(s0 + s < nslabs, (uint32_t)(((s0 + s) * apart + k + 4 * e) * 4)));
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += __uint_as_float(x[s][e / 4][e % 4]);
     }
     const u32x4 wv = *reinterpret_cast<const u32x4*>(w + k);
 #pragma unroll
