@@ -462,3 +462,120 @@ def test_clip_set_keeps_its_places():
     assert abs(float(lib.clip_grads(s, 1e9)) - 450 ** 0.5) < 1e-5
     with pytest.raises(ValueError):
         lib.clip_grads(s, 1.0, out=grads)
+
+
+# ---------------------------------------------------------------- full sizes, on the GPU in 64 bits
+
+@pytest.mark.parametrize("T,K,N", [(512, 8192, 22016), (1000, 4096, 11008), (16, 8192, 22016)])
+def test_gated_full_size(T, K, N):
+    """The benchmark's feed-forward layers (several rounds of tiles, split ones) in norm:
+    H within u / sqrt 3 (its rounding) and a tenth, gradients as above."""
+    print(f"gated {T} x {K} -> {N}", flush=True)
+    lib, r, alpha = _lib(), 64, 16.0
+    g = torch.Generator(device="cuda").manual_seed(T)
+
+    def normal(*shape, scale):
+        return (torch.randn(*shape, generator=g, device="cuda") * scale).bfloat16()
+    sides, dense = [], []
+    for _ in range(2):
+        codes, q8, s2 = lib.quantize_dq(torch.randn(N, K, generator=g, device="cuda") * 0.02)
+        sides.append(dict(codes=codes, q8=q8, s2=s2, A=normal(K, r, scale=K ** -0.5), B=normal(r, N, scale=0.01)))
+        dense.append(lib.dequantize_nf4(codes, q8, s2, N * K).view(N, K))
+    X, dH = normal(T, K, scale=1.0), normal(T, N, scale=1.0)
+    H, saved, XA = lib.gated_fwd(X, *sides, alpha, save=True)
+    got = lib.gated_bwd(dH, X, saved, XA, *sides, alpha)
+    leaves = [X.double().requires_grad_()]
+    pre = []
+    for s, w in zip(sides, dense):
+        A, B = s["A"].double().requires_grad_(), s["B"].double().requires_grad_()
+        leaves += [A, B]
+        pre.append(leaves[0] @ w.double().t() + alpha / r * (leaves[0] @ A) @ B)
+    ref = torch.nn.functional.silu(pre[0]) * pre[1]
+    want = torch.autograd.grad(ref, leaves, dH.double())
+
+    def rel(a, b):
+        return float((a.double() - b).norm() / b.norm())
+    assert rel(H, ref.detach()) <= 1.1 * U / np.sqrt(3)
+    for a, b in zip(got, want):
+        assert rel(a, b) <= NORM
+    lib.device_status()
+
+
+@pytest.mark.parametrize("T,K,V,ignored", [(2048, 4096, 32000, 0.4), (512, 8192, 32003, 0.0), (64, 4096, 128000, 0.1),
+                                           (1300, 1024, 70001, 0.3)])
+def test_loss_full_size(T, K, V, ignored):
+    """Whole vocabularies: several rounds, a last round of half tiles, slabs."""
+    print(f"loss {T} x {K} over {V}", flush=True)
+    lib = _lib()
+    g = torch.Generator(device="cuda").manual_seed(V)
+    W = torch.cat([torch.randn(min(8000, V - i), K, generator=g, device="cuda").mul_(K ** -0.5).bfloat16() for i in range(0, V, 8000)])
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    X = (torch.randn(T, K, generator=g, device="cuda") + 6 * torch.rand(T, 1, generator=g, device="cuda") * W[t].float()).bfloat16()
+    t[torch.rand(T, generator=g, device="cuda") < ignored] = -100
+    loss, lse, mean, dX = lib.head_loss(X, W, t)
+    x, w, on = X.double(), W.double(), t >= 0
+    at = t.clamp(min=0)[:, None]
+    z = x @ w.t()
+    ref_lse = torch.logsumexp(z, 1)
+    ref = torch.where(on, ref_lse - z.gather(1, at)[:, 0], 0.0)
+    p = (z - ref_lse[:, None]).exp_()
+    p.scatter_(1, at, 0.0)
+    p.scatter_(1, at, -p.sum(1, keepdim=True))
+    want = torch.where(on, 1.0 / on.sum(), 0.0)[:, None] * (p @ w)
+    # A logit is off by (K + 2) E |x| |w| (Cauchy) at most, the sums by 2^-17.
+    tol = 2 * (K + 2) * E * x.norm(dim=1) * w.norm(dim=1).max() + 2.0 ** -17
+    assert bool(((loss.double() - ref).abs() <= tol).all())
+    assert bool(((lse.double() - torch.where(on, ref_lse, 0.0)).abs() <= tol + 2.0 ** -22 * ref_lse.abs()).all())
+    assert abs(float(mean) - float(ref.sum() / on.sum())) <= float(tol.max())
+    assert float((dX.double() - want).norm() / want.norm()) <= NORM
+    lib.device_status()
+
+
+# ---------------------------------------------------------------- the binding's refusals
+
+def test_binding_refuses_shapes_and_types():
+    lib, rng = _lib(), _rng(9)
+    gate, _ = _weight(rng, 64, 128, 8, "nf4")
+    up, _ = _weight(rng, 64, 128, 8, "nf4")
+    other, _ = _weight(rng, 72, 128, 8, "nf4")
+    rank, _ = _weight(rng, 64, 128, 16, "nf4")
+    X, dH = _dev(_bf16(rng, 20, 128)), _dev(_bf16(rng, 20, 64))
+    _, saved, XA = lib.gated_fwd(X, gate, up, 16.0, save=True)
+
+    def bad(f, *a, error=ValueError, **k):
+        with pytest.raises(error):
+            f(*a, **k)
+    bad(lib.gated_fwd, X, gate, other, 16.0)
+    bad(lib.gated_fwd, X, gate, rank, 16.0)
+    bad(lib.gated_fwd, X[:, :64].contiguous(), gate, up, 16.0)
+    bad(lib.gated_fwd, X.t(), gate, up, 16.0)
+    bad(lib.gated_fwd, X.float(), gate, up, 16.0, error=TypeError)
+    bad(lib.gated_fwd, X, gate, up, 16.0, act="relu")
+    bad(lib.gated_fwd, X, gate, up, 16.0, qtype="int8")
+    bad(lib.gated_fwd, X, dict(gate, codes=gate["codes"][:-1]), up, 16.0)
+    bad(lib.gated_fwd, X, gate, up, 16.0, H=torch.empty(19, 64, dtype=torch.bfloat16, device="cuda"))
+    bad(lib.gated_fwd, X, gate, up, 16.0, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    bad(lib.gated_bwd, dH[:19], X, saved, XA, gate, up, 16.0)
+    bad(lib.gated_bwd, dH, X, saved[:, :19].contiguous(), XA, gate, up, 16.0)
+    bad(lib.gated_bwd, dH, X, saved.view(torch.bfloat16), XA, gate, up, 16.0, error=TypeError)
+    bad(lib.gated_bwd, dH, X, saved, XA[:1], gate, up, 16.0)
+    bad(lib.gated_bwd, dH, X, saved, XA, gate, up, 16.0, dA_up=torch.empty(8, 128, dtype=torch.bfloat16, device="cuda"))
+
+    W, t = _dev(_bf16(rng, 50, 128)), torch.zeros(20, dtype=torch.int64, device="cuda")
+    bad(lib.head_loss, X, W[:, :64].contiguous(), t)
+    bad(lib.head_loss, X, W, t[:19])
+    bad(lib.head_loss, X, W, t.int(), error=TypeError)
+    bad(lib.head_loss, X, W, t, dloss=torch.zeros(3, device="cuda"))
+    bad(lib.head_loss, X, W, t, grad=False, dX=torch.empty_like(X))
+    bad(lib.head_loss, X, W, t, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    bad(lib.head_loss, _dev(_bf16(rng, 4, 96)), _dev(_bf16(rng, 5, 96)), t[:4], error=lib.QLoRAError)
+
+    g = torch.zeros(10, device="cuda")
+    bad(lib.clip_grads, [g], 1.0, out=[torch.zeros(9, device="cuda")])
+    bad(lib.clip_grads, [g], 1.0, out=[])
+    bad(lib.clip_grads, [g.half()], 1.0, error=TypeError)
+    bad(lib.clip_grads, [torch.zeros(4, 4, device="cuda").t()], 1.0)
+    bad(lib.clip_grads, [g, g], 1.0, error=lib.QLoRAError)                   # twice in place
+    bad(lib.clip_grads, [g[:6], g[4:]], 1.0, error=lib.QLoRAError)
+    bad(lib.clip_grads, [g], float("nan"), error=lib.QLoRAError)
+    assert abs(float(lib.clip_grads([g + 1, g + 1], 0.0)) - 20 ** 0.5) < 1e-5
