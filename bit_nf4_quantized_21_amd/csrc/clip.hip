@@ -17,7 +17,7 @@
 // run backwards: what the first read last is still in the caches.
 //
 // Bound by memory: two reads and a write.  448 gradients of 216 M bf16 values:
-// 290 us, 4.5 TB/s of 1.3 GB.
+// 243 us, 5.3 TB/s of 1.3 GB.
 #include "common.hpp"
 #include "timing.hpp"
 #include "train.hpp"
@@ -29,6 +29,13 @@ constexpr int kSetMax = 112;       // 32 bytes each: the arguments stay below 4 
 constexpr int kThreads = 256;
 constexpr int kChunk = 16384;      // values
 constexpr int kGridMax = 2048;     // workgroups (and partials)
+// From so many bytes of gradients on the second kernel marks its accesses as used
+// once, so that they leave those gradients in the last cache (256 MB) that it still
+// has to read.  Clipping into other tensors and, in parentheses, writing the
+// gradients, clipping them in place and reading them, bf16, us without and with the
+// mark: 43 (82) and 39 (82) at 64 MiB, 70 (157) and 68 (163) at 128, 112 (248) and
+// 97 (245) at 192, 159 (359) and 129 (335) at 256, 317 (725) and 273 (690) at 512.
+constexpr int64_t kStreamBytes = (int64_t)192 << 20;
 
 struct SetEntry {
   const void* grad;
@@ -77,18 +84,42 @@ __device__ __forceinline__ double block_sum(double x, double* red) {
 
 __device__ __forceinline__ double square(float x) { return (double)x * (double)x; }
 
-// Eight consecutive values as they are stored, and as fp32.
+// Eight values of a thread as they are stored.  Where neither side is fp32 they
+// are neighbours; otherwise (SPLIT) two groups of four, kThreads groups apart, so
+// that a wave's access of 16 bytes a lane is without gaps on the wide side too (with
+// gaps, marked stores of fp32 took 96 us instead of 66 at 128 MiB).
 template <bool WIDE>
 struct Raw8 {
   u32x4 u[WIDE ? 2 : 1];
 };
+using u32v2 = __attribute__((ext_vector_type(2))) unsigned int;
+using u32v4 = __attribute__((ext_vector_type(4))) unsigned int;
+// Byte offset of half h of group i (of eight) of a thread's.
+template <bool WIDE, bool SPLIT>
+__device__ __forceinline__ int half_at(int i, int h) {
+  return (SPLIT ? (8 * i + 4 * h) * kThreads + 4 * (int)threadIdx.x : 8 * (i * kThreads + (int)threadIdx.x) + 4 * h) * (WIDE ? 4 : 2);
+}
 // (Buffer views: what lies past a chunk's end reads as zero and is not written,
-// without a branch that would hold the next load back.)
-template <bool WIDE>
+// without a branch that would hold the next load back.)  NT: marked as used once
+// (the instruction's nt bit).
+template <bool WIDE, bool SPLIT, bool NT>
 __device__ __forceinline__ Raw8<WIDE> load8(rsrc_t r, int i) {
+  constexpr int aux = NT ? 2 : 0;
   Raw8<WIDE> x;
-  x.u[0] = buf_load16(r, (uint32_t)i * (WIDE ? 4 : 2));
-  if constexpr (WIDE) x.u[1] = buf_load16(r, (uint32_t)i * 4 + 16);
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      x.u[h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, half_at<true, SPLIT>(i, h), 0, aux));
+  } else if constexpr (SPLIT) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32v2 v = __builtin_bit_cast(u32v2, __builtin_amdgcn_raw_buffer_load_b64(r, half_at<false, true>(i, h), 0, aux));
+      x.u[0][2 * h] = v[0];
+      x.u[0][2 * h + 1] = v[1];
+    }
+  } else {
+    x.u[0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, half_at<false, false>(i, 0), 0, aux));
+  }
   return x;
 }
 template <bool WIDE>
@@ -109,16 +140,23 @@ __device__ __forceinline__ float load1(const void* base, int64_t i) {
   if constexpr (WIDE) return static_cast<const float*>(base)[i];
   else return bf16_to_f32(static_cast<const uint16_t*>(base)[i]);
 }
-__device__ __forceinline__ void buf_store16(rsrc_t r, uint32_t off, u32x4 v) {
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(__attribute__((ext_vector_type(4))) unsigned int, v), r, (int)off, 0, 0);
-}
-template <bool WIDE>
+template <bool WIDE, bool SPLIT, bool NT>
 __device__ __forceinline__ void store8(rsrc_t r, int i, const float (&v)[8]) {
+  constexpr int aux = NT ? 2 : 0;
   if constexpr (WIDE) {
-    buf_store16(r, (uint32_t)i * 4, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
-    buf_store16(r, (uint32_t)i * 4 + 16, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      __builtin_amdgcn_raw_buffer_store_b128(u32v4{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])},
+                                             r, half_at<true, SPLIT>(i, h), 0, aux);
   } else {
-    buf_store16(r, (uint32_t)i * 2, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])});
+    const uint32_t w[4] = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    if constexpr (SPLIT) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        __builtin_amdgcn_raw_buffer_store_b64(u32v2{w[2 * h], w[2 * h + 1]}, r, half_at<false, true>(i, h), 0, aux);
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b128(u32v4{w[0], w[1], w[2], w[3]}, r, half_at<false, false>(i, 0), 0, aux);
+    }
   }
 }
 // A view of n values from value i0 on.
@@ -162,7 +200,7 @@ __device__ __forceinline__ double chunk_squares(const void* g, int64_t i0, int n
     const rsrc_t in = view<WIDE>(g, i0, done);
     Raw8<WIDE> r[kVecs];
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) r[k] = load8<WIDE>(in, (k * kThreads + tid) * 8);
+    for (int k = 0; k < kVecs; ++k) r[k] = load8<WIDE, WIDE, false>(in, k);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       float v[8];
@@ -177,7 +215,7 @@ __device__ __forceinline__ double chunk_squares(const void* g, int64_t i0, int n
 
 // (`out` may be `g` itself: a thread reads what it writes, and a chunk is read
 // before it is written.)
-template <bool WIDE, bool OUT_WIDE>
+template <bool WIDE, bool OUT_WIDE, bool NT>
 __device__ __forceinline__ void chunk_scale(const void* g, void* out, int64_t i0, int n, float c) {
   const int tid = threadIdx.x;
   int done = 0;
@@ -186,14 +224,14 @@ __device__ __forceinline__ void chunk_scale(const void* g, void* out, int64_t i0
     const rsrc_t in = view<WIDE>(g, i0, done), to = view<OUT_WIDE>(out, i0, done);
     Raw8<WIDE> r[kVecs];
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) r[k] = load8<WIDE>(in, (k * kThreads + tid) * 8);
+    for (int k = 0; k < kVecs; ++k) r[k] = load8<WIDE, WIDE || OUT_WIDE, NT>(in, k);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       float v[8];
       values<WIDE>(r[k], v);
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[q] *= c;
-      store8<OUT_WIDE>(to, (k * kThreads + tid) * 8, v);
+      store8<OUT_WIDE, WIDE || OUT_WIDE, NT>(to, k, v);
     }
   }
   for (int i = done + tid; i < n; i += kThreads) store1<OUT_WIDE>(out, i0 + i, load1<WIDE>(g, i0 + i) * c);
@@ -223,6 +261,7 @@ __global__ __launch_bounds__(kThreads) void grads_sumsq_kernel(GradSet s, SetArg
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
+template <bool NT>
 __global__ __launch_bounds__(kThreads) void grads_scale_kernel(GradSet s, SetArgs args,
                                                                const double* __restrict__ partial, int nparts,
                                                                float max_norm, float* norm_out) {
@@ -244,10 +283,10 @@ __global__ __launch_bounds__(kThreads) void grads_scale_kernel(GradSet s, SetArg
     const int64_t i0 = (int64_t)(ch - e[i].first) * kChunk;
     const int n = (int)(e[i].n - i0 < kChunk ? e[i].n - i0 : kChunk);
     switch (e[i].kind & 3) {
-      case 0: chunk_scale<false, false>(e[i].grad, e[i].out, i0, n, c); break;
-      case 1: chunk_scale<true, false>(e[i].grad, e[i].out, i0, n, c); break;
-      case 2: chunk_scale<false, true>(e[i].grad, e[i].out, i0, n, c); break;
-      default: chunk_scale<true, true>(e[i].grad, e[i].out, i0, n, c); break;
+      case 0: chunk_scale<false, false, NT>(e[i].grad, e[i].out, i0, n, c); break;
+      case 1: chunk_scale<true, false, NT>(e[i].grad, e[i].out, i0, n, c); break;
+      case 2: chunk_scale<false, true, NT>(e[i].grad, e[i].out, i0, n, c); break;
+      default: chunk_scale<true, true, NT>(e[i].grad, e[i].out, i0, n, c); break;
     }
   }
 }
@@ -262,7 +301,9 @@ hipError_t launch_clip_grads(int count, const GradTensor* g, float max_norm, flo
   SetEntry* table = reinterpret_cast<SetEntry*>(partial + kGridMax);
   SetArgs args;
   uint32_t at = 0;
+  int64_t bytes = 0;
   for (int i = 0; i < count; ++i) {
+    bytes += g[i].n * (g[i].wide ? 4 : 2);
     args.e[i % kSetMax] = SetEntry{g[i].grad, g[i].out, g[i].n, at, (g[i].wide ? 1u : 0u) | (g[i].out_wide ? 2u : 0u)};
     at += (uint32_t)((g[i].n + kChunk - 1) / kChunk);
     const int filled = i % kSetMax + 1;
@@ -283,8 +324,11 @@ hipError_t launch_clip_grads(int count, const GradTensor* g, float max_norm, flo
   if (e != hipSuccess) return e;
   {
     KernelTimer kt_("grads_scale_kernel", s);
-    hipLaunchKernelGGL(grads_scale_kernel, dim3(max_norm > 0.0f ? grid : 1), dim3(kThreads), 0, s, set, args, partial,
-                       grid, max_norm, norm_out);
+    const dim3 grid2(max_norm > 0.0f ? grid : 1);
+    if (bytes >= kStreamBytes)
+      hipLaunchKernelGGL(grads_scale_kernel<true>, grid2, dim3(kThreads), 0, s, set, args, partial, grid, max_norm, norm_out);
+    else
+      hipLaunchKernelGGL(grads_scale_kernel<false>, grid2, dim3(kThreads), 0, s, set, args, partial, grid, max_norm, norm_out);
   }
   return hipGetLastError();
 }

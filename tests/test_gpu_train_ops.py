@@ -579,3 +579,28 @@ def test_binding_refuses_shapes_and_types():
     bad(lib.clip_grads, [g[:6], g[4:]], 1.0, error=lib.QLoRAError)
     bad(lib.clip_grads, [g], float("nan"), error=lib.QLoRAError)
     assert abs(float(lib.clip_grads([g + 1, g + 1], 0.0)) - 20 ** 0.5) < 1e-5
+
+
+@pytest.mark.parametrize("wide,out_wide", [(False, False), (True, False), (False, True), (True, True)])
+def test_clip_hundreds_of_megabytes(wide, out_wide):
+    # Beyond the caches, where the second kernel's accesses are marked as used once.
+    lib = _lib()
+    print(f"clip large {wide} {out_wide}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    total = (220 << 20) // (4 if wide else 2)
+    lengths = [total // 2 + 3, 16384 * 5, 1, total // 2 - 70001, 0, 77777]
+    grads = [torch.randn(n, device="cuda", generator=gen).to(torch.float32 if wide else torch.bfloat16) for n in lengths]
+    ref = float(sum(g.double().square().sum() for g in grads).sqrt())
+    kept = [g.clone() for g in grads]
+    out = [torch.full((n,), 9.0, dtype=torch.float32 if out_wide else torch.bfloat16, device="cuda") for n in lengths]
+    norm = lib.clip_grads(grads, 0.75, out=out)
+    _check_norm(norm, ref)
+    c = 0.75 / (ref + 1e-6)
+    half = 2.0 ** -24 if out_wide else U
+    for o, g, k in zip(out, grads, kept):
+        assert torch.equal(g, k)
+        want = k.double() * c
+        assert bool(((o.double() - want).abs() <= (half + 3 * E + 5 * E) * want.abs() + 1e-40).all())
+    if wide == out_wide:
+        again = lib.clip_grads(grads, 0.75)          # in place
+        assert torch.equal(again, norm) and all(torch.equal(a, b) for a, b in zip(grads, out))
