@@ -29,13 +29,6 @@ constexpr int kSetMax = 112;       // 32 bytes each: the arguments stay below 4 
 constexpr int kThreads = 256;
 constexpr int kChunk = 16384;      // values
 constexpr int kGridMax = 2048;     // workgroups (and partials)
-// From so many bytes of gradients on the second kernel marks its accesses as used
-// once, so that they leave those gradients in the last cache (256 MB) that it still
-// has to read.  Clipping into other tensors and, in parentheses, writing the
-// gradients, clipping them in place and reading them, bf16, us without and with the
-// mark: 43 (82) and 39 (82) at 64 MiB, 70 (157) and 68 (163) at 128, 112 (248) and
-// 97 (245) at 192, 159 (359) and 129 (335) at 256, 317 (725) and 273 (690) at 512.
-constexpr int64_t kStreamBytes = (int64_t)192 << 20;
 
 struct SetEntry {
   const void* grad;
@@ -261,6 +254,12 @@ __global__ __launch_bounds__(kThreads) void grads_sumsq_kernel(GradSet s, SetArg
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
+// From kStreamBytes of gradients on the second kernel marks its accesses as used
+// once, so that they leave those gradients in the last cache that it still has to
+// read.  Clipping into other tensors and, in parentheses, writing the
+// gradients, clipping them in place and reading them, bf16, us without and with the
+// mark: 43 (82) and 39 (82) at 64 MiB, 70 (157) and 68 (163) at 128, 112 (248) and
+// 97 (245) at 192, 159 (359) and 129 (335) at 256, 317 (725) and 273 (690) at 512.
 template <bool NT>
 __global__ __launch_bounds__(kThreads) void grads_scale_kernel(GradSet s, SetArgs args,
                                                                const double* __restrict__ partial, int nparts,

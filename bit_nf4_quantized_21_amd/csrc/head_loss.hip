@@ -31,7 +31,7 @@
 // learned) over 128000 words take 6.7 ms, 1150 TFLOP/s, with the matrix units
 // busy 74 % (first product) and 62 % (second, 240 tiles on 256 compute units) of
 // the clocks at 1.9 GHz; a step of 64 values takes 1.55 and 1.62 us, that of the
-// library's 8192^3 product 1.53.  Few tokens: memory, 262 MB of W in 60 us.
+// library's 8192^3 product 1.53.  Few tokens: memory, 262 MB of W in 43 us, 6.1 TB/s.
 #include "common.hpp"
 #include "device_state.hpp"
 #include "timing.hpp"
@@ -275,12 +275,19 @@ struct Stages {
   }
 };
 
+// Sixteen bytes a lane into LDS; ONCE: marked as used once (the nt bit).
+template <bool ONCE>
+__device__ __forceinline__ void load_to_lds(rsrc_t r, void* lds_block, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)lds_block, 16, (int)off, 0, 0, ONCE ? 2 : 0);
+}
+
 // First product, one tile: the logits of BT tokens and BV vocabulary rows, and
 // of them the sums of exponentials (one per token and wave) and, for the
-// gradient, the exponentials themselves.
-template <int BT, int NW, int BV, int WV, int WT, bool GRAD>
+// gradient, the exponentials themselves.  The contraction starts at step `first`
+// and goes round.
+template <int BT, int NW, int BV, int WV, int WT, bool GRAD, bool ONCE>
 __device__ __forceinline__ void logits_tile(const Loss& L, int b, int pc, int rows, int r0, int64_t v0,
-                                            const Stages& st) {
+                                            int first, const Stages& st) {
   constexpr int A = BV / WV / 32, B = BT / WT / 32;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int l32 = lane & 31, h = lane >> 5, wv = wave % WV, wt = wave / WV;
@@ -307,11 +314,14 @@ __device__ __forceinline__ void logits_tile(const Loss& L, int b, int pc, int ro
     bo[i] = ok ? (uint32_t)(t * K * 2 + ((dc ^ ((row >> 1) & 7)) << 4)) : kOffNone;
   }
   const int nk = (int)(K / 64);
+  auto at = [&](int kb) __attribute__((always_inline)) {
+    return kb < nk ? (uint32_t)(kb + first < nk ? kb + first : kb + first - nk) * 128 : kOffNone;
+  };
   auto load_w = [&](int stage, int kb, int i) __attribute__((always_inline)) {
-    buf_load16_to_lds(rw, st.w[stage] + (wave * (BV / NW) + 8 * i) * 128, ao[i] + (kb < nk ? (uint32_t)kb * 128 : kOffNone));
+    load_to_lds<ONCE>(rw, st.w[stage] + (wave * (BV / NW) + 8 * i) * 128, ao[i] + at(kb));
   };
   auto load_x = [&](int stage, int kb, int i) __attribute__((always_inline)) {
-    buf_load16_to_lds(rx, st.o[stage] + (wave * (BT / NW) + 8 * i) * 128, bo[i] + (kb < nk ? (uint32_t)kb * 128 : kOffNone));
+    buf_load16_to_lds(rx, st.o[stage] + (wave * (BT / NW) + 8 * i) * 128, bo[i] + at(kb));
   };
   f32x16 acc[A][B];
 #pragma unroll
@@ -411,7 +421,7 @@ __device__ __forceinline__ void logits_tile(const Loss& L, int b, int pc, int ro
 // here; XCD x (workgroup b runs on b % 8) takes a run of them.  Where they would
 // leave a last round of the 256 compute units half empty or emptier, that round
 // takes tiles of half as many vocabulary rows.
-template <int BT, bool GRAD>
+template <int BT, bool GRAD, bool ONCE>
 __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_logits_kernel(Loss L, int b, int pc) {
   using S = Shape<BT>;
   constexpr int BV = S::BV;
@@ -429,14 +439,19 @@ __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_logits_kernel(Los
     const int n = xcd * per + local;
     if (n >= whole) return;
     const TileAt at = tile_at(n, tiles_t, tiles_v);
-    logits_tile<BT, S::kWaves, BV, S::WV, S::WT, GRAD>(L, b, pc, rows, at.t * BT, c0 + (int64_t)at.other * BV, st);
+    // Rows of W a power of two apart lie in the same memory channels, and the tiles
+    // of few tokens read theirs once, side by side: each starts at a column of its
+    // own (1 token, 32000 words: 4096 values 62 -> 56 us, 8192 values 110 -> 99).
+    // Larger tiles share W through the caches and stay together.
+    const int first = BT == 64 ? n % (int)(L.a.K / 64) : 0;
+    logits_tile<BT, S::kWaves, BV, S::WV, S::WT, GRAD, ONCE>(L, b, pc, rows, at.t * BT, c0 + (int64_t)at.other * BV, first, st);
   } else if constexpr (BT == 256) {
     const int per2 = (2 * rest + 7) / 8, n = xcd * per2 + local - per;
     if (!halves || local - per >= per2 || n >= 2 * rest) return;
     const TileAt at = tile_at(whole + n / 2, tiles_t, tiles_v);
     const int64_t v0 = c0 + (int64_t)at.other * BV + (n & 1) * (BV / 2);
     if (v0 >= c1) return;
-    logits_tile<BT, 8, BV / 2, 1, 8, GRAD>(L, b, pc, rows, at.t * BT, v0, st);
+    logits_tile<BT, 8, BV / 2, 1, 8, GRAD, ONCE>(L, b, pc, rows, at.t * BT, v0, 0, st);
   }
 }
 
@@ -476,7 +491,7 @@ __global__ __launch_bounds__(256) void head_lift_kernel(Loss L, int b, int pc) {
 
 // Second product: acc[row][k] += sum over the piece of P[row][v] W[v][k].  The
 // contraction is cut into slabs where the tiles alone would not fill the chip.
-template <int BT>
+template <int BT, bool ONCE>
 __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_grad_kernel(Loss L, int b, int pc) {
   using S = Shape<BT>;
   constexpr int NW = S::kWaves, BK = S::BK, A = BT / S::GT / 32, B = BK / S::GK / 32;
@@ -525,7 +540,7 @@ __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_grad_kernel(Loss 
   auto load_w = [&](int stage, int step, int i) __attribute__((always_inline)) {
     const int64_t v = c0 + (int64_t)(sbeg + step) * 64;
     const rsrc_t rw = make_rsrc(L.a.W + v * K + k0, step < nk ? ((V - v) * K - k0) * 2 : 0);
-    buf_load16_to_lds(rw, st.w[stage] + (wave * ND + i) * 1024, wo[i]);
+    load_to_lds<ONCE>(rw, st.w[stage] + (wave * ND + i) * 1024, wo[i]);
   };
   f32x16 acc[A][B];
 #pragma unroll
@@ -708,7 +723,12 @@ Layout layout(const HeadLossArgs& a, bool grad, char* ws) {
   return l;
 }
 
-template <int BT>
+// Tiles of few tokens read W through once.  From kStreamBytes on they mark these
+// loads so: 16 tokens of 4096, without and with the mark, 187 MiB of W: loss alone 47
+// and 47 us, with the gradient 99 and 97; 250 MiB: 55 and 51, 121 and 115; 1000 MiB:
+// 190 and 169, 422 and 378.  (125 MiB, still in the last cache from the call before:
+// 38 and 44, 73 and 78.)
+template <int BT, bool ONCE>
 hipError_t launch_block(const Layout& l, int b, hipStream_t s) {
   using S = Shape<BT>;
   const Loss& L = l.L;
@@ -720,8 +740,8 @@ hipError_t launch_block(const Layout& l, int b, hipStream_t s) {
     const unsigned grid = 8 * (unsigned)cdiv(tiles_t * cdiv(n, S::BV), 8) + (BT == 256 ? 256 : 0);
     {
       KernelTimer kt_("head_logits_kernel", s);
-      if (grad) hipLaunchKernelGGL((head_logits_kernel<BT, true>), dim3(grid), dim3(64 * S::kWaves), 0, s, L, b, pc);
-      else hipLaunchKernelGGL((head_logits_kernel<BT, false>), dim3(grid), dim3(64 * S::kWaves), 0, s, L, b, pc);
+      if (grad) hipLaunchKernelGGL((head_logits_kernel<BT, true, ONCE>), dim3(grid), dim3(64 * S::kWaves), 0, s, L, b, pc);
+      else hipLaunchKernelGGL((head_logits_kernel<BT, false, ONCE>), dim3(grid), dim3(64 * S::kWaves), 0, s, L, b, pc);
     }
     if (!grad) continue;
     {
@@ -731,7 +751,7 @@ hipError_t launch_block(const Layout& l, int b, hipStream_t s) {
     {
       KernelTimer kt_("head_grad_kernel", s);
       const unsigned g2 = 8 * (unsigned)cdiv((int64_t)tiles_t * cdiv(L.a.K, S::BK), 8);
-      hipLaunchKernelGGL((head_grad_kernel<BT>), dim3(g2 > 256 ? g2 : 256), dim3(64 * S::kWaves), 0, s, L, b, pc);
+      hipLaunchKernelGGL((head_grad_kernel<BT, ONCE>), dim3(g2 > 256 ? g2 : 256), dim3(64 * S::kWaves), 0, s, L, b, pc);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -768,7 +788,9 @@ hipError_t launch_head_loss(const HeadLossArgs& a, void* ws, hipStream_t s) {
                        (int)(l.blocks * l.L.pieces));
   }
   for (int b = 0; b < l.blocks; ++b) {
-    e = small_tiles(a.T) ? launch_block<64>(l, b, s) : launch_block<256>(l, b, s);
+    if (!small_tiles(a.T)) e = launch_block<256, false>(l, b, s);
+    else if (a.V * a.K * 2 >= kStreamBytes) e = launch_block<64, true>(l, b, s);
+    else e = launch_block<64, false>(l, b, s);
     if (e != hipSuccess) return e;
   }
   {

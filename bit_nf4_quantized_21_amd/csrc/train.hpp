@@ -9,6 +9,11 @@
 
 namespace qlora {
 
+// Operands of so many bytes and more that a call reads once, or whose second
+// reading its caches cannot serve, are marked as used once where they are read (three
+// quarters of the last cache, 256 MB: about here the mark begins to pay).
+constexpr int64_t kStreamBytes = (int64_t)192 << 20;
+
 // Softmax cross entropy of T tokens over the rows of a head W [V,K], and its
 // gradient where dX is given.
 struct HeadLossArgs {

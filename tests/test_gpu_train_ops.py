@@ -604,3 +604,37 @@ def test_clip_hundreds_of_megabytes(wide, out_wide):
     if wide == out_wide:
         again = lib.clip_grads(grads, 0.75)          # in place
         assert torch.equal(again, norm) and all(torch.equal(a, b) for a, b in zip(grads, out))
+
+
+@pytest.mark.parametrize("T,K,V", [(1, 4096, 32000), (33, 6656, 16001), (64, 4160, 25007)])
+def test_loss_of_few_tokens_over_a_large_head(T, K, V):
+    """Heads that are read as used once: with and without the gradient, W kept, any start of the contraction."""
+    print(f"loss {T} x {K} over {V}", flush=True)
+    lib = _lib()
+    g = torch.Generator(device="cuda").manual_seed(T)
+    W = (torch.randn(V, K, generator=g, device="cuda") * K ** -0.5).bfloat16()
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    t[0] = V - 1
+    X = (torch.randn(T, K, generator=g, device="cuda") + 3 * W[t].float()).bfloat16()
+    kept = W.clone()
+    loss, lse, mean, dX = lib.head_loss(X, W, t)
+    alone = lib.head_loss(X, W, t, grad=False)
+    x, w, at = X.double(), W.double(), t[:, None]
+    z = x @ w.t()
+    ref_lse = torch.logsumexp(z, 1)
+    ref = ref_lse - z.gather(1, at)[:, 0]
+    p = (z - ref_lse[:, None]).exp_()
+    p.scatter_(1, at, 0.0)
+    p.scatter_(1, at, -p.sum(1, keepdim=True))
+    want = p @ w / T
+    tol = 2 * (K + 2) * E * x.norm(dim=1) * w.norm(dim=1).max() + 2.0 ** -17  # as at full sizes
+    for a in (loss, alone[0]):
+        assert bool(((a.double() - ref).abs() <= tol).all())
+    for a in (lse, alone[1]):
+        assert bool(((a.double() - ref_lse).abs() <= tol + 2.0 ** -22 * ref_lse.abs()).all())
+    assert abs(float(mean) - float(ref.mean())) <= float(tol.max())
+    assert float((dX.double() - want).norm() / want.norm()) <= NORM
+    assert torch.equal(W, kept)
+    again = lib.head_loss(X, W, t)
+    assert torch.equal(again[0], loss) and torch.equal(again[3], dX)
+    lib.device_status()
