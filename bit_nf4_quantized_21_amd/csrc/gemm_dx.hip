@@ -170,10 +170,16 @@ __global__ __launch_bounds__(256, 1) void gemm_dx_kernel(DxGemmParams p, Codeboo
     const int64_t b = ((int64_t)j * 64 + sr) * bpr + skb;
     return __uint_as_float(buf_load4(rs, (uint32_t)((b >> 8) * 4)));
   };
-  // Columns n >= N of the last step read the next row (or zero past the
-  // end): finite values that meet zero W' rows.
+  // Columns n >= N of the last step would be the next token's first ones; they
+  // meet zero W' rows, which an infinity or NaN there would turn into NaN in this
+  // token's row.  So they are zero too: N % 8 == 0, a lane's chunk is whole or
+  // absent, and an absent one's offset is past every view.
   const uint32_t doff = (uint32_t)(xr * N * 2 + 16 * xc);
-  auto load_dy = [&](int j, int i) -> u32x4 { return buf_load16(rd, doff + (uint32_t)(j * 128 + i * 32 * N * 2)); };
+  const uint64_t absent = 0x0101010101010101ull * (N % 64 ? 0xFFu << (N % 64 / 8) & 0xFFu : 0u);  // by lane: xc is lane % 8
+  auto load_dy = [&](int j, int i) -> u32x4 {
+    const bool past = __builtin_amdgcn_inverse_ballot_w64(j == nsteps - 1 ? absent : 0ull);
+    return buf_load16(rd, past ? (uint32_t)-16 : doff + (uint32_t)(j * 128 + i * 32 * N * 2));
+  };
   auto store_row = [&](int base, int i, const u32x4& v) {
     *reinterpret_cast<u32x4*>(smem + base + swz(xr + 32 * i, xc)) = v;
   };

@@ -1,0 +1,50 @@
+"""What calls around a training step must not do: tests that failed on earlier
+kernels, one for each fault."""
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+def _lib():
+    import bit_nf4_quantized_21_amd as lib
+    return lib
+
+
+def _normal(g, *shape, scale=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).bfloat16()
+
+
+def _adapted(g, N, K, r):
+    codes, q8, s2 = _lib().quantize_dq(torch.randn(N, K, generator=g, device="cuda") * 0.05)
+    return dict(codes=codes, q8=q8, s2=s2, A=_normal(g, K, r, scale=K ** -0.5), B=_normal(g, r, N, scale=0.05))
+
+
+@pytest.mark.parametrize("T,N", [(5, 776), (20, 776), (300, 776), (300, 8), (257, 1000), (40, 640)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_input_gradient_of_a_token_is_its_own(T, N, value):
+    """An infinity or NaN in one token's output gradient reaches the input
+    gradient of that token and of no other, whatever features are left over in
+    the last step of 64: bit for bit."""
+    print(f"own row T={T} N={N} {value}", flush=True)
+    lib = _lib()
+    g = torch.Generator(device="cuda").manual_seed(T + N)
+    K, r, alpha = 320, 8, 16.0
+    gate, up = _adapted(g, N, K, r), _adapted(g, N, K, r)
+    X, dH = _normal(g, T, K), _normal(g, T, N)
+    _, saved, XA = lib.gated_fwd(X, gate, up, alpha, save=True)
+    w = (gate["codes"], gate["q8"], gate["s2"], gate["A"], gate["B"], alpha)
+    clean = lib.gated_bwd(dH, X, saved, XA, gate, up, alpha)[0], lib.linear_bwd(dH, X, None, *w)[0]
+    for token in {1, T // 2, T - 1}:
+        for feature in {0, 7, min(N - 1, 50)}:
+            bad = dH.clone()
+            bad[token, feature] = value
+            got = lib.gated_bwd(bad, X, saved, XA, gate, up, alpha)[0], lib.linear_bwd(bad, X, None, *w)[0]
+            others = torch.arange(T, device="cuda") != token
+            for a, b in zip(got, clean):
+                assert torch.equal(a[others], b[others]), (token, feature)
+                assert not bool(torch.isfinite(a[token]).any())
+    lib.device_status()
