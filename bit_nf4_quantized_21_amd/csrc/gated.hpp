@@ -15,7 +15,9 @@ constexpr int kActSilu = 0, kActGelu = 1, kActGeluTanh = 2, kActs = 3;
 
 // act(g) and act'(g).  Sigmoids of large arguments reach 0 and 1 through
 // exponentials that overflow or vanish; the polynomials beside them are held
-// to |g| <= 16, where those have long been reached.
+// to |g| <= 16, where those have long been reached.  A slope's last term takes g
+// itself, not what it is held to (the density is 0 there), so that a g that is no
+// number gives a slope that is none.
 __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
 }
@@ -50,19 +52,19 @@ __device__ __forceinline__ void activation(float g, float& a, float& slope) {
       const float tail = normal_tail(fabsf(c), e);
       const float phi = c < 0.0f ? tail : 1.0f - tail;
       a = g * phi;
-      slope = phi + c * (0.3989422804014327f * e);
+      slope = phi + g * (0.3989422804014327f * e);
     } else {                          // 0.5 (1 + tanh y) is the sigmoid of 2 y
       const float c2 = c * c;
       const float s = sigmoid(c * (1.5957691216057308f + 0.07135481282663148f * c2));
       a = g * s;
-      slope = s + c * s * (1.0f - s) * (1.5957691216057308f + 0.21406443847989444f * c2);
+      slope = s + g * s * (1.0f - s) * (1.5957691216057308f + 0.21406443847989444f * c2);
     }
   }
 }
 
 // A multiplier in 16 bits: sign, 6 bits of exponent, 9 of fraction, which is 10
 // significant bits from 2^-30 up to 2^33 (below, multiples of 2^-39; from there
-// on, infinity), rounded to nearest, ties away from zero.  As bf16 (8 significant
+// on, and for what is no number, infinity), rounded to nearest, ties away from zero.  As bf16 (8 significant
 // bits) the two roundings on the way to a gradient would leave it off by 2.9e-3
 // of the norm; so it is 2.4e-3, its own rounding and that of dG and dU as matrix
 // operands.  multiplier_top leaves the 16 bits in the upper half.

@@ -374,7 +374,8 @@ int qlora_adamw_step(int64_t n, uint16_t* param, float* master, float* m, float*
  *   saved  [2][T][N] 16-bit out, or NULL when no backward follows: what
  *          qlora_gated_bwd multiplies by, act'(G) U and act(G), with 10
  *          significant bits from 2^-30 up to 2^33 (multiples of 2^-39 below,
- *          infinite from there on).
+ *          infinite from there on, and where they are no numbers, so that the
+ *          gradients they enter are not finite).
  *   XA     [2][T][r] fp32 out: X Ag and X Au, for the backward.
  *   workspace of at least qlora_gated_fwd_workspace_bytes(T,K,N,r) bytes.
  * T <= 16 streams both 4-bit weights (decoding); more tokens take the

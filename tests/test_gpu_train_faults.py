@@ -48,3 +48,27 @@ def test_input_gradient_of_a_token_is_its_own(T, N, value):
                 assert torch.equal(a[others], b[others]), (token, feature)
                 assert not bool(torch.isfinite(a[token]).any())
     lib.device_status()
+
+
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("side", ["gate", "up"])
+def test_what_is_no_number_reaches_the_gradients(T, act, side):
+    """Where G or U is no number the kept multipliers are infinite (both where G is,
+    act'(G) U alone where U is), so no gradient they enter comes out finite."""
+    print(f"no number T={T} {act} {side}", flush=True)
+    lib = _lib()
+    g = torch.Generator(device="cuda").manual_seed(T)
+    K, N, r, n = 128, 72, 8, 11
+    gate, up = _adapted(g, N, K, r), _adapted(g, N, K, r)
+    (gate if side == "gate" else up)["B"][:, n] = float("nan")
+    X, dH = _normal(g, T, K), _normal(g, T, N)
+    H, saved, XA = lib.gated_fwd(X, gate, up, 16.0, act=act, save=True)
+    assert bool(torch.isnan(H[:, n]).all()) and bool(torch.isfinite(H[:, :n]).all())
+    infinite = (saved & 0x7FFF) == 0x7FFF
+    assert bool(infinite[0, :, n].all()) and bool(infinite[1, :, n].all()) == (side == "gate")
+    dX, _, dB_gate, _, dB_up = lib.gated_bwd(dH, X, saved, XA, gate, up, 16.0)
+    assert not bool(torch.isfinite(dX).any()) and not bool(torch.isfinite(dB_gate[:, n]).any())
+    assert bool(torch.isfinite(dB_up[:, n]).any()) == (side == "up")
+    assert bool(torch.isfinite(dB_gate[:, :n]).all()) and bool(torch.isfinite(dB_up[:, :n]).all())
+    lib.device_status()
