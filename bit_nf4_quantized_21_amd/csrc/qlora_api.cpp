@@ -87,6 +87,7 @@ const TypeTables* type_tables(int32_t qtype) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 int hip_status(hipError_t e) {
   if (e == hipSuccess) return QLORA_OK;
@@ -557,7 +558,7 @@ int qlora_head_loss(const uint16_t* X, int64_t T, int64_t K, const uint16_t* W, 
   if (!aligned16(mean)) return QLORA_ERR_ALIGN;
   if (T > 0) {
     if (!X || !W || !targets || !loss || !lse) return QLORA_ERR_NULL;
-    if (!aligned16(X) || !aligned16(W) || !aligned16(targets) || !aligned16(dloss) || !aligned16(loss) ||
+    if (!aligned16(X) || !aligned16(W) || !aligned8(targets) || !aligned16(dloss) || !aligned16(loss) ||
         !aligned16(lse) || !aligned16(dX))
       return QLORA_ERR_ALIGN;
     const size_t need = qlora::head_loss_workspace_bytes(T, K, V, dX != nullptr);

@@ -130,6 +130,7 @@ def head_loss(X, W, targets, dloss=None, grad=True, loss=None, lse=None, mean=No
     """Cross entropy of the tokens X [T,K] over the rows of the head W [V,K] (see
     qlora_head_loss); targets int64 [T], a negative one is not learned.
 
+    targets and dloss may be views that start anywhere (labels[1:], weights[1:]).
     dloss: fp32 [T], the gradient of each token's loss; None: that of the mean.
     grad=False leaves dX out.  Returns (loss f32 [T], lse f32 [T], mean f32 [1],
     dX bf16 [T,K] or None)."""
@@ -153,6 +154,12 @@ def head_loss(X, W, targets, dloss=None, grad=True, loss=None, lse=None, mean=No
     elif grad:
         dX = _empty((T, K), torch.bfloat16, X.device, stream)
     _together(X.device, W=W, targets=targets, dloss=dloss, loss=loss, lse=lse, mean=mean, dX=dX, workspace=workspace)
+    if dloss is not None and dloss.data_ptr() % 16:   # the library takes it on 16 bytes
+        if stream is None:
+            dloss = dloss.clone()
+        else:
+            with torch.cuda.stream(stream):           # from and in the order of the call's stream
+                dloss = dloss.clone()
     nbytes = head_loss_workspace_bytes(T, K, V, grad)
     workspace = _workspace(nbytes, X.device, workspace, stream)
     _check(lib().qlora_head_loss(_p(X), T, K, _p(W), V, _p(targets), _p(dloss), _p(loss), _p(lse), _p(mean), _p(dX),

@@ -22,7 +22,8 @@
  * Conventions for every call
  *   - All array pointers are DEVICE pointers (hipMalloc'd or torch CUDA
  *     tensors on the current device) unless stated otherwise; the caller owns
- *     and allocates every buffer.  Every pointer must be 16-byte aligned.
+ *     and allocates every buffer.  Every pointer must be 16-byte aligned where
+ *     the call does not say otherwise.
  *   - bf16 tensors are passed as uint16_t bit patterns.
  *   - `stream` is a hipStream_t passed as void* (NULL = default stream).  All
  *     device work is enqueued asynchronously on it; no call synchronizes.
@@ -49,7 +50,7 @@ typedef enum {
   QLORA_OK = 0,
   QLORA_ERR_NULL = -1,        /* a required pointer is NULL */
   QLORA_ERR_SHAPE = -2,       /* a size is negative, zero where not allowed, or not a required multiple */
-  QLORA_ERR_ALIGN = -3,       /* a pointer is not 16-byte aligned */
+  QLORA_ERR_ALIGN = -3,       /* a pointer is not 16-byte aligned (or as its call says) */
   QLORA_ERR_UNSUPPORTED = -4, /* blocksize != 64 / 256, rank outside [8,128] or not a multiple of 8 */
   QLORA_ERR_HIP = -5,         /* a HIP launch or query failed; see qlora_last_hip_error() */
   QLORA_ERR_WORKSPACE = -6,   /* workspace NULL or smaller than the *_workspace_bytes query */
@@ -429,8 +430,10 @@ int qlora_gated_bwd(int32_t qtype, const uint16_t* dH, const uint16_t* X, const 
  *     p = softmax(z).
  *   X        [T,K] bf16, the tokens' last hidden states.
  *   W        [V,K] bf16, the head.
- *   targets  [T] int64: the token to predict, below V; a negative one (padding,
- *            a prompt) is not learned: its loss, lse and row of dX are zero.
+ *   targets  [T] int64, on 8 bytes (a view of the labels from the second on, the
+ *            shift of every causal model, will do): the token to predict, below
+ *            V; a negative one (padding, a prompt) is not learned: its loss, lse
+ *            and row of dX are zero.
  *            (One of V or more counts as not learned and is reported by
  *            qlora_device_status as QLORA_ERR_INDEX.)
  *   dloss    [T] fp32: the gradient g of each token's loss, or NULL: that of

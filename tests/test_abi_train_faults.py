@@ -1,0 +1,23 @@
+"""What the training step's entry points must not refuse or accept: tests that
+failed on earlier versions, one for each fault (no GPU is touched)."""
+
+import ctypes
+
+import pytest
+
+from bit_nf4_quantized_21_amd import qlora, train
+
+ESHAPE, EALIGN, EWS = -2, -3, -6
+A = 0x10000                       # aligned, never dereferenced: validation fails first
+P = ctypes.c_void_p(A)
+
+
+def test_head_loss_takes_shifted_labels():
+    """targets is read one element at a time: a view on 8 bytes comes as far as the workspace."""
+    L = qlora.lib()
+
+    def f(targets):
+        return L.qlora_head_loss(P, 5, 128, P, 1000, ctypes.c_void_p(targets), None, P, P, P, P, P, 8, None)
+    assert f(A + 8) == EWS and f(A + 24) == EWS and f(A) == EWS
+    for off in (1, 2, 4, 12):
+        assert f(A + off) == EALIGN

@@ -72,3 +72,49 @@ def test_what_is_no_number_reaches_the_gradients(T, act, side):
     assert bool(torch.isfinite(dB_up[:, n]).any()) == (side == "up")
     assert bool(torch.isfinite(dB_gate[:, :n]).all()) and bool(torch.isfinite(dB_up[:, :n]).all())
     lib.device_status()
+
+
+@pytest.mark.parametrize("T", [2, 65, 301])
+@pytest.mark.parametrize("other_stream", [False, True])
+def test_loss_of_shifted_labels(T, other_stream):
+    """labels[1:] and weights[1:], contiguous but off 16 bytes, give what their copies give."""
+    print(f"shifted T={T}", flush=True)
+    lib = _lib()
+    g = torch.Generator(device="cuda").manual_seed(T)
+    X, W = _normal(g, T, 192), _normal(g, 500, 192, scale=0.1)
+    labels = torch.randint(0, 500, (T,), generator=g, device="cuda")
+    labels[T // 2] = -100
+    weights = torch.rand(T, generator=g, device="cuda")
+    want = lib.head_loss(X[:-1], W, labels[1:].clone(), dloss=weights[1:].clone())
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream() if other_stream else None
+    for _ in range(3):
+        got = lib.head_loss(X[:-1], W, labels[1:], dloss=weights[1:], stream=stream)
+        junk = [torch.full((T - 1,), 9.0, device="cuda") for _ in range(8)]     # what was freed may be given away
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del junk
+    assert all(torch.equal(a, b) for a, b in zip(lib.head_loss(X[:-1], W, labels[1:])[:3], want[:3]))
+    lib.device_status()
+
+
+def test_loss_of_shifted_labels_in_a_graph():
+    lib = _lib()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    T = 130
+    X, W = _normal(g, T, 128), _normal(g, 700, 128, scale=0.1)
+    labels = torch.randint(0, 700, (T,), generator=g, device="cuda")
+    weights = torch.rand(T, generator=g, device="cuda")
+    lib.head_loss(X[:-1], W, labels[1:], dloss=weights[1:])      # what is looked up once per process
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = lib.head_loss(X[:-1], W, labels[1:], dloss=weights[1:])
+    for _ in range(4):
+        labels.copy_(torch.randint(0, 700, (T,), generator=g, device="cuda"))
+        weights.copy_(torch.rand(T, generator=g, device="cuda"))
+        want = lib.head_loss(X[:-1], W, labels[1:].clone(), dloss=weights[1:].clone())
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    lib.device_status()
