@@ -57,6 +57,25 @@ def _matrix(t, name):
     return t
 
 
+def _exactly(t, shape, dtype, name):
+    """An input: of these axes and no others (a longer one would be read as if it
+    ended sooner, and every axis after the first from the wrong place)."""
+    if tuple(_dev(t, dtype, name).shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _written(t, shape, dtype, name):
+    """A given output, and as a tensor of `shape` the part of it that is written
+    (the tensor itself where that is all of it)."""
+    if tuple(_given(t, shape, dtype, name).shape) == shape:
+        return t
+    n = 1
+    for x in shape:
+        n *= x
+    return t.view(-1)[:n].view(shape)
+
+
 def gated_fwd_workspace_bytes(T, K, N, r):
     return int(lib().qlora_gated_fwd_workspace_bytes(T, K, N, r))
 
@@ -72,20 +91,21 @@ def gated_fwd(X, gate, up, alpha, act="silu", save=False, H=None, saved=None, XA
 
     act: "silu", "gelu" (erf) or "gelu_tanh".  save=True (or a given `saved`)
     keeps what gated_bwd needs.  Returns (H bf16 [T,N], saved int16 [2,T,N] or
-    None, XA f32 [2,T,r])."""
+    None, XA f32 [2,T,r]); of a given longer `saved` or XA the part that was
+    written, which is what gated_bwd takes."""
     torch = _torch()
     T, K = _matrix(X, "X").shape
     g, u, N, r = _pair(gate, up, X)
     code = _choice(ACTS, act, "act")
     H = _empty((T, N), torch.bfloat16, X.device, stream) if H is None else _given(H, (T, N), torch.bfloat16, "H")
     if saved is not None:
-        _given(saved, (2, T, N), torch.int16, "saved")
+        saved = _written(saved, (2, T, N), torch.int16, "saved")
     elif save:
         saved = _empty((2, T, N), torch.int16, X.device, stream)
     if XA is None:
         XA = _empty((2, T, r), torch.float32, X.device, stream)
     else:
-        _given(XA, (2, T, r), torch.float32, "XA")
+        XA = _written(XA, (2, T, r), torch.float32, "XA")
     _together(X.device, H=H, saved=saved, XA=XA, workspace=workspace)
     nbytes = gated_fwd_workspace_bytes(T, K, N, r)
     workspace = _workspace(nbytes, X.device, workspace, stream)
@@ -103,9 +123,9 @@ def gated_bwd(dH, X, saved, XA, gate, up, alpha, dX=None, dA_gate=None, dB_gate=
     g, u, N, r = _pair(gate, up, X)
     if tuple(_matrix(dH, "dH").shape) != (T, N):
         raise ValueError("dH must be [T,N]")
-    _given(saved, (2, T, N), torch.int16, "saved")
+    _exactly(saved, (2, T, N), torch.int16, "saved")
     if XA is not None:
-        _given(XA, (2, T, r), torch.float32, "XA")
+        _exactly(XA, (2, T, r), torch.float32, "XA")
     outs = []
     for t, shape, name in ((dX, (T, K), "dX"), (dA_gate, (K, r), "dA_gate"), (dB_gate, (r, N), "dB_gate"),
                            (dA_up, (K, r), "dA_up"), (dB_up, (r, N), "dB_up")):
@@ -139,9 +159,9 @@ def head_loss(X, W, targets, dloss=None, grad=True, loss=None, lse=None, mean=No
     V, K2 = _matrix(W, "W").shape
     if K2 != K:
         raise ValueError("X must be [T,K] and W [V,K]")
-    _given(targets, (T,), torch.int64, "targets")
+    _exactly(targets, (T,), torch.int64, "targets")
     if dloss is not None:
-        _given(dloss, (T,), torch.float32, "dloss")
+        _exactly(dloss, (T,), torch.float32, "dloss")
     given = []
     for t, n, name in ((loss, T, "loss"), (lse, T, "lse"), (mean, 1, "mean")):
         given.append(_empty((n,), torch.float32, X.device, stream) if t is None

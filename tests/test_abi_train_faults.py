@@ -21,3 +21,13 @@ def test_head_loss_takes_shifted_labels():
     assert f(A + 8) == EWS and f(A + 24) == EWS and f(A) == EWS
     for off in (1, 2, 4, 12):
         assert f(A + off) == EALIGN
+
+
+@pytest.mark.parametrize("shape", [(6,), (4,), (1, 5), (5, 1), ()])
+def test_inputs_have_exactly_their_axes(monkeypatch, shape):
+    import torch
+    monkeypatch.setattr(train, "_dev", lambda t, dtype, name: t)      # (host tensors)
+    with pytest.raises(ValueError, match="must be"):
+        train._exactly(torch.zeros(shape), (5,), torch.float32, "targets")
+    t = torch.zeros(5)
+    assert train._exactly(t, (5,), torch.float32, "targets") is t

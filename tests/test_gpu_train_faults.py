@@ -118,3 +118,45 @@ def test_loss_of_shifted_labels_in_a_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     lib.device_status()
+
+
+def test_inputs_of_another_length_are_refused():
+    """An input that is too long is no input: T states with T + 1 unshifted labels
+    would pair every token with the wrong word, what was kept for more tokens
+    would be read from the wrong place."""
+    lib = _lib()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    T, K, N, r = 20, 128, 72, 8
+    gate, up = _adapted(g, N, K, r), _adapted(g, N, K, r)
+    X, dH, W = _normal(g, T, K), _normal(g, T, N), _normal(g, 50, K)
+    labels = torch.randint(0, 50, (T + 1,), generator=g, device="cuda")
+    weights = torch.rand(T + 1, generator=g, device="cuda")
+
+    def refused(f, *a, **k):
+        with pytest.raises(ValueError, match="must be"):
+            f(*a, **k)
+    refused(lib.head_loss, X, W, labels)
+    refused(lib.head_loss, X, W, labels[:T - 1])
+    refused(lib.head_loss, X, W, labels[:T].view(1, T))
+    refused(lib.head_loss, X, W, labels[1:], dloss=weights)
+    want = lib.head_loss(X, W, labels[1:].clone(), dloss=weights[:T].clone())
+    assert all(torch.equal(a, b) for a, b in zip(lib.head_loss(X, W, labels[1:], dloss=weights[:T]), want))
+
+    H, saved, XA = lib.gated_fwd(X, gate, up, 16.0, save=True)
+    want = lib.gated_bwd(dH, X, saved, XA, gate, up, 16.0)
+    long_saved = torch.zeros(2 * (T + 5) * N, dtype=torch.int16, device="cuda")
+    long_XA = torch.zeros(2 * (T + 5) * r, device="cuda")
+    for shape in ((2, T + 5, N), (-1,), (T + 5, 2 * N)):
+        refused(lib.gated_bwd, dH, X, long_saved.view(shape), XA, gate, up, 16.0)
+    for shape in ((2, T + 5, r), (-1,)):
+        refused(lib.gated_bwd, dH, X, saved, long_XA.view(shape), gate, up, 16.0)
+    # A buffer kept for more tokens is written at its start, and that part comes back.
+    H2, part, partXA = lib.gated_fwd(X, gate, up, 16.0, saved=long_saved, XA=long_XA)
+    assert part.shape == (2, T, N) and partXA.shape == (2, T, r)
+    assert part.data_ptr() == long_saved.data_ptr() and partXA.data_ptr() == long_XA.data_ptr()
+    assert torch.equal(part, saved) and torch.equal(partXA, XA) and torch.equal(H2, H)
+    assert not bool(long_saved[2 * T * N:].any()) and not bool(long_XA[2 * T * r:].any())
+    assert all(torch.equal(a, b) for a, b in zip(lib.gated_bwd(dH, X, part, partXA, gate, up, 16.0), want))
+    same = lib.gated_fwd(X, gate, up, 16.0, saved=saved, XA=XA)
+    assert same[1] is saved and same[2] is XA
+    lib.device_status()
