@@ -9,11 +9,12 @@
 //
 // Two matrix products, not three: the exponentials are taken relative to a
 // reference that is known before the logits are, so the first product writes
-// exp(z_j - ref) in bf16 at once and the second multiplies it by W; what the
-// sum and its scale are is applied to the result.  The reference is the
-// target's own logit (one dot product per token).  Tiles whose largest logit
-// is more than kLift above it take their own maximum and are reported; a
-// small kernel then brings their rows to one reference again.  So a step
+// exp(z_j) / 2^ref in bf16 at once and the second multiplies it by W; what the
+// sum and its scale are is applied to the result.  The reference is the power of
+// two next to the target's exponential (one dot product per token).  Tiles whose
+// largest exponential is more than kLift powers above it take that one's own and
+// are reported; a small kernel then brings their rows to one reference again,
+// without rounding, since references are whole powers of two.  So a step
 // costs 4 T K V operations where a loss and a later gradient that recomputes
 // the logits would cost 6, and the target's term is left out of the
 // exponentials: its weight 1 - p_t is the sum of the others, which keeps its
@@ -47,8 +48,8 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int64_t kBlockTokens = 4096;
 constexpr int64_t kPieceBytes = int64_t(128) << 20;
-constexpr float kLift = 40.0f;       // e^40 leaves e^48 of fp32's range for sums and weights
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLift = 58.0f;       // 2^58 leaves 2^69 of fp32's range for sums and weights
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
@@ -59,10 +60,10 @@ struct Loss {
   int32_t* list;    // [T] tokens that are learned, ascending
   int32_t* count;   // [1] their number
   float* tz;        // [T] the target's logit
-  float* ref;       // [T] what the token's exponentials are relative to
-  int32_t* lifted;  // [T] the largest logit of a lifted tile, as an ordered integer
+  float* ref;       // [T] the power of two that the token's exponentials are relative to
+  int32_t* lifted;  // [T] the largest reference of a lifted tile, as an ordered integer
   int32_t* flags;   // [blocks * pieces] whether any tile of the piece was lifted
-  float2* stats;    // [block][nstat] (reference, sum) of each row and stretch of kStat columns
+  float2* stats;    // [block][nstat] (reference, sum) of each row and stretch of its columns
   uint16_t* P;      // [block][pitch] exponentials
   float* acc;       // [slabs][rows][K] sum of exponentials times W
   int64_t block;    // tokens of a block
@@ -81,7 +82,14 @@ __device__ __forceinline__ int32_t ordered(float x) {
 __device__ __forceinline__ float from_ordered(int32_t i) { return __uint_as_float((uint32_t)(i ^ ((i >> 31) & 0x7FFFFFFF))); }
 constexpr int32_t kNotLifted = INT32_MIN;
 
-__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+// The reference of a logit: the whole power of two next to its exponential.
+__device__ __forceinline__ float ref_of(float z) { return rintf(z * kLog2e); }
+// 2^d, exactly, for the whole d <= 0 by which references differ (0 where it would
+// be far below every sum; no number if d is none).
+__device__ __forceinline__ float pow2(float d) {
+  const float x = __builtin_amdgcn_ldexpf(1.0f, (int)fmaxf(d, -300.0f));
+  return d == d ? x : d;
+}
 
 // Rows of block b that are learned.
 __device__ __forceinline__ int rows_of(const Loss& L, int64_t b) {
@@ -152,7 +160,7 @@ __global__ __launch_bounds__(1024) void head_begin_kernel(Loss L, int nflags) {
   if (on && at == 0) {
     const float z = part[wave] + part[wave + 1] + part[wave + 2] + part[wave + 3];
     L.tz[t] = z;
-    L.ref[t] = z;
+    L.ref[t] = ref_of(z);
     L.lifted[t] = kNotLifted;
   }
 }
@@ -369,21 +377,18 @@ __device__ __forceinline__ void logits_tile(const Loss& L, int b, int pc, int ro
 #pragma unroll
       for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[a][c][e]);
     m = fmaxf(m, __shfl_xor(m, 32, 64));
-    const bool lift = ok && m - base > kLift;
-    const float ref = lift ? m : base;
+    const bool lift = ok && m * kLog2e - base > kLift;
+    const float ref = lift ? ref_of(m) : base;
     if (GRAD && lift && h == 0) {
-      atomicMax(L.lifted + t, ordered(m));
+      atomicMax(L.lifted + t, ordered(ref));
       atomicOr(L.flags + b * L.pieces + pc, 1);
     }
-    // (One rounding of ref log2 e for all of a token's exponentials: as if ref
-    // were off by half its last bit.)
-    const float ref2 = ref * kLog2e;
     float sum = 0.0f;
 #pragma unroll
     for (int a = 0; a < A; ++a)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        acc[a][c][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[a][c][e], kLog2e, -ref2));
+        acc[a][c][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[a][c][e], kLog2e, -ref));
         sum += acc[a][c][e];
       }
     sum += __shfl_xor(sum, 32, 64);
@@ -456,7 +461,8 @@ __global__ __launch_bounds__(64 * Shape<BT>::kWaves) void head_logits_kernel(Los
 }
 
 // Rows of a piece with a lifted tile: every stretch of exponentials and what
-// was summed before are brought to the row's new reference.
+// was summed before are brought to the row's new reference (by powers of two: no
+// value is rounded again).
 template <int BT>
 __global__ __launch_bounds__(256) void head_lift_kernel(Loss L, int b, int pc) {
   if (L.flags[b * L.pieces + pc] == 0) return;
@@ -470,7 +476,7 @@ __global__ __launch_bounds__(256) void head_lift_kernel(Loss L, int b, int pc) {
     __syncthreads();  // everyone has read them
     if (o == kNotLifted || !(now > old)) continue;
     for (int64_t c = c0 + threadIdx.x * 8; c < c1; c += 256 * 8) {
-      const float f = exp_of(L.stats[(int64_t)i * L.nstat + c / kStretch].x - now);
+      const float f = pow2(L.stats[(int64_t)i * L.nstat + c / kStretch].x - now);
       u32x4* p = reinterpret_cast<u32x4*>(L.P + (int64_t)i * L.pitch + (c - c0));
       u32x4 v = *p;
 #pragma unroll
@@ -478,7 +484,7 @@ __global__ __launch_bounds__(256) void head_lift_kernel(Loss L, int b, int pc) {
       *p = v;
     }
     if (pc > 0) {
-      const float f = exp_of(old - now);
+      const float f = pow2(old - now);
       for (int s = 0; s < nslabs; ++s)
         for (int64_t k = threadIdx.x; k < K; k += 256) L.acc[((int64_t)s * rows + i) * K + k] *= f;
     }
@@ -611,16 +617,19 @@ __global__ __launch_bounds__(256) void head_finish_kernel(Loss L, int b) {
   float sum = 0.0f;
   for (int j = tid; j < L.nstat; j += 256) {
     const float2 s = L.stats[(int64_t)i * L.nstat + j];
-    sum += s.y * exp_of(s.x - ref);
+    sum += s.y * pow2(s.x - ref);
   }
 #pragma unroll
   for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
   if ((tid & 63) == 0) red[tid >> 6] = sum;
   __syncthreads();
   const float rest = red[0] + red[1] + red[2] + red[3];
-  const float own = exp_of(tz - ref), total = rest + own;
+  // The target's exponential is 2^(ref0 + part), part within half a power (held to
+  // it where logits are so large that fp32 has no fractions of one).
+  const float ref0 = ref_of(tz), part = __builtin_amdgcn_fmed3f(__builtin_fmaf(tz, kLog2e, -ref0), -0.5f, 0.5f);
+  const float own = __builtin_amdgcn_exp2f(part) * pow2(ref0 - ref), total = rest + own;
   if (tid == 0) {
-    const float loss = ref == tz ? log1pf(rest) : (ref - tz) + logf(total);
+    const float loss = ref == ref0 ? log1pf(rest / own) : __builtin_fmaf(ref - ref0, kLn2, logf(total) - part * kLn2);
     L.a.loss[t] = loss;
     L.a.lse[t] = tz + loss;
   }

@@ -450,8 +450,9 @@ int qlora_gated_bwd(int32_t qtype, const uint16_t* dH, const uint16_t* X, const 
  *            vocabulary and 4096 tokens), 4096 K 4 bytes or 64 MB of sums, and
  *            8 bytes for every 128 (T <= 64: 32) logits of 4096 tokens.
  * Only learned tokens are multiplied.  Logits and sums are fp32.  The
- * exponentials, relative to the target's, enter the product with W as bf16, so
- * dX is off by at most the square root of two times its own rounding; the
+ * exponentials, relative to a power of two, enter the product with W as bf16,
+ * each rounded once, so dX is off by at most the square root of two times its
+ * own rounding (root mean square); the
  * target's weight 1 - p is the sum of the others', so it keeps its digits for
  * tokens that are nearly certain.  Deterministic.
  */

@@ -160,3 +160,39 @@ def test_inputs_of_another_length_are_refused():
     same = lib.gated_fwd(X, gate, up, 16.0, saved=saved, XA=XA)
     assert same[1] is saved and same[2] is XA
     lib.device_status()
+
+
+@pytest.mark.parametrize("T", [20, 300])
+def test_exponentials_of_lifted_rows_are_rounded_once(T):
+    """Every stretch of words lies far above the target, each by another amount, so
+    all of them take references of their own and are then brought to one.  Each
+    word has a column of its own, so that an element of dX is one exponential times
+    a power of two: it is off by that exponential's rounding to bf16 and its own,
+    u = 2^-8 each, and 2^-15 for what happens in fp32 (arguments up to 58 powers of
+    two, an exponential and a division to an ulp, a sum of 640 terms)."""
+    print(f"lifted T={T}", flush=True)
+    lib = _lib()
+    V = K = 640
+    g = torch.Generator(device="cuda").manual_seed(T)
+    W = (2 * torch.eye(V, device="cuda")).bfloat16()
+    X = (10 + 6 * torch.rand(T, K, generator=g, device="cuda")).bfloat16()        # logits of 20 to 32
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    rows = torch.arange(T, device="cuda")
+    X[rows, t] = -15.0
+    loss, lse, mean, dX = lib.head_loss(X, W, t)
+    z = 2 * X.double()
+    p = torch.softmax(z, 1)
+    rest = p.clone()
+    rest[rows, t] = 0
+    want = 2 * rest / T
+    want[rows, t] = -2 * rest.sum(1) / T
+    u = 2.0 ** -8
+    off = (dX.double() - want).abs() / want.abs()
+    print(float(off.max()) / u)
+    assert float(off.max()) <= (1 + u) ** 2 - 1 + 2.0 ** -15
+    ref = torch.logsumexp(z, 1)
+    # Logits are exact; 2^-17 for exponentials and sum, and 4 roundings of the result.
+    assert bool(((loss.double() - (ref + 30)).abs() <= 2.0 ** -17 + 2.0 ** -22 * (ref + 30)).all())
+    alone = lib.head_loss(X, W, t, grad=False)
+    assert torch.equal(alone[0], loss) and torch.equal(alone[1], lse) and torch.equal(alone[2], mean)
+    lib.device_status()
