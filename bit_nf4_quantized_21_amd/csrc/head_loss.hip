@@ -629,9 +629,12 @@ __global__ __launch_bounds__(256) void head_finish_kernel(Loss L, int b) {
   const float ref0 = ref_of(tz), part = __builtin_amdgcn_fmed3f(__builtin_fmaf(tz, kLog2e, -ref0), -0.5f, 0.5f);
   const float own = __builtin_amdgcn_exp2f(part) * pow2(ref0 - ref), total = rest + own;
   if (tid == 0) {
-    const float loss = ref == ref0 ? log1pf(rest / own) : __builtin_fmaf(ref - ref0, kLn2, logf(total) - part * kLn2);
+    // Each from what it is made of: beside a target far below the others, lse has
+    // digits that the loss has lost.
+    const bool near = ref == ref0;
+    const float loss = near ? log1pf(rest / own) : __builtin_fmaf(ref - ref0, kLn2, logf(total) - part * kLn2);
     L.a.loss[t] = loss;
-    L.a.lse[t] = tz + loss;
+    L.a.lse[t] = near ? tz + loss : __builtin_fmaf(ref, kLn2, logf(total));
   }
   if (!L.a.dX) return;
   const float g = L.a.dloss ? L.a.dloss[t] : 1.0f / (float)*L.count;

@@ -196,3 +196,25 @@ def test_exponentials_of_lifted_rows_are_rounded_once(T):
     alone = lib.head_loss(X, W, t, grad=False)
     assert torch.equal(alone[0], loss) and torch.equal(alone[1], lse) and torch.equal(alone[2], mean)
     lib.device_status()
+
+
+@pytest.mark.parametrize("T,far", [(20, 1e4), (300, 1e4), (70, 1e6), (7, 1e8)])
+def test_log_sum_beside_a_target_far_below(T, far):
+    """The log-sum is that of the other words, whose logits lie between 20 and 32: off
+    by 2^-17 for exponentials and sum and by 2^-22 of itself, however large the loss."""
+    print(f"far target T={T} {far}", flush=True)
+    lib = _lib()
+    V = K = 640
+    g = torch.Generator(device="cuda").manual_seed(T)
+    W = (2 * torch.eye(V, device="cuda")).bfloat16()
+    X = (10 + 6 * torch.rand(T, K, generator=g, device="cuda")).bfloat16()
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    X[torch.arange(T, device="cuda"), t] = -far / 2
+    z = 2 * X.double()
+    ref = torch.logsumexp(z, 1)
+    want = ref - z.gather(1, t[:, None])[:, 0]
+    for grad in (True, False):
+        loss, lse, _, _ = lib.head_loss(X, W, t, grad=grad)
+        assert bool(((lse.double() - ref).abs() <= 2.0 ** -17 + 2.0 ** -22 * ref).all())
+        assert bool(((loss.double() - want).abs() <= 2.0 ** -17 + 2.0 ** -22 * want).all())
+    lib.device_status()
