@@ -216,9 +216,10 @@ class GradSet:
             kinds = _grad_type(g, "a gradient"), _grad_type(o, "an output")
             if o.numel() != g.numel():
                 raise ValueError(f"output {i} holds {o.numel()} values, its gradient {g.numel()}")
-            if device is not None and (g.device, o.device) != (device, device):
+            if device is None:
+                device = g.device
+            if (g.device, o.device) != (device, device):
                 raise ValueError("all gradients and outputs must be on one GPU")
-            device = g.device
             self.descs[i] = Grad(g.data_ptr(), o.data_ptr(), g.numel(), *kinds)
         self.device = device
         self.workspace_bytes = clip_grads_workspace_bytes(len(self.grads))

@@ -31,3 +31,26 @@ def test_inputs_have_exactly_their_axes(monkeypatch, shape):
         train._exactly(torch.zeros(shape), (5,), torch.float32, "targets")
     t = torch.zeros(5)
     assert train._exactly(t, (5,), torch.float32, "targets") is t
+
+
+class _OnGPU:
+    """What GradSet looks at in a tensor on one of several GPUs."""
+
+    def __init__(self, index, n=4):
+        import torch
+        self.device, self._n = torch.device("cuda", index), n
+
+    def numel(self):
+        return self._n
+
+    def data_ptr(self):
+        return A
+
+
+@pytest.mark.parametrize("grads,outs", [((0,), (1,)), ((1,), (0,)), ((0, 0), (1, 0)), ((0, 1), (0, 1)), ((0, 0), (0, 1))])
+def test_gradients_and_outputs_on_two_gpus_are_refused(monkeypatch, grads, outs):
+    """The first gradient's output, too."""
+    monkeypatch.setattr(train, "_grad_type", lambda t, name: 0)
+    with pytest.raises(ValueError, match="one GPU"):
+        train.GradSet([_OnGPU(i) for i in grads], [_OnGPU(i) for i in outs])
+    train.GradSet([_OnGPU(1), _OnGPU(1)], [_OnGPU(1), _OnGPU(1)])
