@@ -10,10 +10,9 @@
 // two kernels directly, more are first written to the workspace by launches that
 // do nothing else.  Both kernels see one row of chunks of kChunk values over all
 // tensors, and each workgroup takes a run of neighbours: it looks its first
-// tensor up and then only steps on.  Squares are summed eight at a time
-// in fp32 and from there on in fp64; each workgroup leaves one partial, and every
-// workgroup of the second kernel adds the partials in the same order, so the
-// result does not depend on timing.  The second kernel walks its
+// tensor up and then only steps on.  Squares are summed in fp64; each workgroup
+// leaves one partial, and every workgroup of the second kernel adds the partials
+// in the same order, so the result does not depend on timing.  The second kernel walks its
 // run backwards: what the first read last is still in the caches.
 //
 // Bound by memory: two reads and a write.  448 gradients of 216 M bf16 values:
@@ -167,14 +166,10 @@ __device__ __forceinline__ bool on16(const void* p) { return (reinterpret_cast<u
 
 constexpr int kVecs = kChunk / (8 * kThreads);  // groups of eight values of a thread in a whole chunk
 
-// The squares of eight values: summed in fp32 where neither overflow nor what
-// underflows could be seen in the sum (the smallest square is then below 2^-24 of
-// it), else in fp64.  fp64 conversions for every value took as long as the memory.
+// The squares of eight values.  (Summed in fp32, eight at a time, where they are in
+// its range, they take as long: the norm of 226 M values, in fp32 and in fp64, bf16
+// 88.1 and 88.4 us, fp32 162.6 and 161.1; of 67 M fp32 values 43.9 and 45.0.)
 __device__ __forceinline__ double squares8(const float (&v)[8]) {
-  float s = v[0] * v[0];
-#pragma unroll
-  for (int q = 1; q < 8; ++q) s = __builtin_fmaf(v[q], v[q], s);
-  if (s > 1e-30f && s < 1e30f) return (double)s;
   double x = 0.0;
 #pragma unroll
   for (int q = 0; q < 8; ++q) x += square(v[q]);

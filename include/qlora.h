@@ -465,8 +465,7 @@ int qlora_head_loss(const uint16_t* X, int64_t T, int64_t K, const uint16_t* W, 
  * Global norm of many gradients, and clipping (QLoRA project page, challenges:
  * gradient clipping keeps training stable), where the gradients of a model's
  * adapters are tensors of their own:
- *     |g| = sqrt(sum of all values' squares)     (eight at a time in fp32 where
- *            they are in its range, then fp64, in a fixed order)
+ *     |g| = sqrt(sum of all values' squares)     (fp64, in a fixed order)
  *     out = c g,   c = min(1, max_norm / (|g| + 1e-6)).
  *   grads      host array of `count` descriptors (0 <= count <= 65536):
  *     grad     n values (n >= 0), bf16 or fp32 (type), aligned to its elements

@@ -218,3 +218,32 @@ def test_log_sum_beside_a_target_far_below(T, far):
         assert bool(((lse.double() - ref).abs() <= 2.0 ** -17 + 2.0 ** -22 * ref).all())
         assert bool(((loss.double() - want).abs() <= 2.0 ** -17 + 2.0 ** -22 * want).all())
     lib.device_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_norm_of_equal_values_is_rounded_once(dtype):
+    """Roundings that all go the same way add up: of many equal values the norm is
+    off by its own rounding, 2^-24, and what fp64 leaves (50000 terms of 2^-53)."""
+    lib = _lib()
+    n = 50000
+    for i in range(40):
+        v = torch.full((n,), 1.0 + i / 41, device="cuda").to(dtype)
+        ref = float(n ** 0.5 * v[0].double())
+        assert abs(float(lib.clip_grads([v], 0.0)) - ref) <= 2.0 ** -24 * (1 + 2.0 ** -12) * ref, i
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_clip_of_gradients_that_are_all_zero(dtype):
+    """As every dA is while B = 0: the norm is that of the others, and all stay as they are said."""
+    lib = _lib()
+    zeros = [torch.zeros(n, dtype=dtype, device="cuda") for n in (70000, 3, 16384)]
+    others = [torch.full((n,), 2.0, dtype=dtype, device="cuda") for n in (4, 60000)]
+    assert float(lib.clip_grads(zeros, 1.0)) == 0 and not any(bool(z.any()) for z in zeros)
+    norm = lib.clip_grads(zeros + others, 1.0)
+    ref = 2 * 60004 ** 0.5
+    assert abs(float(norm) - ref) <= 2.0 ** -24 * 1.01 * ref
+    assert not any(bool(z.any()) for z in zeros)
+    want = 2 / ref
+    half = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8
+    for o in others:   # the coefficient in fp32 (2^-24), the product in fp32, its rounding; 1e-6 beside the norm
+        assert bool(((o.double() - want).abs() <= (half + 2 * 2.0 ** -24 + 1e-6 / ref) * want).all())
