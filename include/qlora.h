@@ -445,16 +445,19 @@ int qlora_gated_bwd(int32_t qtype, const uint16_t* dH, const uint16_t* X, const 
  *   0 <= T <= 2^23 (0: mean is set to 0), K a multiple of 64 in [64, 2^20],
  *   1 <= V <= 2^30; T*K*2 bytes below 2^31, T * ceil(V / 32) below 2^31.
  *   Outputs must not overlap inputs.
- *   workspace  qlora_head_loss_workspace_bytes(T,K,V,dX != NULL) bytes: with a
- *            gradient at most 128 MB of exponentials (of a piece of the
- *            vocabulary and 4096 tokens), 4096 K 4 bytes or 64 MB of sums, and
- *            8 bytes for every 128 (T <= 64: 32) logits of 4096 tokens.
+ *   workspace  qlora_head_loss_workspace_bytes(T,K,V,dX != NULL) bytes.  With B
+ *            the smaller of T and 4096 these are at most 16 a token, 8 for
+ *            every 128 (T <= 64: 32) words of B tokens, and 256 for each of nine
+ *            arrays' ends; with a gradient also 129 MiB of exponentials (B tokens
+ *            and a piece of the vocabulary), 4 for each piece of every 4096
+ *            tokens, of which there are V B / 2^25 + 1 at most, and 4 B K or
+ *            64 MiB of sums, whichever is more.
  * Only learned tokens are multiplied.  Logits and sums are fp32.  The
  * exponentials, relative to a power of two, enter the product with W as bf16,
  * each rounded once, so dX is off by at most the square root of two times its
- * own rounding (root mean square); the
- * target's weight 1 - p is the sum of the others', so it keeps its digits for
- * tokens that are nearly certain.  Deterministic.
+ * own rounding (root mean square).  The target's weight 1 - p is the sum of the
+ * others', so it keeps its digits for tokens that are nearly certain.
+ * Deterministic.
  */
 size_t qlora_head_loss_workspace_bytes(int64_t T, int64_t K, int64_t V, int32_t with_grad);
 int qlora_head_loss(const uint16_t* X, int64_t T, int64_t K, const uint16_t* W, int64_t V, const int64_t* targets,

@@ -54,3 +54,18 @@ def test_gradients_and_outputs_on_two_gpus_are_refused(monkeypatch, grads, outs)
     with pytest.raises(ValueError, match="one GPU"):
         train.GradSet([_OnGPU(i) for i in grads], [_OnGPU(i) for i in outs])
     train.GradSet([_OnGPU(1), _OnGPU(1)], [_OnGPU(1), _OnGPU(1)])
+
+
+@pytest.mark.parametrize("T", [1, 17, 64, 65, 100, 512, 2048, 4095, 4096, 4097, 10000])
+def test_head_loss_workspace_is_what_the_header_says(T):
+    f = qlora.lib().qlora_head_loss_workspace_bytes
+    for K in (64, 4096, 8192, 65536):
+        for V in (1, 31, 1000, 16384, 32000, 50021, 128000, 1 << 20, 1 << 25):
+            if T * K * 2 >= 1 << 31 or T * -(-V // 32) >= 1 << 31:
+                continue
+            B = min(T, 4096)
+            plain = 16 * T + 8 * B * -(-V // (32 if T <= 64 else 128)) + 9 * 256
+            # (A call without a gradient takes the vocabulary in one piece.)
+            assert 0 < f(T, K, V, 0) <= plain + 4 * -(-T // 4096), (T, K, V)
+            pieces = 4 * (V * B // (1 << 25) + 1) * -(-T // 4096)
+            assert 0 < f(T, K, V, 1) <= plain + (129 << 20) + pieces + max(4 * B * K, 64 << 20), (T, K, V)

@@ -247,3 +247,35 @@ def test_clip_of_gradients_that_are_all_zero(dtype):
     half = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8
     for o in others:   # the coefficient in fp32 (2^-24), the product in fp32, its rounding; 1e-6 beside the norm
         assert bool(((o.double() - want).abs() <= (half + 2 * 2.0 ** -24 + 1e-6 / ref) * want).all())
+
+
+def test_clip_of_hundreds_of_tensors_in_a_graph():
+    """More tensors than the kernels' arguments hold: their table is written to the
+    workspace by launches of its own, in a captured call on every replay."""
+    lib = _lib()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    lengths = [1 + (i * 7919) % 5000 for i in range(300)]
+    kinds = [torch.float32 if i % 3 else torch.bfloat16 for i in range(300)]
+    grads = [torch.randn(n, generator=g, device="cuda").to(k) for n, k in zip(lengths, kinds)]
+    flat = torch.zeros(sum(lengths), dtype=torch.bfloat16, device="cuda")
+    out = list(flat.split(lengths))
+    other = [torch.zeros_like(x) for x in grads]
+    lib.clip_grads(grads, 0.5, out=out)      # what is looked up once per process
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm = lib.clip_grads(grads, 0.5, out=out)
+        norm2 = lib.clip_grads(other, 0.5)
+    for i in range(4):
+        for x, y in zip(grads, other):
+            x.copy_(torch.randn(x.shape, generator=g, device="cuda") * 10.0 ** -i)
+            y.copy_(x)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = flat.clone()
+        want = torch.zeros_like(flat)
+        assert torch.equal(lib.clip_grads(grads, 0.5, out=list(want.split(lengths))), norm)
+        assert torch.equal(got, want) and torch.equal(norm, norm2)
+        lib.clip_grads(grads, 0.5)
+        assert all(torch.equal(x, y) for x, y in zip(grads, other))
