@@ -42,7 +42,7 @@
 // PAIR: the sum of two linears' input gradients (the gate and up linears of a
 // gated feed-forward block, which share their input): the contraction runs
 // over the rows of the first, then of the second, into the same accumulators
-// (512 tokens, 8192 <- 22016: 0.35 ms, 1070 TFLOP/s).
+// (512 tokens, 8192 <- 22016: 0.354 ms, 1040 TFLOP/s).
 #include "common.hpp"
 #include "timing.hpp"
 #include "gemm.hpp"

@@ -47,7 +47,7 @@
 // 32 features of the gate's and of the up's weight, so both sums of an output
 // meet in one lane, and H = act(G) U (and the multipliers that the backward
 // needs) is computed from the fp32 sums; neither G nor U is written.  4096 tokens
-// 6656 -> 17920: 1.71 ms, 1160 TFLOP/s; a tile's start and end take 24 us beside
+// 6656 -> 17920: 1.66 ms, 1180 TFLOP/s; a tile's start and end take 24 us beside
 // 1.72 for each of its steps (adapters 8, stores 6, activation 4).
 #include "common.hpp"
 #include "gated.hpp"

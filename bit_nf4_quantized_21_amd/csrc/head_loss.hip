@@ -29,7 +29,7 @@
 // logits, sums and the products' accumulation are fp32.
 //
 // Bound by matrix instructions and power: 4096 tokens of 4096 (a tenth not
-// learned) over 128000 words take 6.7 ms, 1150 TFLOP/s, with the matrix units
+// learned) over 128000 words take 6.8 ms, 1130 TFLOP/s, with the matrix units
 // busy 74 % (first product) and 62 % (second, 240 tiles on 256 compute units) of
 // the clocks at 1.9 GHz; a step of 64 values takes 1.55 and 1.62 us, that of the
 // library's 8192^3 product 1.53.  Few tokens: memory, 262 MB of W in 43 us, 6.1 TB/s.

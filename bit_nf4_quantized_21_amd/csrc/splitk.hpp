@@ -166,9 +166,12 @@ inline SplitPlan make_split_plan(int64_t tiles, int64_t steps) {
 }
 
 // The plan of a gated pair's GEMMs: split only where that leaves a workgroup more
-// than 15 steps less to do, since the hand-off costs as much (257 tokens x 776
-// features, forward, in one slice and in four: K = 1024 45.8 and 49.2 us, K = 1536
-// 54.0 and 51.9, K = 4096 95.7 and 62.4).
+// than 15 steps less to do, since the hand-off costs about as much.  In one slice and
+// in four, us a call, steps of 64 saved in parentheses: forward, 257 tokens x 776
+// features, 47.2 and 50.6 (12), 55.8 and 53.9 (18), 96.3 and 67.2 (48); 512 x 4096,
+// which takes 64 tiles instead of 14, 50.4 and 60.2 (12), 60.9 and 64.4 (18), 70.1 and
+// 66.6 (24); backward, 512 x 4096 inputs, 62.2 and 64.2 (9), 67.8 and 62.8 (12), 79.4
+// and 66.5 (18).  So 15 is a middle: within 7 % of the better one on either side.
 inline SplitPlan make_pair_plan(int64_t tiles, int64_t steps) {
   SplitPlan pl = make_split_plan(tiles, steps);
   if (pl.S > 1 && pl.steps - pl.steps_per <= 15) {
